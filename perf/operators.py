@@ -185,9 +185,9 @@ def _log_softmax_stats(logits, t):
     y = logits.float() / t
     top = y.amax(1, keepdim=True)
     top = torch.where(top == -math.inf, torch.zeros_like(top), top)
-    lse = (y - top).exp().sum(1).log() + top[:, 0]
-    empty = lse == -math.inf
-    log_q = y - torch.where(empty, torch.zeros_like(lse), lse)[:, None]
+    total = (y - top).exp().sum(1).log()  # -inf where the row is empty
+    lse = total + top[:, 0]
+    log_q = (y - top) - torch.where(total == -math.inf, torch.zeros_like(total), total)[:, None]
     q = log_q.exp()
     entropy = -torch.where(y == -math.inf, torch.zeros_like(q), q * log_q).sum(1)
     return {"y": y, "lse": lse, "q": q, "log_q": log_q, "entropy": entropy}
@@ -202,7 +202,7 @@ def _top_plain(logits, s, k):
     key = (order << 32) + (0x7FFFFFFF - torch.arange(vocab, device=logits.device))
     count = min(k, vocab)
     index = 0x7FFFFFFF - (torch.topk(key, count, dim=1).values & 0xFFFFFFFF)
-    value = s["y"].gather(1, index) - s["lse"][:, None]
+    value = s["log_q"].gather(1, index)
     none = s["y"].gather(1, index) == -math.inf
     top_logprob = torch.full((logits.shape[0], k), -math.inf, device=logits.device)
     top_index = torch.full((logits.shape[0], k), -1, dtype=torch.int32, device=logits.device)
@@ -217,9 +217,8 @@ def _logprobs_plain(state):
     s = _log_softmax_stats(logits, case["temperature"])
     given = (tokens >= 0) & (tokens < vocab)
     at = tokens.clamp(0, vocab - 1)[:, None]
-    y = s["y"].gather(1, at)[:, 0]
-    logprob = torch.where(y == -math.inf, y, y - s["lse"])
-    out = {"logprob": torch.where(given, logprob, torch.zeros_like(y)), "lse": s["lse"]}
+    logprob = s["log_q"].gather(1, at)[:, 0]
+    out = {"logprob": torch.where(given, logprob, torch.zeros_like(logprob)), "lse": s["lse"]}
     if case["entropy"]:
         out["entropy"] = s["entropy"]
     if case["op"] == "logprobs" and case["k"]:
@@ -245,9 +244,12 @@ def _logprobs_gradient_plain(state, lse=None, entropy=None):
         factor = factor + state["d_entropy"][:, None] * spread
         live = live | (state["d_entropy"] != 0)
     grad = -q * factor
+    # at the token itself 1 - q without cancellation
     at = tokens.clamp(0, vocab - 1)[:, None]
-    hit = torch.where(log_q.gather(1, at)[:, 0] == -math.inf, torch.zeros_like(weight), weight)
-    grad.scatter_add_(1, at, hit[:, None])
+    own_log_q = log_q.gather(1, at)[:, 0]
+    hit = grad.gather(1, at)[:, 0] + weight * q.gather(1, at)[:, 0] - weight * torch.expm1(own_log_q)
+    hit = torch.where(own_log_q == -math.inf, torch.zeros_like(hit), hit)
+    grad.scatter_(1, at, torch.where(given, hit, grad.gather(1, at)[:, 0])[:, None])
     grad = torch.where((live & (lse != -math.inf))[:, None], grad / t, torch.zeros_like(grad))
     return grad.to(logits.dtype)
 
@@ -265,8 +267,7 @@ def _distill_plain(logits, teacher, index, t, tail):
     else:
         top = z.amax(1, keepdim=True)
         top = torch.where(top == -math.inf, torch.zeros_like(top), top)
-        total = (z - top).exp().sum(1, keepdim=True).log() + top
-        log_p = torch.where(z == -math.inf, z, z - total)
+        log_p = torch.where(z == -math.inf, z, (z - top) - (z - top).exp().sum(1, keepdim=True).log())
     p = log_p.exp()
     y = logits.float() / t
     inside = torch.zeros(logits.shape[0], vocab + 1, dtype=torch.bool, device=logits.device)
@@ -275,33 +276,42 @@ def _distill_plain(logits, teacher, index, t, tail):
     top = y.amax(1, keepdim=True)
     top = torch.where(top == -math.inf, torch.zeros_like(top), top)
     e = (y - top).exp()
-    lse = e.sum(1).log() + top[:, 0]
-    rest = torch.where(inside, torch.zeros_like(e), e).sum(1).log() + top[:, 0]
-    rest = torch.where(rest == -math.inf, rest, rest - lse)
+    total = e.sum(1).log()
+    lse = total + top[:, 0]
+    rest = torch.where(inside, torch.zeros_like(e), e).sum(1).log()
+    rest = torch.where(rest == -math.inf, rest, rest - total)
     picked = y.gather(1, at.clamp(max=vocab - 1))
-    log_q = torch.where(picked == -math.inf, picked, picked - lse[:, None])
+    log_q = torch.where(picked == -math.inf, picked, (picked - top) - total[:, None])
     loss = torch.where(p > 0, p * (log_p - log_q), torch.zeros_like(p)).sum(1)
-    p_rest = (1 - p.sum(1)).clamp(min=0) if tail else torch.zeros_like(lse)
+    # 1 - sum p without the largest p's cancellation
+    largest, place = log_p.max(1)
+    others = p.scatter(1, place[:, None], 0.0).sum(1)
+    lacking = -torch.expm1(largest) - others if tail else torch.zeros_like(lse)
+    p_rest = lacking.clamp(min=0)
     p_rest = torch.where(rest == -math.inf, torch.zeros_like(p_rest), p_rest)
     any_entry = kept.any(1) if tail else (p > 0).any(1)
     loss = loss + torch.where(p_rest > 0, p_rest * (p_rest.log() - rest), torch.zeros_like(p_rest))
     loss = torch.where(any_entry, loss, torch.zeros_like(loss))
-    return {"loss": loss, "lse": lse, "rest": rest if tail else None, "y": y, "p": p, "at": at, "kept": kept,
-            "inside": inside, "p_rest": p_rest, "any": any_entry}
+    return {"loss": loss, "lse": lse, "rest": rest if tail else None, "y": y, "p": p, "log_p": log_p, "log_q": log_q,
+            "at": at, "inside": inside, "p_rest": p_rest, "excess": p_rest - lacking, "any": any_entry}
 
 
 def _distill_gradient_plain(state, plain):
     case, d_loss = state["case"], state["d_loss"]
     t, vocab = case["temperature"], state["logits"].shape[1]
-    y, p, p_rest = plain["y"], plain["p"], plain["p_rest"]
+    y, p, p_rest, excess = plain["y"], plain["p"], plain["p_rest"], plain["excess"][:, None]
     lse = torch.where(plain["lse"] == -math.inf, torch.zeros_like(plain["lse"]), plain["lse"])
-    grad = (y - lse[:, None]).exp() * (p.sum(1) + p_rest)[:, None]
+    # sum p + p_rest is 1 + excess
+    grad = (y - lse[:, None]).exp() * (1 + excess)
     if case["tail"]:
         rest = torch.where(plain["rest"] == -math.inf, torch.zeros_like(lse), plain["rest"])
-        share = (y - (lse + rest)[:, None]).exp() * p_rest[:, None]
-        grad = grad - torch.where(plain["inside"], torch.zeros_like(share), share)
-    target = torch.zeros(y.shape[0], vocab + 1, device=y.device).scatter_(1, plain["at"], p)[:, :vocab]
-    grad = grad - torch.where(y == -math.inf, torch.zeros_like(target), target)
+        grad = grad - (y - (lse + rest)[:, None]).exp() * p_rest[:, None]
+    # at the teacher's entries q - p without cancellation
+    log_q, log_p = plain["log_q"], plain["log_p"]
+    apart = torch.where(p > 0, p * torch.expm1(log_q - log_p), log_q.exp()) + log_q.exp() * excess
+    apart = torch.where(log_q == -math.inf, torch.zeros_like(apart), apart)
+    wide = torch.zeros(y.shape[0], vocab + 1, device=y.device).scatter_(1, plain["at"], apart)[:, :vocab]
+    grad = torch.where(plain["inside"], wide, grad)
     live = plain["any"] & (d_loss != 0) & (plain["lse"] != -math.inf)
     grad = torch.where(live[:, None], grad * (d_loss / t)[:, None], torch.zeros_like(grad))
     return grad.to(state["logits"].dtype)
@@ -318,8 +328,9 @@ def _run_plain(state):
     plain = _distill_plain(state["logits"], state["teacher"], state["index"], case["temperature"], case["tail"])
     if case["op"] == "distill_backward":
         # the forward pass's statistics stand for those of this one
-        plain["lse"] = state["lse"]
-        plain["rest"] = state["rest"] if case["tail"] else None
+        plain["lse"], plain["rest"] = state["lse"], state["rest"]
+        picked = plain["y"].gather(1, plain["at"].clamp(max=plain["y"].shape[1] - 1))
+        plain["log_q"] = torch.where(picked == -math.inf, picked, picked - state["lse"][:, None])
         return {"d_logits": _distill_gradient_plain(state, plain)}
     out = {"loss": plain["loss"], "lse": plain["lse"]}
     if case["tail"]:
@@ -392,9 +403,11 @@ def _exact_rows(case, s, rows):
     n, vocab = x.shape
     zero = x.new_zeros(())
     y = x / t
-    lse = torch.logsumexp(y, 1)
+    # a backward pass takes the forward's 32-bit statistics for what they are
+    given_stats = op.endswith("_backward")
+    lse = s["lse"][rows].double() if given_stats else torch.logsumexp(y, 1)
     dead = torch.isneginf(lse)
-    q = torch.softmax(y, 1).masked_fill(dead[:, None], 0.0)
+    q = (y - lse.masked_fill(dead, 0.0)[:, None]).exp()
     out = {}
     if op.startswith("logprobs"):
         tokens = s["tokens"][rows].long()
@@ -402,7 +415,7 @@ def _exact_rows(case, s, rows):
         line = torch.arange(n, device=x.device)
         chosen = torch.zeros(n, vocab, dtype=torch.bool, device=x.device)
         chosen[line[given], tokens[given]] = True
-        entropy = -torch.special.xlogy(q, q).sum(1)
+        entropy = s["entropy"][rows].double() if given_stats and case["entropy"] else -torch.special.xlogy(q, q).sum(1)
         if op != "logprobs_backward":
             logprob = x.new_zeros(n)
             logprob[given] = y[line[given], tokens[given]] - lse[given]
@@ -441,6 +454,8 @@ def _exact_rows(case, s, rows):
         p = p.masked_fill(nothing[:, None], 0.0)
         target[r, index[r, j]] = p[r, j]
         outside_mass = torch.where(member, zero, q).sum(1)
+        if given_stats and case["tail"]:
+            outside_mass = s["rest"][rows].double().exp()
         # log q where the target has mass; what is masked there has log q = -inf
         log_q = torch.where(torch.isneginf(y), y, y - lse[:, None])
         loss = torch.where(target > 0, target * (target.log() - log_q), zero).sum(1)

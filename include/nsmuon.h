@@ -248,6 +248,103 @@ int nsm_gemm(const void* a, int lda, const void* b, int ldb, void* out, int ldo,
              size_t scratch_bytes, nsm_stream_t stream);
 size_t nsm_gemm_scratch_bytes(int M, int N, int flags);
 
+/* ---- Losses over a vocabulary ------------------------------------------------------
+ * What turns a model's logits into the gradients an optimizer step consumes: the log
+ * probabilities of given tokens (cross-entropy, policy gradients, scoring) and
+ * distillation from a teacher's top logits.  The pages have no counterpart.
+ *
+ * For one row x of `vocab` logits at temperature t, y = x / t:
+ *     lse     = log sum_v exp(y_v)            q_v = exp(y_v - lse)
+ *     logprob = y_token - lse                 entropy = -sum_v q_v log q_v  (0 log 0 = 0)
+ *
+ * Conventions of these calls:
+ *   - logits: device, rows x vocab elements of `dtype` (NSM_BF16, NSM_FP16 or NSM_FP32) at
+ *     row stride ld >= vocab elements, unit column stride, aligned to an element (16-byte
+ *     aligned rows are fastest).  1 <= vocab <= 2^20; rows may be 0 (nothing is launched).
+ *   - Sums and statistics are fp32; a gradient has the logits' type and is rounded once.
+ *   - temperature in [1e-6, 1e6].  Gradients are with respect to the logits as given, so
+ *     they carry the factor 1 / t.
+ *   - d_logits may be the logits themselves (same pointer and stride: in place); otherwise
+ *     no buffer that a call writes may overlap another one.
+ *   - A logit of -inf is a masked token: q = 0, its gradient is 0.  In a row of nothing
+ *     else lse is -inf, logprob -inf, entropy 0 and the gradient 0.  The lowest finite
+ *     values are ordinary logits.  A NaN or +inf makes its row's results NaN (top_index
+ *     -1); a row of weight 0 has a gradient of zeros whatever it holds.
+ *   - `*_wide`: index arrays hold int64 (else int32).  An index outside [0, vocab), such
+ *     as -100 or -1, stands for no token and no entry.
+ *   - Deterministic: identical inputs give bit-identical outputs, and a row's result does
+ *     not depend on the other rows. */
+#define NSM_BF16 0
+#define NSM_FP16 1
+#define NSM_FP32 2
+
+/* Log probabilities of given tokens, with entropy and top alternatives.
+ *   tokens       device, one per row, or NULL (then logprob must be NULL)
+ *   k            top alternatives per row, 0 to 128
+ *   logprob, entropy, lse   device, fp32, rows; each may be NULL.  logprob is 0 in a row
+ *                without a token.
+ *   top_logprob, top_index  device, fp32 / int32, rows x k (NULL with k = 0): the k largest
+ *                logits in descending order, equal ones by ascending index, as log
+ *                probabilities and indexes; where fewer than k logits are above -inf, -inf
+ *                and -1.  They are nsm_distill's teacher entries (with its tail). */
+int nsm_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                 const void* tokens, int tokens_wide, float temperature, int k,
+                 float* logprob, float* entropy, float* lse, float* top_logprob,
+                 int32_t* top_index, nsm_stream_t stream);
+
+/* Forward and backward in one call, for weights known beforehand (cross-entropy:
+ * d_logprob = -mask / count): the forward's logprob, entropy and lse (each may be NULL)
+ * and the gradient of sum_r d_logprob[r] logprob_r + d_entropy[r] entropy_r.
+ *   d_logprob, d_entropy  device, fp32, rows; one of the two may be NULL (weights 0) */
+int nsm_logprobs_grad(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                      const void* tokens, int tokens_wide, float temperature,
+                      const float* d_logprob, const float* d_entropy, void* d_logits, int64_t ldd,
+                      float* logprob, float* entropy, float* lse, nsm_stream_t stream);
+
+/* The backward pass alone, from the lse (and, with d_entropy, the entropy) that
+ * nsm_logprobs gave for the same logits and temperature. */
+int nsm_logprobs_backward(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                          const void* tokens, int tokens_wide, float temperature,
+                          const float* lse, const float* entropy, const float* d_logprob,
+                          const float* d_entropy, void* d_logits, int64_t ldd, nsm_stream_t stream);
+
+/* Distillation from a teacher's top logits: per row, k entries of a score and a token
+ * index, and the forward Kullback-Leibler divergence from the student's softmax.
+ *     tail == 0: p = softmax over the entries of teacher / t
+ *                loss = sum_j p_j (log p_j - log q_{i_j})
+ *     tail != 0: teacher holds log probabilities at this temperature, p_j = exp(teacher_j);
+ *                every other token is one bucket, p_rest = max(0, 1 - sum_j p_j) and
+ *                q_rest = sum of q outside the entries:
+ *                loss = sum_j p_j (log p_j - log q_{i_j}) + p_rest (log p_rest - log q_rest)
+ *                (the last term is left out where the student has nothing there)
+ * An entry whose index is outside [0, vocab), or was given before in the same row, does not
+ * count; a row without entries has loss 0 and gradient 0.  Mass on a masked token makes
+ * the loss +inf.
+ *   teacher  device, rows x k of teacher_dtype (NSM_BF16 / NSM_FP16 / NSM_FP32), row stride ldt
+ *   index    device, rows x k of int64 (index_wide != 0) or int32, row stride ldi
+ *   k        1 to 128
+ *   loss     device, fp32, rows;  lse, rest: device, fp32, rows, each may be NULL: the
+ *            student's lse, and log q_rest (-inf where nothing is left), for the backward */
+int nsm_distill(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                const void* teacher, int teacher_dtype, int64_t ldt, const void* index,
+                int index_wide, int64_t ldi, int k, float temperature, int tail, float* loss,
+                float* lse, float* rest, nsm_stream_t stream);
+
+/* Forward and backward in one call: loss, lse and rest (each may be NULL) and the gradient
+ * of sum_r d_loss[r] loss_r.  d_loss: device, fp32, rows, or NULL (weights 1). */
+int nsm_distill_grad(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                     const void* teacher, int teacher_dtype, int64_t ldt, const void* index,
+                     int index_wide, int64_t ldi, int k, float temperature, int tail,
+                     const float* d_loss, void* d_logits, int64_t ldd, float* loss, float* lse,
+                     float* rest, nsm_stream_t stream);
+
+/* The backward pass alone, from nsm_distill's lse and (with the tail) rest. */
+int nsm_distill_backward(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                         const void* teacher, int teacher_dtype, int64_t ldt, const void* index,
+                         int index_wide, int64_t ldi, int k, float temperature, int tail,
+                         const float* lse, const float* rest, const float* d_loss, void* d_logits,
+                         int64_t ldd, nsm_stream_t stream);
+
 /* Synchronises `stream`, then reads and clears the device status word that kernels set
  * when a bounded wait expires (or, in the checked build, when a bounds check fails).
  * *status_out = NSM_OK, NSM_ERR_TIMEOUT or NSM_ERR_BOUNDS.  Returns NSM_ERR_CUDA if the
@@ -267,6 +364,8 @@ int nsm_device_status(nsm_stream_t stream, int* status_out);
 #define NSM_KERNEL_TO_CLASS   6  /* k_to_class (bounds checks only) */
 #define NSM_KERNEL_FROM_CLASS 7  /* k_from_class: apply or export (bounds checks only) */
 #define NSM_KERNEL_ADAMW      8  /* k_adamw (bounds checks only) */
+#define NSM_KERNEL_LOGPROBS   9  /* log probabilities of tokens, and their gradient */
+#define NSM_KERNEL_DISTILL   10  /* distillation from top logits, and its gradient */
 #define NSM_ROLE_PRODUCER     1  /* the thread issuing TMA loads */
 #define NSM_ROLE_MMA          2  /* the thread issuing tensor-core MMAs */
 #define NSM_ROLE_EPILOGUE     3  /* the epilogue warps draining TMEM */
@@ -300,6 +399,8 @@ int nsm_device_status(nsm_stream_t stream, int* status_out);
 #define NSM_SITE_SLOT_STORE     21  /* store to a matrix's slot in the working layout */
 #define NSM_SITE_FLAT           22  /* AdamW's access to its flat group */
 #define NSM_SITE_SELFTEST_BOUNDS 23 /* nsm_bounds_selftest's check of an index past its range */
+#define NSM_SITE_LOGITS         24  /* load of a row of logits */
+#define NSM_SITE_GRADIENT       25  /* store to a row of the logits' gradient */
 
 /* nsm_device_status with the location: synchronises `stream`, reads and clears the
  * status word.  *status_out = NSM_OK, NSM_ERR_TIMEOUT or NSM_ERR_BOUNDS; then *kernel_out,
@@ -340,7 +441,7 @@ int nsm_bounds_selftest(nsm_stream_t stream);
 int nsm_copy_to_device(void* dst, const void* src, size_t bytes, int ctas, nsm_stream_t stream);
 
 /* Kernel timing for profiling.  While enabled, every kernel launch of muon_step,
- * muon_orthogonalize, adamw_step and nsm_gemm is bracketed by CUDA events on the
+ * muon_orthogonalize, adamw_step, nsm_gemm, nsm_logprobs* and nsm_distill* is bracketed by CUDA events on the
  * caller's stream.  nsm_timing_read_kind synchronises the recorded events and returns,
  * summed since the last reset for one kind of kernel: *ms (device time), *launches and
  * *work (the algorithmic work of those launches: flops for NSM_KIND_GEMM, bytes that
@@ -358,13 +459,15 @@ int nsm_copy_to_device(void* dst, const void* src, size_t bytes, int ctas, nsm_s
 #define NSM_KIND_SMALL     6  /* whole Newton-Schulz chains of matrices with m <= 128 (bytes:
                                   every read and write of X; the kernel is HBM-bound) */
 #define NSM_KIND_GRAD_NORM 7  /* the orthogonalisation's pass: sums of G^2, largest |G| */
+#define NSM_KIND_LOGPROBS  8  /* nsm_logprobs*: logits read, and gradients written */
+#define NSM_KIND_DISTILL   9  /* nsm_distill*: logits read, and gradients written */
 int nsm_timing_enable(int enable);
 int nsm_timing_read(double* gemm_ms, int64_t* gemm_launches, double* gemm_flops);
 int nsm_timing_read_kind(int kind, double* ms, int64_t* launches, double* work);
 int nsm_timing_reset(void);
 
 /* Number of kernel launches the last successful muon_step / muon_orthogonalize /
- * adamw_step call made on this host thread. */
+ * adamw_step / nsm_logprobs* / nsm_distill* call made on this host thread. */
 int nsm_last_launch_count(void);
 
 /* Process-wide launch options.  They select between the library's own equivalent paths,

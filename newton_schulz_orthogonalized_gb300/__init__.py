@@ -114,6 +114,19 @@ def lib() -> ctypes.CDLL:
     L.nsm_gemm.restype = ctypes.c_int
     L.nsm_gemm_scratch_bytes.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int]
     L.nsm_gemm_scratch_bytes.restype = ctypes.c_size_t
+    _i64, _int, _f32 = ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    rows_of_logits = [_vp, _int, _i64, _i64, _i64]
+    tokens_and_t = [_vp, _int, _f32]
+    entries = [_vp, _int, _i64, _vp, _int, _i64, _int, _f32, _int]
+    L.nsm_logprobs.argtypes = rows_of_logits + tokens_and_t + [_int, _vp, _vp, _vp, _vp, _vp, _vp]
+    L.nsm_logprobs_grad.argtypes = rows_of_logits + tokens_and_t + [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp]
+    L.nsm_logprobs_backward.argtypes = rows_of_logits + tokens_and_t + [_vp, _vp, _vp, _vp, _vp, _i64, _vp]
+    L.nsm_distill.argtypes = rows_of_logits + entries + [_vp, _vp, _vp, _vp]
+    L.nsm_distill_grad.argtypes = rows_of_logits + entries + [_vp, _vp, _i64, _vp, _vp, _vp, _vp]
+    L.nsm_distill_backward.argtypes = rows_of_logits + entries + [_vp, _vp, _vp, _vp, _i64, _vp]
+    for f in (L.nsm_logprobs, L.nsm_logprobs_grad, L.nsm_logprobs_backward, L.nsm_distill, L.nsm_distill_grad,
+              L.nsm_distill_backward):
+        f.restype = ctypes.c_int
     L.nsm_device_status.argtypes = [_vp, ctypes.POINTER(ctypes.c_int)]
     L.nsm_device_status.restype = ctypes.c_int
     _ip = ctypes.POINTER(ctypes.c_int)
@@ -366,6 +379,190 @@ def gemm(a, b, out, aux=None, b_mn_major: bool = False, alpha: float = 1.0, beta
                           float(diag), _ptr(scratch), scratch.numel(), _stream_ptr(stream)))
 
 
+# ---------------------------------------------------------------- losses over a vocabulary
+
+TOP_MAX_K = 128
+DISTILL_MAX_K = 128
+_torch_codes: Optional[Tuple[dict, dict]] = None
+
+
+def _codes() -> Tuple[dict, dict]:
+    """torch's names of the logits' types and of the index types, as the library's codes."""
+    global _torch_codes
+    if _torch_codes is None:
+        import torch
+        _torch_codes = ({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}, {torch.int32: 0, torch.int64: 1})
+    return _torch_codes
+
+
+def _matrix(name: str, t, codes, rows: int, cols: int, device) -> Tuple[int, int, int]:
+    """(pointer, type code, row stride) of a rows x cols tensor with unit column stride."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
+    code = codes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} has type {t.dtype}: one of {[str(c) for c in codes]} is wanted")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
+        raise ValueError(f"{name} has shape {tuple(shape)}: ({rows}, {cols}) is wanted")
+    if cols > 1 and stride[1] != 1:
+        raise ValueError(f"{name} has column stride {stride[1]}: 1 is wanted")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}: {device} is wanted")
+    return t.data_ptr(), code, (stride[0] if rows > 1 else max(stride[0], cols))
+
+
+def _numbers(name: str, t, shape: Tuple[int, ...], device, dtype=None) -> int:
+    """Pointer of a contiguous tensor of that shape, float32 unless `dtype` says otherwise; 0 for None."""
+    if t is None:
+        return 0
+    import torch
+    if t.dtype != (dtype or torch.float32):
+        raise ValueError(f"{name} has type {t.dtype}: {dtype or torch.float32} is wanted")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} is not a contiguous tensor of shape {shape}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}: {device} is wanted")
+    return t.data_ptr()
+
+
+def _logits(logits) -> Tuple[int, int, int, int, int]:
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits is not a matrix of rows x vocab in device memory")
+    rows, vocab = logits.shape
+    ptr, code, ld = _matrix("logits", logits, _codes()[0], rows, vocab, logits.device)
+    return ptr, code, rows, vocab, ld
+
+
+def _tokens(tokens, rows: int, device) -> Tuple[int, int]:
+    if tokens is None:
+        return 0, 0
+    code = _codes()[1].get(tokens.dtype)
+    if code is None:
+        raise ValueError(f"tokens has type {tokens.dtype}: torch.int32 or torch.int64 is wanted")
+    return _numbers("tokens", tokens, (rows,), device, tokens.dtype), code
+
+
+def _gradient(name: str, t, logits) -> Tuple[int, int]:
+    if t is not None and t.dtype != logits.dtype:
+        raise ValueError(f"{name} has type {t.dtype}: the logits' {logits.dtype} is wanted")
+    ptr, _, ld = _matrix(name, t, _codes()[0], logits.shape[0], logits.shape[1], logits.device)
+    return ptr, ld
+
+
+def _entries(teacher, index, rows: int, device) -> Tuple[int, int, int, int, int, int, int]:
+    if teacher is None or teacher.dim() != 2:
+        raise ValueError("teacher is not a matrix of rows x k")
+    k = teacher.shape[1]
+    t_ptr, t_code, ldt = _matrix("teacher", teacher, _codes()[0], rows, k, device)
+    i_ptr, wide, ldi = _matrix("index", index, _codes()[1], rows, k, device)
+    return t_ptr, t_code, ldt, i_ptr, wide, ldi, k
+
+
+def logprobs(logits, tokens, logprob=None, entropy=None, lse=None, top_logprob=None, top_index=None,
+             temperature: float = 1.0, stream=None) -> None:
+    """Log probabilities of given tokens, with entropy and top alternatives.
+
+    ``logits`` is rows x vocab (bf16, fp16 or fp32, unit column stride, any row stride);
+    ``tokens`` one int32 or int64 index per row (an index outside the vocabulary, such as
+    -100: no token) or None.  Writes the outputs that are given: ``logprob``, ``entropy``
+    and ``lse`` (float32, one per row), and the k largest logits as log probabilities
+    ``top_logprob`` (float32, rows x k) with their indexes ``top_index`` (int32, rows x k),
+    ties by ascending index."""
+    ptr, code, rows, vocab, ld = _logits(logits)
+    dev = logits.device
+    t_ptr, wide = _tokens(tokens, rows, dev)
+    k = 0
+    if top_logprob is not None or top_index is not None:
+        if top_logprob is None or top_index is None or top_logprob.dim() != 2:
+            raise ValueError("top_logprob and top_index go together, as matrices of rows x k")
+        import torch
+        k = top_logprob.shape[1]
+        top_l = _numbers("top_logprob", top_logprob, (rows, k), dev)
+        top_i = _numbers("top_index", top_index, (rows, k), dev, torch.int32)
+    else:
+        top_l = top_i = 0
+    _check(lib().nsm_logprobs(ptr, code, rows, vocab, ld, t_ptr, wide, float(temperature), k,
+                              _numbers("logprob", logprob, (rows,), dev), _numbers("entropy", entropy, (rows,), dev),
+                              _numbers("lse", lse, (rows,), dev), top_l, top_i, _stream_ptr(stream)))
+
+
+def logprobs_grad(logits, tokens, d_logprob, d_entropy, d_logits, logprob=None, entropy=None, lse=None,
+                  temperature: float = 1.0, stream=None) -> None:
+    """:func:`logprobs` with the gradient in the same pass, for weights known beforehand:
+    writes ``d_logits``, the gradient of sum(d_logprob * logprob + d_entropy * entropy)
+    (one of the two weights may be None), in the logits' type; it may be ``logits`` itself."""
+    ptr, code, rows, vocab, ld = _logits(logits)
+    dev = logits.device
+    t_ptr, wide = _tokens(tokens, rows, dev)
+    g_ptr, ldd = _gradient("d_logits", d_logits, logits)
+    _check(lib().nsm_logprobs_grad(ptr, code, rows, vocab, ld, t_ptr, wide, float(temperature),
+                                   _numbers("d_logprob", d_logprob, (rows,), dev),
+                                   _numbers("d_entropy", d_entropy, (rows,), dev), g_ptr, ldd,
+                                   _numbers("logprob", logprob, (rows,), dev),
+                                   _numbers("entropy", entropy, (rows,), dev), _numbers("lse", lse, (rows,), dev),
+                                   _stream_ptr(stream)))
+
+
+def logprobs_backward(logits, tokens, lse, entropy, d_logprob, d_entropy, d_logits, temperature: float = 1.0,
+                      stream=None) -> None:
+    """The backward pass of :func:`logprobs` alone, from its ``lse`` (and ``entropy``, needed
+    with ``d_entropy``)."""
+    ptr, code, rows, vocab, ld = _logits(logits)
+    dev = logits.device
+    t_ptr, wide = _tokens(tokens, rows, dev)
+    g_ptr, ldd = _gradient("d_logits", d_logits, logits)
+    _check(lib().nsm_logprobs_backward(ptr, code, rows, vocab, ld, t_ptr, wide, float(temperature),
+                                       _numbers("lse", lse, (rows,), dev), _numbers("entropy", entropy, (rows,), dev),
+                                       _numbers("d_logprob", d_logprob, (rows,), dev),
+                                       _numbers("d_entropy", d_entropy, (rows,), dev), g_ptr, ldd,
+                                       _stream_ptr(stream)))
+
+
+def distill(logits, teacher, index, loss, lse=None, rest=None, temperature: float = 1.0, tail: bool = False,
+            stream=None) -> None:
+    """Distillation from a teacher's top logits: per row, the divergence of the student's
+    softmax from the teacher's k entries (``teacher`` scores, ``index`` int32 or int64).
+
+    Without ``tail`` the teacher is the softmax over its entries at ``temperature``; with
+    it ``teacher`` holds log probabilities at that temperature (``top_logprob`` of
+    :func:`logprobs`) and the rest of the row is one bucket.  An index outside the
+    vocabulary, or given before in its row, does not count.  Writes ``loss`` and, where
+    given, the student's ``lse`` and ``rest`` (log of its mass outside the entries)."""
+    ptr, code, rows, vocab, ld = _logits(logits)
+    dev = logits.device
+    e = _entries(teacher, index, rows, dev)
+    _check(lib().nsm_distill(ptr, code, rows, vocab, ld, *e, float(temperature), 1 if tail else 0,
+                             _numbers("loss", loss, (rows,), dev), _numbers("lse", lse, (rows,), dev),
+                             _numbers("rest", rest, (rows,), dev), _stream_ptr(stream)))
+
+
+def distill_grad(logits, teacher, index, d_loss, d_logits, loss=None, lse=None, rest=None,
+                 temperature: float = 1.0, tail: bool = False, stream=None) -> None:
+    """:func:`distill` with the gradient of sum(d_loss * loss) in the same pass (``d_loss``
+    None: weights 1); ``d_logits`` has the logits' type and may be ``logits`` itself."""
+    ptr, code, rows, vocab, ld = _logits(logits)
+    dev = logits.device
+    e = _entries(teacher, index, rows, dev)
+    g_ptr, ldd = _gradient("d_logits", d_logits, logits)
+    _check(lib().nsm_distill_grad(ptr, code, rows, vocab, ld, *e, float(temperature), 1 if tail else 0,
+                                  _numbers("d_loss", d_loss, (rows,), dev), g_ptr, ldd,
+                                  _numbers("loss", loss, (rows,), dev), _numbers("lse", lse, (rows,), dev),
+                                  _numbers("rest", rest, (rows,), dev), _stream_ptr(stream)))
+
+
+def distill_backward(logits, teacher, index, lse, rest, d_loss, d_logits, temperature: float = 1.0,
+                     tail: bool = False, stream=None) -> None:
+    """The backward pass of :func:`distill` alone, from its ``lse`` and (with ``tail``) ``rest``."""
+    ptr, code, rows, vocab, ld = _logits(logits)
+    dev = logits.device
+    e = _entries(teacher, index, rows, dev)
+    g_ptr, ldd = _gradient("d_logits", d_logits, logits)
+    _check(lib().nsm_distill_backward(ptr, code, rows, vocab, ld, *e, float(temperature), 1 if tail else 0,
+                                      _numbers("lse", lse, (rows,), dev), _numbers("rest", rest, (rows,), dev),
+                                      _numbers("d_loss", d_loss, (rows,), dev), g_ptr, ldd, _stream_ptr(stream)))
+
+
 def device_status(stream=None) -> int:
     """Synchronises the stream; returns NSM_OK, NSM_ERR_TIMEOUT or (checked build)
     NSM_ERR_BOUNDS, and clears the record."""
@@ -438,10 +635,12 @@ def timing_reset() -> None:
     lib().nsm_timing_reset()
 
 
-KIND_GEMM, KIND_MOMENTUM, KIND_NORM, KIND_LAYOUT, KIND_APPLY, KIND_ADAMW, KIND_SMALL, KIND_GRAD_NORM = range(8)
+KIND_GEMM, KIND_MOMENTUM, KIND_NORM, KIND_LAYOUT, KIND_APPLY, KIND_ADAMW, KIND_SMALL, KIND_GRAD_NORM, \
+    KIND_LOGPROBS, KIND_DISTILL = range(10)
 KIND_NAMES = {KIND_GEMM: "k_ns_gemm", KIND_MOMENTUM: "k_momentum_class", KIND_NORM: "k_scale_finalize",
               KIND_LAYOUT: "k_to_class", KIND_APPLY: "k_from_class", KIND_ADAMW: "k_adamw",
-              KIND_SMALL: "k_ns_small", KIND_GRAD_NORM: "k_grad_norm"}
+              KIND_SMALL: "k_ns_small", KIND_GRAD_NORM: "k_grad_norm",
+              KIND_LOGPROBS: "k_logprobs", KIND_DISTILL: "k_distill"}
 
 
 def timing_read(kind: int = KIND_GEMM) -> Tuple[float, int, float]:

@@ -911,7 +911,7 @@ Plan* get_plan(const int32_t* shapes, const int64_t* offsets, int n, int method,
 // ---------------------------------------------------------------- timing
 
 // Kernel kinds the timing hooks distinguish (NSM_KIND_* in the header).
-constexpr int kKinds = 8;
+constexpr int kKinds = 10;
 
 struct Timing {
   std::mutex mu;
@@ -1040,6 +1040,162 @@ int device_views(const void* in_bf16, const void* out_bf16, const void** in, con
   rc = device_view(out_bf16, "out_bf16", out);
   if (rc != NSM_OK) return rc;
   if (!aligned(*in, 16) || !aligned(*out, 16)) return fail(NSM_ERR_ALIGN, "a device mapping is not 16-byte aligned");
+  return NSM_OK;
+}
+
+// ---- losses over a vocabulary
+
+// A buffer of a call: no written one may overlap another (device memory is not looked at).
+struct Range {
+  const void* p;
+  size_t bytes;
+  bool written;
+};
+
+int check_ranges(const Range* ranges, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (!ranges[i].p) continue;
+    for (int j = 0; j < i; ++j) {
+      if (ranges[j].p && (ranges[i].written || ranges[j].written) &&
+          ranges_overlap(ranges[i].p, ranges[i].bytes, ranges[j].p, ranges[j].bytes))
+        return fail(NSM_ERR_ARG, "a buffer that the call writes overlaps another one");
+    }
+  }
+  return NSM_OK;
+}
+
+size_t number_bytes(int dtype) { return dtype == NSM_FP32 ? 4 : 2; }
+
+// Bytes from the first to the last element of rows x cols at row stride ld.
+size_t span_bytes(int64_t rows, int64_t ld, int64_t cols, size_t size) {
+  return (size_t(rows - 1) * size_t(ld) + size_t(cols)) * size;
+}
+
+// rows x cols elements of `size` bytes at row stride ld: non-negative sizes whose span stays
+// far from the address space's end.
+int check_matrix(const char* what, const void* p, int64_t rows, int64_t ld, int64_t cols, size_t size) {
+  if (!p) return fail(NSM_ERR_NULL, "%s is NULL", what);
+  if (!aligned(p, size)) return fail(NSM_ERR_ALIGN, "%s is not aligned to its %zu-byte elements", what, size);
+  if (ld < cols) return fail(NSM_ERR_SHAPE, "%s: row stride %lld is less than the row's %lld elements", what,
+                             static_cast<long long>(ld), static_cast<long long>(cols));
+  if (ld > (int64_t(1) << 60) / rows) return fail(NSM_ERR_SHAPE, "%s: rows times row stride overflows", what);
+  return NSM_OK;
+}
+
+// Fills `v`; for rows == 0 there is nothing to check beyond the sizes.
+int check_vocab(VocabArgs& v, const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                float temperature, void* d_logits, int64_t ldd) {
+  if (dtype != NSM_BF16 && dtype != NSM_FP16 && dtype != NSM_FP32) return fail(NSM_ERR_ARG, "unknown logits type %d", dtype);
+  if (rows < 0 || rows > INT32_MAX) return fail(NSM_ERR_SHAPE, "rows = %lld not in [0, 2^31 - 1]", static_cast<long long>(rows));
+  if (vocab < 1 || vocab > kVocabMax)
+    return fail(NSM_ERR_SHAPE, "vocab = %lld not in [1, %d]", static_cast<long long>(vocab), kVocabMax);
+  if (!(temperature >= 1e-6f && temperature <= 1e6f)) return fail(NSM_ERR_ARG, "temperature must lie in [1e-6, 1e6]");
+  v = VocabArgs{};
+  v.logits = logits;
+  v.d_logits = d_logits;
+  v.rows = rows;
+  v.ld = ld;
+  v.ldd = ldd;
+  v.vocab = static_cast<int32_t>(vocab);
+  v.dtype = dtype;
+  v.t = temperature;
+  v.inv_t = 1.f / temperature;
+  v.c = static_cast<float>(1.4426950408889634 / double(temperature));
+  if (rows == 0) return NSM_OK;
+  const size_t size = number_bytes(dtype);
+  int rc = check_matrix("logits", logits, rows, ld, vocab, size);
+  if (rc != NSM_OK) return rc;
+  if (d_logits) {
+    rc = check_matrix("d_logits", d_logits, rows, ldd, vocab, size);
+    if (rc != NSM_OK) return rc;
+    // in place, or apart
+    if (!(d_logits == logits && ldd == ld) &&
+        ranges_overlap(logits, span_bytes(rows, ld, vocab, size), d_logits, span_bytes(rows, ldd, vocab, size)))
+      return fail(NSM_ERR_ARG, "d_logits overlaps logits without being the same rows");
+  }
+  return NSM_OK;
+}
+
+int check_numbers(const char* what, const void* p, size_t size) {
+  if (p && !aligned(p, size)) return fail(NSM_ERR_ALIGN, "%s is not aligned to its %zu-byte elements", what, size);
+  return NSM_OK;
+}
+
+double vocab_work(const VocabArgs& v) {
+  return double(v.rows) * v.vocab * double(number_bytes(v.dtype)) * (v.d_logits ? 2.0 : 1.0);
+}
+
+int run_logprobs(LogprobArgs& a, nsm_stream_t stream_) {
+  const VocabArgs& v = a.v;
+  if (v.rows == 0) {
+    t_last_launches = 0;
+    return NSM_OK;
+  }
+  int rc;
+  const size_t size = number_bytes(v.dtype), n = size_t(v.rows) * 4;
+  const struct { const char* what; const void* p; size_t size; } numbers[] = {
+      {"tokens", a.tokens, a.tokens_wide ? size_t(8) : size_t(4)}, {"logprob", a.logprob, 4}, {"entropy", a.entropy, 4},
+      {"lse", a.lse, 4}, {"top_logprob", a.top_logprob, 4}, {"top_index", a.top_index, 4},
+      {"d_logprob", a.d_logprob, 4}, {"d_entropy", a.d_entropy, 4}, {"lse", a.in_lse, 4}, {"entropy", a.in_entropy, 4}};
+  for (const auto& x : numbers)
+    if ((rc = check_numbers(x.what, x.p, x.size)) != NSM_OK) return rc;
+  const bool in_place = v.d_logits == v.logits;
+  const Range ranges[] = {{v.logits, span_bytes(v.rows, v.ld, v.vocab, size), in_place},
+                          {in_place ? nullptr : v.d_logits, span_bytes(v.rows, v.ldd, v.vocab, size), true},
+                          {a.tokens, size_t(v.rows) * (a.tokens_wide ? 8 : 4), false},
+                          {a.logprob, n, true}, {a.entropy, n, true}, {a.lse, n, true},
+                          {a.k ? a.top_logprob : nullptr, n * size_t(a.k), true},
+                          {a.k ? a.top_index : nullptr, n * size_t(a.k), true},
+                          {a.d_logprob, n, false}, {a.d_entropy, n, false}, {a.in_lse, n, false}, {a.in_entropy, n, false}};
+  if ((rc = check_ranges(ranges, int(sizeof ranges / sizeof ranges[0]))) != NSM_OK) return rc;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const PdlScope pdl(v.rows * v.vocab);
+  cudaError_t e;
+  {
+    TimedLaunch t(stream, NSM_KIND_LOGPROBS, vocab_work(v));
+    e = launch_logprobs(a, stream);
+  }
+  if (e != cudaSuccess) return fail_cuda(e, "log-probability launch");
+  t_last_launches = 1;
+  return NSM_OK;
+}
+
+// The teacher's part of `a` and the launch.
+int run_distill(DistillArgs& a, nsm_stream_t stream_) {
+  const VocabArgs& v = a.v;
+  if (a.k < 1 || a.k > kDistillMaxK) return fail(NSM_ERR_ARG, "k = %d not in [1, %d]", a.k, kDistillMaxK);
+  if (a.teacher_dtype != NSM_BF16 && a.teacher_dtype != NSM_FP16 && a.teacher_dtype != NSM_FP32)
+    return fail(NSM_ERR_ARG, "unknown teacher type %d", a.teacher_dtype);
+  if (v.rows == 0) {
+    t_last_launches = 0;
+    return NSM_OK;
+  }
+  const size_t size = number_bytes(v.dtype), tsize = number_bytes(a.teacher_dtype), isize = a.index_wide ? 8 : 4;
+  const size_t n = size_t(v.rows) * 4;
+  int rc = check_matrix("teacher", a.teacher, v.rows, a.ldt, a.k, tsize);
+  if (rc != NSM_OK) return rc;
+  if ((rc = check_matrix("index", a.index, v.rows, a.ldi, a.k, isize)) != NSM_OK) return rc;
+  const struct { const char* what; const void* p; } numbers[] = {{"loss", a.loss}, {"lse", a.lse}, {"rest", a.rest},
+                                                                 {"d_loss", a.d_loss}, {"lse", a.in_lse}, {"rest", a.in_rest}};
+  for (const auto& x : numbers)
+    if ((rc = check_numbers(x.what, x.p, 4)) != NSM_OK) return rc;
+  const bool in_place = v.d_logits == v.logits;
+  const Range ranges[] = {{v.logits, span_bytes(v.rows, v.ld, v.vocab, size), in_place},
+                          {in_place ? nullptr : v.d_logits, span_bytes(v.rows, v.ldd, v.vocab, size), true},
+                          {a.teacher, span_bytes(v.rows, a.ldt, a.k, tsize), false},
+                          {a.index, span_bytes(v.rows, a.ldi, a.k, isize), false},
+                          {a.loss, n, true}, {a.lse, n, true}, {a.rest, n, true},
+                          {a.d_loss, n, false}, {a.in_lse, n, false}, {a.in_rest, n, false}};
+  if ((rc = check_ranges(ranges, int(sizeof ranges / sizeof ranges[0]))) != NSM_OK) return rc;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const PdlScope pdl(v.rows * v.vocab);
+  cudaError_t e;
+  {
+    TimedLaunch t(stream, NSM_KIND_DISTILL, vocab_work(v));
+    e = launch_distill(a, stream);
+  }
+  if (e != cudaSuccess) return fail_cuda(e, "distillation launch");
+  t_last_launches = 1;
   return NSM_OK;
 }
 
@@ -1221,7 +1377,7 @@ using namespace nsm;
 
 extern "C" {
 
-int nsm_version(void) { return 100; }
+int nsm_version(void) { return 200; }
 
 const char* nsm_last_error(void) { return t_last_error.c_str(); }
 
@@ -1650,6 +1806,135 @@ int muon_orthogonalize_noalloc(const void* in_bf16, void* out_bf16, const int64_
   if (rc != NSM_OK) return rc;
   t_last_launches = launches;
   return NSM_OK;
+}
+
+int nsm_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld, const void* tokens,
+                 int tokens_wide, float temperature, int k, float* logprob, float* entropy, float* lse,
+                 float* top_logprob, int32_t* top_index, nsm_stream_t stream) {
+  LogprobArgs a{};
+  const int rc = check_vocab(a.v, logits, dtype, rows, vocab, ld, temperature, nullptr, 0);
+  if (rc != NSM_OK) return rc;
+  if (k < 0 || k > kTopMaxK) return fail(NSM_ERR_ARG, "k = %d not in [0, %d]", k, kTopMaxK);
+  if (rows > 0) {
+    if (k > 0 && (!top_logprob || !top_index)) return fail(NSM_ERR_NULL, "top_logprob or top_index is NULL");
+    if (logprob && !tokens) return fail(NSM_ERR_NULL, "logprob is asked for without tokens");
+    if (!logprob && !entropy && !lse && k == 0) return fail(NSM_ERR_NULL, "no output is asked for");
+  }
+  a.tokens = tokens;
+  a.tokens_wide = tokens_wide != 0;
+  a.k = k;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top_logprob = top_logprob;
+  a.top_index = top_index;
+  return run_logprobs(a, stream);
+}
+
+int nsm_logprobs_grad(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld, const void* tokens,
+                      int tokens_wide, float temperature, const float* d_logprob, const float* d_entropy,
+                      void* d_logits, int64_t ldd, float* logprob, float* entropy, float* lse, nsm_stream_t stream) {
+  if (rows > 0 && !d_logits) return fail(NSM_ERR_NULL, "d_logits is NULL");
+  LogprobArgs a{};
+  const int rc = check_vocab(a.v, logits, dtype, rows, vocab, ld, temperature, d_logits, ldd);
+  if (rc != NSM_OK) return rc;
+  if (rows > 0 && !d_logprob && !d_entropy) return fail(NSM_ERR_NULL, "neither d_logprob nor d_entropy is given");
+  if (rows > 0 && (d_logprob || logprob) && !tokens) return fail(NSM_ERR_NULL, "tokens is NULL");
+  a.tokens = tokens;
+  a.tokens_wide = tokens_wide != 0;
+  a.d_logprob = d_logprob;
+  a.d_entropy = d_entropy;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.lse = lse;
+  return run_logprobs(a, stream);
+}
+
+int nsm_logprobs_backward(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld, const void* tokens,
+                          int tokens_wide, float temperature, const float* lse, const float* entropy,
+                          const float* d_logprob, const float* d_entropy, void* d_logits, int64_t ldd,
+                          nsm_stream_t stream) {
+  if (rows > 0 && (!d_logits || !lse)) return fail(NSM_ERR_NULL, "d_logits or lse is NULL");
+  LogprobArgs a{};
+  const int rc = check_vocab(a.v, logits, dtype, rows, vocab, ld, temperature, d_logits, ldd);
+  if (rc != NSM_OK) return rc;
+  if (rows > 0 && !d_logprob && !d_entropy) return fail(NSM_ERR_NULL, "neither d_logprob nor d_entropy is given");
+  if (rows > 0 && d_logprob && !tokens) return fail(NSM_ERR_NULL, "tokens is NULL");
+  if (rows > 0 && d_entropy && !entropy) return fail(NSM_ERR_NULL, "d_entropy is given without entropy");
+  a.tokens = tokens;
+  a.tokens_wide = tokens_wide != 0;
+  a.d_logprob = d_logprob;
+  a.d_entropy = d_entropy;
+  a.in_lse = lse;
+  a.in_entropy = entropy;
+  return run_logprobs(a, stream);
+}
+
+int nsm_distill(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld, const void* teacher,
+                int teacher_dtype, int64_t ldt, const void* index, int index_wide, int64_t ldi, int k,
+                float temperature, int tail, float* loss, float* lse, float* rest, nsm_stream_t stream) {
+  DistillArgs a{};
+  const int rc = check_vocab(a.v, logits, dtype, rows, vocab, ld, temperature, nullptr, 0);
+  if (rc != NSM_OK) return rc;
+  if (rows > 0 && !loss) return fail(NSM_ERR_NULL, "loss is NULL");
+  a.teacher = teacher;
+  a.index = index;
+  a.ldt = ldt;
+  a.ldi = ldi;
+  a.teacher_dtype = teacher_dtype;
+  a.index_wide = index_wide != 0;
+  a.k = k;
+  a.tail = tail != 0;
+  a.loss = loss;
+  a.lse = lse;
+  a.rest = rest;
+  return run_distill(a, stream);
+}
+
+int nsm_distill_grad(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld, const void* teacher,
+                     int teacher_dtype, int64_t ldt, const void* index, int index_wide, int64_t ldi, int k,
+                     float temperature, int tail, const float* d_loss, void* d_logits, int64_t ldd, float* loss,
+                     float* lse, float* rest, nsm_stream_t stream) {
+  if (rows > 0 && !d_logits) return fail(NSM_ERR_NULL, "d_logits is NULL");
+  DistillArgs a{};
+  const int rc = check_vocab(a.v, logits, dtype, rows, vocab, ld, temperature, d_logits, ldd);
+  if (rc != NSM_OK) return rc;
+  a.teacher = teacher;
+  a.index = index;
+  a.ldt = ldt;
+  a.ldi = ldi;
+  a.teacher_dtype = teacher_dtype;
+  a.index_wide = index_wide != 0;
+  a.k = k;
+  a.tail = tail != 0;
+  a.d_loss = d_loss;
+  a.loss = loss;
+  a.lse = lse;
+  a.rest = rest;
+  return run_distill(a, stream);
+}
+
+int nsm_distill_backward(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld, const void* teacher,
+                         int teacher_dtype, int64_t ldt, const void* index, int index_wide, int64_t ldi, int k,
+                         float temperature, int tail, const float* lse, const float* rest, const float* d_loss,
+                         void* d_logits, int64_t ldd, nsm_stream_t stream) {
+  if (rows > 0 && (!d_logits || !lse)) return fail(NSM_ERR_NULL, "d_logits or lse is NULL");
+  if (rows > 0 && tail && !rest) return fail(NSM_ERR_NULL, "the tail's backward pass needs rest");
+  DistillArgs a{};
+  const int rc = check_vocab(a.v, logits, dtype, rows, vocab, ld, temperature, d_logits, ldd);
+  if (rc != NSM_OK) return rc;
+  a.teacher = teacher;
+  a.index = index;
+  a.ldt = ldt;
+  a.ldi = ldi;
+  a.teacher_dtype = teacher_dtype;
+  a.index_wide = index_wide != 0;
+  a.k = k;
+  a.tail = tail != 0;
+  a.d_loss = d_loss;
+  a.in_lse = lse;
+  a.in_rest = rest;
+  return run_distill(a, stream);
 }
 
 int nsm_device_status(nsm_stream_t stream, int* status_out) {

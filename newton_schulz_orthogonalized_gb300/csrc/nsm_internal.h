@@ -222,6 +222,39 @@ struct SmallOp {
 static_assert(sizeof(SmallOp) == 52, "SmallOp layout");
 constexpr int kSmallMaxOps = 96;
 
+// ---- losses over a vocabulary
+
+constexpr int kVocabMax = 1 << 20;     // logits per row at most
+constexpr int kTopMaxK = 128;          // top alternatives per row at most
+constexpr int kDistillMaxK = 128;      // teacher entries per row at most
+
+// Rows of logits at temperature t and, for a gradient, where it goes.
+struct VocabArgs {
+  const void* logits;
+  void* d_logits;    // NULL: no gradient
+  int64_t rows, ld, ldd;
+  int32_t vocab, dtype;
+  float t, inv_t, c;  // c = log2(e) / t
+};
+struct LogprobArgs {
+  VocabArgs v;
+  const void* tokens;  // NULL: no row has a token
+  int32_t tokens_wide, k;
+  float *logprob, *entropy, *lse, *top_logprob;
+  int32_t* top_index;
+  const float *d_logprob, *d_entropy;
+  const float *in_lse, *in_entropy;  // in_lse != NULL: the backward pass alone
+};
+struct DistillArgs {
+  VocabArgs v;
+  const void *teacher, *index;
+  int64_t ldt, ldi;
+  int32_t teacher_dtype, index_wide, k, tail;
+  float *loss, *lse, *rest;
+  const float* d_loss;
+  const float *in_lse, *in_rest;  // in_lse != NULL: the backward pass alone
+};
+
 // ---- launchers (defined in the .cu files) ---------------------------------------
 
 // Runs `ops` for every job; the final pass stores O into its X buffer.
@@ -270,6 +303,9 @@ cudaError_t launch_gemm(const GemmLaunch& l, int num_sms, cudaStream_t stream);
 // bytes from page-locked host memory (src_mapped: its device mapping) to device memory, by
 // `ctas` CTAs of SM loads
 cudaError_t launch_copy_h2d(void* dst, const void* src_mapped, size_t bytes, int ctas, cudaStream_t stream);
+
+cudaError_t launch_logprobs(const LogprobArgs& args, cudaStream_t stream);
+cudaError_t launch_distill(const DistillArgs& args, cudaStream_t stream);
 
 int* device_status_ptr();
 // One CTA whose bounded wait expires after limit_ns and records kDevTimeout.

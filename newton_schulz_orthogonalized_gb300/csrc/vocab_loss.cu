@@ -16,8 +16,12 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "launch.cuh"
 #include "nsm_internal.h"
+#include "ptx.cuh"
 
 namespace nsm {
 namespace {
@@ -32,30 +36,143 @@ constexpr float kRefSlack = 16.f;
 // log2 q below this is a q of 0 in fp32: it bounds 0 * -inf in entropy terms
 constexpr float kLog2Floor = -200.f;
 constexpr int kTopCandidates = 1024;
+constexpr int kMaxCluster = 8;
 
+// Two fp32 values in one 64-bit register: add, multiply and fused multiply-add of both are
+// one instruction each.
+using Pair = uint64_t;
+__device__ __forceinline__ Pair make_pair(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split_pair(Pair p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair pair_mul(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair pair_fma(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A 16-byte vector of one of the logits' types.
 template <typename T>
 struct Elem;
 template <>
 struct Elem<float> {
   static constexpr int kVec = 4;
   static constexpr int kKeyLowBit = 0;  // lowest bit in which two values' keys can differ
+  static constexpr uint32_t kNegInfBits = 0xff800000u;
   static __device__ __forceinline__ float to_float(float v) { return v; }
   static __device__ __forceinline__ float from_float(float v) { return v; }
+  static __device__ __forceinline__ void unpack(const uint4& r, Pair (&x)[2]) {
+    x[0] = (static_cast<Pair>(r.y) << 32) | r.x;
+    x[1] = (static_cast<Pair>(r.w) << 32) | r.z;
+  }
+  static __device__ __forceinline__ uint4 pack(const Pair (&x)[2]) {
+    return make_uint4(static_cast<uint32_t>(x[0]), static_cast<uint32_t>(x[0] >> 32), static_cast<uint32_t>(x[1]),
+                      static_cast<uint32_t>(x[1] >> 32));
+  }
+  static __device__ __forceinline__ float largest(const uint4& r) {  // NaNs aside
+    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  }
 };
 template <>
 struct Elem<__nv_bfloat16> {
   static constexpr int kVec = 8;
   static constexpr int kKeyLowBit = 16;
+  static constexpr uint32_t kNegInfBits = 0xff80u;
   static __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
   static __device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
+  static __device__ __forceinline__ Pair widen(uint32_t w) {
+    return (static_cast<Pair>(w & 0xffff0000u) << 32) | (w << 16);
+  }
+  static __device__ __forceinline__ uint32_t narrow(Pair p) {
+    float lo, hi;
+    split_pair(p, lo, hi);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ void unpack(const uint4& r, Pair (&x)[4]) {
+    x[0] = widen(r.x);
+    x[1] = widen(r.y);
+    x[2] = widen(r.z);
+    x[3] = widen(r.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const Pair (&x)[4]) {
+    return make_uint4(narrow(x[0]), narrow(x[1]), narrow(x[2]), narrow(x[3]));
+  }
+  static __device__ __forceinline__ float largest(const uint4& r) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r);
+    const float2 m = __bfloat1622float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+    return fmaxf(m.x, m.y);
+  }
 };
 template <>
 struct Elem<__half> {
   static constexpr int kVec = 8;
   static constexpr int kKeyLowBit = 13;
+  static constexpr uint32_t kNegInfBits = 0xfc00u;
   static __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
   static __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
+  static __device__ __forceinline__ Pair widen(uint32_t w) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return make_pair(f.x, f.y);
+  }
+  static __device__ __forceinline__ uint32_t narrow(Pair p) {
+    float lo, hi;
+    split_pair(p, lo, hi);
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ void unpack(const uint4& r, Pair (&x)[4]) {
+    x[0] = widen(r.x);
+    x[1] = widen(r.y);
+    x[2] = widen(r.z);
+    x[3] = widen(r.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const Pair (&x)[4]) {
+    return make_uint4(narrow(x[0]), narrow(x[1]), narrow(x[2]), narrow(x[3]));
+  }
+  static __device__ __forceinline__ float largest(const uint4& r) {
+    const __half2* h = reinterpret_cast<const __half2*>(&r);
+    const float2 m = __half22float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+    return fmaxf(m.x, m.y);
+  }
 };
+
+// Element e of a vector, and the vector with element e replaced (e may vary at run time).
+template <typename T>
+__device__ __forceinline__ float vec_get(const uint4& r, int e) {
+  return Elem<T>::to_float(reinterpret_cast<const T*>(&r)[e]);
+}
+template <typename T>
+__device__ __forceinline__ void vec_mask(uint4& r, uint32_t bits) {  // -inf where a bit is set
+  uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (sizeof(T) == 4) {
+      if (bits >> j & 1) w[j] = Elem<T>::kNegInfBits;
+    } else {
+      if (bits >> (2 * j) & 1) w[j] = (w[j] & 0xffff0000u) | Elem<T>::kNegInfBits;
+      if (bits >> (2 * j + 1) & 1) w[j] = (w[j] & 0x0000ffffu) | (Elem<T>::kNegInfBits << 16);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void vec_set(uint4& r, int e, float v) {
+  reinterpret_cast<T*>(&r)[e] = Elem<T>::from_float(v);
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -70,78 +187,112 @@ struct Row {
   static constexpr int kVec = Elem<T>::kVec;
   T* p;
   int vocab, lead, nvec;
-  __device__ __forceinline__ Row(T* base, int vocab_) : p(base), vocab(vocab_) {
+  int* status;
+  int kernel;
+  __device__ __forceinline__ Row(T* base, int vocab_, int* status_, int kernel_)
+      : p(base), vocab(vocab_), status(status_), kernel(kernel_) {
     lead = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15) / sizeof(T));
     nvec = (vocab + lead + kVec - 1) / kVec;
   }
   __device__ __forceinline__ int first(int i) const { return i * kVec - lead; }
   __device__ __forceinline__ bool whole(int i) const { return first(i) >= 0 && first(i) + kVec <= vocab; }
-  // elements outside the row read as -inf
-  __device__ __forceinline__ void load(int i, float (&f)[kVec], int* status, int kernel) const {
+  __device__ __forceinline__ uint4 load_whole(int i) const {
+    if (!bounds_ok(i >= 0 && whole(i) && (reinterpret_cast<uintptr_t>(p + first(i)) & 15) == 0, status, kernel, 0,
+                   NSM_SITE_LOGITS))
+      return make_uint4(0, 0, 0, 0);
+    return *reinterpret_cast<const uint4*>(p + first(i));
+  }
+  // vector i of the row, with -inf outside it
+  __device__ __forceinline__ uint4 load(int i) const {
     const int e0 = first(i);
-    if (whole(i)) {
-      if (!bounds_ok(i >= 0 && (reinterpret_cast<uintptr_t>(p + e0) & 15) == 0, status, kernel, 0, NSM_SITE_LOGITS)) {
+    if (whole(i)) return load_whole(i);
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    T* h = reinterpret_cast<T*>(&raw);
+    uint32_t none = 0;
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) f[e] = kNegInf;
-        return;
-      }
-      const uint4 raw = *reinterpret_cast<const uint4*>(p + e0);
-      const T* h = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) f[e] = Elem<T>::to_float(h[e]);
+    for (int e = 0; e < kVec; ++e) {
+      const int v = e0 + e;
+      if (v >= 0 && v < vocab) h[e] = p[v]; else none |= 1u << e;
+    }
+    vec_mask<T>(raw, none);
+    return raw;
+  }
+  // writes kVec gradients whose first element is e0 of the row, as one 16-byte store where
+  // the vector is whole and aligned
+  __device__ __forceinline__ void store(int e0, const uint4& raw) const {
+    if (!bounds_ok(e0 > -kVec && e0 < vocab, status, kernel, 0, NSM_SITE_GRADIENT)) return;
+    if (e0 >= 0 && e0 + kVec <= vocab && (reinterpret_cast<uintptr_t>(p + e0) & 15) == 0) {
+      *reinterpret_cast<uint4*>(p + e0) = raw;
     } else {
+      const T* h = reinterpret_cast<const T*>(&raw);
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
         const int v = e0 + e;
-        f[e] = v >= 0 && v < vocab ? Elem<T>::to_float(p[v]) : kNegInf;
+        if (v >= 0 && v < vocab) p[v] = h[e];
       }
     }
   }
 };
 
-// Writes kVec gradients whose first element is e0 of a row, as one 16-byte store where the
-// vector is whole and the gradient's row is aligned like the logits'.
+// The part of a row's vectors that one block takes: whole vectors [begin, end), of which
+// thread t has every kVocabThreads-th from begin + t on, and the row's ragged first and last
+// vector (-1: not here), which threads kHeadThread and kTailThread have as well.
+constexpr int kHeadThread = 0, kTailThread = 32;
+struct Part {
+  int begin, end, head, tail;
+};
+
 template <typename T>
-__device__ __forceinline__ void store_vec(T* row, int vocab, int e0, const float (&g)[Elem<T>::kVec], int* status,
-                                          int kernel) {
-  constexpr int kVec = Elem<T>::kVec;
-  const bool whole = e0 >= 0 && e0 + kVec <= vocab;
-  if (whole && (reinterpret_cast<uintptr_t>(row + e0) & 15) == 0) {
-    uint4 raw;
-    T* h = reinterpret_cast<T*>(&raw);
+__device__ __forceinline__ Part part_of(const Row<T>& row, int piece, int pieces) {
+  const int whole_begin = row.lead > 0 ? 1 : 0;
+  const int whole_end = max(whole_begin, (row.vocab + row.lead) / Elem<T>::kVec);
+  const int count = whole_end - whole_begin, each = (count + pieces - 1) / pieces;
+  Part part;
+  part.begin = whole_begin + min(count, piece * each);
+  part.end = whole_begin + min(count, (piece + 1) * each);
+  part.head = row.lead > 0 && piece == 0 ? 0 : -1;
+  part.tail = whole_end < row.nvec && piece == pieces - 1 ? whole_end : -1;
+  return part;
+}
+
+// use(i, vector) for every vector of the part that this thread has, four loads in flight.
+template <typename T, typename F>
+__device__ __forceinline__ void for_vectors(const Row<T>& row, const Part& part, F&& use) {
+  int i = part.begin + static_cast<int>(threadIdx.x);
+  for (; i + 3 * kVocabThreads < part.end; i += 4 * kVocabThreads) {
+    uint4 raw[4];
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) h[e] = Elem<T>::from_float(g[e]);
-    *reinterpret_cast<uint4*>(row + e0) = raw;
-  } else {
+    for (int u = 0; u < 4; ++u) raw[u] = row.load_whole(i + u * kVocabThreads);
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      const int v = e0 + e;
-      if (v >= 0 && v < vocab) row[v] = Elem<T>::from_float(g[e]);
-    }
+    for (int u = 0; u < 4; ++u) use(i + u * kVocabThreads, raw[u]);
   }
+  for (; i < part.end; i += kVocabThreads) use(i, row.load_whole(i));
+  if (part.head >= 0 && threadIdx.x == kHeadThread) use(part.head, row.load(part.head));
+  if (part.tail >= 0 && threadIdx.x == kTailThread) use(part.tail, row.load(part.tail));
 }
 
 template <typename T>
-__device__ __forceinline__ void zero_row(T* row, int vocab, int* status, int kernel) {
-  const Row<T> out(row, vocab);
-  float g[Elem<T>::kVec] = {};
-  for (int i = threadIdx.x; i < out.nvec; i += kVocabThreads) store_vec<T>(row, vocab, out.first(i), g, status, kernel);
+__device__ __forceinline__ void zero_part(const Row<T>& out, int piece, int pieces) {
+  const Part part = part_of(out, piece, pieces);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int i = part.begin + static_cast<int>(threadIdx.x); i < part.end; i += kVocabThreads) out.store(out.first(i), zero);
+  if (part.head >= 0 && threadIdx.x == kHeadThread) out.store(out.first(part.head), zero);
+  if (part.tail >= 0 && threadIdx.x == kTailThread) out.store(out.first(part.tail), zero);
 }
 
-// A sum of exponentials s = sum 2^((x - ref) c) with its sum of y 2^y (y the exponent), the
-// largest x and where this thread met it first.
+// A sum of exponentials s = sum 2^y, y = (x - ref) c, with sum y 2^y (both in two halves, one
+// per element of a pair), the largest x and the vector where this thread met it first.
 struct Sums {
   float ref = 0.f, limit = kNegInf;  // no reference yet: every finite logit exceeds the limit
-  float s = 0.f, sy = 0.f;
+  Pair s = 0, sy = 0;
   float max = kNegInf;
   int max_vec = -1;
 };
 
-template <int N, bool ENT>
-__device__ __forceinline__ void add_vec(Sums& a, const float (&f)[N], int i, float c) {
-  float m = f[0];
-#pragma unroll
-  for (int e = 1; e < N; ++e) m = fmaxf(m, f[e]);
+template <typename T, bool ENT>
+__device__ __forceinline__ void add_vec(Sums& a, const uint4& raw, int i, float c) {
+  constexpr int kPairs = Elem<T>::kVec / 2;
+  const float m = Elem<T>::largest(raw);
   if (m > a.max) {
     a.max = m;
     a.max_vec = i;
@@ -149,64 +300,114 @@ __device__ __forceinline__ void add_vec(Sums& a, const float (&f)[N], int i, flo
   if (m > a.limit) {
     if (a.limit != kNegInf) {  // move what is there to the new reference
       const float d = (a.ref - m) * c, r = ex2(d);
-      if (ENT) a.sy = r > 0.f ? r * (a.sy + d * a.s) : 0.f;
-      a.s *= r;
+      if (ENT) a.sy = r > 0.f ? pair_mul(make_pair(r, r), pair_fma(make_pair(d, d), a.s, a.sy)) : 0;
+      a.s = pair_mul(a.s, make_pair(r, r));
     }
     a.ref = m;
     a.limit = m + kRefSlack / c;
   }
-  float s = 0.f, sy = 0.f;
+  Pair x[kPairs];
+  Elem<T>::unpack(raw, x);
+  const Pair minus_ref = make_pair(-a.ref, -a.ref), cc = make_pair(c, c);
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const float y = (f[e] - a.ref) * c;
-    const float x = ex2(y);
-    s += x;
-    if (ENT) sy += x * fmaxf(y, kLog2Floor);
+  for (int j = 0; j < kPairs; ++j) {
+    const Pair y = pair_mul(pair_add(x[j], minus_ref), cc);
+    float y0, y1;
+    split_pair(y, y0, y1);
+    const Pair e = make_pair(ex2(y0), ex2(y1));
+    a.s = pair_add(a.s, e);
+    if (ENT) a.sy = pair_fma(e, make_pair(fmaxf(y0, kLog2Floor), fmaxf(y1, kLog2Floor)), a.sy);
   }
-  a.s += s;
-  if (ENT) a.sy += sy;
-}
-
-// Two sums relative to the larger of their maxima (max is then the reference).
-__device__ __forceinline__ void rebase(float& s, float& sy, float ref, float max, float c) {
-  const float d = (ref - max) * c;
-  const float r = max == kNegInf ? 0.f : ex2(d);  // nothing there: s is 0 (or a NaN, which stays)
-  sy = r > 0.f ? r * (sy + d * s) : r * s;
-  s *= r;
 }
 
 struct Totals {
   float max, s, sy;
 };
 
-__device__ __forceinline__ Totals merge(const Totals& a, const Totals& b, float c) {
-  Totals t;
-  t.max = fmaxf(a.max, b.max);
-  float as = a.s, asy = a.sy, bs = b.s, bsy = b.sy;
-  if (a.max != t.max) rebase(as, asy, a.max, a.max == kNegInf ? kNegInf : t.max, c);
-  if (b.max != t.max) rebase(bs, bsy, b.max, b.max == kNegInf ? kNegInf : t.max, c);
-  t.s = as + bs;
-  t.sy = asy + bsy;
+// Moves sums from their reference to `max` (>= ref); what has no reference is 0, or a NaN.
+template <bool ENT>
+__device__ __forceinline__ void rebase(float& s, float& sy, float ref, float max, float c) {
+  const float d = (ref - max) * c;
+  const float r = ref == kNegInf ? 0.f : ex2(d);
+  if (ENT) sy = r > 0.f ? r * (sy + d * s) : r * s;
+  s *= r;
+}
+
+// Totals of a group of `N` (a power of two) lanes, the same in every lane, in a fixed order.
+template <bool ENT, int N>
+__device__ __forceinline__ Totals group_totals(float ref, float max, float s, float sy, float c) {
+  Totals t{max, s, sy};
+#pragma unroll
+  for (int o = N / 2; o; o >>= 1) t.max = fmaxf(t.max, __shfl_xor_sync(~0u, t.max, o));
+  rebase<ENT>(t.s, t.sy, ref, t.max, c);
+#pragma unroll
+  for (int o = N / 2; o; o >>= 1) {
+    t.s += __shfl_xor_sync(~0u, t.s, o);
+    if (ENT) t.sy += __shfl_xor_sync(~0u, t.sy, o);
+  }
   return t;
 }
 
-// The block's sums relative to its largest logit, the same in every thread (fixed order).
-__device__ __forceinline__ Totals block_totals(const Sums& a, float c, Totals* parts) {
-  Totals t{a.max, a.s, a.sy};
-  if (a.max != kNegInf) rebase(t.s, t.sy, a.ref, a.max, c);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const Totals other{__shfl_xor_sync(~0u, t.max, o), __shfl_xor_sync(~0u, t.s, o), __shfl_xor_sync(~0u, t.sy, o)};
-    // the same operand order in both lanes of a pair
-    t = (threadIdx.x & o) ? merge(other, t, c) : merge(t, other, c);
+template <bool ENT>
+__device__ __forceinline__ Totals warp_totals(const Sums& a, float c) {
+  float s0, s1, y0 = 0.f, y1 = 0.f;
+  split_pair(a.s, s0, s1);
+  if (ENT) split_pair(a.sy, y0, y1);
+  return group_totals<ENT, 32>(a.limit == kNegInf ? kNegInf : a.ref, a.max, s0 + s1, y0 + y1, c);
+}
+
+// The totals of every CTA's threads of a cluster relative to the row's largest logit, the
+// same in every thread: warps, then CTAs, in a fixed order.  With more than one CTA, each has
+// arrived at the cluster's barrier before; the next use of `sh` needs a barrier.
+struct TotalsShared {
+  Totals warp[kVocabWarps];
+  Totals cta[kMaxCluster];
+};
+template <bool ENT>
+__device__ __forceinline__ Totals row_totals(const Sums& a, float c, TotalsShared& sh, int ctas) {
+  const Totals w = warp_totals<ENT>(a, c);
+  if ((threadIdx.x & 31) == 0) sh.warp[threadIdx.x >> 5] = w;
+  __syncthreads();
+  const Totals v = sh.warp[threadIdx.x & (kVocabWarps - 1)];
+  const Totals mine = group_totals<ENT, kVocabWarps>(v.max, v.max, v.s, v.sy, c);
+  if (ctas == 1) return mine;
+  ptx::cluster_wait();  // every CTA runs (they arrived when they started)
+  if (static_cast<int>(threadIdx.x) < ctas) {
+    const uint32_t to = ptx::mapa_shared(ptx::smem_u32(&sh.cta[ptx::cluster_ctarank()]), threadIdx.x);
+    ptx::st_cluster_f32(to, mine.max);
+    ptx::st_cluster_f32(to + 4, mine.s);
+    ptx::st_cluster_f32(to + 8, mine.sy);
   }
-  if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = t;
-  __syncthreads();
-  t = parts[0];
-#pragma unroll
-  for (int w = 1; w < kVocabWarps; ++w) t = merge(t, parts[w], c);
-  __syncthreads();
+  ptx::cluster_sync();
+  Totals t{kNegInf, 0.f, 0.f};
+  for (int r = 0; r < ctas; ++r) t.max = fmaxf(t.max, sh.cta[r].max);
+  for (int r = 0; r < ctas; ++r) {
+    Totals o = sh.cta[r];
+    rebase<ENT>(o.s, o.sy, o.max, t.max, c);
+    t.s += o.s;
+    t.sy += o.sy;
+  }
   return t;
+}
+
+// One vector of gradients q (ca + cb log2 q), q = 2^((x - ref) c - log2_s).
+template <typename T, bool ENT>
+__device__ __forceinline__ uint4 gradient_vec(const uint4& raw, float ref, float c, float log2_s, float ca, float cb) {
+  constexpr int kPairs = Elem<T>::kVec / 2;
+  Pair x[kPairs];
+  Elem<T>::unpack(raw, x);
+  const Pair minus_ref = make_pair(-ref, -ref), cc = make_pair(c, c), minus_log = make_pair(-log2_s, -log2_s);
+#pragma unroll
+  for (int j = 0; j < kPairs; ++j) {
+    const Pair y = pair_fma(pair_add(x[j], minus_ref), cc, minus_log);
+    float y0, y1;
+    split_pair(y, y0, y1);
+    const Pair q = make_pair(ex2(y0), ex2(y1));
+    const Pair f = ENT ? pair_fma(make_pair(fmaxf(y0, kLog2Floor), fmaxf(y1, kLog2Floor)), make_pair(cb, cb), make_pair(ca, ca))
+                       : make_pair(ca, ca);
+    x[j] = pair_mul(q, f);
+  }
+  return Elem<T>::pack(x);
 }
 
 __device__ __forceinline__ int64_t load_index(const void* p, int wide, int64_t i) {
@@ -220,7 +421,11 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   const uint32_t u = __float_as_uint(f + 0.f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
+}
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
+static_assert(kTopCandidates >= kMaxCluster * kTopMaxK, "every CTA's k largest fit");
 
 struct TopShared {
   uint32_t key[kVocabThreads];
@@ -228,8 +433,10 @@ struct TopShared {
   int32_t list[kVocabThreads];
   uint64_t cand[kTopCandidates];
   uint64_t best[kVocabWarps];
+  uint64_t gathered[kMaxCluster * kTopMaxK];  // rank 0: every CTA's own k largest
   uint32_t bound_key, bound_tie_top;
   int32_t bound_vec, nlist, ncand;
+  uint32_t taken[kMaxCluster];                // how many keys each CTA gave
 };
 
 __device__ __forceinline__ uint64_t full_key(float f, int v) {
@@ -296,12 +503,23 @@ __device__ __forceinline__ void top_bound(TopShared& sh, int k) {
   }
 }
 
-// The row's k largest logits, from every thread's largest one and where it met it.
-template <typename T>
-__device__ __forceinline__ void row_top(const Row<T>& row, const Sums& a, int k, float max, float inv_t, float log_s,
-                                        float* out_value, int32_t* out_index, TopShared& sh, int* status) {
+// Places `n` distinct keys in descending order: put(place, key) for the first k.
+template <typename F>
+__device__ __forceinline__ void place_keys(const uint64_t* keys, int n, int k, F&& put) {
+  for (int j = threadIdx.x; j < n; j += kVocabThreads) {
+    const uint64_t mine = keys[j];
+    int place = 0;
+    for (int o = 0; o < n; ++o) place += keys[o] > mine;
+    if (place < k) put(place, mine);
+  }
+}
+
+// The k largest logits of the block's part of a row, from every thread's largest one and
+// where it met it: put(place, key), and the number of places that were filled.
+template <typename T, typename F>
+__device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, const Sums& a, int k, TopShared& sh, F&& put) {
   constexpr int kVec = Elem<T>::kVec;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   sh.key[tid] = order_key(a.max);
   sh.vec[tid] = a.max_vec;
   __syncthreads();
@@ -312,162 +530,221 @@ __device__ __forceinline__ void row_top(const Row<T>& row, const Sums& a, int k,
   const uint32_t key = sh.key[tid];
   if (key >= bound && (key > tie_top || a.max_vec <= bound_vec)) sh.list[atomicAdd(&sh.nlist, 1)] = tid;
   __syncthreads();
-  const int nlist = sh.nlist, lane = tid & 31;
-  for (int q = tid >> 5; q < nlist; q += kVocabWarps) {
-    for (int i = sh.list[q] + lane * kVocabThreads; i < row.nvec; i += 32 * kVocabThreads) {
-      float f[kVec];
-      row.load(i, f, status, NSM_KERNEL_LOGPROBS);
+  const int nlist = sh.nlist;
+  auto offer = [&](int i) {
+    const uint4 raw = row.load(i);
+    if (order_key(Elem<T>::largest(raw)) < bound) return;
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const uint32_t ek = order_key(f[e]);
-        if (ek >= bound && (ek > tie_top || i <= bound_vec)) {
-          const int at = atomicAdd(&sh.ncand, 1);
-          if (at < kTopCandidates) sh.cand[at] = full_key(f[e], row.first(i) + e);
-        }
+    for (int e = 0; e < kVec; ++e) {
+      const float f = vec_get<T>(raw, e);
+      const uint32_t ek = order_key(f);
+      if (ek >= bound && (ek > tie_top || i <= bound_vec)) {
+        const int at = atomicAdd(&sh.ncand, 1);
+        if (at < kTopCandidates) sh.cand[at] = full_key(f, row.first(i) + e);
       }
     }
+  };
+  for (int q = tid >> 5; q < nlist; q += kVocabWarps) {
+    const int owner = sh.list[q];
+    for (int i = part.begin + owner + lane * kVocabThreads; i < part.end; i += 32 * kVocabThreads) offer(i);
+    if (owner == kHeadThread && part.head >= 0 && lane == 0) offer(part.head);
+    if (owner == kTailThread && part.tail >= 0 && lane == 0) offer(part.tail);
   }
   __syncthreads();
   const int ncand = sh.ncand;
   if (ncand <= kTopCandidates) {
-    // keys are distinct: a candidate's place is the number of larger ones
-    for (int j = tid; j < ncand; j += kVocabThreads) {
-      const uint64_t mine = sh.cand[j];
-      int place = 0;
-      for (int o = 0; o < ncand; ++o) place += sh.cand[o] > mine;
-      if (place < k) {
-        const int v = static_cast<int>(0xffffffffu - static_cast<uint32_t>(mine));
-        out_index[place] = v;
-        out_value[place] = (Elem<T>::to_float(row.p[v]) - max) * inv_t - log_s;
+    place_keys(sh.cand, ncand, k, put);
+    return min(ncand, k);
+  }
+  // so many logits above the bound sit in few threads: one block-wide maximum per place
+  uint64_t last = ~0ull;
+  for (int j = 0; j < k; ++j) {
+    uint64_t best = 0;
+    for_vectors(row, part, [&](int i, const uint4& raw) {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        const uint64_t fk = full_key(vec_get<T>(raw, e), row.first(i) + e);
+        if (fk < last && fk > best && static_cast<uint32_t>(fk >> 32) > kKeyNegInf) best = fk;
       }
+    });
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const uint64_t other = __shfl_xor_sync(~0u, best, o);
+      best = other > best ? other : best;
     }
-    for (int j = ncand + tid; j < k; j += kVocabThreads) {
-      out_index[j] = -1;
-      out_value[j] = kNegInf;
-    }
+    if (lane == 0) sh.best[tid >> 5] = best;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kVocabWarps; ++w) best = sh.best[w] > best ? sh.best[w] : best;
+    __syncthreads();
+    last = best;  // more than kTopCandidates >= k logits are there
+    if (tid == 0) put(j, best);
+  }
+  return k;
+}
+
+// The row's k largest logits: of the block's part, or gathered from the cluster's parts.
+template <typename T>
+__device__ __forceinline__ void row_top(const Row<T>& row, const Part& part, const Sums& a, int k, float max, float inv_t,
+                                        float log_s, float* out_value, int32_t* out_index, TopShared& sh, int ctas) {
+  auto write = [&](int place, uint64_t key) {
+    const int v = static_cast<int>(0xffffffffu - static_cast<uint32_t>(key));
+    out_index[place] = v;
+    out_value[place] = (key_value(static_cast<uint32_t>(key >> 32)) - max) * inv_t - log_s;
+  };
+  int found;
+  if (ctas == 1) {
+    found = part_top<T>(row, part, a, k, sh, write);
   } else {
-    // so many logits above the bound sit in few threads: one block-wide maximum per place
-    uint64_t last = ~0ull;
-    for (int j = 0; j < k; ++j) {
-      uint64_t best = 0;
-      for (int i = tid; i < row.nvec; i += kVocabThreads) {
-        float f[kVec];
-        row.load(i, f, status, NSM_KERNEL_LOGPROBS);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          const uint64_t fk = full_key(f[e], row.first(i) + e);
-          if (fk < last && fk > best && order_key(f[e]) > kKeyNegInf) best = fk;
-        }
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const uint64_t other = __shfl_xor_sync(~0u, best, o);
-        best = other > best ? other : best;
-      }
-      if (lane == 0) sh.best[tid >> 5] = best;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kVocabWarps; ++w) best = sh.best[w] > best ? sh.best[w] : best;
-      __syncthreads();
-      last = best;  // more than kTopCandidates >= k logits are there
-      if (tid == 0) {
-        const int v = static_cast<int>(0xffffffffu - static_cast<uint32_t>(best));
-        out_index[j] = v;
-        out_value[j] = (Elem<T>::to_float(row.p[v]) - max) * inv_t - log_s;
-      }
+    const uint32_t rank = ptx::cluster_ctarank();
+    const uint32_t to = ptx::mapa_shared(ptx::smem_u32(&sh.gathered[rank * kTopMaxK]), 0);
+    const int mine = part_top<T>(row, part, a, k, sh, [&](int place, uint64_t key) { ptx::st_cluster_u64(to + place * 8, key); });
+    if (threadIdx.x == 0) ptx::st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.taken[rank]), 0), mine);
+    ptx::cluster_sync();
+    if (rank != 0) return;
+    // closed up, in kTopCandidates = kMaxCluster kTopMaxK places
+    int total = 0;
+    for (int r = 0; r < ctas; ++r) {
+      const int n = static_cast<int>(sh.taken[r]);
+      for (int j = threadIdx.x; j < n; j += kVocabThreads) sh.cand[total + j] = sh.gathered[r * kTopMaxK + j];
+      total += n;
     }
+    __syncthreads();
+    place_keys(sh.cand, total, k, write);
+    found = min(total, k);
+  }
+  for (int j = found + threadIdx.x; j < k; j += kVocabThreads) {
+    out_index[j] = -1;
+    out_value[j] = kNegInf;
   }
 }
 
 // ---------------------------------------------------------------- log probabilities
 
-template <typename T, bool FWD, bool GRAD>
+// What the gradient pass of a row needs: q (ca + cb log2 q) / ..., and the token's own value.
+struct TokenGradient {
+  float ref, log2_s, ca, cb, at_token;
+  bool zero;
+};
+
+// w logprob + h entropy: d/dx = (w (1[token] - q) - h q (log q + entropy)) / t
+__device__ __forceinline__ TokenGradient token_gradient(float w, float h, float ref, float log_s, float log2_s,
+                                                        float entropy, float x_token, bool empty, float inv_t) {
+  TokenGradient k;
+  k.zero = empty || (w == 0.f && h == 0.f);
+  k.ref = ref;
+  k.log2_s = log2_s;
+  k.ca = -(w + h * entropy) * inv_t;
+  k.cb = -h * kLn2 * inv_t;
+  k.at_token = 0.f;
+  const float log_q = (x_token - ref) * inv_t - log_s;
+  // at the token 1 - q without cancellation; 0 where it is masked
+  if (log_q != kNegInf) k.at_token = -(w * expm1f(log_q) + (h == 0.f ? 0.f : h * expf(log_q) * (log_q + entropy))) * inv_t;
+  return k;
+}
+
+template <typename T, bool ENT>
+__device__ __forceinline__ void store_token_gradient(const Row<T>& out, int e0, const uint4& raw, const TokenGradient& k,
+                                                     int token, float c) {
+  uint4 grad = gradient_vec<T, ENT>(raw, k.ref, c, k.log2_s, k.ca, k.cb);
+  if (token >= e0 && token < e0 + Elem<T>::kVec) {
+#pragma unroll
+    for (int e = 0; e < Elem<T>::kVec; ++e)
+      if (e0 + e == token) vec_set<T>(grad, e, k.at_token);
+  }
+  out.store(e0, grad);
+}
+
+// A cluster of CTAs per row (one CTA where there are rows enough).
+template <typename T, bool ENT, bool GRAD>
 __global__ void __launch_bounds__(kVocabThreads) k_logprobs(const LogprobArgs g, int* status) {
-  constexpr int kVec = Elem<T>::kVec;
-  __shared__ Totals parts[kVocabWarps];
-  __shared__ TopShared top;
+  __shared__ TotalsShared totals;
+  __shared__ typename std::conditional<GRAD, int, TopShared>::type top;
   grid_dependency_sync();
   release_dependents();
-  const int64_t r = blockIdx.x;
+  const int ctas = static_cast<int>(ptx::cluster_nctarank()), rank = static_cast<int>(ptx::cluster_ctarank());
+  if (ctas > 1) ptx::cluster_arrive();
+  const int64_t r = blockIdx.x / ctas;
   const int vocab = g.v.vocab;
   const float c = g.v.c, inv_t = g.v.inv_t;
-  const Row<T> row(static_cast<T*>(const_cast<void*>(g.v.logits)) + r * g.v.ld, vocab);
-  int64_t token = g.tokens ? load_index(g.tokens, g.tokens_wide, r) : -1;
-  if (token < 0 || token >= vocab) token = -1;
-  float ref, log_s, log2_s, entropy = 0.f;
-  bool empty;
-  const float x_token = token >= 0 ? Elem<T>::to_float(row.p[token]) : 0.f;
-  if (FWD) {
-    Sums a;
-    for (int i = threadIdx.x; i < row.nvec; i += kVocabThreads) {
-      float f[kVec];
-      row.load(i, f, status, NSM_KERNEL_LOGPROBS);
-      add_vec<kVec, true>(a, f, i, c);
+  const Row<T> row(static_cast<T*>(const_cast<void*>(g.v.logits)) + r * g.v.ld, vocab, status, NSM_KERNEL_LOGPROBS);
+  const Part part = part_of(row, rank, ctas);
+  int64_t token64 = g.tokens ? load_index(g.tokens, g.tokens_wide, r) : -1;
+  const int token = token64 < 0 || token64 >= vocab ? -1 : static_cast<int>(token64);
+  const float x_token = token >= 0 ? Elem<T>::to_float(row.p[token]) : kNegInf;
+  Sums a;
+  for_vectors(row, part, [&](int i, const uint4& raw) { add_vec<T, ENT>(a, raw, i, c); });
+  const Totals t = row_totals<ENT>(a, c, totals, ctas);
+  const bool empty = t.max == kNegInf && t.s == 0.f;  // a row of NaN has a NaN sum
+  const float ref = empty ? 0.f : t.max, log_s = empty ? 0.f : logf(t.s);
+  float entropy = 0.f;
+  if (ENT && !empty) {
+    entropy = log_s - kLn2 * (t.sy / t.s);
+    if (entropy < 0.f) entropy = 0.f;
+  }
+  if (rank == 0 && threadIdx.x == 0) {
+    if (g.lse) g.lse[r] = empty ? kNegInf : ref * inv_t + log_s;
+    if (ENT && g.entropy) g.entropy[r] = entropy;
+    if (g.logprob) g.logprob[r] = token < 0 ? 0.f : (empty ? kNegInf : (x_token - ref) * inv_t - log_s);
+  }
+  if constexpr (GRAD) {
+    const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, NSM_KERNEL_LOGPROBS);
+    const float w = g.d_logprob && token >= 0 ? g.d_logprob[r] : 0.f;
+    const float h = ENT && g.d_entropy ? g.d_entropy[r] : 0.f;
+    const TokenGradient k = token_gradient(w, h, ref, log_s, empty ? 0.f : log2f(t.s), entropy, x_token, empty, inv_t);
+    if (k.zero) {
+      zero_part(out, rank, ctas);
+    } else {
+      for_vectors(row, part, [&](int i, const uint4& raw) { store_token_gradient<T, ENT>(out, row.first(i), raw, k, token, c); });
     }
-    const Totals t = block_totals(a, c, parts);
-    empty = t.max == kNegInf && t.s == 0.f;  // a row of NaN has a NaN sum
-    ref = empty ? 0.f : t.max;
-    log2_s = empty ? 0.f : log2f(t.s);
-    log_s = empty ? 0.f : logf(t.s);
-    if (!empty) {
-      entropy = log_s - kLn2 * (t.sy / t.s);
-      if (entropy < 0.f) entropy = 0.f;
-    }
-    if (threadIdx.x == 0) {
-      if (g.lse) g.lse[r] = empty ? kNegInf : ref * inv_t + log_s;
-      if (g.entropy) g.entropy[r] = entropy;
-      if (g.logprob) g.logprob[r] = token < 0 ? 0.f : (empty ? kNegInf : (x_token - ref) * inv_t - log_s);
-    }
-    if (g.k > 0) {
-      float* value = g.top_logprob + r * g.k;
-      int32_t* index = g.top_index + r * g.k;
-      if (log_s != log_s) {  // NaN or +inf in the row
+  } else if (g.k > 0) {
+    float* value = g.top_logprob + r * g.k;
+    int32_t* index = g.top_index + r * g.k;
+    if (log_s != log_s) {  // NaN or +inf in the row
+      if (rank == 0) {
         for (int j = threadIdx.x; j < g.k; j += kVocabThreads) {
           value[j] = log_s;
           index[j] = -1;
         }
-      } else {
-        row_top<T>(row, a, g.k, ref, inv_t, log_s, value, index, top, status);
       }
+    } else {
+      row_top<T>(row, part, a, g.k, ref, inv_t, log_s, value, index, top, ctas);
     }
-  } else {
-    const float lse = g.in_lse[r];
-    empty = lse == kNegInf;
-    ref = empty ? 0.f : lse * g.v.t;
-    log2_s = log_s = 0.f;
-    if (g.d_entropy) entropy = g.in_entropy[r];
   }
-  if (GRAD) {
-    T* out = static_cast<T*>(g.v.d_logits) + r * g.v.ldd;
+}
+
+// The backward pass alone: pieces of rows, every element on its own.
+template <typename T, bool ENT>
+__global__ void __launch_bounds__(kVocabThreads) k_logprobs_backward(const LogprobArgs g, int pieces, int* status) {
+  grid_dependency_sync();
+  release_dependents();
+  const int vocab = g.v.vocab;
+  const float c = g.v.c, inv_t = g.v.inv_t;
+  const int64_t total = g.v.rows * pieces;
+  for (int64_t work = blockIdx.x; work < total; work += gridDim.x) {
+    const int64_t r = work / pieces;
+    const int piece = static_cast<int>(work - r * pieces);
+    const Row<T> row(static_cast<T*>(const_cast<void*>(g.v.logits)) + r * g.v.ld, vocab, status, NSM_KERNEL_LOGPROBS);
+    const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, NSM_KERNEL_LOGPROBS);
+    const int64_t token64 = g.tokens ? load_index(g.tokens, g.tokens_wide, r) : -1;
+    const int token = token64 < 0 || token64 >= vocab ? -1 : static_cast<int>(token64);
     const float w = g.d_logprob && token >= 0 ? g.d_logprob[r] : 0.f;
-    const float h = g.d_entropy ? g.d_entropy[r] : 0.f;
+    const float h = ENT && g.d_entropy ? g.d_entropy[r] : 0.f;
+    const float lse = g.in_lse[r];
+    const bool empty = lse == kNegInf;
     if (empty || (w == 0.f && h == 0.f)) {
-      zero_row<T>(out, vocab, status, NSM_KERNEL_LOGPROBS);
-      return;
+      zero_part(out, piece, pieces);
+      continue;
     }
-    // -q (w + h (log q + entropy)) / t = q (ca + cb log2 q)
-    const float ca = -(w + h * entropy) * inv_t, cb = -h * kLn2 * inv_t;
-    float g_token = 0.f;
-    const float log_q = (x_token - ref) * inv_t - log_s;
-    if (log_q != kNegInf) {  // at the token 1 - q without cancellation; 0 where it is masked
-      g_token = -(w * expm1f(log_q) + h * expf(log_q) * (log_q + entropy)) * inv_t;
-    }
-    for (int i = threadIdx.x; i < row.nvec; i += kVocabThreads) {
-      float f[kVec];
-      row.load(i, f, status, NSM_KERNEL_LOGPROBS);
-      const int e0 = row.first(i);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const float y = (f[e] - ref) * c - log2_s;
-        f[e] = ex2(y) * (ca + cb * fmaxf(y, kLog2Floor));
-      }
-      if (token >= e0 && token < e0 + kVec) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e)
-          if (e0 + e == token) f[e] = g_token;
-      }
-      store_vec<T>(out, vocab, e0, f, status, NSM_KERNEL_LOGPROBS);
-    }
+    // in place, another block may have written the token's own gradient already: only the
+    // block that has the token's vector needs its logit, and reads it before it writes
+    const Part part = part_of(row, piece, pieces);
+    const int at = token < 0 ? -2 : (token + row.lead) / Elem<T>::kVec;
+    const bool here = (at >= part.begin && at < part.end) || at == part.head || at == part.tail;
+    const float x_token = here ? Elem<T>::to_float(row.p[token]) : kNegInf;
+    const TokenGradient k = token_gradient(w, h, lse * g.v.t, 0.f, 0.f, ENT ? g.in_entropy[r] : 0.f, x_token, empty, inv_t);
+    __syncthreads();  // every thread has read the token's logit
+    for_vectors(row, part, [&](int i, const uint4& raw) { store_token_gradient<T, ENT>(out, row.first(i), raw, k, token, c); });
   }
 }
 
@@ -475,26 +752,13 @@ __global__ void __launch_bounds__(kVocabThreads) k_logprobs(const LogprobArgs g,
 
 struct DistillShared {
   int32_t index[kDistillMaxK];   // -1: the entry does not count
-  float x[kDistillMaxK];         // the student's logit there
-  float log_p[kDistillMaxK];
-  Totals parts[kVocabWarps];
   float sum[kVocabWarps];
   double dsum[kVocabWarps];
+  TotalsShared rest, entries;
 };
 
-__device__ __forceinline__ float block_sum(float v, float* parts) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = parts[0];
-#pragma unroll
-  for (int w = 1; w < kVocabWarps; ++w) v += parts[w];
-  __syncthreads();
-  return v;
-}
-
-__device__ __forceinline__ double block_sum(double v, double* parts) {
+template <typename V>
+__device__ __forceinline__ V block_sum(V v, V* parts) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = v;
@@ -524,193 +788,303 @@ __device__ __forceinline__ float load_number(const void* p, int dtype, int64_t i
   return static_cast<const float*>(p)[i];
 }
 
-template <typename T, bool FWD, bool GRAD>
-__global__ void __launch_bounds__(kVocabThreads) k_distill(const DistillArgs g, int* status) {
-  constexpr int kVec = Elem<T>::kVec;
-  extern __shared__ __align__(16) uint8_t members[];  // FWD: a bit per element of vector i in byte i
-  __shared__ DistillShared sh;
-  static_assert(kDistillMaxK <= kVocabThreads, "one thread per entry");
-  grid_dependency_sync();
-  release_dependents();
-  const int64_t r = blockIdx.x;
-  const int tid = threadIdx.x, k = g.k, vocab = g.v.vocab;
-  const float c = g.v.c, inv_t = g.v.inv_t;
-  const Row<T> row(static_cast<T*>(const_cast<void*>(g.v.logits)) + r * g.v.ld, vocab);
+// The teacher of a row: thread j < k has entry j (mine: its token, -1 where it does not
+// count; of equal indexes the first counts), its log p and the student's logit there.
+struct Teacher {
+  int mine;
+  float log_p, p, x;
+  float p_rest, lacking;  // the tail's 1 - sum p, and that as at least 0
+  bool any;               // there is a target
+};
 
-  // the teacher's entries: of equal indexes the first counts
+template <typename T>
+__device__ __forceinline__ Teacher read_teacher(const DistillArgs& g, int64_t r, const Row<T>& row, DistillShared& sh) {
+  static_assert(kDistillMaxK <= kVocabThreads, "one thread per entry");
+  const int tid = threadIdx.x, k = g.k;
+  Teacher t{-1, kNegInf, 0.f, kNegInf, 0.f, 0.f, false};
   float z = kNegInf;
   if (tid < k) {
     const int64_t v = load_index(g.index, g.index_wide, r * g.ldi + tid);
-    const bool in = v >= 0 && v < vocab;
-    sh.index[tid] = in ? static_cast<int32_t>(v) : -1;
-    sh.x[tid] = in ? Elem<T>::to_float(row.p[v]) : 0.f;
     z = load_number(g.teacher, g.teacher_dtype, r * g.ldt + tid);
-  }
-  if (FWD) {
-    for (int i = tid; i < (row.nvec + 3) / 4; i += kVocabThreads) reinterpret_cast<uint32_t*>(members)[i] = 0;
+    t.mine = v >= 0 && v < row.vocab ? static_cast<int>(v) : -1;
+    sh.index[tid] = t.mine;
   }
   __syncthreads();
-  int mine = tid < k ? sh.index[tid] : -1;
-  for (int j = 0; j < tid && mine >= 0; ++j)
-    if (sh.index[j] == mine) mine = -1;
+  for (int j = 0; j < tid && t.mine >= 0; ++j)
+    if (sh.index[j] == t.mine) t.mine = -1;
   __syncthreads();
-  if (tid < k) sh.index[tid] = mine;
-  if (FWD && mine >= 0) {
-    const int at = mine + row.lead, i = at / kVec;
-    atomicOr(reinterpret_cast<uint32_t*>(members) + i / 4, 1u << (8 * (i & 3) + at % kVec));
-  }
-  const bool counts = mine >= 0;
-  float log_p = kNegInf;
-  float p_rest = 0.f, lacking = 0.f;
-  bool any;
+  if (tid < k) sh.index[tid] = t.mine;
+  const bool counts = t.mine >= 0;
+  if (counts) t.x = Elem<T>::to_float(row.p[t.mine]);
   if (g.tail) {
-    if (counts) log_p = z;
+    if (counts) t.log_p = z;
     // 1 - sum p: the teacher's rest is often a small difference, so in 64 bits
-    const double sum = block_sum(counts ? exp(static_cast<double>(log_p)) : 0.0, sh.dsum);
-    lacking = static_cast<float>(1.0 - sum);
-    p_rest = lacking > 0.f ? lacking : (lacking != lacking ? lacking : 0.f);
-    any = __syncthreads_or(counts);
+    const double sum = block_sum(counts ? exp(static_cast<double>(z)) : 0.0, sh.dsum);
+    t.lacking = static_cast<float>(1.0 - sum);
+    t.p_rest = t.lacking < 0.f ? 0.f : t.lacking;
+    t.any = __syncthreads_or(counts);
   } else {
-    const float y = counts ? z * inv_t : kNegInf;
+    const float y = counts ? z * g.v.inv_t : kNegInf;
     const float m = block_max(y, sh.sum);
     // a NaN entry makes the sum, and with it every p, a NaN
     const float total = block_sum(!counts ? 0.f : (m != kNegInf ? expf(y - m) : (y != y ? y : 0.f)), sh.sum);
-    if (counts && !(y == kNegInf)) log_p = (y - m) - logf(total);
-    any = m != kNegInf || total != total;
+    if (counts && !(y == kNegInf)) t.log_p = (y - m) - logf(total);
+    t.any = m != kNegInf || total != total;
   }
-  if (tid < k) sh.log_p[tid] = log_p;
-  const float p = expf(log_p);
-  const float x_mine = counts ? sh.x[tid] : kNegInf;
+  t.p = expf(t.log_p);
+  return t;
+}
 
-  // the student: the row outside S first, then S
-  float rest_ref = 0.f, rest_log2 = 0.f;  // q_v / q_r = 2^((x_v - rest_ref) c - rest_log2)
-  float lse_ref = 0.f, lse_log = 0.f;     // log q_v = (x_v - lse_ref) / t - lse_log
-  float rest;                             // log q_r
-  bool empty;
-  if (FWD) {
-    Sums a;
-    for (int i = tid; i < row.nvec; i += kVocabThreads) {
-      float f[kVec];
-      row.load(i, f, status, NSM_KERNEL_DISTILL);
-      const uint32_t bits = members[i];
-      if (bits) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e)
-          if (bits >> e & 1) f[e] = kNegInf;
-      }
-      add_vec<kVec, false>(a, f, i, c);
-    }
-    const Totals out = block_totals(a, c, sh.parts);
-    Sums b;
-    if (counts) {
-      const float f[1] = {x_mine};
-      add_vec<1, false>(b, f, 0, c);
-    }
-    const Totals all = merge(out, block_totals(b, c, sh.parts), c);
-    empty = all.max == kNegInf && all.s == 0.f;
-    lse_ref = empty ? 0.f : all.max;
-    lse_log = empty ? 0.f : logf(all.s);
-    const bool no_rest = out.max == kNegInf && out.s == 0.f;
-    rest_ref = no_rest ? 0.f : out.max;
-    rest_log2 = no_rest ? 0.f : log2f(out.s);
-    rest = no_rest ? kNegInf : (out.max - lse_ref) * inv_t + (logf(out.s) - lse_log);
-    const float log_q = (x_mine - lse_ref) * inv_t - lse_log;
-    if (rest == kNegInf) p_rest = 0.f;
-    float term = p > 0.f || p != p ? p * (log_p - log_q) : 0.f;
-    float loss = block_sum(term, sh.sum);
+// What the gradient pass of a row needs: outside the entries scale 2^((x - ref) c - log2_s).
+struct EntryGradient {
+  float ref, log2_s, scale;
+  float mine;  // at this thread's own entry
+};
+
+// w loss: d/dx = w / t (q (1 + excess) - p) at the entries, and outside them, with the tail,
+// q (1 + excess) - p_rest q / q_rest = (q / q_rest) (q_rest (1 + excess) - p_rest).
+// log q_v = (x_v - lse_ref) / t - lse_log, q_v / q_rest = 2^((x_v - rest_ref) c - rest_log2).
+__device__ __forceinline__ EntryGradient entry_gradient(const Teacher& t, float w, int tail, float lse_ref, float lse_log,
+                                                        float rest_ref, float rest_log2, float rest, float inv_t) {
+  EntryGradient k;
+  const float p_rest = rest == kNegInf ? 0.f : t.p_rest;
+  const float excess = tail ? p_rest - t.lacking : 0.f;  // sum p + p_rest - 1
+  const float unit = w * inv_t;
+  if (tail) {
+    k.ref = rest_ref;
+    k.log2_s = rest_log2;
+    k.scale = rest == kNegInf ? 0.f : unit * (expf(rest) * (1.f + excess) - p_rest);
+  } else {
+    k.ref = lse_ref;
+    k.log2_s = lse_log * (1.f / kLn2);
+    k.scale = unit;
+  }
+  k.mine = 0.f;
+  const float log_q = (t.x - lse_ref) * inv_t - lse_log;
+  if (t.mine >= 0 && log_q != kNegInf) {  // q - p without cancellation
+    const float q = expf(log_q);
+    k.mine = unit * ((t.p > 0.f || t.p != t.p ? t.p * expm1f(log_q - t.log_p) : q) + q * excess);
+  }
+  return k;
+}
+
+template <typename T>
+__device__ __forceinline__ bool in_part(const Row<T>& row, const Part& part, int v) {
+  const int at = (v + row.lead) / Elem<T>::kVec;
+  return (at >= part.begin && at < part.end) || at == part.head || at == part.tail;
+}
+
+// The dense pass over the block's part, then the entries' own values over what it wrote there.
+template <typename T>
+__device__ __forceinline__ void store_entry_gradients(const Row<T>& row, const Row<T>& out, const Part& part,
+                                                      const Teacher& t, const EntryGradient& k, float c) {
+  for_vectors(row, part, [&](int i, const uint4& raw) {
+    out.store(row.first(i), gradient_vec<T, false>(raw, k.ref, c, k.log2_s, k.scale, 0.f));
+  });
+  __syncthreads();
+  if (t.mine >= 0 && in_part(row, part, t.mine)) out.p[t.mine] = Elem<T>::from_float(k.mine);
+}
+
+template <typename T, bool GRAD>
+__global__ void __launch_bounds__(kVocabThreads) k_distill(const DistillArgs g, int* status) {
+  constexpr int kVec = Elem<T>::kVec;
+  extern __shared__ __align__(16) uint8_t members[];  // a bit per element of vector i in byte i - part's first
+  __shared__ DistillShared sh;
+  grid_dependency_sync();
+  release_dependents();
+  const int ctas = static_cast<int>(ptx::cluster_nctarank()), rank = static_cast<int>(ptx::cluster_ctarank());
+  if (ctas > 1) ptx::cluster_arrive();
+  const int64_t r = blockIdx.x / ctas;
+  const int tid = threadIdx.x, vocab = g.v.vocab;
+  const float c = g.v.c, inv_t = g.v.inv_t;
+  const Row<T> row(static_cast<T*>(const_cast<void*>(g.v.logits)) + r * g.v.ld, vocab, status, NSM_KERNEL_DISTILL);
+  const Part part = part_of(row, rank, ctas);
+  // head is vector begin - 1 and tail vector end: the part's vectors from `base` on
+  const int base = part.head >= 0 ? part.head : part.begin;
+  const int bytes = (part.tail >= 0 ? part.tail + 1 : part.end) - base;
+  for (int i = tid; i < (bytes + 15) / 16; i += kVocabThreads) reinterpret_cast<uint4*>(members)[i] = make_uint4(0, 0, 0, 0);
+  const Teacher t = read_teacher<T>(g, r, row, sh);  // has barriers
+  if (t.mine >= 0 && in_part(row, part, t.mine)) {
+    const int at = t.mine + row.lead, i = at / kVec - base;
+    atomicOr(reinterpret_cast<uint32_t*>(members) + i / 4, 1u << (8 * (i & 3) + at % kVec));
+  }
+  __syncthreads();
+
+  // the student: the row outside the entries, and the entries
+  Sums a;
+  for_vectors(row, part, [&](int i, const uint4& raw) {
+    const uint32_t bits = members[i - base];
+    uint4 v = raw;
+    if (bits) vec_mask<T>(v, bits);
+    add_vec<T, false>(a, v, i, c);
+  });
+  const Totals outside = row_totals<false>(a, c, sh.rest, ctas);
+  Sums b;
+  if (t.mine >= 0 && t.x != kNegInf) {  // one term, relative to itself (a NaN stays one)
+    b.ref = b.limit = b.max = t.x;
+    b.s = make_pair(t.x - t.x + 1.f, 0.f);
+  }
+  const Totals inside = row_totals<false>(b, c, sh.entries, 1);
+  Totals all{fmaxf(outside.max, inside.max), outside.s, 0.f};
+  float inside_s = inside.s, none = 0.f;
+  rebase<false>(all.s, none, outside.max, all.max, c);
+  rebase<false>(inside_s, none, inside.max, all.max, c);
+  all.s += inside_s;
+  const bool empty = all.max == kNegInf && all.s == 0.f;
+  const bool no_rest = outside.max == kNegInf && outside.s == 0.f;
+  const float lse_ref = empty ? 0.f : all.max, lse_log = empty ? 0.f : logf(all.s);
+  const float rest_ref = no_rest ? 0.f : outside.max;
+  const float rest = no_rest ? kNegInf : (outside.max - lse_ref) * inv_t + (logf(outside.s) - lse_log);
+  if (g.loss || g.lse || g.rest) {
+    const float log_q = (t.x - lse_ref) * inv_t - lse_log;
+    const float p_rest = rest == kNegInf ? 0.f : t.p_rest;
+    float loss = block_sum(t.p > 0.f || t.p != t.p ? t.p * (t.log_p - log_q) : 0.f, sh.sum);
     if (p_rest > 0.f || p_rest != p_rest) loss += p_rest * (logf(p_rest) - rest);
-    if (tid == 0) {
-      if (g.loss) g.loss[r] = any ? loss : 0.f;
+    if (rank == 0 && tid == 0) {
+      if (g.loss) g.loss[r] = t.any ? loss : 0.f;
       if (g.lse) g.lse[r] = empty ? kNegInf : lse_ref * inv_t + lse_log;
       if (g.rest) g.rest[r] = rest;
     }
-  } else {
-    const float lse = g.in_lse[r];
-    empty = lse == kNegInf;
-    lse_ref = empty ? 0.f : lse * g.v.t;
-    rest = g.tail ? g.in_rest[r] : 0.f;
-    rest_ref = empty || rest == kNegInf ? 0.f : (lse + rest) * g.v.t;
-    if (rest == kNegInf) p_rest = 0.f;
   }
-  if (GRAD) {
-    T* out = static_cast<T*>(g.v.d_logits) + r * g.v.ldd;
+  if constexpr (GRAD) {
+    const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, NSM_KERNEL_DISTILL);
     const float w = g.d_loss ? g.d_loss[r] : 1.f;
-    if (empty || !any || w == 0.f) {
-      zero_row<T>(out, vocab, status, NSM_KERNEL_DISTILL);
+    if (empty || !t.any || w == 0.f) {
+      zero_part(out, rank, ctas);
       return;
     }
-    const float excess = g.tail ? p_rest - lacking : 0.f;  // sum p + p_rest - 1
-    const float scale = w * inv_t;
-    // outside S, with the tail: q (1 + excess) - p_rest q / q_r = (q / q_r) (q_r (1 + excess) - p_rest)
-    float ref, log2_s, coef;
-    if (g.tail) {
-      ref = rest_ref;
-      log2_s = rest_log2;
-      coef = rest == kNegInf ? 0.f : scale * (expf(rest) * (1.f + excess) - p_rest);
-    } else {
-      ref = lse_ref;
-      log2_s = lse_log * (1.f / kLn2);
-      coef = scale;
-    }
-    float g_mine = 0.f;  // in S: q (1 + excess) - p, q - p without cancellation
-    const float log_q = (x_mine - lse_ref) * inv_t - lse_log;
-    if (counts && log_q != kNegInf) {
-      const float q = expf(log_q);
-      g_mine = scale * ((p > 0.f || p != p ? p * expm1f(log_q - log_p) : q) + q * excess);
-    }
-    for (int i = tid; i < row.nvec; i += kVocabThreads) {
-      float f[kVec];
-      row.load(i, f, status, NSM_KERNEL_DISTILL);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) f[e] = ex2((f[e] - ref) * c - log2_s) * coef;
-      store_vec<T>(out, vocab, row.first(i), f, status, NSM_KERNEL_DISTILL);
-    }
-    __syncthreads();  // the entries' own values go over what the pass wrote there
-    if (counts) out[mine] = Elem<T>::from_float(g_mine);
+    const EntryGradient k = entry_gradient(t, w, g.tail, lse_ref, lse_log, rest_ref, no_rest ? 0.f : log2f(outside.s), rest, inv_t);
+    store_entry_gradients(row, out, part, t, k, c);
   }
 }
 
-template <typename K, typename A>
-cudaError_t launch_rows(K* kernel, const A& args, size_t smem, cudaStream_t stream) {
-  int* status = device_status_ptr();
-  if (!status) return cudaErrorInvalidSymbol;
+// The backward pass alone, in pieces of rows.
+template <typename T>
+__global__ void __launch_bounds__(kVocabThreads) k_distill_backward(const DistillArgs g, int pieces, int* status) {
+  __shared__ DistillShared sh;
+  grid_dependency_sync();
+  release_dependents();
+  const int vocab = g.v.vocab;
+  const int64_t total = g.v.rows * pieces;
+  for (int64_t work = blockIdx.x; work < total; work += gridDim.x) {
+    const int64_t r = work / pieces;
+    const int piece = static_cast<int>(work - r * pieces);
+    const Row<T> row(static_cast<T*>(const_cast<void*>(g.v.logits)) + r * g.v.ld, vocab, status, NSM_KERNEL_DISTILL);
+    const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, NSM_KERNEL_DISTILL);
+    const float w = g.d_loss ? g.d_loss[r] : 1.f;
+    const float lse = g.in_lse[r], rest = g.tail ? g.in_rest[r] : 0.f;
+    if (w == 0.f || lse == kNegInf) {
+      zero_part(out, piece, pieces);
+      continue;
+    }
+    const Teacher t = read_teacher<T>(g, r, row, sh);
+    if (!t.any) {
+      zero_part(out, piece, pieces);
+    } else {
+      const EntryGradient k = entry_gradient(t, w, g.tail, lse * g.v.t, 0.f, rest == kNegInf ? 0.f : (lse + rest) * g.v.t, 0.f,
+                                             rest, g.v.inv_t);
+      store_entry_gradients(row, out, part_of(row, piece, pieces), t, k, g.v.c);
+    }
+    __syncthreads();  // sh is free again
+  }
+}
+
+// ---------------------------------------------------------------- launches
+
+// CTAs per row: where there are fewer rows than the GPU takes blocks at a time, a cluster
+// shares each row, down to two vectors of a thread.
+int cluster_for(int64_t rows, int nvec) {
+  int ctas = 1;
+  while (ctas < kMaxCluster && rows * ctas < 4 * 152 && nvec >= ctas * 4 * kVocabThreads) ctas *= 2;
+  return ctas;
+}
+
+// Pieces per row of a backward pass: `most` vectors each, less where rows are few.
+int pieces_for(int64_t rows, int nvec, int most) {
+  int each = most;
+  while (each > kVocabThreads && rows * ((nvec + each - 1) / each) < 8 * 152) each /= 2;
+  return (nvec + each - 1) / each;
+}
+
+template <typename T>
+int vectors_of(int vocab) {
+  return (vocab + 2 * Elem<T>::kVec - 2) / Elem<T>::kVec;  // at any alignment
+}
+
+template <typename... K, typename... A>
+cudaError_t launch_clusters(void (*kernel)(K...), int64_t grid, int ctas, size_t smem, cudaStream_t stream, A... args) {
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  if (const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(args.v.rows)), dim3(kVocabThreads), smem, stream, args, status))
-    return e;
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kVocabThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (pdl_enabled()) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (ctas > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<K>(args)...);
 }
 
 template <typename T>
-cudaError_t launch_logprobs_t(const LogprobArgs& a, cudaStream_t stream) {
-  if (a.in_lse) return launch_rows(k_logprobs<T, false, true>, a, 0, stream);
-  if (a.v.d_logits) return launch_rows(k_logprobs<T, true, true>, a, 0, stream);
-  return launch_rows(k_logprobs<T, true, false>, a, 0, stream);
+cudaError_t launch_logprobs_t(const LogprobArgs& a, int* status, cudaStream_t stream) {
+  const int nvec = vectors_of<T>(a.v.vocab);
+  if (a.in_lse) {
+    const int pieces = pieces_for(a.v.rows, nvec, 4 * kVocabThreads);
+    const int64_t grid = std::min<int64_t>(a.v.rows * pieces, 1 << 30);
+    return launch_clusters(a.d_entropy ? k_logprobs_backward<T, true> : k_logprobs_backward<T, false>, grid, 1, 0, stream, a,
+                           pieces, status);
+  }
+  const int ctas = cluster_for(a.v.rows, nvec);
+  const int64_t grid = a.v.rows * ctas;
+  if (a.v.d_logits)
+    return launch_clusters(a.d_entropy || a.entropy ? k_logprobs<T, true, true> : k_logprobs<T, false, true>, grid, ctas, 0,
+                           stream, a, status);
+  return launch_clusters(a.entropy ? k_logprobs<T, true, false> : k_logprobs<T, false, false>, grid, ctas, 0, stream, a, status);
 }
 
 template <typename T>
-cudaError_t launch_distill_t(const DistillArgs& a, cudaStream_t stream) {
-  const size_t nvec = (static_cast<size_t>(a.v.vocab) + 2 * Elem<T>::kVec) / Elem<T>::kVec;
-  const size_t smem = (nvec + 15) / 16 * 16;
-  if (a.in_lse) return launch_rows(k_distill<T, false, true>, a, 0, stream);
-  if (a.v.d_logits) return launch_rows(k_distill<T, true, true>, a, smem, stream);
-  return launch_rows(k_distill<T, true, false>, a, smem, stream);
+cudaError_t launch_distill_t(const DistillArgs& a, int* status, cudaStream_t stream) {
+  const int nvec = vectors_of<T>(a.v.vocab);
+  if (a.in_lse) {
+    const int pieces = pieces_for(a.v.rows, nvec, 16 * kVocabThreads);
+    const int64_t grid = std::min<int64_t>(a.v.rows * pieces, 1 << 30);
+    return launch_clusters(k_distill_backward<T>, grid, 1, 0, stream, a, pieces, status);
+  }
+  const int ctas = cluster_for(a.v.rows, nvec);
+  const size_t smem = (static_cast<size_t>((nvec + ctas - 1) / ctas) + 2 + 15) / 16 * 16;
+  return launch_clusters(a.v.d_logits ? k_distill<T, true> : k_distill<T, false>, a.v.rows * ctas, ctas, smem, stream, a, status);
 }
 
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t stream) {
-  if (a.v.dtype == NSM_BF16) return launch_logprobs_t<__nv_bfloat16>(a, stream);
-  if (a.v.dtype == NSM_FP16) return launch_logprobs_t<__half>(a, stream);
-  return launch_logprobs_t<float>(a, stream);
+  int* status = device_status_ptr();
+  if (!status) return cudaErrorInvalidSymbol;
+  if (a.v.dtype == NSM_BF16) return launch_logprobs_t<__nv_bfloat16>(a, status, stream);
+  if (a.v.dtype == NSM_FP16) return launch_logprobs_t<__half>(a, status, stream);
+  return launch_logprobs_t<float>(a, status, stream);
 }
 
 cudaError_t launch_distill(const DistillArgs& a, cudaStream_t stream) {
-  if (a.v.dtype == NSM_BF16) return launch_distill_t<__nv_bfloat16>(a, stream);
-  if (a.v.dtype == NSM_FP16) return launch_distill_t<__half>(a, stream);
-  return launch_distill_t<float>(a, stream);
+  int* status = device_status_ptr();
+  if (!status) return cudaErrorInvalidSymbol;
+  if (a.v.dtype == NSM_BF16) return launch_distill_t<__nv_bfloat16>(a, status, stream);
+  if (a.v.dtype == NSM_FP16) return launch_distill_t<__half>(a, status, stream);
+  return launch_distill_t<float>(a, status, stream);
 }
 
 }  // namespace nsm

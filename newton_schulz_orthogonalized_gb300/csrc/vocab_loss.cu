@@ -10,9 +10,9 @@
 //                q_v (1 + excess) - p_v in S and q_v (1 + excess) - p_r q_v / q_r outside,
 //                where 1 + excess = sum p + p_r
 //
-// One block per row: a pass over the row's 16-byte vectors with a running sum of
-// exponentials relative to a running reference, then (for the gradient) a second pass.
-// Sums and statistics are fp32, a gradient is rounded once.
+// A cluster of blocks per row (one block where rows are many): a pass over the row's 16-byte
+// vectors with a running sum of exponentials relative to a running reference, then (for the
+// gradient) a second pass.  Sums and statistics are fp32, a gradient is rounded once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -255,20 +255,36 @@ __device__ __forceinline__ Part part_of(const Row<T>& row, int piece, int pieces
   return part;
 }
 
-// use(i, vector) for every vector of the part that this thread has, four loads in flight.
-template <typename T, typename F>
-__device__ __forceinline__ void for_vectors(const Row<T>& row, const Part& part, F&& use) {
-  int i = part.begin + static_cast<int>(threadIdx.x);
-  for (; i + 3 * kVocabThreads < part.end; i += 4 * kVocabThreads) {
+// use(i, vector) for every vector of the part that this thread has, four loads in flight;
+// done(n) after the n-th four of them (the ragged ones come last and are not counted).
+template <typename T, typename F, typename D>
+__device__ __forceinline__ void for_batches(const Row<T>& row, const Part& part, F&& use, D&& done) {
+  int i = part.begin + static_cast<int>(threadIdx.x), n = 0;
+  for (; i + 3 * kVocabThreads < part.end; i += 4 * kVocabThreads, ++n) {
     uint4 raw[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) raw[u] = row.load_whole(i + u * kVocabThreads);
 #pragma unroll
     for (int u = 0; u < 4; ++u) use(i + u * kVocabThreads, raw[u]);
+    done(n);
   }
-  for (; i < part.end; i += kVocabThreads) use(i, row.load_whole(i));
+  if (i < part.end) {  // three at most, their loads together too
+    uint4 raw[3];
+#pragma unroll
+    for (int u = 0; u < 3; ++u)
+      if (i + u * kVocabThreads < part.end) raw[u] = row.load_whole(i + u * kVocabThreads);
+#pragma unroll
+    for (int u = 0; u < 3; ++u)
+      if (i + u * kVocabThreads < part.end) use(i + u * kVocabThreads, raw[u]);
+    done(n);
+  }
   if (part.head >= 0 && threadIdx.x == kHeadThread) use(part.head, row.load(part.head));
   if (part.tail >= 0 && threadIdx.x == kTailThread) use(part.tail, row.load(part.tail));
+}
+
+template <typename T, typename F>
+__device__ __forceinline__ void for_vectors(const Row<T>& row, const Part& part, F&& use) {
+  for_batches(row, part, use, [](int) {});
 }
 
 template <typename T>
@@ -289,8 +305,9 @@ struct Sums {
   int max_vec = -1;
 };
 
+// Adds a vector; its largest element.
 template <typename T, bool ENT>
-__device__ __forceinline__ void add_vec(Sums& a, const uint4& raw, int i, float c) {
+__device__ __forceinline__ float add_vec(Sums& a, const uint4& raw, int i, float c) {
   constexpr int kPairs = Elem<T>::kVec / 2;
   const float m = Elem<T>::largest(raw);
   if (m > a.max) {
@@ -318,6 +335,7 @@ __device__ __forceinline__ void add_vec(Sums& a, const uint4& raw, int i, float 
     a.s = pair_add(a.s, e);
     if (ENT) a.sy = pair_fma(e, make_pair(fmaxf(y0, kLog2Floor), fmaxf(y1, kLog2Floor)), a.sy);
   }
+  return m;
 }
 
 struct Totals {
@@ -427,25 +445,48 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
 static_assert(kTopCandidates >= kMaxCluster * kTopMaxK, "every CTA's k largest fit");
 
+constexpr int kTopGroups = 32;   // groups of batches per thread at most
+constexpr int kTopList = 1024;
 struct TopShared {
   uint32_t key[kVocabThreads];
   int32_t vec[kVocabThreads];
-  int32_t list[kVocabThreads];
+  uint32_t list[kTopList];                    // group * kVocabThreads + thread
   uint64_t cand[kTopCandidates];
   uint64_t best[kVocabWarps];
-  uint64_t gathered[kMaxCluster * kTopMaxK];  // rank 0: every CTA's own k largest
   uint32_t bound_key, bound_tie_top;
   int32_t bound_vec, nlist, ncand;
   uint32_t taken[kMaxCluster];                // how many keys each CTA gave
+};
+
+// The largest logit of every group of a thread's batches: which groups can hold one of the
+// row's k largest, without reading the row again.  A 16-bit key where that tells two values
+// of the type apart.
+template <typename T>
+struct TopGroups {
+  using Key = typename std::conditional<Elem<T>::kKeyLowBit == 16, uint16_t, uint32_t>::type;
+  Key* top;       // [group][thread], in shared memory; a thread reads what it wrote itself
+  int shift;      // batches per group: 1 << shift
+  float running;
+  __device__ __forceinline__ void batch(int n) {
+    const uint32_t key = order_key(running);
+    top[(n >> shift) * kVocabThreads + threadIdx.x] = static_cast<Key>(sizeof(Key) == 2 ? key >> 16 : key);
+    if ((n + 1) >> shift != n >> shift) running = kNegInf;
+  }
+  // the largest key that the group can hold
+  __device__ __forceinline__ uint32_t largest(int group) const {
+    const uint32_t key = top[group * kVocabThreads + threadIdx.x];
+    return sizeof(Key) == 2 ? key << 16 | 0xffffu : key;
+  }
 };
 
 __device__ __forceinline__ uint64_t full_key(float f, int v) {
   return (static_cast<uint64_t>(order_key(f)) << 32) | (0xffffffffu - static_cast<uint32_t>(v));
 }
 
-// The first warp finds a bound that at least k threads' largest logits reach: the k-th
-// largest of them (bits below kKeyLowBit do not tell two values apart), and where more than
-// k reach it, the vector number up to which the ones equal to it are needed.
+// The first warp finds a bound that at least k threads' largest logits reach, and few more:
+// the k-th largest of them, bit by bit until that holds (bits below kKeyLowBit do not tell two
+// values apart), and where too many are equal to it, the vector number up to which they are
+// needed.
 template <typename T>
 __device__ __forceinline__ void top_bound(TopShared& sh, int k) {
   constexpr int kLow = Elem<T>::kKeyLowBit;
@@ -454,38 +495,63 @@ __device__ __forceinline__ void top_bound(TopShared& sh, int k) {
   uint32_t key[kPer];
   int vec[kPer];
   int valid = 0;
+  uint32_t high = 0, low = ~0u;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     key[j] = sh.key[j * 32 + lane];
     vec[j] = sh.vec[j * 32 + lane];
     valid += key[j] > kKeyNegInf;
+    high = max(high, key[j]);
+    low = min(low, key[j]);
   }
   valid = __reduce_add_sync(~0u, valid);
   uint32_t bound = kKeyNegInf + 1, tie_top = kKeyNegInf;
   int bound_vec = 0x7fffffff;
   if (valid > k) {
-    bound = 0;
-    int reach = valid;
-    for (int b = 31; b >= kLow && reach != k; --b) {
-      const uint32_t test = bound | (1u << b);
-      int n = 0;
+    high = __reduce_max_sync(~0u, high);
+    low = __reduce_min_sync(~0u, low);
+    // bits above the first in which the keys differ are common to all
+    int b = high == low ? kLow - 1 : 31 - __clz(high ^ low);
+    bound = b >= 31 ? 0 : high >> (b + 1) << (b + 1);
+    if (b < kLow) bound = high >> kLow << kLow;
+    int reach = kVocabThreads;
+    // a few more threads than k cost less than the steps that would tell them apart
+    const int enough = k + 4 + k / 4;
+    // two bits at a time: the counts of three thresholds side by side in one sum
+    static_assert(kVocabThreads < 1 << 10, "ten bits hold a count");
+    for (; b >= kLow && reach > enough; b -= 2) {
+      const uint32_t half = b > kLow ? 1u << (b - 1) : 0u, one = 1u << b;  // the last bit alone: half 0
+      uint32_t n = 0;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) n += key[j] >= test;
+      for (int j = 0; j < kPer; ++j)
+        n += (key[j] >= (bound | half) ? 1u : 0u) + (key[j] >= (bound | one) ? 1u << 10 : 0u) +
+             (key[j] >= (bound | one | half) ? 1u << 20 : 0u);
       n = __reduce_add_sync(~0u, n);
-      if (n >= k) {
-        bound = test;
-        reach = n;
+      const int n1 = n & 1023, n2 = n >> 10 & 1023, n3 = n >> 20;
+      if (n3 >= k) {
+        bound |= one | half;
+        reach = n3;
+      } else if (n2 >= k) {
+        bound |= one;
+        reach = n2;
+      } else if (n1 >= k) {
+        bound |= half;
+        reach = n1;
       }
     }
     if (bound <= kKeyNegInf) bound = kKeyNegInf + 1;
-    if (reach > k) {  // every bit is fixed: the threads that tie differ below kLow at most
+    if (reach > enough) {  // every bit is fixed: the threads that tie differ below kLow at most
       tie_top = bound | ((1u << kLow) - 1u);
       int above = 0;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) above += key[j] > tie_top;
       above = __reduce_add_sync(~0u, above);
+      int most = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) most = max(most, vec[j]);
+      most = __reduce_max_sync(~0u, most);
       bound_vec = 0;
-      for (int b = 30; b >= 0; --b) {
+      for (int b = 31 - __clz(most | 1); b >= 0; --b) {
         const int test = bound_vec | ((1 << b) - 1);
         int n = 0;
 #pragma unroll
@@ -509,6 +575,7 @@ __device__ __forceinline__ void place_keys(const uint64_t* keys, int n, int k, F
   for (int j = threadIdx.x; j < n; j += kVocabThreads) {
     const uint64_t mine = keys[j];
     int place = 0;
+#pragma unroll 8
     for (int o = 0; o < n; ++o) place += keys[o] > mine;
     if (place < k) put(place, mine);
   }
@@ -517,7 +584,8 @@ __device__ __forceinline__ void place_keys(const uint64_t* keys, int n, int k, F
 // The k largest logits of the block's part of a row, from every thread's largest one and
 // where it met it: put(place, key), and the number of places that were filled.
 template <typename T, typename F>
-__device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, const Sums& a, int k, TopShared& sh, F&& put) {
+__device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, const Sums& a, const TopGroups<T>& groups, int k,
+                                        TopShared& sh, F&& put) {
   constexpr int kVec = Elem<T>::kVec;
   const int tid = threadIdx.x, lane = tid & 31;
   sh.key[tid] = order_key(a.max);
@@ -527,36 +595,49 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
   __syncthreads();
   const uint32_t bound = sh.bound_key, tie_top = sh.bound_tie_top;
   const int bound_vec = sh.bound_vec;
-  const uint32_t key = sh.key[tid];
-  if (key >= bound && (key > tie_top || a.max_vec <= bound_vec)) sh.list[atomicAdd(&sh.nlist, 1)] = tid;
+  const int per = 4 << groups.shift;  // vectors of a group
+  if (sh.key[tid] >= bound) {
+    for (int j = 0; part.begin + tid + j * per * kVocabThreads < part.end; ++j) {
+      const uint32_t largest = groups.largest(j);
+      if (largest >= bound && (largest > tie_top || part.begin + tid + j * per * kVocabThreads <= bound_vec)) {
+        const int at = atomicAdd(&sh.nlist, 1);
+        if (at < kTopList) sh.list[at] = j * kVocabThreads + tid;
+      }
+    }
+  }
   __syncthreads();
   const int nlist = sh.nlist;
   auto offer = [&](int i) {
     const uint4 raw = row.load(i);
-    if (order_key(Elem<T>::largest(raw)) < bound) return;
+    uint32_t hits = 0;  // a bit per element that reaches the bound
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
-      const float f = vec_get<T>(raw, e);
-      const uint32_t ek = order_key(f);
-      if (ek >= bound && (ek > tie_top || i <= bound_vec)) {
-        const int at = atomicAdd(&sh.ncand, 1);
-        if (at < kTopCandidates) sh.cand[at] = full_key(f, row.first(i) + e);
-      }
+      const uint32_t key = order_key(vec_get<T>(raw, e));
+      if (key >= bound && (key > tie_top || i <= bound_vec)) hits |= 1u << e;
+    }
+    if (hits == 0) return;
+    int at = atomicAdd(&sh.ncand, __popc(hits));
+    for (; hits; hits &= hits - 1, ++at) {
+      const int e = __ffs(hits) - 1;
+      if (at < kTopCandidates) sh.cand[at] = full_key(Elem<T>::to_float(row.p[row.first(i) + e]), row.first(i) + e);
     }
   };
-  for (int q = tid >> 5; q < nlist; q += kVocabWarps) {
-    const int owner = sh.list[q];
-    for (int i = part.begin + owner + lane * kVocabThreads; i < part.end; i += 32 * kVocabThreads) offer(i);
-    if (owner == kHeadThread && part.head >= 0 && lane == 0) offer(part.head);
-    if (owner == kTailThread && part.tail >= 0 && lane == 0) offer(part.tail);
+  if (nlist <= kTopList) {
+    for (int q = tid; q < nlist * per; q += kVocabThreads) {
+      const int item = static_cast<int>(sh.list[q / per]), j = item / kVocabThreads, owner = item % kVocabThreads;
+      const int i = part.begin + owner + (j * per + q % per) * kVocabThreads;
+      if (i < part.end) offer(i);
+    }
+    if (part.head >= 0 && tid == kHeadThread) offer(part.head);
+    if (part.tail >= 0 && tid == kTailThread) offer(part.tail);
   }
   __syncthreads();
   const int ncand = sh.ncand;
-  if (ncand <= kTopCandidates) {
+  if (nlist <= kTopList && ncand <= kTopCandidates) {
     place_keys(sh.cand, ncand, k, put);
     return min(ncand, k);
   }
-  // so many logits above the bound sit in few threads: one block-wide maximum per place
+  // many logits above the bound sit in few threads: one block-wide maximum per place
   uint64_t last = ~0ull;
   for (int j = 0; j < k; ++j) {
     uint64_t best = 0;
@@ -577,7 +658,8 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
 #pragma unroll
     for (int w = 0; w < kVocabWarps; ++w) best = sh.best[w] > best ? sh.best[w] : best;
     __syncthreads();
-    last = best;  // more than kTopCandidates >= k logits are there
+    if (best == 0) return j;  // nothing above -inf is left
+    last = best;
     if (tid == 0) put(j, best);
   }
   return k;
@@ -585,8 +667,9 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
 
 // The row's k largest logits: of the block's part, or gathered from the cluster's parts.
 template <typename T>
-__device__ __forceinline__ void row_top(const Row<T>& row, const Part& part, const Sums& a, int k, float max, float inv_t,
-                                        float log_s, float* out_value, int32_t* out_index, TopShared& sh, int ctas) {
+__device__ __forceinline__ void row_top(const Row<T>& row, const Part& part, const Sums& a, const TopGroups<T>& groups, int k,
+                                        float max, float inv_t, float log_s, float* out_value, int32_t* out_index, TopShared& sh,
+                                        uint64_t* gathered, int ctas) {
   auto write = [&](int place, uint64_t key) {
     const int v = static_cast<int>(0xffffffffu - static_cast<uint32_t>(key));
     out_index[place] = v;
@@ -594,11 +677,11 @@ __device__ __forceinline__ void row_top(const Row<T>& row, const Part& part, con
   };
   int found;
   if (ctas == 1) {
-    found = part_top<T>(row, part, a, k, sh, write);
+    found = part_top<T>(row, part, a, groups, k, sh, write);
   } else {
     const uint32_t rank = ptx::cluster_ctarank();
-    const uint32_t to = ptx::mapa_shared(ptx::smem_u32(&sh.gathered[rank * kTopMaxK]), 0);
-    const int mine = part_top<T>(row, part, a, k, sh, [&](int place, uint64_t key) { ptx::st_cluster_u64(to + place * 8, key); });
+    const uint32_t to = ptx::mapa_shared(ptx::smem_u32(gathered + rank * k), 0);
+    const int mine = part_top<T>(row, part, a, groups, k, sh, [&](int place, uint64_t key) { ptx::st_cluster_u64(to + place * 8, key); });
     if (threadIdx.x == 0) ptx::st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.taken[rank]), 0), mine);
     ptx::cluster_sync();
     if (rank != 0) return;
@@ -606,7 +689,7 @@ __device__ __forceinline__ void row_top(const Row<T>& row, const Part& part, con
     int total = 0;
     for (int r = 0; r < ctas; ++r) {
       const int n = static_cast<int>(sh.taken[r]);
-      for (int j = threadIdx.x; j < n; j += kVocabThreads) sh.cand[total + j] = sh.gathered[r * kTopMaxK + j];
+      for (int j = threadIdx.x; j < n; j += kVocabThreads) sh.cand[total + j] = gathered[r * k + j];
       total += n;
     }
     __syncthreads();
@@ -655,11 +738,13 @@ __device__ __forceinline__ void store_token_gradient(const Row<T>& out, int e0, 
   out.store(e0, grad);
 }
 
-// A cluster of CTAs per row (one CTA where there are rows enough).
-template <typename T, bool ENT, bool GRAD>
-__global__ void __launch_bounds__(kVocabThreads) k_logprobs(const LogprobArgs g, int* status) {
+// A cluster of CTAs per row (one CTA where there are rows enough).  TOP: dynamic shared
+// memory holds rank 0's gathered keys (ctas k of them where ctas > 1), then the groups' tops.
+template <typename T, bool ENT, bool TOP, bool GRAD>
+__global__ void __launch_bounds__(kVocabThreads, TOP ? 6 : 5) k_logprobs(const LogprobArgs g, int group_shift, int* status) {
+  extern __shared__ __align__(16) uint8_t dynamic[];
   __shared__ TotalsShared totals;
-  __shared__ typename std::conditional<GRAD, int, TopShared>::type top;
+  __shared__ typename std::conditional<TOP, TopShared, int>::type top;
   grid_dependency_sync();
   release_dependents();
   const int ctas = static_cast<int>(ptx::cluster_nctarank()), rank = static_cast<int>(ptx::cluster_ctarank());
@@ -672,8 +757,17 @@ __global__ void __launch_bounds__(kVocabThreads) k_logprobs(const LogprobArgs g,
   int64_t token64 = g.tokens ? load_index(g.tokens, g.tokens_wide, r) : -1;
   const int token = token64 < 0 || token64 >= vocab ? -1 : static_cast<int>(token64);
   const float x_token = token >= 0 ? Elem<T>::to_float(row.p[token]) : kNegInf;
+  uint64_t* gathered = reinterpret_cast<uint64_t*>(dynamic);
+  TopGroups<T> groups{reinterpret_cast<typename TopGroups<T>::Key*>(gathered + (ctas > 1 ? ctas * g.k : 0)), group_shift, kNegInf};
   Sums a;
-  for_vectors(row, part, [&](int i, const uint4& raw) { add_vec<T, ENT>(a, raw, i, c); });
+  for_batches(row, part,
+              [&](int i, const uint4& raw) {
+                const float m = add_vec<T, ENT>(a, raw, i, c);
+                if (TOP) groups.running = fmaxf(groups.running, m);
+              },
+              [&](int n) {
+                if (TOP) groups.batch(n);
+              });
   const Totals t = row_totals<ENT>(a, c, totals, ctas);
   const bool empty = t.max == kNegInf && t.s == 0.f;  // a row of NaN has a NaN sum
   const float ref = empty ? 0.f : t.max, log_s = empty ? 0.f : logf(t.s);
@@ -697,7 +791,8 @@ __global__ void __launch_bounds__(kVocabThreads) k_logprobs(const LogprobArgs g,
     } else {
       for_vectors(row, part, [&](int i, const uint4& raw) { store_token_gradient<T, ENT>(out, row.first(i), raw, k, token, c); });
     }
-  } else if (g.k > 0) {
+  }
+  if constexpr (TOP) {
     float* value = g.top_logprob + r * g.k;
     int32_t* index = g.top_index + r * g.k;
     if (log_s != log_s) {  // NaN or +inf in the row
@@ -708,14 +803,14 @@ __global__ void __launch_bounds__(kVocabThreads) k_logprobs(const LogprobArgs g,
         }
       }
     } else {
-      row_top<T>(row, part, a, g.k, ref, inv_t, log_s, value, index, top, ctas);
+      row_top<T>(row, part, a, groups, g.k, ref, inv_t, log_s, value, index, top, gathered, ctas);
     }
   }
 }
 
 // The backward pass alone: pieces of rows, every element on its own.
 template <typename T, bool ENT>
-__global__ void __launch_bounds__(kVocabThreads) k_logprobs_backward(const LogprobArgs g, int pieces, int* status) {
+__global__ void __launch_bounds__(kVocabThreads, 6) k_logprobs_backward(const LogprobArgs g, int pieces, int* status) {
   grid_dependency_sync();
   release_dependents();
   const int vocab = g.v.vocab;
@@ -886,7 +981,7 @@ __device__ __forceinline__ void store_entry_gradients(const Row<T>& row, const R
 }
 
 template <typename T, bool GRAD>
-__global__ void __launch_bounds__(kVocabThreads) k_distill(const DistillArgs g, int* status) {
+__global__ void __launch_bounds__(kVocabThreads, 5) k_distill(const DistillArgs g, int* status) {
   constexpr int kVec = Elem<T>::kVec;
   extern __shared__ __align__(16) uint8_t members[];  // a bit per element of vector i in byte i - part's first
   __shared__ DistillShared sh;
@@ -960,7 +1055,7 @@ __global__ void __launch_bounds__(kVocabThreads) k_distill(const DistillArgs g, 
 
 // The backward pass alone, in pieces of rows.
 template <typename T>
-__global__ void __launch_bounds__(kVocabThreads) k_distill_backward(const DistillArgs g, int pieces, int* status) {
+__global__ void __launch_bounds__(kVocabThreads, 6) k_distill_backward(const DistillArgs g, int pieces, int* status) {
   __shared__ DistillShared sh;
   grid_dependency_sync();
   release_dependents();
@@ -1051,9 +1146,18 @@ cudaError_t launch_logprobs_t(const LogprobArgs& a, int* status, cudaStream_t st
   const int ctas = cluster_for(a.v.rows, nvec);
   const int64_t grid = a.v.rows * ctas;
   if (a.v.d_logits)
-    return launch_clusters(a.d_entropy || a.entropy ? k_logprobs<T, true, true> : k_logprobs<T, false, true>, grid, ctas, 0,
-                           stream, a, status);
-  return launch_clusters(a.entropy ? k_logprobs<T, true, false> : k_logprobs<T, false, false>, grid, ctas, 0, stream, a, status);
+    return launch_clusters(a.d_entropy || a.entropy ? k_logprobs<T, true, false, true> : k_logprobs<T, false, false, true>,
+                           grid, ctas, 0, stream, a, 0, status);
+  if (a.k == 0)
+    return launch_clusters(a.entropy ? k_logprobs<T, true, false, false> : k_logprobs<T, false, false, false>, grid, ctas, 0,
+                           stream, a, 0, status);
+  const int batches = ((nvec + ctas - 1) / ctas + 4 * kVocabThreads - 1) / (4 * kVocabThreads);
+  int shift = 0;
+  while (((batches + (1 << shift) - 1) >> shift) > kTopGroups) ++shift;
+  const size_t smem = (ctas > 1 ? size_t(ctas) * a.k * 8 : 0) +
+                      size_t((batches + (1 << shift) - 1) >> shift) * kVocabThreads * sizeof(typename TopGroups<T>::Key);
+  return launch_clusters(a.entropy ? k_logprobs<T, true, true, false> : k_logprobs<T, false, true, false>, grid, ctas, smem,
+                         stream, a, shift, status);
 }
 
 template <typename T>

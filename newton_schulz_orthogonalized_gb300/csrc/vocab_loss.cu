@@ -26,8 +26,7 @@
 namespace nsm {
 namespace {
 
-constexpr int kVocabThreads = 256;
-constexpr int kVocabWarps = kVocabThreads / 32;
+constexpr int kMaxWarps = 8;  // of the blocks below: NT = 32, 64, ..., 256 threads
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
 // A thread's reference moves only when a logit exceeds it by this many binary orders:
@@ -235,7 +234,7 @@ struct Row {
 };
 
 // The part of a row's vectors that one block takes: whole vectors [begin, end), of which
-// thread t has every kVocabThreads-th from begin + t on, and the row's ragged first and last
+// thread t of NT has every NT-th from begin + t on, and the row's ragged first and last
 // vector (-1: not here), which threads kHeadThread and kTailThread have as well.
 constexpr int kHeadThread = 0, kTailThread = 32;
 struct Part {
@@ -257,41 +256,41 @@ __device__ __forceinline__ Part part_of(const Row<T>& row, int piece, int pieces
 
 // use(i, vector) for every vector of the part that this thread has, four loads in flight;
 // done(n) after the n-th four of them (the ragged ones come last and are not counted).
-template <typename T, typename F, typename D>
+template <int NT, typename T, typename F, typename D>
 __device__ __forceinline__ void for_batches(const Row<T>& row, const Part& part, F&& use, D&& done) {
   int i = part.begin + static_cast<int>(threadIdx.x), n = 0;
-  for (; i + 3 * kVocabThreads < part.end; i += 4 * kVocabThreads, ++n) {
+  for (; i + 3 * NT < part.end; i += 4 * NT, ++n) {
     uint4 raw[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) raw[u] = row.load_whole(i + u * kVocabThreads);
+    for (int u = 0; u < 4; ++u) raw[u] = row.load_whole(i + u * NT);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) use(i + u * kVocabThreads, raw[u]);
+    for (int u = 0; u < 4; ++u) use(i + u * NT, raw[u]);
     done(n);
   }
   if (i < part.end) {  // three at most, their loads together too
     uint4 raw[3];
 #pragma unroll
     for (int u = 0; u < 3; ++u)
-      if (i + u * kVocabThreads < part.end) raw[u] = row.load_whole(i + u * kVocabThreads);
+      if (i + u * NT < part.end) raw[u] = row.load_whole(i + u * NT);
 #pragma unroll
     for (int u = 0; u < 3; ++u)
-      if (i + u * kVocabThreads < part.end) use(i + u * kVocabThreads, raw[u]);
+      if (i + u * NT < part.end) use(i + u * NT, raw[u]);
     done(n);
   }
   if (part.head >= 0 && threadIdx.x == kHeadThread) use(part.head, row.load(part.head));
   if (part.tail >= 0 && threadIdx.x == kTailThread) use(part.tail, row.load(part.tail));
 }
 
-template <typename T, typename F>
+template <int NT, typename T, typename F>
 __device__ __forceinline__ void for_vectors(const Row<T>& row, const Part& part, F&& use) {
-  for_batches(row, part, use, [](int) {});
+  for_batches<NT>(row, part, use, [](int) {});
 }
 
-template <typename T>
+template <int NT, typename T>
 __device__ __forceinline__ void zero_part(const Row<T>& out, int piece, int pieces) {
   const Part part = part_of(out, piece, pieces);
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int i = part.begin + static_cast<int>(threadIdx.x); i < part.end; i += kVocabThreads) out.store(out.first(i), zero);
+  for (int i = part.begin + static_cast<int>(threadIdx.x); i < part.end; i += NT) out.store(out.first(i), zero);
   if (part.head >= 0 && threadIdx.x == kHeadThread) out.store(out.first(part.head), zero);
   if (part.tail >= 0 && threadIdx.x == kTailThread) out.store(out.first(part.tail), zero);
 }
@@ -376,18 +375,19 @@ __device__ __forceinline__ Totals warp_totals(const Sums& a, float c) {
 
 // The totals of every CTA's threads of a cluster relative to the row's largest logit, the
 // same in every thread: warps, then CTAs, in a fixed order.  With more than one CTA, each has
-// arrived at the cluster's barrier before; the next use of `sh` needs a barrier.
+// arrived at the cluster's barrier before; the next use of `sh` needs a barrier.  Every thread
+// of the block calls this, the sums of the first NT count.
 struct TotalsShared {
-  Totals warp[kVocabWarps];
+  Totals warp[kMaxWarps];
   Totals cta[kMaxCluster];
 };
-template <bool ENT>
+template <bool ENT, int NT>
 __device__ __forceinline__ Totals row_totals(const Sums& a, float c, TotalsShared& sh, int ctas) {
   const Totals w = warp_totals<ENT>(a, c);
-  if ((threadIdx.x & 31) == 0) sh.warp[threadIdx.x >> 5] = w;
+  if ((threadIdx.x & 31) == 0 && threadIdx.x < NT) sh.warp[threadIdx.x >> 5] = w;
   __syncthreads();
-  const Totals v = sh.warp[threadIdx.x & (kVocabWarps - 1)];
-  const Totals mine = group_totals<ENT, kVocabWarps>(v.max, v.max, v.s, v.sy, c);
+  const Totals v = sh.warp[threadIdx.x & (NT / 32 - 1)];
+  const Totals mine = group_totals<ENT, NT / 32>(v.max, v.max, v.s, v.sy, c);
   if (ctas == 1) return mine;
   ptx::cluster_wait();  // every CTA runs (they arrived when they started)
   if (static_cast<int>(threadIdx.x) < ctas) {
@@ -445,14 +445,15 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
 static_assert(kTopCandidates >= kMaxCluster * kTopMaxK, "every CTA's k largest fit");
 
+constexpr int kTopThreads = 256, kTopWarps = kTopThreads / 32;
 constexpr int kTopGroups = 32;   // groups of batches per thread at most
 constexpr int kTopList = 1024;
 struct TopShared {
-  uint32_t key[kVocabThreads];
-  int32_t vec[kVocabThreads];
-  uint32_t list[kTopList];                    // group * kVocabThreads + thread
+  uint32_t key[kTopThreads];
+  int32_t vec[kTopThreads];
+  uint32_t list[kTopList];                    // group * kTopThreads + thread
   uint64_t cand[kTopCandidates];
-  uint64_t best[kVocabWarps];
+  uint64_t best[kTopWarps];
   uint32_t bound_key, bound_tie_top;
   int32_t bound_vec, nlist, ncand;
   uint32_t taken[kMaxCluster];                // how many keys each CTA gave
@@ -469,12 +470,12 @@ struct TopGroups {
   float running;
   __device__ __forceinline__ void batch(int n) {
     const uint32_t key = order_key(running);
-    top[(n >> shift) * kVocabThreads + threadIdx.x] = static_cast<Key>(sizeof(Key) == 2 ? key >> 16 : key);
+    top[(n >> shift) * kTopThreads + threadIdx.x] = static_cast<Key>(sizeof(Key) == 2 ? key >> 16 : key);
     if ((n + 1) >> shift != n >> shift) running = kNegInf;
   }
   // the largest key that the group can hold
   __device__ __forceinline__ uint32_t largest(int group) const {
-    const uint32_t key = top[group * kVocabThreads + threadIdx.x];
+    const uint32_t key = top[group * kTopThreads + threadIdx.x];
     return sizeof(Key) == 2 ? key << 16 | 0xffffu : key;
   }
 };
@@ -490,7 +491,7 @@ __device__ __forceinline__ uint64_t full_key(float f, int v) {
 template <typename T>
 __device__ __forceinline__ void top_bound(TopShared& sh, int k) {
   constexpr int kLow = Elem<T>::kKeyLowBit;
-  constexpr int kPer = kVocabThreads / 32;
+  constexpr int kPer = kTopThreads / 32;
   const int lane = threadIdx.x;
   uint32_t key[kPer];
   int vec[kPer];
@@ -514,11 +515,11 @@ __device__ __forceinline__ void top_bound(TopShared& sh, int k) {
     int b = high == low ? kLow - 1 : 31 - __clz(high ^ low);
     bound = b >= 31 ? 0 : high >> (b + 1) << (b + 1);
     if (b < kLow) bound = high >> kLow << kLow;
-    int reach = kVocabThreads;
+    int reach = kTopThreads;
     // a few more threads than k cost less than the steps that would tell them apart
     const int enough = k + 4 + k / 4;
     // two bits at a time: the counts of three thresholds side by side in one sum
-    static_assert(kVocabThreads < 1 << 10, "ten bits hold a count");
+    static_assert(kTopThreads < 1 << 10, "ten bits hold a count");
     for (; b >= kLow && reach > enough; b -= 2) {
       const uint32_t half = b > kLow ? 1u << (b - 1) : 0u, one = 1u << b;  // the last bit alone: half 0
       uint32_t n = 0;
@@ -572,7 +573,7 @@ __device__ __forceinline__ void top_bound(TopShared& sh, int k) {
 // Places `n` distinct keys in descending order: put(place, key) for the first k.
 template <typename F>
 __device__ __forceinline__ void place_keys(const uint64_t* keys, int n, int k, F&& put) {
-  for (int j = threadIdx.x; j < n; j += kVocabThreads) {
+  for (int j = threadIdx.x; j < n; j += kTopThreads) {
     const uint64_t mine = keys[j];
     int place = 0;
 #pragma unroll 8
@@ -597,11 +598,11 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
   const int bound_vec = sh.bound_vec;
   const int per = 4 << groups.shift;  // vectors of a group
   if (sh.key[tid] >= bound) {
-    for (int j = 0; part.begin + tid + j * per * kVocabThreads < part.end; ++j) {
+    for (int j = 0; part.begin + tid + j * per * kTopThreads < part.end; ++j) {
       const uint32_t largest = groups.largest(j);
-      if (largest >= bound && (largest > tie_top || part.begin + tid + j * per * kVocabThreads <= bound_vec)) {
+      if (largest >= bound && (largest > tie_top || part.begin + tid + j * per * kTopThreads <= bound_vec)) {
         const int at = atomicAdd(&sh.nlist, 1);
-        if (at < kTopList) sh.list[at] = j * kVocabThreads + tid;
+        if (at < kTopList) sh.list[at] = j * kTopThreads + tid;
       }
     }
   }
@@ -623,9 +624,9 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
     }
   };
   if (nlist <= kTopList) {
-    for (int q = tid; q < nlist * per; q += kVocabThreads) {
-      const int item = static_cast<int>(sh.list[q / per]), j = item / kVocabThreads, owner = item % kVocabThreads;
-      const int i = part.begin + owner + (j * per + q % per) * kVocabThreads;
+    for (int q = tid; q < nlist * per; q += kTopThreads) {
+      const int item = static_cast<int>(sh.list[q / per]), j = item / kTopThreads, owner = item % kTopThreads;
+      const int i = part.begin + owner + (j * per + q % per) * kTopThreads;
       if (i < part.end) offer(i);
     }
     if (part.head >= 0 && tid == kHeadThread) offer(part.head);
@@ -641,7 +642,7 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
   uint64_t last = ~0ull;
   for (int j = 0; j < k; ++j) {
     uint64_t best = 0;
-    for_vectors(row, part, [&](int i, const uint4& raw) {
+    for_vectors<kTopThreads>(row, part, [&](int i, const uint4& raw) {
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
         const uint64_t fk = full_key(vec_get<T>(raw, e), row.first(i) + e);
@@ -656,7 +657,7 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
     if (lane == 0) sh.best[tid >> 5] = best;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kVocabWarps; ++w) best = sh.best[w] > best ? sh.best[w] : best;
+    for (int w = 0; w < kTopWarps; ++w) best = sh.best[w] > best ? sh.best[w] : best;
     __syncthreads();
     if (best == 0) return j;  // nothing above -inf is left
     last = best;
@@ -689,18 +690,107 @@ __device__ __forceinline__ void row_top(const Row<T>& row, const Part& part, con
     int total = 0;
     for (int r = 0; r < ctas; ++r) {
       const int n = static_cast<int>(sh.taken[r]);
-      for (int j = threadIdx.x; j < n; j += kVocabThreads) sh.cand[total + j] = gathered[r * k + j];
+      for (int j = threadIdx.x; j < n; j += kTopThreads) sh.cand[total + j] = gathered[r * k + j];
       total += n;
     }
     __syncthreads();
     place_keys(sh.cand, total, k, write);
     found = min(total, k);
   }
-  for (int j = found + threadIdx.x; j < k; j += kVocabThreads) {
+  for (int j = found + threadIdx.x; j < k; j += kTopThreads) {
     out_index[j] = -1;
     out_value[j] = kNegInf;
   }
 }
+
+// ---------------------------------------------------------------- rows kept on chip
+
+// A block's part of a row in shared memory: vector i at v[i - base].  The whole vectors come
+// by bulk copies in chunks, each with a barrier of its own, so that the pass over the first
+// runs while the others arrive; the ragged ones by plain loads of the threads that have them.
+constexpr int kSlabChunks = 4;
+constexpr uint64_t kSlabWaitNs = 2000000000ull;
+struct SlabShared {
+  uint64_t full[kSlabChunks];
+  int abort;
+};
+
+template <typename T, int NT>
+struct Slab {
+  uint4* v;
+  SlabShared* sh;
+  Part part;
+  int base, each;  // vectors per chunk
+  int* status;
+  int kernel;
+
+  __device__ __forceinline__ void start(const Row<T>& row, const Part& part_, uint4* shared, SlabShared* sh_) {
+    v = shared;
+    sh = sh_;
+    part = part_;
+    status = row.status;
+    kernel = row.kernel;
+    base = part.head >= 0 ? part.head : part.begin;
+    each = (part.end - part.begin + kSlabChunks * NT - 1) / (kSlabChunks * NT) * NT;
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int q = 0; q < kSlabChunks; ++q) ptx::mbar_init(ptx::smem_u32(&sh->full[q]), 1);
+      sh->abort = 0;
+      ptx::fence_mbarrier_init();
+#pragma unroll
+      for (int q = 0; q < kSlabChunks; ++q) {
+        const int b = min(part.end, part.begin + q * each), e = min(part.end, b + each);
+        const uint32_t bar = ptx::smem_u32(&sh->full[q]);
+        bool load = e > b;
+        if (load)
+          load = bounds_ok(row.whole(b) && row.whole(e - 1) && (reinterpret_cast<uintptr_t>(row.p + row.first(b)) & 15) == 0,
+                           status, kernel, NSM_ROLE_PRODUCER, NSM_SITE_LOGITS);
+        ptx::mbar_arrive_expect_tx(bar, load ? (e - b) * 16 : 0);
+        if (load) ptx::bulk_load(ptx::smem_u32(v + (b - base)), row.p + row.first(b), (e - b) * 16, bar);
+      }
+    }
+    if (part.head >= 0 && threadIdx.x == kHeadThread) v[part.head - base] = row.load(part.head);
+    if (part.tail >= 0 && threadIdx.x == kTailThread) v[part.tail - base] = row.load(part.tail);
+    __syncthreads();  // the barriers are there
+  }
+  __device__ __forceinline__ void wait(int q) const { wait_on(&sh->full[q]); }
+  // Until a barrier's first phase is over.  After a wait that ran out (recorded) the block goes on with
+  // what is there, so that every barrier is still met; drain() then waits once more.
+  __device__ __forceinline__ void wait_on(uint64_t* bar) const {
+    if (!ptx::mbar_wait_bounded(ptx::smem_u32(bar), 0, &sh->abort, kSlabWaitNs)) {
+      record_timeout(status, kernel, NSM_ROLE_PRODUCER, NSM_SITE_STAGE_FULL);
+      sh->abort = 1;
+    }
+  }
+  // use(i, vector) for this thread's vectors of chunk q.
+  template <typename F>
+  __device__ __forceinline__ void chunk(int q, F&& use) const {
+    const int b = min(part.end, part.begin + q * each), e = min(part.end, b + each);
+#pragma unroll 2
+    for (int i = b + static_cast<int>(threadIdx.x); i < e; i += NT) use(i, v[i - base]);
+  }
+  template <typename F>
+  __device__ __forceinline__ void ragged(F&& use) const {
+    if (part.head >= 0 && threadIdx.x == kHeadThread) use(part.head, v[part.head - base]);
+    if (part.tail >= 0 && threadIdx.x == kTailThread) use(part.tail, v[part.tail - base]);
+  }
+  template <typename F>
+  __device__ __forceinline__ void all(F&& use) const {
+#pragma unroll 2
+    for (int i = part.begin + static_cast<int>(threadIdx.x); i < part.end; i += NT) use(i, v[i - base]);
+    ragged(use);
+  }
+  // Before the block ends: no copy into its shared memory may be in flight.
+  __device__ __forceinline__ void drain() const {
+    if (*static_cast<volatile int*>(&sh->abort) == 0) return;
+    int never = 0;
+    if (threadIdx.x == 0) {
+      for (int q = 0; q < kSlabChunks; ++q)
+        if (!ptx::mbar_wait_bounded(ptx::smem_u32(&sh->full[q]), 0, &never, kSlabWaitNs)) break;
+    }
+    __syncthreads();
+  }
+};
 
 // ---------------------------------------------------------------- log probabilities
 
@@ -740,8 +830,8 @@ __device__ __forceinline__ void store_token_gradient(const Row<T>& out, int e0, 
 
 // A cluster of CTAs per row (one CTA where there are rows enough).  TOP: dynamic shared
 // memory holds rank 0's gathered keys (ctas k of them where ctas > 1), then the groups' tops.
-template <typename T, bool ENT, bool TOP, bool GRAD>
-__global__ void __launch_bounds__(kVocabThreads, TOP ? 6 : 5) k_logprobs(const LogprobArgs g, int group_shift, int* status) {
+template <typename T, bool ENT, bool TOP, bool GRAD, int NT = TOP ? kTopThreads : GRAD ? 256 : 128>
+__global__ void __launch_bounds__(NT, TOP ? 6 : 1280 / NT) k_logprobs(const LogprobArgs g, int group_shift, int* status) {
   extern __shared__ __align__(16) uint8_t dynamic[];
   __shared__ TotalsShared totals;
   __shared__ typename std::conditional<TOP, TopShared, int>::type top;
@@ -760,7 +850,7 @@ __global__ void __launch_bounds__(kVocabThreads, TOP ? 6 : 5) k_logprobs(const L
   uint64_t* gathered = reinterpret_cast<uint64_t*>(dynamic);
   TopGroups<T> groups{reinterpret_cast<typename TopGroups<T>::Key*>(gathered + (ctas > 1 ? ctas * g.k : 0)), group_shift, kNegInf};
   Sums a;
-  for_batches(row, part,
+  for_batches<NT>(row, part,
               [&](int i, const uint4& raw) {
                 const float m = add_vec<T, ENT>(a, raw, i, c);
                 if (TOP) groups.running = fmaxf(groups.running, m);
@@ -768,7 +858,7 @@ __global__ void __launch_bounds__(kVocabThreads, TOP ? 6 : 5) k_logprobs(const L
               [&](int n) {
                 if (TOP) groups.batch(n);
               });
-  const Totals t = row_totals<ENT>(a, c, totals, ctas);
+  const Totals t = row_totals<ENT, NT>(a, c, totals, ctas);
   const bool empty = t.max == kNegInf && t.s == 0.f;  // a row of NaN has a NaN sum
   const float ref = empty ? 0.f : t.max, log_s = empty ? 0.f : logf(t.s);
   float entropy = 0.f;
@@ -787,9 +877,9 @@ __global__ void __launch_bounds__(kVocabThreads, TOP ? 6 : 5) k_logprobs(const L
     const float h = ENT && g.d_entropy ? g.d_entropy[r] : 0.f;
     const TokenGradient k = token_gradient(w, h, ref, log_s, empty ? 0.f : log2f(t.s), entropy, x_token, empty, inv_t);
     if (k.zero) {
-      zero_part(out, rank, ctas);
+      zero_part<NT>(out, rank, ctas);
     } else {
-      for_vectors(row, part, [&](int i, const uint4& raw) { store_token_gradient<T, ENT>(out, row.first(i), raw, k, token, c); });
+      for_vectors<NT>(row, part, [&](int i, const uint4& raw) { store_token_gradient<T, ENT>(out, row.first(i), raw, k, token, c); });
     }
   }
   if constexpr (TOP) {
@@ -797,7 +887,7 @@ __global__ void __launch_bounds__(kVocabThreads, TOP ? 6 : 5) k_logprobs(const L
     int32_t* index = g.top_index + r * g.k;
     if (log_s != log_s) {  // NaN or +inf in the row
       if (rank == 0) {
-        for (int j = threadIdx.x; j < g.k; j += kVocabThreads) {
+        for (int j = threadIdx.x; j < g.k; j += NT) {
           value[j] = log_s;
           index[j] = -1;
         }
@@ -808,9 +898,62 @@ __global__ void __launch_bounds__(kVocabThreads, TOP ? 6 : 5) k_logprobs(const L
   }
 }
 
+// Forward and backward in one pass over memory: the row stays in the shared memory of the
+// cluster's blocks between its sums and its gradient.
+template <typename T, bool ENT, int NT>
+__global__ void __launch_bounds__(NT) k_logprobs_resident(const LogprobArgs g, int* status) {
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  __shared__ TotalsShared totals;
+  __shared__ SlabShared slab_shared;
+  grid_dependency_sync();
+  release_dependents();
+  const int ctas = static_cast<int>(ptx::cluster_nctarank()), rank = static_cast<int>(ptx::cluster_ctarank());
+  if (ctas > 1) ptx::cluster_arrive();
+  const int64_t r = blockIdx.x / ctas;
+  const int vocab = g.v.vocab;
+  const float c = g.v.c, inv_t = g.v.inv_t;
+  const Row<T> row(static_cast<T*>(const_cast<void*>(g.v.logits)) + r * g.v.ld, vocab, status, NSM_KERNEL_LOGPROBS);
+  const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, NSM_KERNEL_LOGPROBS);
+  Slab<T, NT> slab;
+  slab.start(row, part_of(row, rank, ctas), reinterpret_cast<uint4*>(dynamic), &slab_shared);
+  const int64_t token64 = g.tokens ? load_index(g.tokens, g.tokens_wide, r) : -1;
+  const int token = token64 < 0 || token64 >= vocab ? -1 : static_cast<int>(token64);
+  const float x_token = token >= 0 ? Elem<T>::to_float(row.p[token]) : kNegInf;
+  const float w = g.d_logprob && token >= 0 ? g.d_logprob[r] : 0.f;
+  const float h = ENT && g.d_entropy ? g.d_entropy[r] : 0.f;
+  Sums a;
+  auto add = [&](int i, const uint4& raw) { add_vec<T, ENT>(a, raw, i, c); };
+  slab.ragged(add);
+#pragma unroll 1
+  for (int q = 0; q < kSlabChunks; ++q) {
+    slab.wait(q);
+    slab.chunk(q, add);
+  }
+  const Totals t = row_totals<ENT, NT>(a, c, totals, ctas);
+  const bool empty = t.max == kNegInf && t.s == 0.f;
+  const float ref = empty ? 0.f : t.max, log_s = empty ? 0.f : logf(t.s);
+  float entropy = 0.f;
+  if (ENT && !empty) {
+    entropy = log_s - kLn2 * (t.sy / t.s);
+    if (entropy < 0.f) entropy = 0.f;
+  }
+  if (rank == 0 && threadIdx.x == 0) {
+    if (g.lse) g.lse[r] = empty ? kNegInf : ref * inv_t + log_s;
+    if (ENT && g.entropy) g.entropy[r] = entropy;
+    if (g.logprob) g.logprob[r] = token < 0 ? 0.f : (empty ? kNegInf : (x_token - ref) * inv_t - log_s);
+  }
+  const TokenGradient k = token_gradient(w, h, ref, log_s, empty ? 0.f : log2f(t.s), entropy, x_token, empty, inv_t);
+  if (k.zero) {
+    zero_part<NT>(out, rank, ctas);
+  } else {
+    slab.all([&](int i, const uint4& raw) { store_token_gradient<T, ENT>(out, row.first(i), raw, k, token, c); });
+  }
+  slab.drain();
+}
+
 // The backward pass alone: pieces of rows, every element on its own.
-template <typename T, bool ENT>
-__global__ void __launch_bounds__(kVocabThreads, 6) k_logprobs_backward(const LogprobArgs g, int pieces, int* status) {
+template <typename T, bool ENT, int NT = 256>
+__global__ void __launch_bounds__(NT, 6) k_logprobs_backward(const LogprobArgs g, int pieces, int* status) {
   grid_dependency_sync();
   release_dependents();
   const int vocab = g.v.vocab;
@@ -828,7 +971,7 @@ __global__ void __launch_bounds__(kVocabThreads, 6) k_logprobs_backward(const Lo
     const float lse = g.in_lse[r];
     const bool empty = lse == kNegInf;
     if (empty || (w == 0.f && h == 0.f)) {
-      zero_part(out, piece, pieces);
+      zero_part<NT>(out, piece, pieces);
       continue;
     }
     // in place, another block may have written the token's own gradient already: only the
@@ -839,43 +982,11 @@ __global__ void __launch_bounds__(kVocabThreads, 6) k_logprobs_backward(const Lo
     const float x_token = here ? Elem<T>::to_float(row.p[token]) : kNegInf;
     const TokenGradient k = token_gradient(w, h, lse * g.v.t, 0.f, 0.f, ENT ? g.in_entropy[r] : 0.f, x_token, empty, inv_t);
     __syncthreads();  // every thread has read the token's logit
-    for_vectors(row, part, [&](int i, const uint4& raw) { store_token_gradient<T, ENT>(out, row.first(i), raw, k, token, c); });
+    for_vectors<NT>(row, part, [&](int i, const uint4& raw) { store_token_gradient<T, ENT>(out, row.first(i), raw, k, token, c); });
   }
 }
 
 // ---------------------------------------------------------------- distillation
-
-struct DistillShared {
-  int32_t index[kDistillMaxK];   // -1: the entry does not count
-  float sum[kVocabWarps];
-  double dsum[kVocabWarps];
-  TotalsShared rest, entries;
-};
-
-template <typename V>
-__device__ __forceinline__ V block_sum(V v, V* parts) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = parts[0];
-#pragma unroll
-  for (int w = 1; w < kVocabWarps; ++w) v += parts[w];
-  __syncthreads();
-  return v;
-}
-
-__device__ __forceinline__ float block_max(float v, float* parts) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
-  if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = parts[0];
-#pragma unroll
-  for (int w = 1; w < kVocabWarps; ++w) v = fmaxf(v, parts[w]);
-  __syncthreads();
-  return v;
-}
 
 __device__ __forceinline__ float load_number(const void* p, int dtype, int64_t i) {
   if (dtype == NSM_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
@@ -883,82 +994,199 @@ __device__ __forceinline__ float load_number(const void* p, int dtype, int64_t i
   return static_cast<const float*>(p)[i];
 }
 
-// The teacher of a row: thread j < k has entry j (mine: its token, -1 where it does not
-// count; of equal indexes the first counts), its log p and the student's logit there.
-struct Teacher {
-  int mine;
-  float log_p, p, x;
-  float p_rest, lacking;  // the tail's 1 - sum p, and that as at least 0
-  bool any;               // there is a target
+template <typename V>
+__device__ __forceinline__ V warp_sum(V v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+  return v;
+}
+
+// The teacher of a row lives in one warp (a warp of its own beside the ones that sum the row,
+// so that its many small steps cost them no time): lane l has entries l, l + 32, ...
+constexpr int kLaneEntries = kDistillMaxK / 32;
+struct Entries {
+  int v[kLaneEntries];  // its token, -1 where it does not count
+  float log_p[kLaneEntries], p[kLaneEntries], x[kLaneEntries];  // x: the student's logit
+};
+// What the row's other threads need of it.
+struct TeacherStats {
+  Totals inside;          // the student's sum over the entries
+  float p_rest, lacking;  // the tail's 1 - sum p, as at least 0 and as it is
+  int any;                // there is a target
 };
 
-template <typename T>
-__device__ __forceinline__ Teacher read_teacher(const DistillArgs& g, int64_t r, const Row<T>& row, DistillShared& sh) {
-  static_assert(kDistillMaxK <= kVocabThreads, "one thread per entry");
-  const int tid = threadIdx.x, k = g.k;
-  Teacher t{-1, kNegInf, 0.f, kNegInf, 0.f, 0.f, false};
-  float z = kNegInf;
-  if (tid < k) {
-    const int64_t v = load_index(g.index, g.index_wide, r * g.ldi + tid);
-    z = load_number(g.teacher, g.teacher_dtype, r * g.ldt + tid);
-    t.mine = v >= 0 && v < row.vocab ? static_cast<int>(v) : -1;
-    sh.index[tid] = t.mine;
+// The entries' tokens and scores (in log_p); equal tokens are still there.
+__device__ __forceinline__ void load_entries(Entries& e, const DistillArgs& g, int64_t r) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int u = 0; u < kLaneEntries; ++u) {
+    e.v[u] = -1;
+    e.x[u] = e.log_p[u] = kNegInf;
+    if (lane + 32 * u < g.k) {
+      e.log_p[u] = load_number(g.teacher, g.teacher_dtype, r * g.ldt + lane + 32 * u);
+      const int64_t v = load_index(g.index, g.index_wide, r * g.ldi + lane + 32 * u);
+      if (v >= 0 && v < g.v.vocab) e.v[u] = static_cast<int>(v);
+    }
   }
-  __syncthreads();
-  for (int j = 0; j < tid && t.mine >= 0; ++j)
-    if (sh.index[j] == t.mine) t.mine = -1;
-  __syncthreads();
-  if (tid < k) sh.index[tid] = t.mine;
-  const bool counts = t.mine >= 0;
-  if (counts) t.x = Elem<T>::to_float(row.p[t.mine]);
+}
+
+// The student's logits at the entries' tokens, read from the row.
+template <typename T>
+__device__ __forceinline__ void load_logits(Entries& e, const Row<T>& row) {
+#pragma unroll
+  for (int u = 0; u < kLaneEntries; ++u)
+    if (e.v[u] >= 0) e.x[u] = Elem<T>::to_float(row.p[e.v[u]]);
+}
+
+// Of equal tokens the first counts; then the teacher's probabilities and, for the forward pass
+// (INSIDE), the student's sum.
+template <bool INSIDE>
+__device__ __forceinline__ TeacherStats teacher_stats(Entries& e, const DistillArgs& g) {
+  const int lane = threadIdx.x & 31;
+  const float c = g.v.c;
+#pragma unroll
+  for (int u = kLaneEntries - 1; u >= 0; --u) {  // later groups first: earlier ones are whole
+    if (32 * u >= g.k) continue;
+    int v = e.v[u];
+    const uint32_t same = __match_any_sync(~0u, v >= 0 ? v : -1 - lane);
+    if (same & ((1u << lane) - 1u)) v = -1;
+#pragma unroll
+    for (int w = 0; w < u; ++w)
+#pragma unroll 8
+      for (int l = 0; l < 32; ++l)
+        if (__shfl_sync(~0u, e.v[w], l) == v) v = -1;
+    if (v < 0) e.x[u] = e.log_p[u] = kNegInf;
+    e.v[u] = v;
+  }
+#pragma unroll
+  for (int u = 0; u < kLaneEntries; ++u)
+    if (e.v[u] < 0) e.log_p[u] = kNegInf;
+  TeacherStats t;
+  t.p_rest = t.lacking = 0.f;
   if (g.tail) {
-    if (counts) t.log_p = z;
-    // 1 - sum p: the teacher's rest is often a small difference, so in 64 bits
-    const double sum = block_sum(counts ? exp(static_cast<double>(z)) : 0.0, sh.dsum);
-    t.lacking = static_cast<float>(1.0 - sum);
+    // 1 - sum p as (1 - largest p) - the others: the teacher's rest is often a small part of
+    // what its first entry leaves (64-bit sums are too slow here: they cost half the row's time)
+    float m = kNegInf, others = 0.f;
+    bool some = false;
+#pragma unroll
+    for (int u = 0; u < kLaneEntries; ++u) {
+      m = fmaxf(m, e.log_p[u]);
+      some |= e.v[u] >= 0;
+    }
+    const float largest = warp_max(m);
+    bool taken = false;
+#pragma unroll
+    for (int u = 0; u < kLaneEntries; ++u) {
+      if (32 * u >= g.k) continue;
+      const uint32_t at = __ballot_sync(~0u, !taken && e.log_p[u] == largest);  // its first holder
+      const bool is_largest = at && (at & -at) == 1u << lane && !taken;
+      if (!is_largest && !(e.log_p[u] == kNegInf)) others += expf(e.log_p[u]);
+      taken |= at != 0;
+    }
+    t.lacking = (largest == kNegInf ? 1.f : -expm1f(largest)) - warp_sum(others);
     t.p_rest = t.lacking < 0.f ? 0.f : t.lacking;
-    t.any = __syncthreads_or(counts);
+    t.any = __any_sync(~0u, some);
   } else {
-    const float y = counts ? z * g.v.inv_t : kNegInf;
-    const float m = block_max(y, sh.sum);
-    // a NaN entry makes the sum, and with it every p, a NaN
-    const float total = block_sum(!counts ? 0.f : (m != kNegInf ? expf(y - m) : (y != y ? y : 0.f)), sh.sum);
-    if (counts && !(y == kNegInf)) t.log_p = (y - m) - logf(total);
+    float m = kNegInf, total = 0.f;
+#pragma unroll
+    for (int u = 0; u < kLaneEntries; ++u) {
+      if (e.v[u] >= 0) e.log_p[u] *= g.v.inv_t;
+      m = fmaxf(m, e.log_p[u]);
+    }
+    m = warp_max(m);
+#pragma unroll
+    for (int u = 0; u < kLaneEntries; ++u)  // a NaN entry makes the sum, and with it every p, a NaN
+      if (e.v[u] >= 0 && !(e.log_p[u] == kNegInf)) total += m == kNegInf ? e.log_p[u] : expf(e.log_p[u] - m);
+    total = warp_sum(total);
+    const float log_total = logf(total);
+#pragma unroll
+    for (int u = 0; u < kLaneEntries; ++u)
+      if (!(e.log_p[u] == kNegInf)) e.log_p[u] = (e.log_p[u] - m) - log_total;
     t.any = m != kNegInf || total != total;
   }
-  t.p = expf(t.log_p);
+#pragma unroll
+  for (int u = 0; u < kLaneEntries; ++u) e.p[u] = expf(e.log_p[u]);
+  t.inside = Totals{kNegInf, 0.f, 0.f};
+  if (!INSIDE) return t;
+  float max = kNegInf, s = 0.f;
+#pragma unroll
+  for (int u = 0; u < kLaneEntries; ++u) max = fmaxf(max, e.x[u]);
+  max = warp_max(max);
+#pragma unroll
+  for (int u = 0; u < kLaneEntries; ++u)
+    if (!(e.x[u] == kNegInf)) s += max == kNegInf ? e.x[u] : ex2((e.x[u] - max) * c);  // a NaN stays one
+  t.inside = Totals{max, warp_sum(s), 0.f};
   return t;
 }
 
-// What the gradient pass of a row needs: outside the entries scale 2^((x - ref) c - log2_s).
-struct EntryGradient {
-  float ref, log2_s, scale;
-  float mine;  // at this thread's own entry
+// The student's row: log q_v = (x_v - lse_ref) / t - lse_log,
+// q_v / q_rest = 2^((x_v - rest_ref) c - rest_log2), rest = log q_rest.
+struct Student {
+  float lse_ref, lse_log, rest_ref, rest_log2, rest;
+  bool empty;
 };
 
-// w loss: d/dx = w / t (q (1 + excess) - p) at the entries, and outside them, with the tail,
-// q (1 + excess) - p_rest q / q_rest = (q / q_rest) (q_rest (1 + excess) - p_rest).
-// log q_v = (x_v - lse_ref) / t - lse_log, q_v / q_rest = 2^((x_v - rest_ref) c - rest_log2).
-__device__ __forceinline__ EntryGradient entry_gradient(const Teacher& t, float w, int tail, float lse_ref, float lse_log,
-                                                        float rest_ref, float rest_log2, float rest, float inv_t) {
-  EntryGradient k;
-  const float p_rest = rest == kNegInf ? 0.f : t.p_rest;
-  const float excess = tail ? p_rest - t.lacking : 0.f;  // sum p + p_rest - 1
-  const float unit = w * inv_t;
-  if (tail) {
-    k.ref = rest_ref;
-    k.log2_s = rest_log2;
-    k.scale = rest == kNegInf ? 0.f : unit * (expf(rest) * (1.f + excess) - p_rest);
-  } else {
-    k.ref = lse_ref;
-    k.log2_s = lse_log * (1.f / kLn2);
-    k.scale = unit;
+__device__ __forceinline__ Student student_of(const TeacherStats& t, const Totals& outside, float c, float inv_t) {
+  Totals all{fmaxf(outside.max, t.inside.max), outside.s, 0.f};
+  float inside_s = t.inside.s, none = 0.f;
+  rebase<false>(all.s, none, outside.max, all.max, c);
+  rebase<false>(inside_s, none, t.inside.max, all.max, c);
+  all.s += inside_s;
+  Student st;
+  st.empty = all.max == kNegInf && all.s == 0.f;
+  const bool no_rest = outside.max == kNegInf && outside.s == 0.f;
+  st.lse_ref = st.empty ? 0.f : all.max;
+  st.lse_log = st.empty ? 0.f : logf(all.s);
+  st.rest_ref = no_rest ? 0.f : outside.max;
+  st.rest_log2 = no_rest ? 0.f : log2f(outside.s);
+  st.rest = no_rest ? kNegInf : (outside.max - st.lse_ref) * inv_t + (logf(outside.s) - st.lse_log);
+  return st;
+}
+
+// The teacher's warp writes the row's loss, lse and rest.
+__device__ __forceinline__ void write_loss(const DistillArgs& g, int64_t r, const Entries& e, const TeacherStats& t,
+                                           const Student& st) {
+  const float inv_t = g.v.inv_t, p_rest = st.rest == kNegInf ? 0.f : t.p_rest;
+  float loss = 0.f;
+#pragma unroll
+  for (int u = 0; u < kLaneEntries; ++u)
+    if (e.p[u] > 0.f || e.p[u] != e.p[u]) loss += e.p[u] * (e.log_p[u] - ((e.x[u] - st.lse_ref) * inv_t - st.lse_log));
+  loss = warp_sum(loss);
+  if (p_rest > 0.f || p_rest != p_rest) loss += p_rest * (logf(p_rest) - st.rest);
+  if ((threadIdx.x & 31) == 0) {
+    if (g.loss) g.loss[r] = t.any ? loss : 0.f;
+    if (g.lse) g.lse[r] = st.empty ? kNegInf : st.lse_ref * inv_t + st.lse_log;
+    if (g.rest) g.rest[r] = st.rest;
   }
-  k.mine = 0.f;
-  const float log_q = (t.x - lse_ref) * inv_t - lse_log;
-  if (t.mine >= 0 && log_q != kNegInf) {  // q - p without cancellation
-    const float q = expf(log_q);
-    k.mine = unit * ((t.p > 0.f || t.p != t.p ? t.p * expm1f(log_q - t.log_p) : q) + q * excess);
+}
+
+// w loss: d/dx = w / t (q (1 + excess) - p) at the entries, and outside them, with the tail,
+// q (1 + excess) - p_rest q / q_rest = (q / q_rest) (q_rest (1 + excess) - p_rest), as
+// scale 2^((x - ref) c - log2_s).  excess = sum p + p_rest - 1.
+struct EntryGradient {
+  float ref, log2_s, scale, unit, excess;
+  bool zero;
+};
+
+__device__ __forceinline__ EntryGradient entry_gradient(const TeacherStats& t, const Student& s, float w, int tail, float inv_t) {
+  EntryGradient k;
+  k.zero = s.empty || !t.any || w == 0.f;
+  const float p_rest = s.rest == kNegInf ? 0.f : t.p_rest;
+  k.excess = tail ? p_rest - t.lacking : 0.f;
+  k.unit = w * inv_t;
+  if (tail) {
+    k.ref = s.rest_ref;
+    k.log2_s = s.rest_log2;
+    k.scale = s.rest == kNegInf ? 0.f : k.unit * (expf(s.rest) * (1.f + k.excess) - p_rest);
+  } else {
+    k.ref = s.lse_ref;
+    k.log2_s = s.lse_log * (1.f / kLn2);
+    k.scale = k.unit;
   }
   return k;
 }
@@ -969,118 +1197,221 @@ __device__ __forceinline__ bool in_part(const Row<T>& row, const Part& part, int
   return (at >= part.begin && at < part.end) || at == part.head || at == part.tail;
 }
 
-// The dense pass over the block's part, then the entries' own values over what it wrote there.
+// The teacher's warp writes the gradients at the entries of the block's part, over what the
+// pass over the row wrote there.
 template <typename T>
-__device__ __forceinline__ void store_entry_gradients(const Row<T>& row, const Row<T>& out, const Part& part,
-                                                      const Teacher& t, const EntryGradient& k, float c) {
-  for_vectors(row, part, [&](int i, const uint4& raw) {
-    out.store(row.first(i), gradient_vec<T, false>(raw, k.ref, c, k.log2_s, k.scale, 0.f));
-  });
-  __syncthreads();
-  if (t.mine >= 0 && in_part(row, part, t.mine)) out.p[t.mine] = Elem<T>::from_float(k.mine);
+__device__ __forceinline__ void store_entries(const Row<T>& row, const Row<T>& out, const Part& part, const Entries& e,
+                                              const Student& s, const EntryGradient& k, float inv_t) {
+#pragma unroll
+  for (int u = 0; u < kLaneEntries; ++u) {
+    if (e.v[u] < 0 || !in_part(row, part, e.v[u])) continue;
+    const float log_q = (e.x[u] - s.lse_ref) * inv_t - s.lse_log, p = e.p[u];
+    float grad = 0.f;
+    if (log_q != kNegInf) {  // q - p without cancellation
+      const float q = expf(log_q);
+      grad = k.unit * ((p > 0.f || p != p ? p * expm1f(log_q - e.log_p[u]) : q) + q * k.excess);
+    }
+    if (bounds_ok(e.v[u] < out.vocab, out.status, out.kernel, 0, NSM_SITE_GRADIENT)) out.p[e.v[u]] = Elem<T>::from_float(grad);
+  }
 }
 
-template <typename T, bool GRAD>
-__global__ void __launch_bounds__(kVocabThreads, 5) k_distill(const DistillArgs g, int* status) {
+// NT threads sum the row (a cluster of blocks per row where rows are few), a warp more has the
+// teacher.  GRAD: rows too long to stay in shared memory, read a second time.
+template <typename T, bool GRAD, int NT>
+__global__ void __launch_bounds__(NT + 32) k_distill(const DistillArgs g, int* status) {
   constexpr int kVec = Elem<T>::kVec;
   extern __shared__ __align__(16) uint8_t members[];  // a bit per element of vector i in byte i - part's first
-  __shared__ DistillShared sh;
+  __shared__ TotalsShared totals;
+  __shared__ TeacherStats shared_stats;
   grid_dependency_sync();
   release_dependents();
   const int ctas = static_cast<int>(ptx::cluster_nctarank()), rank = static_cast<int>(ptx::cluster_ctarank());
   if (ctas > 1) ptx::cluster_arrive();
   const int64_t r = blockIdx.x / ctas;
   const int tid = threadIdx.x, vocab = g.v.vocab;
+  const bool teacher = tid >= NT;
   const float c = g.v.c, inv_t = g.v.inv_t;
   const Row<T> row(static_cast<T*>(const_cast<void*>(g.v.logits)) + r * g.v.ld, vocab, status, NSM_KERNEL_DISTILL);
   const Part part = part_of(row, rank, ctas);
   // head is vector begin - 1 and tail vector end: the part's vectors from `base` on
   const int base = part.head >= 0 ? part.head : part.begin;
   const int bytes = (part.tail >= 0 ? part.tail + 1 : part.end) - base;
-  for (int i = tid; i < (bytes + 15) / 16; i += kVocabThreads) reinterpret_cast<uint4*>(members)[i] = make_uint4(0, 0, 0, 0);
-  const Teacher t = read_teacher<T>(g, r, row, sh);  // has barriers
-  if (t.mine >= 0 && in_part(row, part, t.mine)) {
-    const int at = t.mine + row.lead, i = at / kVec - base;
-    atomicOr(reinterpret_cast<uint32_t*>(members) + i / 4, 1u << (8 * (i & 3) + at % kVec));
+  Entries e;
+  Sums a;
+  if (teacher) load_entries(e, g, r);
+  else
+    for (int i = tid; i < (bytes + 15) / 16; i += NT) reinterpret_cast<uint4*>(members)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  if (teacher) {
+#pragma unroll
+    for (int u = 0; u < kLaneEntries; ++u) {
+      if (e.v[u] >= 0 && in_part(row, part, e.v[u])) {
+        const int at = e.v[u] + row.lead, i = at / kVec - base;
+        atomicOr(reinterpret_cast<uint32_t*>(members) + i / 4, 1u << (8 * (i & 3) + at % kVec));
+      }
+    }
   }
   __syncthreads();
-
-  // the student: the row outside the entries, and the entries
-  Sums a;
-  for_vectors(row, part, [&](int i, const uint4& raw) {
-    const uint32_t bits = members[i - base];
-    uint4 v = raw;
-    if (bits) vec_mask<T>(v, bits);
-    add_vec<T, false>(a, v, i, c);
-  });
-  const Totals outside = row_totals<false>(a, c, sh.rest, ctas);
-  Sums b;
-  if (t.mine >= 0 && t.x != kNegInf) {  // one term, relative to itself (a NaN stays one)
-    b.ref = b.limit = b.max = t.x;
-    b.s = make_pair(t.x - t.x + 1.f, 0.f);
+  if (teacher) {
+    load_logits(e, row);
+    const TeacherStats t = teacher_stats<true>(e, g);
+    if (tid == NT) shared_stats = t;
+  } else {  // the student outside the entries
+    for_vectors<NT>(row, part, [&](int i, const uint4& raw) {
+      const uint32_t bits = members[i - base];
+      uint4 v = raw;
+      if (bits) vec_mask<T>(v, bits);
+      add_vec<T, false>(a, v, i, c);
+    });
   }
-  const Totals inside = row_totals<false>(b, c, sh.entries, 1);
-  Totals all{fmaxf(outside.max, inside.max), outside.s, 0.f};
-  float inside_s = inside.s, none = 0.f;
-  rebase<false>(all.s, none, outside.max, all.max, c);
-  rebase<false>(inside_s, none, inside.max, all.max, c);
-  all.s += inside_s;
-  const bool empty = all.max == kNegInf && all.s == 0.f;
-  const bool no_rest = outside.max == kNegInf && outside.s == 0.f;
-  const float lse_ref = empty ? 0.f : all.max, lse_log = empty ? 0.f : logf(all.s);
-  const float rest_ref = no_rest ? 0.f : outside.max;
-  const float rest = no_rest ? kNegInf : (outside.max - lse_ref) * inv_t + (logf(outside.s) - lse_log);
-  if (g.loss || g.lse || g.rest) {
-    const float log_q = (t.x - lse_ref) * inv_t - lse_log;
-    const float p_rest = rest == kNegInf ? 0.f : t.p_rest;
-    float loss = block_sum(t.p > 0.f || t.p != t.p ? t.p * (t.log_p - log_q) : 0.f, sh.sum);
-    if (p_rest > 0.f || p_rest != p_rest) loss += p_rest * (logf(p_rest) - rest);
-    if (rank == 0 && tid == 0) {
-      if (g.loss) g.loss[r] = t.any ? loss : 0.f;
-      if (g.lse) g.lse[r] = empty ? kNegInf : lse_ref * inv_t + lse_log;
-      if (g.rest) g.rest[r] = rest;
-    }
-  }
+  const Totals outside = row_totals<false, NT>(a, c, totals, ctas);
+  const TeacherStats t = shared_stats;
+  const Student st = student_of(t, outside, c, inv_t);
+  if (teacher && rank == 0) write_loss(g, r, e, t, st);
   if constexpr (GRAD) {
     const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, NSM_KERNEL_DISTILL);
-    const float w = g.d_loss ? g.d_loss[r] : 1.f;
-    if (empty || !t.any || w == 0.f) {
-      zero_part(out, rank, ctas);
-      return;
+    const EntryGradient k = entry_gradient(t, st, g.d_loss ? g.d_loss[r] : 1.f, g.tail, inv_t);
+    if (!teacher) {
+      if (k.zero) zero_part<NT>(out, rank, ctas);
+      else
+        for_vectors<NT>(row, part, [&](int i, const uint4& raw) {
+          out.store(row.first(i), gradient_vec<T, false>(raw, k.ref, c, k.log2_s, k.scale, 0.f));
+        });
     }
-    const EntryGradient k = entry_gradient(t, w, g.tail, lse_ref, lse_log, rest_ref, no_rest ? 0.f : log2f(outside.s), rest, inv_t);
-    store_entry_gradients(row, out, part, t, k, c);
+    __syncthreads();
+    if (teacher && !k.zero) store_entries(row, out, part, e, st, k, inv_t);
   }
 }
 
+// Forward and backward in one pass over memory, as k_logprobs_resident.
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs g, int* status) {
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  __shared__ TotalsShared totals;
+  __shared__ TeacherStats shared_stats;
+  __shared__ SlabShared slab_shared;
+  __shared__ uint64_t ready[kSlabChunks];
+  grid_dependency_sync();
+  release_dependents();
+  const int ctas = static_cast<int>(ptx::cluster_nctarank()), rank = static_cast<int>(ptx::cluster_ctarank());
+  if (ctas > 1) ptx::cluster_arrive();
+  const int64_t r = blockIdx.x / ctas;
+  const int tid = threadIdx.x, vocab = g.v.vocab;
+  const bool teacher = tid >= NT;
+  const float c = g.v.c, inv_t = g.v.inv_t;
+  const Row<T> row(static_cast<T*>(const_cast<void*>(g.v.logits)) + r * g.v.ld, vocab, status, NSM_KERNEL_DISTILL);
+  const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, NSM_KERNEL_DISTILL);
+  const Part part = part_of(row, rank, ctas);
+  if (tid < kSlabChunks) ptx::mbar_init(ptx::smem_u32(&ready[tid]), 1);
+  Slab<T, NT> slab;
+  slab.start(row, part, reinterpret_cast<uint4*>(dynamic), &slab_shared);  // ends with a barrier
+  Entries e;
+  Sums a;
+  if (teacher) {
+    load_entries(e, g, r);
+    // what other blocks of the cluster hold of the row comes from memory
+    T elsewhere[kLaneEntries];
+#pragma unroll
+    for (int u = 0; u < kLaneEntries; ++u)
+      if (e.v[u] >= 0 && !in_part(row, part, e.v[u])) elsewhere[u] = row.p[e.v[u]];
+    // The entries leave the sums outside them: chunk by chunk as it arrives, their logits are
+    // taken and -inf goes in their place.
+    for (int q = 0; q < kSlabChunks; ++q) {
+      slab.wait(q);
+      uint32_t mine = 0;
+#pragma unroll
+      for (int u = 0; u < kLaneEntries; ++u) {
+        if (e.v[u] < 0) continue;
+        const int at = (e.v[u] + row.lead) / Elem<T>::kVec;
+        if ((at >= part.begin + q * slab.each && at < min(part.end, part.begin + (q + 1) * slab.each)) ||
+            (q == 0 && (at == part.head || at == part.tail))) {
+          e.x[u] = Elem<T>::to_float(reinterpret_cast<T*>(slab.v)[e.v[u] + row.lead - slab.base * Elem<T>::kVec]);
+          mine |= 1u << u;
+        }
+      }
+      __syncwarp();  // equal tokens have all read
+#pragma unroll
+      for (int u = 0; u < kLaneEntries; ++u)
+        if (mine >> u & 1)
+          reinterpret_cast<T*>(slab.v)[e.v[u] + row.lead - slab.base * Elem<T>::kVec] = Elem<T>::from_float(kNegInf);
+      __syncwarp();
+      if (tid == NT) ptx::mbar_arrive(ptx::smem_u32(&ready[q]));
+    }
+#pragma unroll
+    for (int u = 0; u < kLaneEntries; ++u)
+      if (e.v[u] >= 0 && !in_part(row, part, e.v[u])) e.x[u] = Elem<T>::to_float(elsewhere[u]);
+    const TeacherStats t = teacher_stats<true>(e, g);
+    if (tid == NT) shared_stats = t;
+  } else {
+    auto add = [&](int i, const uint4& raw) { add_vec<T, false>(a, raw, i, c); };
+#pragma unroll 1
+    for (int q = 0; q < kSlabChunks; ++q) {
+      slab.wait(q);
+      slab.wait_on(&ready[q]);
+      slab.chunk(q, add);
+      if (q == 0) slab.ragged(add);
+    }
+  }
+  const Totals outside = row_totals<false, NT>(a, c, totals, ctas);
+  const TeacherStats t = shared_stats;
+  const Student st = student_of(t, outside, c, inv_t);
+  const EntryGradient k = entry_gradient(t, st, g.d_loss ? g.d_loss[r] : 1.f, g.tail, inv_t);
+  if (teacher) {
+    if (rank == 0) write_loss(g, r, e, t, st);
+  } else if (k.zero) {
+    zero_part<NT>(out, rank, ctas);
+  } else {
+    slab.all([&](int i, const uint4& raw) {
+      out.store(row.first(i), gradient_vec<T, false>(raw, k.ref, c, k.log2_s, k.scale, 0.f));
+    });
+  }
+  __syncthreads();
+  if (teacher && !k.zero) store_entries(row, out, part, e, st, k, inv_t);
+  slab.drain();
+}
+
 // The backward pass alone, in pieces of rows.
-template <typename T>
-__global__ void __launch_bounds__(kVocabThreads, 6) k_distill_backward(const DistillArgs g, int pieces, int* status) {
-  __shared__ DistillShared sh;
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT + 32) k_distill_backward(const DistillArgs g, int pieces, int* status) {
+  __shared__ TeacherStats shared_stats;
   grid_dependency_sync();
   release_dependents();
   const int vocab = g.v.vocab;
+  const float c = g.v.c, inv_t = g.v.inv_t;
+  const bool teacher = threadIdx.x >= NT;
   const int64_t total = g.v.rows * pieces;
   for (int64_t work = blockIdx.x; work < total; work += gridDim.x) {
     const int64_t r = work / pieces;
     const int piece = static_cast<int>(work - r * pieces);
     const Row<T> row(static_cast<T*>(const_cast<void*>(g.v.logits)) + r * g.v.ld, vocab, status, NSM_KERNEL_DISTILL);
     const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, NSM_KERNEL_DISTILL);
+    const Part part = part_of(row, piece, pieces);
     const float w = g.d_loss ? g.d_loss[r] : 1.f;
     const float lse = g.in_lse[r], rest = g.tail ? g.in_rest[r] : 0.f;
     if (w == 0.f || lse == kNegInf) {
-      zero_part(out, piece, pieces);
+      if (!teacher) zero_part<NT>(out, piece, pieces);
       continue;
     }
-    const Teacher t = read_teacher<T>(g, r, row, sh);
-    if (!t.any) {
-      zero_part(out, piece, pieces);
-    } else {
-      const EntryGradient k = entry_gradient(t, w, g.tail, lse * g.v.t, 0.f, rest == kNegInf ? 0.f : (lse + rest) * g.v.t, 0.f,
-                                             rest, g.v.inv_t);
-      store_entry_gradients(row, out, part_of(row, piece, pieces), t, k, g.v.c);
+    const Student st{lse * g.v.t, 0.f, rest == kNegInf ? 0.f : (lse + rest) * g.v.t, 0.f, rest, false};
+    Entries e;
+    if (teacher) {
+      load_entries(e, g, r);
+      load_logits(e, row);
+      const TeacherStats t = teacher_stats<false>(e, g);
+      if (threadIdx.x == NT) shared_stats = t;
     }
-    __syncthreads();  // sh is free again
+    __syncthreads();
+    const TeacherStats t = shared_stats;
+    const EntryGradient k = entry_gradient(t, st, w, g.tail, inv_t);
+    if (!teacher) {
+      if (k.zero) zero_part<NT>(out, piece, pieces);
+      else
+        for_vectors<NT>(row, part, [&](int i, const uint4& raw) {
+          out.store(row.first(i), gradient_vec<T, false>(raw, k.ref, c, k.log2_s, k.scale, 0.f));
+        });
+    }
+    __syncthreads();  // and shared_stats is free again
+    if (teacher && !k.zero) store_entries(row, out, part, e, st, k, inv_t);
   }
 }
 
@@ -1088,17 +1419,31 @@ __global__ void __launch_bounds__(kVocabThreads, 6) k_distill_backward(const Dis
 
 // CTAs per row: where there are fewer rows than the GPU takes blocks at a time, a cluster
 // shares each row, down to two vectors of a thread.
-int cluster_for(int64_t rows, int nvec) {
+int cluster_for(int64_t rows, int nvec, int NT) {
   int ctas = 1;
-  while (ctas < kMaxCluster && rows * ctas < 4 * 152 && nvec >= ctas * 4 * kVocabThreads) ctas *= 2;
+  while (ctas < kMaxCluster && rows * ctas * NT < 1024 * 152 && nvec >= ctas * 4 * NT) ctas *= 2;
   return ctas;
 }
 
 // Pieces per row of a backward pass: `most` vectors each, less where rows are few.
-int pieces_for(int64_t rows, int nvec, int most) {
+int pieces_for(int64_t rows, int nvec, int most, int least) {
   int each = most;
-  while (each > kVocabThreads && rows * ((nvec + each - 1) / each) < 8 * 152) each /= 2;
+  while (each > least && rows * ((nvec + each - 1) / each) < 8 * 152) each /= 2;
   return (nvec + each - 1) / each;
+}
+
+constexpr int kResidentThreads = 256;
+constexpr size_t kSlabBytes = 76 << 10, kSlabMost = 216 << 10;
+
+size_t slab_bytes(int nvec, int ctas) { return (static_cast<size_t>((nvec + ctas - 1) / ctas) + 2) * 16; }
+
+// CTAs per row that keep it in shared memory, 0 where it does not fit.
+int resident_for(int64_t rows, int nvec) {
+  int ctas = 1;
+  while (ctas < kMaxCluster && slab_bytes(nvec, ctas) > kSlabBytes) ctas *= 2;
+  if (slab_bytes(nvec, ctas) > kSlabMost) return 0;
+  while (ctas < kMaxCluster && rows * ctas * kResidentThreads < 1024 * 152 && nvec >= ctas * 4 * kResidentThreads) ctas *= 2;
+  return ctas;
 }
 
 template <typename T>
@@ -1107,14 +1452,14 @@ int vectors_of(int vocab) {
 }
 
 template <typename... K, typename... A>
-cudaError_t launch_clusters(void (*kernel)(K...), int64_t grid, int ctas, size_t smem, cudaStream_t stream, A... args) {
+cudaError_t launch_clusters(void (*kernel)(K...), int threads, int64_t grid, int ctas, size_t smem, cudaStream_t stream, A... args) {
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kVocabThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -1138,39 +1483,56 @@ template <typename T>
 cudaError_t launch_logprobs_t(const LogprobArgs& a, int* status, cudaStream_t stream) {
   const int nvec = vectors_of<T>(a.v.vocab);
   if (a.in_lse) {
-    const int pieces = pieces_for(a.v.rows, nvec, 4 * kVocabThreads);
+    constexpr int kThreads = 256;
+    const int pieces = pieces_for(a.v.rows, nvec, 4 * kThreads, kThreads);
     const int64_t grid = std::min<int64_t>(a.v.rows * pieces, 1 << 30);
-    return launch_clusters(a.d_entropy ? k_logprobs_backward<T, true> : k_logprobs_backward<T, false>, grid, 1, 0, stream, a,
-                           pieces, status);
+    return launch_clusters(a.d_entropy ? k_logprobs_backward<T, true, kThreads> : k_logprobs_backward<T, false, kThreads>,
+                           kThreads, grid, 1, 0, stream, a, pieces, status);
   }
-  const int ctas = cluster_for(a.v.rows, nvec);
+  if (a.v.d_logits) {
+    if (const int ctas = resident_for(a.v.rows, nvec))
+      return launch_clusters(a.d_entropy || a.entropy ? k_logprobs_resident<T, true, kResidentThreads>
+                                                      : k_logprobs_resident<T, false, kResidentThreads>,
+                             kResidentThreads, a.v.rows * ctas, ctas, slab_bytes(nvec, ctas), stream, a, status);
+  }
+  const int threads = a.v.d_logits || a.k > 0 ? 256 : 128;
+  const int ctas = cluster_for(a.v.rows, nvec, threads);
   const int64_t grid = a.v.rows * ctas;
   if (a.v.d_logits)
     return launch_clusters(a.d_entropy || a.entropy ? k_logprobs<T, true, false, true> : k_logprobs<T, false, false, true>,
-                           grid, ctas, 0, stream, a, 0, status);
+                           threads, grid, ctas, 0, stream, a, 0, status);
   if (a.k == 0)
-    return launch_clusters(a.entropy ? k_logprobs<T, true, false, false> : k_logprobs<T, false, false, false>, grid, ctas, 0,
-                           stream, a, 0, status);
-  const int batches = ((nvec + ctas - 1) / ctas + 4 * kVocabThreads - 1) / (4 * kVocabThreads);
+    return launch_clusters(a.entropy ? k_logprobs<T, true, false, false> : k_logprobs<T, false, false, false>, threads, grid,
+                           ctas, 0, stream, a, 0, status);
+  const int batches = ((nvec + ctas - 1) / ctas + 4 * kTopThreads - 1) / (4 * kTopThreads);
   int shift = 0;
   while (((batches + (1 << shift) - 1) >> shift) > kTopGroups) ++shift;
   const size_t smem = (ctas > 1 ? size_t(ctas) * a.k * 8 : 0) +
-                      size_t((batches + (1 << shift) - 1) >> shift) * kVocabThreads * sizeof(typename TopGroups<T>::Key);
-  return launch_clusters(a.entropy ? k_logprobs<T, true, true, false> : k_logprobs<T, false, true, false>, grid, ctas, smem,
-                         stream, a, shift, status);
+                      size_t((batches + (1 << shift) - 1) >> shift) * kTopThreads * sizeof(typename TopGroups<T>::Key);
+  return launch_clusters(a.entropy ? k_logprobs<T, true, true, false> : k_logprobs<T, false, true, false>, threads, grid, ctas,
+                         smem, stream, a, shift, status);
 }
 
 template <typename T>
 cudaError_t launch_distill_t(const DistillArgs& a, int* status, cudaStream_t stream) {
   const int nvec = vectors_of<T>(a.v.vocab);
   if (a.in_lse) {
-    const int pieces = pieces_for(a.v.rows, nvec, 16 * kVocabThreads);
+    constexpr int kThreads = 256;
+    const int pieces = pieces_for(a.v.rows, nvec, 16 * kThreads, kThreads);
     const int64_t grid = std::min<int64_t>(a.v.rows * pieces, 1 << 30);
-    return launch_clusters(k_distill_backward<T>, grid, 1, 0, stream, a, pieces, status);
+    return launch_clusters(k_distill_backward<T, kThreads>, kThreads + 32, grid, 1, 0, stream, a, pieces, status);
   }
-  const int ctas = cluster_for(a.v.rows, nvec);
+  if (a.v.d_logits) {
+    if (const int ctas = resident_for(a.v.rows, nvec))
+      return launch_clusters(k_distill_resident<T, kResidentThreads>, kResidentThreads + 32, a.v.rows * ctas, ctas,
+                             slab_bytes(nvec, ctas), stream, a, status);
+  }
+  constexpr int kThreads = 128, kGradThreads = 256;
+  const int threads = a.v.d_logits ? kGradThreads : kThreads;
+  const int ctas = cluster_for(a.v.rows, nvec, threads);
   const size_t smem = (static_cast<size_t>((nvec + ctas - 1) / ctas) + 2 + 15) / 16 * 16;
-  return launch_clusters(a.v.d_logits ? k_distill<T, true> : k_distill<T, false>, a.v.rows * ctas, ctas, smem, stream, a, status);
+  return launch_clusters(a.v.d_logits ? k_distill<T, true, kGradThreads> : k_distill<T, false, kThreads>, threads + 32,
+                         a.v.rows * ctas, ctas, smem, stream, a, status);
 }
 
 }  // namespace

@@ -36,6 +36,7 @@ constexpr float kRefSlack = 16.f;
 constexpr float kLog2Floor = -200.f;
 constexpr int kTopCandidates = 1024;
 constexpr int kMaxCluster = 8;
+constexpr uint64_t kWaitNs = 2000000000ull;  // a wait's limit
 
 // Two fp32 values in one 64-bit register: add, multiply and fused multiply-add of both are
 // one instruction each.
@@ -216,6 +217,11 @@ struct Row {
     vec_mask<T>(raw, none);
     return raw;
   }
+  // writes vector i, which is whole
+  __device__ __forceinline__ void store_whole(int i, const uint4& raw) const {
+    if (!bounds_ok(whole(i) && (reinterpret_cast<uintptr_t>(p + first(i)) & 15) == 0, status, kernel, 0, NSM_SITE_GRADIENT)) return;
+    *reinterpret_cast<uint4*>(p + first(i)) = raw;
+  }
   // writes kVec gradients whose first element is e0 of the row, as one 16-byte store where
   // the vector is whole and aligned
   __device__ __forceinline__ void store(int e0, const uint4& raw) const {
@@ -254,7 +260,7 @@ __device__ __forceinline__ Part part_of(const Row<T>& row, int piece, int pieces
   return part;
 }
 
-// use(i, vector) for every vector of the part that this thread has, four loads in flight;
+// use(i, vector, whole) for every vector of the part that this thread has, four loads in flight;
 // done(n) after the n-th four of them (the ragged ones come last and are not counted).
 template <int NT, typename T, typename F, typename D>
 __device__ __forceinline__ void for_batches(const Row<T>& row, const Part& part, F&& use, D&& done) {
@@ -264,7 +270,7 @@ __device__ __forceinline__ void for_batches(const Row<T>& row, const Part& part,
 #pragma unroll
     for (int u = 0; u < 4; ++u) raw[u] = row.load_whole(i + u * NT);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) use(i + u * NT, raw[u]);
+    for (int u = 0; u < 4; ++u) use(i + u * NT, raw[u], true);
     done(n);
   }
   if (i < part.end) {  // three at most, their loads together too
@@ -274,11 +280,11 @@ __device__ __forceinline__ void for_batches(const Row<T>& row, const Part& part,
       if (i + u * NT < part.end) raw[u] = row.load_whole(i + u * NT);
 #pragma unroll
     for (int u = 0; u < 3; ++u)
-      if (i + u * NT < part.end) use(i + u * NT, raw[u]);
+      if (i + u * NT < part.end) use(i + u * NT, raw[u], true);
     done(n);
   }
-  if (part.head >= 0 && threadIdx.x == kHeadThread) use(part.head, row.load(part.head));
-  if (part.tail >= 0 && threadIdx.x == kTailThread) use(part.tail, row.load(part.tail));
+  if (part.head >= 0 && threadIdx.x == kHeadThread) use(part.head, row.load(part.head), false);
+  if (part.tail >= 0 && threadIdx.x == kTailThread) use(part.tail, row.load(part.tail), false);
 }
 
 template <int NT, typename T, typename F>
@@ -296,23 +302,21 @@ __device__ __forceinline__ void zero_part(const Row<T>& out, int piece, int piec
 }
 
 // A sum of exponentials s = sum 2^y, y = (x - ref) c, with sum y 2^y (both in two halves, one
-// per element of a pair), the largest x and the vector where this thread met it first.
+// per element of a pair), and the largest x.  (x - ref) c and not x c - ref c in one fused step:
+// the latter needs a correction for its rounding and a second way for the types' lowest values,
+// which cost more than the step saves (8192 x 8000 bf16, loss and gradient: 75 us for 62).
 struct Sums {
   float ref = 0.f, limit = kNegInf;  // no reference yet: every finite logit exceeds the limit
   Pair s = 0, sy = 0;
   float max = kNegInf;
-  int max_vec = -1;
 };
 
 // Adds a vector; its largest element.
 template <typename T, bool ENT>
-__device__ __forceinline__ float add_vec(Sums& a, const uint4& raw, int i, float c) {
+__device__ __forceinline__ float add_vec(Sums& a, const uint4& raw, float c) {
   constexpr int kPairs = Elem<T>::kVec / 2;
   const float m = Elem<T>::largest(raw);
-  if (m > a.max) {
-    a.max = m;
-    a.max_vec = i;
-  }
+  a.max = fmaxf(a.max, m);
   if (m > a.limit) {
     if (a.limit != kNegInf) {  // move what is there to the new reference
       const float d = (a.ref - m) * c, r = ex2(d);
@@ -374,29 +378,47 @@ __device__ __forceinline__ Totals warp_totals(const Sums& a, float c) {
 }
 
 // The totals of every CTA's threads of a cluster relative to the row's largest logit, the
-// same in every thread: warps, then CTAs, in a fixed order.  With more than one CTA, each has
-// arrived at the cluster's barrier before; the next use of `sh` needs a barrier.  Every thread
-// of the block calls this, the sums of the first NT count.
+// same in every thread: warps, then CTAs, in a fixed order.  Every thread of the block calls
+// this, the sums of the first NT count; the next use of `sh` needs a barrier.  The CTAs
+// exchange theirs through a barrier in shared memory that counts one arrival from each: only
+// the threads that send wait for their stores, not the whole block.  With more than one CTA,
+// start_totals comes first.
 struct TotalsShared {
   Totals warp[kMaxWarps];
   Totals cta[kMaxCluster];
+  uint64_t joined;
+  int abort;
 };
+__device__ __forceinline__ void start_totals(TotalsShared& sh, int ctas) {
+  if (ctas == 1) return;
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(ptx::smem_u32(&sh.joined), ctas);
+    sh.abort = 0;
+    ptx::fence_mbarrier_init();
+  }
+  __syncwarp();
+  ptx::cluster_arrive();  // the wait is in row_totals: by then every CTA runs
+}
 template <bool ENT, int NT>
-__device__ __forceinline__ Totals row_totals(const Sums& a, float c, TotalsShared& sh, int ctas) {
+__device__ __forceinline__ Totals row_totals(const Sums& a, float c, TotalsShared& sh, int ctas, int* status, int kernel) {
   const Totals w = warp_totals<ENT>(a, c);
   if ((threadIdx.x & 31) == 0 && threadIdx.x < NT) sh.warp[threadIdx.x >> 5] = w;
+  if (ctas > 1) ptx::cluster_wait();
   __syncthreads();
   const Totals v = sh.warp[threadIdx.x & (NT / 32 - 1)];
   const Totals mine = group_totals<ENT, NT / 32>(v.max, v.max, v.s, v.sy, c);
   if (ctas == 1) return mine;
-  ptx::cluster_wait();  // every CTA runs (they arrived when they started)
   if (static_cast<int>(threadIdx.x) < ctas) {
     const uint32_t to = ptx::mapa_shared(ptx::smem_u32(&sh.cta[ptx::cluster_ctarank()]), threadIdx.x);
     ptx::st_cluster_f32(to, mine.max);
     ptx::st_cluster_f32(to + 4, mine.s);
     ptx::st_cluster_f32(to + 8, mine.sy);
+    ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&sh.joined), threadIdx.x));
   }
-  ptx::cluster_sync();
+  if (!ptx::mbar_wait_bounded_cluster(ptx::smem_u32(&sh.joined), 0, &sh.abort, kWaitNs)) {
+    record_timeout(status, kernel, NSM_ROLE_EPILOGUE, NSM_SITE_ACC_FULL);
+    *static_cast<volatile int*>(&sh.abort) = 1;
+  }
   Totals t{kNegInf, 0.f, 0.f};
   for (int r = 0; r < ctas; ++r) t.max = fmaxf(t.max, sh.cta[r].max);
   for (int r = 0; r < ctas; ++r) {
@@ -457,6 +479,19 @@ struct TopShared {
   uint32_t bound_key, bound_tie_top;
   int32_t bound_vec, nlist, ncand;
   uint32_t taken[kMaxCluster];                // how many keys each CTA gave
+};
+
+// A thread's largest logit and the vector where it met it first.
+template <typename T>
+struct TopMax {
+  float max = kNegInf;
+  int max_vec = -1;
+  __device__ __forceinline__ void see(float m, int i) {
+    if (m > max) {
+      max = m;
+      max_vec = i;
+    }
+  }
 };
 
 // The largest logit of every group of a thread's batches: which groups can hold one of the
@@ -585,7 +620,7 @@ __device__ __forceinline__ void place_keys(const uint64_t* keys, int n, int k, F
 // The k largest logits of the block's part of a row, from every thread's largest one and
 // where it met it: put(place, key), and the number of places that were filled.
 template <typename T, typename F>
-__device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, const Sums& a, const TopGroups<T>& groups, int k,
+__device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, const TopMax<T>& a, const TopGroups<T>& groups, int k,
                                         TopShared& sh, F&& put) {
   constexpr int kVec = Elem<T>::kVec;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -642,7 +677,7 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
   uint64_t last = ~0ull;
   for (int j = 0; j < k; ++j) {
     uint64_t best = 0;
-    for_vectors<kTopThreads>(row, part, [&](int i, const uint4& raw) {
+    for_vectors<kTopThreads>(row, part, [&](int i, const uint4& raw, bool) {
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
         const uint64_t fk = full_key(vec_get<T>(raw, e), row.first(i) + e);
@@ -668,7 +703,7 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
 
 // The row's k largest logits: of the block's part, or gathered from the cluster's parts.
 template <typename T>
-__device__ __forceinline__ void row_top(const Row<T>& row, const Part& part, const Sums& a, const TopGroups<T>& groups, int k,
+__device__ __forceinline__ void row_top(const Row<T>& row, const Part& part, const TopMax<T>& a, const TopGroups<T>& groups, int k,
                                         float max, float inv_t, float log_s, float* out_value, int32_t* out_index, TopShared& sh,
                                         uint64_t* gathered, int ctas) {
   auto write = [&](int place, uint64_t key) {
@@ -709,7 +744,6 @@ __device__ __forceinline__ void row_top(const Row<T>& row, const Part& part, con
 // by bulk copies in chunks, each with a barrier of its own, so that the pass over the first
 // runs while the others arrive; the ragged ones by plain loads of the threads that have them.
 constexpr int kSlabChunks = 4;
-constexpr uint64_t kSlabWaitNs = 2000000000ull;
 struct SlabShared {
   uint64_t full[kSlabChunks];
   int abort;
@@ -731,7 +765,7 @@ struct Slab {
     status = row.status;
     kernel = row.kernel;
     base = part.head >= 0 ? part.head : part.begin;
-    each = (part.end - part.begin + kSlabChunks * NT - 1) / (kSlabChunks * NT) * NT;
+    each = max(2, (part.end - part.begin + kSlabChunks * NT - 1) / (kSlabChunks * NT)) * NT;
     if (threadIdx.x == 0) {
 #pragma unroll
       for (int q = 0; q < kSlabChunks; ++q) ptx::mbar_init(ptx::smem_u32(&sh->full[q]), 1);
@@ -757,7 +791,7 @@ struct Slab {
   // Until a barrier's first phase is over.  After a wait that ran out (recorded) the block goes on with
   // what is there, so that every barrier is still met; drain() then waits once more.
   __device__ __forceinline__ void wait_on(uint64_t* bar) const {
-    if (!ptx::mbar_wait_bounded(ptx::smem_u32(bar), 0, &sh->abort, kSlabWaitNs)) {
+    if (!ptx::mbar_wait_bounded(ptx::smem_u32(bar), 0, &sh->abort, kWaitNs)) {
       record_timeout(status, kernel, NSM_ROLE_PRODUCER, NSM_SITE_STAGE_FULL);
       sh->abort = 1;
     }
@@ -767,17 +801,17 @@ struct Slab {
   __device__ __forceinline__ void chunk(int q, F&& use) const {
     const int b = min(part.end, part.begin + q * each), e = min(part.end, b + each);
 #pragma unroll 2
-    for (int i = b + static_cast<int>(threadIdx.x); i < e; i += NT) use(i, v[i - base]);
+    for (int i = b + static_cast<int>(threadIdx.x); i < e; i += NT) use(i, v[i - base], true);
   }
   template <typename F>
   __device__ __forceinline__ void ragged(F&& use) const {
-    if (part.head >= 0 && threadIdx.x == kHeadThread) use(part.head, v[part.head - base]);
-    if (part.tail >= 0 && threadIdx.x == kTailThread) use(part.tail, v[part.tail - base]);
+    if (part.head >= 0 && threadIdx.x == kHeadThread) use(part.head, v[part.head - base], false);
+    if (part.tail >= 0 && threadIdx.x == kTailThread) use(part.tail, v[part.tail - base], false);
   }
   template <typename F>
   __device__ __forceinline__ void all(F&& use) const {
 #pragma unroll 2
-    for (int i = part.begin + static_cast<int>(threadIdx.x); i < part.end; i += NT) use(i, v[i - base]);
+    for (int i = part.begin + static_cast<int>(threadIdx.x); i < part.end; i += NT) use(i, v[i - base], true);
     ragged(use);
   }
   // Before the block ends: no copy into its shared memory may be in flight.
@@ -786,7 +820,7 @@ struct Slab {
     int never = 0;
     if (threadIdx.x == 0) {
       for (int q = 0; q < kSlabChunks; ++q)
-        if (!ptx::mbar_wait_bounded(ptx::smem_u32(&sh->full[q]), 0, &never, kSlabWaitNs)) break;
+        if (!ptx::mbar_wait_bounded(ptx::smem_u32(&sh->full[q]), 0, &never, kWaitNs)) break;
     }
     __syncthreads();
   }
@@ -794,38 +828,85 @@ struct Slab {
 
 // ---------------------------------------------------------------- log probabilities
 
-// What the gradient pass of a row needs: q (ca + cb log2 q) / ..., and the token's own value.
+// A row's statistics from its totals: log q_v = (x_v - ref) / t - log_s.
+struct RowLogprob {
+  float ref, log_s, log2_s, entropy;
+  bool empty;
+};
+
+template <bool ENT>
+__device__ __forceinline__ RowLogprob row_logprob(const Totals& t, float inv_t) {
+  RowLogprob s;
+  s.empty = t.max == kNegInf && t.s == 0.f;  // a row of NaN has a NaN sum
+  s.ref = s.empty ? 0.f : t.max;
+  s.log_s = s.empty ? 0.f : logf(t.s);
+  s.log2_s = s.empty ? 0.f : log2f(t.s);
+  s.entropy = 0.f;
+  if (ENT && !s.empty) {
+    s.entropy = s.log_s - kLn2 * (t.sy / t.s);
+    if (s.entropy < 0.f) s.entropy = 0.f;
+  }
+  return s;
+}
+
+// One thread writes the row's numbers.
+template <bool ENT>
+__device__ __forceinline__ void write_logprob(const LogprobArgs& g, int64_t r, const RowLogprob& s, int token, float x_token,
+                                              float inv_t) {
+  if (g.lse) g.lse[r] = s.empty ? kNegInf : s.ref * inv_t + s.log_s;
+  if (ENT && g.entropy) g.entropy[r] = s.entropy;
+  if (g.logprob) g.logprob[r] = token < 0 ? 0.f : (s.empty ? kNegInf : (x_token - s.ref) * inv_t - s.log_s);
+}
+
+// What the gradient pass of a row needs: q (ca + cb log2 q), and the token's own value.
 struct TokenGradient {
-  float ref, log2_s, ca, cb, at_token;
+  float ref, log2_s, ca, cb;
   bool zero;
 };
 
-// w logprob + h entropy: d/dx = (w (1[token] - q) - h q (log q + entropy)) / t
-__device__ __forceinline__ TokenGradient token_gradient(float w, float h, float ref, float log_s, float log2_s,
-                                                        float entropy, float x_token, bool empty, float inv_t) {
+// w logprob + h entropy: d/dx = (w (1[token] - q) - h q (log q + entropy)) / t.  low: what the
+// reference lost to rounding.
+__device__ __forceinline__ TokenGradient token_gradient(float w, float h, const RowLogprob& s, float low, float c, float inv_t) {
   TokenGradient k;
-  k.zero = empty || (w == 0.f && h == 0.f);
-  k.ref = ref;
-  k.log2_s = log2_s;
-  k.ca = -(w + h * entropy) * inv_t;
+  k.zero = s.empty || (w == 0.f && h == 0.f);
+  k.ref = s.ref;
+  k.log2_s = fmaf(low, c, s.log2_s);
+  k.ca = -(w + h * s.entropy) * inv_t;
   k.cb = -h * kLn2 * inv_t;
-  k.at_token = 0.f;
-  const float log_q = (x_token - ref) * inv_t - log_s;
-  // at the token 1 - q without cancellation; 0 where it is masked
-  if (log_q != kNegInf) k.at_token = -(w * expm1f(log_q) + (h == 0.f ? 0.f : h * expf(log_q) * (log_q + entropy))) * inv_t;
   return k;
 }
 
-template <typename T, bool ENT>
-__device__ __forceinline__ void store_token_gradient(const Row<T>& out, int e0, const uint4& raw, const TokenGradient& k,
-                                                     int token, float c) {
-  uint4 grad = gradient_vec<T, ENT>(raw, k.ref, c, k.log2_s, k.ca, k.cb);
-  if (token >= e0 && token < e0 + Elem<T>::kVec) {
-#pragma unroll
-    for (int e = 0; e < Elem<T>::kVec; ++e)
-      if (e0 + e == token) vec_set<T>(grad, e, k.at_token);
-  }
-  out.store(e0, grad);
+// The gradient at the token itself: 1 - q without cancellation; 0 where it is masked.
+__device__ __forceinline__ float gradient_at_token(float w, float h, const RowLogprob& s, float low, float x_token, float inv_t) {
+  const float log_q = ((x_token - s.ref) - low) * inv_t - s.log_s;
+  if (log_q == kNegInf) return 0.f;
+  return -(w * expm1f(log_q) + (h == 0.f ? 0.f : h * expf(log_q) * (log_q + s.entropy))) * inv_t;
+}
+
+// The gradients of the vectors that each(use) gives this thread, and then the token's own over
+// what was written there (at_token()), by the thread that wrote it (`mine`).  same: gradient and logits are
+// aligned alike, so that whole vectors are whole 16-byte stores.
+template <typename T, bool ENT, typename E, typename F>
+__device__ __forceinline__ void store_token_gradients(const Row<T>& row, const Row<T>& out, const Part& part, const TokenGradient& k,
+                                                      int token, bool mine, float c, E&& each, F&& at_token) {
+  const bool same = row.lead == out.lead;
+  each([&](int i, const uint4& raw, bool whole) {
+    const uint4 grad = gradient_vec<T, ENT>(raw, k.ref, c, k.log2_s, k.ca, k.cb);
+    if (whole && same) out.store_whole(i, grad);
+    else out.store(row.first(i), grad);
+  });
+  if (mine && bounds_ok(token >= 0 && token < out.vocab, out.status, out.kernel, 0, NSM_SITE_GRADIENT))
+    out.p[token] = Elem<T>::from_float(at_token());
+}
+
+// Whether thread `tid` of NT has the vector that holds element v (v < 0: no).
+template <int NT, typename T>
+__device__ __forceinline__ bool owns(const Row<T>& row, const Part& part, int v) {
+  if (v < 0) return false;
+  const int at = (v + row.lead) / Elem<T>::kVec, tid = threadIdx.x;
+  if (at == part.head) return tid == kHeadThread;
+  if (at == part.tail) return tid == kTailThread;
+  return at >= part.begin && at < part.end && (at - part.begin) % NT == tid;
 }
 
 // A cluster of CTAs per row (one CTA where there are rows enough).  TOP: dynamic shared
@@ -838,7 +919,7 @@ __global__ void __launch_bounds__(NT, TOP ? 6 : 1280 / NT) k_logprobs(const Logp
   grid_dependency_sync();
   release_dependents();
   const int ctas = static_cast<int>(ptx::cluster_nctarank()), rank = static_cast<int>(ptx::cluster_ctarank());
-  if (ctas > 1) ptx::cluster_arrive();
+  start_totals(totals, ctas);
   const int64_t r = blockIdx.x / ctas;
   const int vocab = g.v.vocab;
   const float c = g.v.c, inv_t = g.v.inv_t;
@@ -850,50 +931,46 @@ __global__ void __launch_bounds__(NT, TOP ? 6 : 1280 / NT) k_logprobs(const Logp
   uint64_t* gathered = reinterpret_cast<uint64_t*>(dynamic);
   TopGroups<T> groups{reinterpret_cast<typename TopGroups<T>::Key*>(gathered + (ctas > 1 ? ctas * g.k : 0)), group_shift, kNegInf};
   Sums a;
+  TopMax<T> seen;
   for_batches<NT>(row, part,
-              [&](int i, const uint4& raw) {
-                const float m = add_vec<T, ENT>(a, raw, i, c);
-                if (TOP) groups.running = fmaxf(groups.running, m);
+              [&](int i, const uint4& raw, bool) {
+                const float m = add_vec<T, ENT>(a, raw, c);
+                if (TOP) {
+                  seen.see(m, i);
+                  groups.running = fmaxf(groups.running, m);
+                }
               },
               [&](int n) {
                 if (TOP) groups.batch(n);
               });
-  const Totals t = row_totals<ENT, NT>(a, c, totals, ctas);
-  const bool empty = t.max == kNegInf && t.s == 0.f;  // a row of NaN has a NaN sum
-  const float ref = empty ? 0.f : t.max, log_s = empty ? 0.f : logf(t.s);
-  float entropy = 0.f;
-  if (ENT && !empty) {
-    entropy = log_s - kLn2 * (t.sy / t.s);
-    if (entropy < 0.f) entropy = 0.f;
-  }
-  if (rank == 0 && threadIdx.x == 0) {
-    if (g.lse) g.lse[r] = empty ? kNegInf : ref * inv_t + log_s;
-    if (ENT && g.entropy) g.entropy[r] = entropy;
-    if (g.logprob) g.logprob[r] = token < 0 ? 0.f : (empty ? kNegInf : (x_token - ref) * inv_t - log_s);
-  }
+  const Totals t = row_totals<ENT, NT>(a, c, totals, ctas, status, NSM_KERNEL_LOGPROBS);
+  const RowLogprob s = row_logprob<ENT>(t, inv_t);
+  if (rank == 0 && threadIdx.x == 0) write_logprob<ENT>(g, r, s, token, x_token, inv_t);
   if constexpr (GRAD) {
     const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, NSM_KERNEL_LOGPROBS);
     const float w = g.d_logprob && token >= 0 ? g.d_logprob[r] : 0.f;
     const float h = ENT && g.d_entropy ? g.d_entropy[r] : 0.f;
-    const TokenGradient k = token_gradient(w, h, ref, log_s, empty ? 0.f : log2f(t.s), entropy, x_token, empty, inv_t);
+    const TokenGradient k = token_gradient(w, h, s, 0.f, c, inv_t);
     if (k.zero) {
       zero_part<NT>(out, rank, ctas);
     } else {
-      for_vectors<NT>(row, part, [&](int i, const uint4& raw) { store_token_gradient<T, ENT>(out, row.first(i), raw, k, token, c); });
+      store_token_gradients<T, ENT>(row, out, part, k, token, owns<NT>(row, part, token), c,
+                                    [&](auto&& use) { for_vectors<NT>(row, part, use); },
+                                    [&] { return gradient_at_token(w, h, s, 0.f, x_token, inv_t); });
     }
   }
   if constexpr (TOP) {
     float* value = g.top_logprob + r * g.k;
     int32_t* index = g.top_index + r * g.k;
-    if (log_s != log_s) {  // NaN or +inf in the row
+    if (s.log_s != s.log_s) {  // NaN or +inf in the row
       if (rank == 0) {
         for (int j = threadIdx.x; j < g.k; j += NT) {
-          value[j] = log_s;
+          value[j] = s.log_s;
           index[j] = -1;
         }
       }
     } else {
-      row_top<T>(row, part, a, groups, g.k, ref, inv_t, log_s, value, index, top, gathered, ctas);
+      row_top<T>(row, part, seen, groups, g.k, s.ref, inv_t, s.log_s, value, index, top, gathered, ctas);
     }
   }
 }
@@ -908,7 +985,7 @@ __global__ void __launch_bounds__(NT) k_logprobs_resident(const LogprobArgs g, i
   grid_dependency_sync();
   release_dependents();
   const int ctas = static_cast<int>(ptx::cluster_nctarank()), rank = static_cast<int>(ptx::cluster_ctarank());
-  if (ctas > 1) ptx::cluster_arrive();
+  start_totals(totals, ctas);
   const int64_t r = blockIdx.x / ctas;
   const int vocab = g.v.vocab;
   const float c = g.v.c, inv_t = g.v.inv_t;
@@ -922,31 +999,22 @@ __global__ void __launch_bounds__(NT) k_logprobs_resident(const LogprobArgs g, i
   const float w = g.d_logprob && token >= 0 ? g.d_logprob[r] : 0.f;
   const float h = ENT && g.d_entropy ? g.d_entropy[r] : 0.f;
   Sums a;
-  auto add = [&](int i, const uint4& raw) { add_vec<T, ENT>(a, raw, i, c); };
+  auto add = [&](int, const uint4& raw, bool) { add_vec<T, ENT>(a, raw, c); };
   slab.ragged(add);
 #pragma unroll 1
   for (int q = 0; q < kSlabChunks; ++q) {
     slab.wait(q);
     slab.chunk(q, add);
   }
-  const Totals t = row_totals<ENT, NT>(a, c, totals, ctas);
-  const bool empty = t.max == kNegInf && t.s == 0.f;
-  const float ref = empty ? 0.f : t.max, log_s = empty ? 0.f : logf(t.s);
-  float entropy = 0.f;
-  if (ENT && !empty) {
-    entropy = log_s - kLn2 * (t.sy / t.s);
-    if (entropy < 0.f) entropy = 0.f;
-  }
-  if (rank == 0 && threadIdx.x == 0) {
-    if (g.lse) g.lse[r] = empty ? kNegInf : ref * inv_t + log_s;
-    if (ENT && g.entropy) g.entropy[r] = entropy;
-    if (g.logprob) g.logprob[r] = token < 0 ? 0.f : (empty ? kNegInf : (x_token - ref) * inv_t - log_s);
-  }
-  const TokenGradient k = token_gradient(w, h, ref, log_s, empty ? 0.f : log2f(t.s), entropy, x_token, empty, inv_t);
+  const Totals t = row_totals<ENT, NT>(a, c, totals, ctas, status, NSM_KERNEL_LOGPROBS);
+  const RowLogprob s = row_logprob<ENT>(t, inv_t);
+  if (rank == 0 && threadIdx.x == 0) write_logprob<ENT>(g, r, s, token, x_token, inv_t);
+  const TokenGradient k = token_gradient(w, h, s, 0.f, c, inv_t);
   if (k.zero) {
     zero_part<NT>(out, rank, ctas);
   } else {
-    slab.all([&](int i, const uint4& raw) { store_token_gradient<T, ENT>(out, row.first(i), raw, k, token, c); });
+    store_token_gradients<T, ENT>(row, out, slab.part, k, token, owns<NT>(row, slab.part, token), c, [&](auto&& use) { slab.all(use); },
+                                  [&] { return gradient_at_token(w, h, s, 0.f, x_token, inv_t); });
   }
   slab.drain();
 }
@@ -969,20 +1037,20 @@ __global__ void __launch_bounds__(NT, 6) k_logprobs_backward(const LogprobArgs g
     const float w = g.d_logprob && token >= 0 ? g.d_logprob[r] : 0.f;
     const float h = ENT && g.d_entropy ? g.d_entropy[r] : 0.f;
     const float lse = g.in_lse[r];
-    const bool empty = lse == kNegInf;
-    if (empty || (w == 0.f && h == 0.f)) {
+    const float ref = lse * g.v.t, low = fmaf(lse, g.v.t, -ref);
+    const RowLogprob s{ref, 0.f, 0.f, ENT && g.d_entropy ? g.in_entropy[r] : 0.f, lse == kNegInf};
+    if (s.empty || (w == 0.f && h == 0.f)) {
       zero_part<NT>(out, piece, pieces);
       continue;
     }
     // in place, another block may have written the token's own gradient already: only the
-    // block that has the token's vector needs its logit, and reads it before it writes
+    // thread that has the token's vector reads its logit, before it writes there
     const Part part = part_of(row, piece, pieces);
-    const int at = token < 0 ? -2 : (token + row.lead) / Elem<T>::kVec;
-    const bool here = (at >= part.begin && at < part.end) || at == part.head || at == part.tail;
-    const float x_token = here ? Elem<T>::to_float(row.p[token]) : kNegInf;
-    const TokenGradient k = token_gradient(w, h, lse * g.v.t, 0.f, 0.f, ENT ? g.in_entropy[r] : 0.f, x_token, empty, inv_t);
-    __syncthreads();  // every thread has read the token's logit
-    for_vectors<NT>(row, part, [&](int i, const uint4& raw) { store_token_gradient<T, ENT>(out, row.first(i), raw, k, token, c); });
+    const bool mine = owns<NT>(row, part, token);
+    const float x_token = mine ? Elem<T>::to_float(row.p[token]) : kNegInf;
+    const TokenGradient k = token_gradient(w, h, s, low, c, inv_t);
+    store_token_gradients<T, ENT>(row, out, part, k, token, mine, c, [&](auto&& use) { for_vectors<NT>(row, part, use); },
+                                  [&] { return gradient_at_token(w, h, s, low, x_token, inv_t); });
   }
 }
 
@@ -1043,12 +1111,10 @@ __device__ __forceinline__ void load_logits(Entries& e, const Row<T>& row) {
     if (e.v[u] >= 0) e.x[u] = Elem<T>::to_float(row.p[e.v[u]]);
 }
 
-// Of equal tokens the first counts; then the teacher's probabilities and, for the forward pass
-// (INSIDE), the student's sum.
-template <bool INSIDE>
+// Of equal tokens the first counts; then the teacher's probabilities (the student is not asked
+// yet: while its row is on the way).
 __device__ __forceinline__ TeacherStats teacher_stats(Entries& e, const DistillArgs& g) {
   const int lane = threadIdx.x & 31;
-  const float c = g.v.c;
 #pragma unroll
   for (int u = kLaneEntries - 1; u >= 0; --u) {  // later groups first: earlier ones are whole
     if (32 * u >= g.k) continue;
@@ -1060,7 +1126,6 @@ __device__ __forceinline__ TeacherStats teacher_stats(Entries& e, const DistillA
 #pragma unroll 8
       for (int l = 0; l < 32; ++l)
         if (__shfl_sync(~0u, e.v[w], l) == v) v = -1;
-    if (v < 0) e.x[u] = e.log_p[u] = kNegInf;
     e.v[u] = v;
   }
 #pragma unroll
@@ -1112,7 +1177,11 @@ __device__ __forceinline__ TeacherStats teacher_stats(Entries& e, const DistillA
 #pragma unroll
   for (int u = 0; u < kLaneEntries; ++u) e.p[u] = expf(e.log_p[u]);
   t.inside = Totals{kNegInf, 0.f, 0.f};
-  if (!INSIDE) return t;
+  return t;
+}
+
+// The student's sum over the entries that count.
+__device__ __forceinline__ Totals inside_totals(const Entries& e, float c) {
   float max = kNegInf, s = 0.f;
 #pragma unroll
   for (int u = 0; u < kLaneEntries; ++u) max = fmaxf(max, e.x[u]);
@@ -1120,15 +1189,16 @@ __device__ __forceinline__ TeacherStats teacher_stats(Entries& e, const DistillA
 #pragma unroll
   for (int u = 0; u < kLaneEntries; ++u)
     if (!(e.x[u] == kNegInf)) s += max == kNegInf ? e.x[u] : ex2((e.x[u] - max) * c);  // a NaN stays one
-  t.inside = Totals{max, warp_sum(s), 0.f};
-  return t;
+  return Totals{max, warp_sum(s), 0.f};
 }
 
 // The student's row: log q_v = (x_v - lse_ref) / t - lse_log,
-// q_v / q_rest = 2^((x_v - rest_ref) c - rest_log2), rest = log q_rest.
+// rest = log q_rest, with rest_ref where the sum outside the entries stands.
+// *_low: what the references lost to rounding.
 struct Student {
-  float lse_ref, lse_log, rest_ref, rest_log2, rest;
+  float lse_ref, lse_log, rest_ref, rest;
   bool empty;
+  float lse_low, rest_low;
 };
 
 __device__ __forceinline__ Student student_of(const TeacherStats& t, const Totals& outside, float c, float inv_t) {
@@ -1138,12 +1208,12 @@ __device__ __forceinline__ Student student_of(const TeacherStats& t, const Total
   rebase<false>(inside_s, none, t.inside.max, all.max, c);
   all.s += inside_s;
   Student st;
+  st.lse_low = st.rest_low = 0.f;
   st.empty = all.max == kNegInf && all.s == 0.f;
   const bool no_rest = outside.max == kNegInf && outside.s == 0.f;
   st.lse_ref = st.empty ? 0.f : all.max;
   st.lse_log = st.empty ? 0.f : logf(all.s);
   st.rest_ref = no_rest ? 0.f : outside.max;
-  st.rest_log2 = no_rest ? 0.f : log2f(outside.s);
   st.rest = no_rest ? kNegInf : (outside.max - st.lse_ref) * inv_t + (logf(outside.s) - st.lse_log);
   return st;
 }
@@ -1173,21 +1243,36 @@ struct EntryGradient {
   bool zero;
 };
 
-__device__ __forceinline__ EntryGradient entry_gradient(const TeacherStats& t, const Student& s, float w, int tail, float inv_t) {
+// From the sums outside the entries; what the threads of the dense pass need.
+__device__ __forceinline__ EntryGradient entry_gradient(const TeacherStats& t, const Totals& outside, float w, int tail, float c,
+                                                        float inv_t) {
+  float all_max = fmaxf(outside.max, t.inside.max), out_s = outside.s, in_s = t.inside.s, none = 0.f;
+  rebase<false>(out_s, none, outside.max, all_max, c);
+  rebase<false>(in_s, none, t.inside.max, all_max, c);
+  const float all_s = out_s + in_s;
+  const bool empty = all_max == kNegInf && all_s == 0.f, no_rest = outside.max == kNegInf && outside.s == 0.f;
+  EntryGradient k;
+  k.zero = empty || !t.any || w == 0.f;
+  const float p_rest = no_rest ? 0.f : t.p_rest;
+  k.excess = tail ? p_rest - t.lacking : 0.f;
+  k.unit = w * inv_t;
+  k.ref = tail ? outside.max : all_max;
+  k.log2_s = log2f(tail ? outside.s : all_s);
+  k.scale = tail ? k.unit * (out_s / all_s * (1.f + k.excess) - p_rest) : k.unit;
+  if (tail && no_rest) k.ref = k.log2_s = k.scale = 0.f;  // nothing is there
+  return k;
+}
+// From the statistics that the forward pass left.
+__device__ __forceinline__ EntryGradient entry_gradient(const TeacherStats& t, const Student& s, float w, int tail, float c,
+                                                        float inv_t) {
   EntryGradient k;
   k.zero = s.empty || !t.any || w == 0.f;
   const float p_rest = s.rest == kNegInf ? 0.f : t.p_rest;
   k.excess = tail ? p_rest - t.lacking : 0.f;
   k.unit = w * inv_t;
-  if (tail) {
-    k.ref = s.rest_ref;
-    k.log2_s = s.rest_log2;
-    k.scale = s.rest == kNegInf ? 0.f : k.unit * (expf(s.rest) * (1.f + k.excess) - p_rest);
-  } else {
-    k.ref = s.lse_ref;
-    k.log2_s = s.lse_log * (1.f / kLn2);
-    k.scale = k.unit;
-  }
+  k.ref = tail ? s.rest_ref : s.lse_ref;
+  k.log2_s = (tail ? s.rest_low : s.lse_low) * c;
+  k.scale = !tail ? k.unit : s.rest == kNegInf ? 0.f : k.unit * (expf(s.rest) * (1.f + k.excess) - p_rest);
   return k;
 }
 
@@ -1195,6 +1280,14 @@ template <typename T>
 __device__ __forceinline__ bool in_part(const Row<T>& row, const Part& part, int v) {
   const int at = (v + row.lead) / Elem<T>::kVec;
   return (at >= part.begin && at < part.end) || at == part.head || at == part.tail;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_dense(const Row<T>& row, const Row<T>& out, int i, const uint4& raw, bool whole,
+                                            const EntryGradient& k, float c) {
+  const uint4 grad = gradient_vec<T, false>(raw, k.ref, c, k.log2_s, k.scale, 0.f);
+  if (whole && row.lead == out.lead) out.store_whole(i, grad);
+  else out.store(row.first(i), grad);
 }
 
 // The teacher's warp writes the gradients at the entries of the block's part, over what the
@@ -1205,7 +1298,7 @@ __device__ __forceinline__ void store_entries(const Row<T>& row, const Row<T>& o
 #pragma unroll
   for (int u = 0; u < kLaneEntries; ++u) {
     if (e.v[u] < 0 || !in_part(row, part, e.v[u])) continue;
-    const float log_q = (e.x[u] - s.lse_ref) * inv_t - s.lse_log, p = e.p[u];
+    const float log_q = ((e.x[u] - s.lse_ref) - s.lse_low) * inv_t - s.lse_log, p = e.p[u];
     float grad = 0.f;
     if (log_q != kNegInf) {  // q - p without cancellation
       const float q = expf(log_q);
@@ -1226,7 +1319,7 @@ __global__ void __launch_bounds__(NT + 32) k_distill(const DistillArgs g, int* s
   grid_dependency_sync();
   release_dependents();
   const int ctas = static_cast<int>(ptx::cluster_nctarank()), rank = static_cast<int>(ptx::cluster_ctarank());
-  if (ctas > 1) ptx::cluster_arrive();
+  start_totals(totals, ctas);
   const int64_t r = blockIdx.x / ctas;
   const int tid = threadIdx.x, vocab = g.v.vocab;
   const bool teacher = tid >= NT;
@@ -1253,29 +1346,33 @@ __global__ void __launch_bounds__(NT + 32) k_distill(const DistillArgs g, int* s
   }
   __syncthreads();
   if (teacher) {
+    TeacherStats t = teacher_stats(e, g);
     load_logits(e, row);
-    const TeacherStats t = teacher_stats<true>(e, g);
+    t.inside = inside_totals(e, c);
     if (tid == NT) shared_stats = t;
   } else {  // the student outside the entries
-    for_vectors<NT>(row, part, [&](int i, const uint4& raw) {
+    for_vectors<NT>(row, part, [&](int i, const uint4& raw, bool) {
       const uint32_t bits = members[i - base];
       uint4 v = raw;
       if (bits) vec_mask<T>(v, bits);
-      add_vec<T, false>(a, v, i, c);
+      add_vec<T, false>(a, v, c);
     });
   }
-  const Totals outside = row_totals<false, NT>(a, c, totals, ctas);
+  const Totals outside = row_totals<false, NT>(a, c, totals, ctas, status, NSM_KERNEL_DISTILL);
   const TeacherStats t = shared_stats;
-  const Student st = student_of(t, outside, c, inv_t);
-  if (teacher && rank == 0) write_loss(g, r, e, t, st);
+  Student st;
+  if (teacher) {
+    st = student_of(t, outside, c, inv_t);
+    if (rank == 0) write_loss(g, r, e, t, st);
+  }
   if constexpr (GRAD) {
     const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, NSM_KERNEL_DISTILL);
-    const EntryGradient k = entry_gradient(t, st, g.d_loss ? g.d_loss[r] : 1.f, g.tail, inv_t);
+    const EntryGradient k = entry_gradient(t, outside, g.d_loss ? g.d_loss[r] : 1.f, g.tail, c, inv_t);
     if (!teacher) {
       if (k.zero) zero_part<NT>(out, rank, ctas);
       else
-        for_vectors<NT>(row, part, [&](int i, const uint4& raw) {
-          out.store(row.first(i), gradient_vec<T, false>(raw, k.ref, c, k.log2_s, k.scale, 0.f));
+        for_vectors<NT>(row, part, [&](int i, const uint4& raw, bool whole) {
+          store_dense(row, out, i, raw, whole, k, c);
         });
     }
     __syncthreads();
@@ -1294,7 +1391,7 @@ __global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs 
   grid_dependency_sync();
   release_dependents();
   const int ctas = static_cast<int>(ptx::cluster_nctarank()), rank = static_cast<int>(ptx::cluster_ctarank());
-  if (ctas > 1) ptx::cluster_arrive();
+  start_totals(totals, ctas);
   const int64_t r = blockIdx.x / ctas;
   const int tid = threadIdx.x, vocab = g.v.vocab;
   const bool teacher = tid >= NT;
@@ -1305,10 +1402,12 @@ __global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs 
   if (tid < kSlabChunks) ptx::mbar_init(ptx::smem_u32(&ready[tid]), 1);
   Slab<T, NT> slab;
   slab.start(row, part, reinterpret_cast<uint4*>(dynamic), &slab_shared);  // ends with a barrier
+  const float w = g.d_loss ? g.d_loss[r] : 1.f;
   Entries e;
   Sums a;
   if (teacher) {
     load_entries(e, g, r);
+    TeacherStats t = teacher_stats(e, g);
     // what other blocks of the cluster hold of the row comes from memory
     T elsewhere[kLaneEntries];
 #pragma unroll
@@ -1329,7 +1428,6 @@ __global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs 
           mine |= 1u << u;
         }
       }
-      __syncwarp();  // equal tokens have all read
 #pragma unroll
       for (int u = 0; u < kLaneEntries; ++u)
         if (mine >> u & 1)
@@ -1340,10 +1438,10 @@ __global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs 
 #pragma unroll
     for (int u = 0; u < kLaneEntries; ++u)
       if (e.v[u] >= 0 && !in_part(row, part, e.v[u])) e.x[u] = Elem<T>::to_float(elsewhere[u]);
-    const TeacherStats t = teacher_stats<true>(e, g);
+    t.inside = inside_totals(e, c);
     if (tid == NT) shared_stats = t;
   } else {
-    auto add = [&](int i, const uint4& raw) { add_vec<T, false>(a, raw, i, c); };
+    auto add = [&](int, const uint4& raw, bool) { add_vec<T, false>(a, raw, c); };
 #pragma unroll 1
     for (int q = 0; q < kSlabChunks; ++q) {
       slab.wait(q);
@@ -1352,17 +1450,17 @@ __global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs 
       if (q == 0) slab.ragged(add);
     }
   }
-  const Totals outside = row_totals<false, NT>(a, c, totals, ctas);
+  const Totals outside = row_totals<false, NT>(a, c, totals, ctas, status, NSM_KERNEL_DISTILL);
   const TeacherStats t = shared_stats;
-  const Student st = student_of(t, outside, c, inv_t);
-  const EntryGradient k = entry_gradient(t, st, g.d_loss ? g.d_loss[r] : 1.f, g.tail, inv_t);
+  const EntryGradient k = entry_gradient(t, outside, w, g.tail, c, inv_t);
+  Student st;
   if (teacher) {
+    st = student_of(t, outside, c, inv_t);
     if (rank == 0) write_loss(g, r, e, t, st);
   } else if (k.zero) {
     zero_part<NT>(out, rank, ctas);
   } else {
-    slab.all([&](int i, const uint4& raw) {
-      out.store(row.first(i), gradient_vec<T, false>(raw, k.ref, c, k.log2_s, k.scale, 0.f));
+    slab.all([&](int i, const uint4& raw, bool whole) { store_dense(row, out, i, raw, whole, k, c);
     });
   }
   __syncthreads();
@@ -1392,22 +1490,28 @@ __global__ void __launch_bounds__(NT + 32) k_distill_backward(const DistillArgs 
       if (!teacher) zero_part<NT>(out, piece, pieces);
       continue;
     }
-    const Student st{lse * g.v.t, 0.f, rest == kNegInf ? 0.f : (lse + rest) * g.v.t, 0.f, rest, false};
+    Student st{lse * g.v.t, 0.f, 0.f, rest, false, 0.f, 0.f};
+    st.lse_low = fmaf(lse, g.v.t, -st.lse_ref);
+    if (rest != kNegInf) {
+      const float sum = lse + rest, b = sum - lse;
+      st.rest_ref = sum * g.v.t;
+      st.rest_low = fmaf(sum, g.v.t, -st.rest_ref) + ((lse - (sum - b)) + (rest - b)) * g.v.t;
+    }
     Entries e;
     if (teacher) {
       load_entries(e, g, r);
-      load_logits(e, row);
-      const TeacherStats t = teacher_stats<false>(e, g);
+      const TeacherStats t = teacher_stats(e, g);
+      load_logits(e, row);  // of entries that count, in time for store_entries
       if (threadIdx.x == NT) shared_stats = t;
     }
     __syncthreads();
     const TeacherStats t = shared_stats;
-    const EntryGradient k = entry_gradient(t, st, w, g.tail, inv_t);
+    const EntryGradient k = entry_gradient(t, st, w, g.tail, c, inv_t);
     if (!teacher) {
       if (k.zero) zero_part<NT>(out, piece, pieces);
       else
-        for_vectors<NT>(row, part, [&](int i, const uint4& raw) {
-          out.store(row.first(i), gradient_vec<T, false>(raw, k.ref, c, k.log2_s, k.scale, 0.f));
+        for_vectors<NT>(row, part, [&](int i, const uint4& raw, bool whole) {
+          store_dense(row, out, i, raw, whole, k, c);
         });
     }
     __syncthreads();  // and shared_stats is free again
@@ -1432,18 +1536,32 @@ int pieces_for(int64_t rows, int nvec, int most, int least) {
   return (nvec + each - 1) / each;
 }
 
-constexpr int kResidentThreads = 256;
-constexpr size_t kSlabBytes = 76 << 10, kSlabMost = 216 << 10;
+#ifndef NSM_SLAB
+#define NSM_SLAB 76
+#endif
+#ifndef NSM_RT
+#define NSM_RT 0
+#endif
+#ifndef NSM_PER
+#define NSM_PER 8
+#endif
+constexpr size_t kSlabBytes = NSM_SLAB << 10, kSlabMost = 216 << 10;
 
 size_t slab_bytes(int nvec, int ctas) { return (static_cast<size_t>((nvec + ctas - 1) / ctas) + 2) * 16; }
 
-// CTAs per row that keep it in shared memory, 0 where it does not fit.
-int resident_for(int64_t rows, int nvec) {
-  int ctas = 1;
-  while (ctas < kMaxCluster && slab_bytes(nvec, ctas) > kSlabBytes) ctas *= 2;
-  if (slab_bytes(nvec, ctas) > kSlabMost) return 0;
-  while (ctas < kMaxCluster && rows * ctas * kResidentThreads < 1024 * 152 && nvec >= ctas * 4 * kResidentThreads) ctas *= 2;
-  return ctas;
+// Threads and CTAs per row that keep it in shared memory; ctas 0 where it does not fit.
+struct Resident {
+  int threads, ctas;
+};
+Resident resident_for(int64_t rows, int nvec) {
+  Resident r{256, 1};
+  while (r.ctas < kMaxCluster && slab_bytes(nvec, r.ctas) > kSlabBytes) r.ctas *= 2;
+  if (slab_bytes(nvec, r.ctas) > kSlabMost) return Resident{0, 0};
+  if (NSM_RT) r.threads = NSM_RT;
+  else
+    while (r.threads > 64 && nvec < r.threads * NSM_PER) r.threads /= 2;
+  while (r.ctas < kMaxCluster && rows * r.ctas * r.threads < 1024 * 152 && nvec >= r.ctas * 4 * r.threads) r.ctas *= 2;
+  return r;
 }
 
 template <typename T>
@@ -1490,10 +1608,14 @@ cudaError_t launch_logprobs_t(const LogprobArgs& a, int* status, cudaStream_t st
                            kThreads, grid, 1, 0, stream, a, pieces, status);
   }
   if (a.v.d_logits) {
-    if (const int ctas = resident_for(a.v.rows, nvec))
-      return launch_clusters(a.d_entropy || a.entropy ? k_logprobs_resident<T, true, kResidentThreads>
-                                                      : k_logprobs_resident<T, false, kResidentThreads>,
-                             kResidentThreads, a.v.rows * ctas, ctas, slab_bytes(nvec, ctas), stream, a, status);
+    const Resident r = resident_for(a.v.rows, nvec);
+    if (r.ctas) {
+      const bool ent = a.d_entropy || a.entropy;
+      auto* kernel = r.threads == 64    ? (ent ? k_logprobs_resident<T, true, 64> : k_logprobs_resident<T, false, 64>)
+                     : r.threads == 128 ? (ent ? k_logprobs_resident<T, true, 128> : k_logprobs_resident<T, false, 128>)
+                                        : (ent ? k_logprobs_resident<T, true, 256> : k_logprobs_resident<T, false, 256>);
+      return launch_clusters(kernel, r.threads, a.v.rows * r.ctas, r.ctas, slab_bytes(nvec, r.ctas), stream, a, status);
+    }
   }
   const int threads = a.v.d_logits || a.k > 0 ? 256 : 128;
   const int ctas = cluster_for(a.v.rows, nvec, threads);
@@ -1523,9 +1645,13 @@ cudaError_t launch_distill_t(const DistillArgs& a, int* status, cudaStream_t str
     return launch_clusters(k_distill_backward<T, kThreads>, kThreads + 32, grid, 1, 0, stream, a, pieces, status);
   }
   if (a.v.d_logits) {
-    if (const int ctas = resident_for(a.v.rows, nvec))
-      return launch_clusters(k_distill_resident<T, kResidentThreads>, kResidentThreads + 32, a.v.rows * ctas, ctas,
-                             slab_bytes(nvec, ctas), stream, a, status);
+    const Resident r = resident_for(a.v.rows, nvec);
+    if (r.ctas) {
+      auto* kernel = r.threads == 64    ? k_distill_resident<T, 64>
+                     : r.threads == 128 ? k_distill_resident<T, 128>
+                                        : k_distill_resident<T, 256>;
+      return launch_clusters(kernel, r.threads + 32, a.v.rows * r.ctas, r.ctas, slab_bytes(nvec, r.ctas), stream, a, status);
+    }
   }
   constexpr int kThreads = 128, kGradThreads = 256;
   const int threads = a.v.d_logits ? kGradThreads : kThreads;

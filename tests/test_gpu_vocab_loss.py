@@ -387,6 +387,99 @@ def test_distill_entries(nsm, k, tail):
     check_distill(nsm, x[:, :100], "fp32", k, 1.0, tail, "fp16" if not tail else "fp32", seed=k)
 
 
+RING = [("bf16", 50257, 640, 0), ("fp16", 100003, 320, 1), ("fp32", 33001, 640, 3), ("fp32", 70001, 320, 0),
+        ("bf16", 131072, 330, 0), ("bf16", 262147, 100, 5), ("bf16", 40000, 700, 8)]
+
+
+@pytest.mark.parametrize("dtype,vocab,rows,pad", RING)
+@pytest.mark.parametrize("op", ["logprobs", "entropy", "distill", "tail"])
+def test_gradients_of_many_long_rows(nsm, dtype, vocab, rows, pad, op):
+    # rows enough to go round the GPU, each too long for several to a block's shared memory:
+    # against the oracle for some of every kind of row, and every row's numbers
+    base = make_rows(vocab, 16, vocab)
+    order = np.arange(rows) % 16
+    buf = torch.full((rows * (vocab + pad) + 8,), float("nan"), dtype=TYPES[dtype], device="cuda")
+    logits = buf[3:3 + rows * (vocab + pad)].view(rows, vocab + pad)[:, :vocab]
+    logits.copy_(torch.from_numpy(base).to(TYPES[dtype]).cuda()[torch.from_numpy(order).cuda()])
+    # rows differ by one logit each
+    spot = torch.arange(rows, device="cuda") * 131 % vocab
+    alive = ~torch.isinf(logits[torch.arange(rows, device="cuda"), spot])
+    logits[torch.arange(rows, device="cuda")[alive], spot[alive]] += 1.0
+    rng = np.random.default_rng(vocab)
+    w = rng.normal(size=rows).astype(np.float32)
+    w[::11] = 0.0
+    weight = torch.from_numpy(w).cuda()
+    t = 1.1
+    sample = sorted({0, rows - 1, *range(rows // 2, rows // 2 + 8), *rng.integers(0, rows, 6).tolist()})
+    seen = logits[sample].double().cpu().numpy()
+    o = outputs(rows)
+    g = torch.full_like(logits, float("nan"))
+    e = e_of(vocab)
+    q, log_q = softmax(seen, t)
+    if op in ("logprobs", "entropy"):
+        tokens = make_tokens(vocab, rows, vocab)
+        h = (rng.normal(size=rows) * 0.2).astype(np.float32) if op == "entropy" else None
+        d_h = torch.from_numpy(h).cuda() if h is not None else None
+        tk = torch.from_numpy(tokens).cuda()
+        nsm.logprobs_grad(logits, tk, weight, d_h, g, o["logprob"], o["entropy"], o["lse"], temperature=t)
+        fwd = ref.logprobs(seen, tokens[sample], t)
+        close(o["logprob"][sample], fwd["logprob"], 2 * e + 4 * U * finite(fwd["logprob"]), "logprob")
+        close(o["entropy"][sample], fwd["entropy"], 2 * e * (1 + finite(fwd["entropy"])), "entropy")
+        want = ref.logprobs_grad(seen, tokens[sample], w[sample], None if h is None else h[sample], t)
+        scale = (np.abs(w[sample]) + (0 if h is None else np.abs(h[sample]) * (1 + finite(fwd["entropy"])))) / t
+        close(g[sample], want, gradient_tolerance(dtype, vocab, want, scale, q, log_q, tokens[sample]), "gradient")
+        alone = torch.empty(rows, device="cuda")
+        nsm.logprobs(logits, tk, alone, temperature=t)
+        close(o["logprob"], alone.double().cpu().numpy(), 4 * e + 8 * U * finite(alone.double().cpu().numpy()), "logprob")
+        back = torch.full_like(logits, float("nan"))
+        nsm.logprobs_backward(logits, tk, o["lse"], o["entropy"], weight, d_h, back, temperature=t)
+        again = torch.full_like(logits, float("nan"))
+        nsm.logprobs_grad(logits, tk, weight, d_h, again, temperature=t)
+        nsm.logprobs_grad(logits, tk, weight, d_h, logits, temperature=t)
+    else:
+        tail = op == "tail"
+        z16, index16 = make_entries(7, base, 40, t, tail)
+        z, index = z16[order], index16[order]
+        teacher, ix = torch.from_numpy(z).float().cuda(), torch.from_numpy(index).cuda()
+        z = teacher.double().cpu().numpy()
+        nsm.distill_grad(logits, teacher, ix, weight, g, o["loss"], o["lse"], o["rest"], temperature=t, tail=tail)
+        fwd = ref.distill(seen, z[sample], index[sample], t, tail)
+        logs = finite(fwd["lse"]) + finite(seen).max(axis=1) / t + 40
+        tol = 4 * e + 8 * U * logs * (1 if tail else 2) + 4 * U * finite(fwd["loss"])
+        close(o["loss"][sample], fwd["loss"], tol, "loss")
+        want = ref.distill_grad(seen, z[sample], index[sample], w[sample], t, tail)
+        p = np.zeros_like(q)
+        for j, r in enumerate(sample):
+            tok, pr, _, p_rest, some = ref._teacher(seen[j], z[r], index[r], t, tail)
+            if some:
+                p[j, tok] = pr
+                if tail and np.isfinite(fwd["rest"][j]):
+                    out = np.ones(vocab, dtype=bool)
+                    out[tok] = False
+                    p[j, out] += p_rest * np.exp(log_q[j, out] - fwd["rest"][j])
+        rel = 2 * e + 4 * U * (finite(log_q) + logs[:, None])
+        tol = (np.abs(w[sample]) / t)[:, None] * (q + p) * rel + 1.01 * STEP[dtype] * finite(want) + SMALLEST[dtype]
+        close(g[sample], want, tol, "gradient")
+        alone = torch.empty(rows, device="cuda")
+        nsm.distill(logits, teacher, ix, alone, temperature=t, tail=tail)
+        ref_loss = alone.double().cpu().numpy()
+        span = 40 + float(logits.float()[torch.isfinite(logits)].abs().max()) / t
+        close(o["loss"], ref_loss, 8 * e + 32 * U * span * 2 + 8 * U * finite(ref_loss), "loss")
+        back = torch.full_like(logits, float("nan"))
+        nsm.distill_backward(logits, teacher, ix, o["lse"], o["rest"] if tail else None, weight, back, temperature=t, tail=tail)
+        again = torch.full_like(logits, float("nan"))
+        nsm.distill_grad(logits, teacher, ix, weight, again, temperature=t, tail=tail)
+        nsm.distill_grad(logits, teacher, ix, weight, logits, temperature=t, tail=tail)
+    assert torch.equal(again, g)  # the same bits again
+    assert torch.equal(logits, g)  # and in place
+    # every row against the backward pass alone, whose statistics carry their own rounding: a
+    # step of the type and the statistics' error on values of at most the row's weight
+    far = (back.float() - g.float()).abs()
+    lse_size = 8 * e + 16 * U * (float(o["lse"][torch.isfinite(o["lse"])].abs().max()) + 40)
+    allowed = 2.1 * STEP[dtype] * g.float().abs() + lse_size * (2 * weight.abs() / t + 1)[:, None] * 2 + 2 * SMALLEST[dtype]
+    assert bool((far <= allowed).all())
+
+
 def test_distill_without_weights_is_weight_one(nsm):
     x = make_rows(11, 8, 700)
     logits, seen = on_gpu(x, "fp32")

@@ -1056,12 +1056,6 @@ __global__ void __launch_bounds__(NT, 6) k_logprobs_backward(const LogprobArgs g
 
 // ---------------------------------------------------------------- distillation
 
-__device__ __forceinline__ float load_number(const void* p, int dtype, int64_t i) {
-  if (dtype == NSM_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  if (dtype == NSM_FP16) return __half2float(static_cast<const __half*>(p)[i]);
-  return static_cast<const float*>(p)[i];
-}
-
 template <typename V>
 __device__ __forceinline__ V warp_sum(V v) {
 #pragma unroll
@@ -1088,18 +1082,40 @@ struct TeacherStats {
   int any;                // there is a target
 };
 
-// The entries' tokens and scores (in log_p); equal tokens are still there.
+template <typename V>
+__device__ __forceinline__ V load_if(bool p, const void* from, int64_t i, V otherwise) {
+  return p ? static_cast<const V*>(from)[i] : otherwise;
+}
+
+// The entries' tokens and scores (in log_p); equal tokens are still there.  Every load is on its
+// way before the first is looked at: under load each takes microseconds.
 __device__ __forceinline__ void load_entries(Entries& e, const DistillArgs& g, int64_t r) {
   const int lane = threadIdx.x & 31;
+  const int64_t at_index = r * g.ldi + lane, at_score = r * g.ldt + lane;
+  int64_t v[kLaneEntries];
+  if (g.index_wide) {
+#pragma unroll
+    for (int u = 0; u < kLaneEntries; ++u) v[u] = load_if<int64_t>(lane + 32 * u < g.k, g.index, at_index + 32 * u, -1);
+  } else {
+#pragma unroll
+    for (int u = 0; u < kLaneEntries; ++u) v[u] = load_if<int32_t>(lane + 32 * u < g.k, g.index, at_index + 32 * u, -1);
+  }
+  if (g.teacher_dtype == NSM_FP32) {
+#pragma unroll
+    for (int u = 0; u < kLaneEntries; ++u) e.log_p[u] = load_if<float>(lane + 32 * u < g.k, g.teacher, at_score + 32 * u, kNegInf);
+  } else {
+    const bool bf16 = g.teacher_dtype == NSM_BF16;
+    uint16_t h[kLaneEntries];
+#pragma unroll
+    for (int u = 0; u < kLaneEntries; ++u) h[u] = load_if<uint16_t>(lane + 32 * u < g.k, g.teacher, at_score + 32 * u, 0);
+#pragma unroll
+    for (int u = 0; u < kLaneEntries; ++u)
+      e.log_p[u] = bf16 ? __bfloat162float(__ushort_as_bfloat16(h[u])) : __half2float(__ushort_as_half(h[u]));
+  }
 #pragma unroll
   for (int u = 0; u < kLaneEntries; ++u) {
-    e.v[u] = -1;
-    e.x[u] = e.log_p[u] = kNegInf;
-    if (lane + 32 * u < g.k) {
-      e.log_p[u] = load_number(g.teacher, g.teacher_dtype, r * g.ldt + lane + 32 * u);
-      const int64_t v = load_index(g.index, g.index_wide, r * g.ldi + lane + 32 * u);
-      if (v >= 0 && v < g.v.vocab) e.v[u] = static_cast<int>(v);
-    }
+    e.v[u] = v[u] >= 0 && v[u] < g.v.vocab ? static_cast<int>(v[u]) : -1;
+    e.x[u] = kNegInf;
   }
 }
 
@@ -1184,11 +1200,12 @@ __device__ __forceinline__ TeacherStats teacher_stats(Entries& e, const DistillA
 __device__ __forceinline__ Totals inside_totals(const Entries& e, float c) {
   float max = kNegInf, s = 0.f;
 #pragma unroll
-  for (int u = 0; u < kLaneEntries; ++u) max = fmaxf(max, e.x[u]);
+  for (int u = 0; u < kLaneEntries; ++u)
+    if (e.v[u] >= 0) max = fmaxf(max, e.x[u]);
   max = warp_max(max);
 #pragma unroll
   for (int u = 0; u < kLaneEntries; ++u)
-    if (!(e.x[u] == kNegInf)) s += max == kNegInf ? e.x[u] : ex2((e.x[u] - max) * c);  // a NaN stays one
+    if (e.v[u] >= 0 && !(e.x[u] == kNegInf)) s += max == kNegInf ? e.x[u] : ex2((e.x[u] - max) * c);  // a NaN stays one
   return Totals{max, warp_sum(s), 0.f};
 }
 
@@ -1215,6 +1232,19 @@ __device__ __forceinline__ Student student_of(const TeacherStats& t, const Total
   st.lse_log = st.empty ? 0.f : logf(all.s);
   st.rest_ref = no_rest ? 0.f : outside.max;
   st.rest = no_rest ? kNegInf : (outside.max - st.lse_ref) * inv_t + (logf(outside.s) - st.lse_log);
+  return st;
+}
+
+// The same from the lse and rest that the forward pass left.
+__device__ __forceinline__ Student student_from(const DistillArgs& g, int64_t r) {
+  const float lse = g.in_lse[r], rest = g.tail ? g.in_rest[r] : 0.f, t = g.v.t;
+  Student st{lse * t, 0.f, 0.f, rest, lse == kNegInf, 0.f, 0.f};
+  st.lse_low = fmaf(lse, t, -st.lse_ref);
+  if (rest != kNegInf) {
+    const float sum = lse + rest, b = sum - lse;  // and the sum's rounding, exactly
+    st.rest_ref = sum * t;
+    st.rest_low = fmaf(sum, t, -st.rest_ref) + ((lse - (sum - b)) + (rest - b)) * t;
+  }
   return st;
 }
 
@@ -1407,37 +1437,41 @@ __global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs 
   Sums a;
   if (teacher) {
     load_entries(e, g, r);
-    TeacherStats t = teacher_stats(e, g);
-    // what other blocks of the cluster hold of the row comes from memory
+    // What other blocks of the cluster hold of the row comes from memory; of the rest, the chunk
+    // it comes with and its place there.
     T elsewhere[kLaneEntries];
+    int chunk_of[kLaneEntries];
+    T* place[kLaneEntries];
 #pragma unroll
-    for (int u = 0; u < kLaneEntries; ++u)
-      if (e.v[u] >= 0 && !in_part(row, part, e.v[u])) elsewhere[u] = row.p[e.v[u]];
+    for (int u = 0; u < kLaneEntries; ++u) {
+      const int at = (e.v[u] + row.lead) / Elem<T>::kVec, from = at - part.begin;
+      chunk_of[u] = -1;
+      place[u] = reinterpret_cast<T*>(slab.v) + (e.v[u] + row.lead - slab.base * Elem<T>::kVec);
+      if (e.v[u] < 0) continue;
+      if (at >= part.begin && at < part.end) chunk_of[u] = (from >= slab.each) + (from >= 2 * slab.each) + (from >= 3 * slab.each);
+      else if (at == part.head || at == part.tail) chunk_of[u] = 0;
+      else elsewhere[u] = row.p[e.v[u]];
+    }
     // The entries leave the sums outside them: chunk by chunk as it arrives, their logits are
     // taken and -inf goes in their place.
+    static_assert(kSlabChunks == 4, "three comparisons find the chunk");
+#pragma unroll 1
     for (int q = 0; q < kSlabChunks; ++q) {
       slab.wait(q);
-      uint32_t mine = 0;
-#pragma unroll
-      for (int u = 0; u < kLaneEntries; ++u) {
-        if (e.v[u] < 0) continue;
-        const int at = (e.v[u] + row.lead) / Elem<T>::kVec;
-        if ((at >= part.begin + q * slab.each && at < min(part.end, part.begin + (q + 1) * slab.each)) ||
-            (q == 0 && (at == part.head || at == part.tail))) {
-          e.x[u] = Elem<T>::to_float(reinterpret_cast<T*>(slab.v)[e.v[u] + row.lead - slab.base * Elem<T>::kVec]);
-          mine |= 1u << u;
-        }
-      }
 #pragma unroll
       for (int u = 0; u < kLaneEntries; ++u)
-        if (mine >> u & 1)
-          reinterpret_cast<T*>(slab.v)[e.v[u] + row.lead - slab.base * Elem<T>::kVec] = Elem<T>::from_float(kNegInf);
+        if (chunk_of[u] == q) e.x[u] = Elem<T>::to_float(*place[u]);
+      __syncwarp();  // equal tokens have all read
+#pragma unroll
+      for (int u = 0; u < kLaneEntries; ++u)
+        if (chunk_of[u] == q) *place[u] = Elem<T>::from_float(kNegInf);
       __syncwarp();
       if (tid == NT) ptx::mbar_arrive(ptx::smem_u32(&ready[q]));
     }
+    TeacherStats t = teacher_stats(e, g);  // while the other warps are in the row
 #pragma unroll
     for (int u = 0; u < kLaneEntries; ++u)
-      if (e.v[u] >= 0 && !in_part(row, part, e.v[u])) e.x[u] = Elem<T>::to_float(elsewhere[u]);
+      if (e.v[u] >= 0 && chunk_of[u] < 0) e.x[u] = Elem<T>::to_float(elsewhere[u]);
     t.inside = inside_totals(e, c);
     if (tid == NT) shared_stats = t;
   } else {
@@ -1485,18 +1519,11 @@ __global__ void __launch_bounds__(NT + 32) k_distill_backward(const DistillArgs 
     const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, NSM_KERNEL_DISTILL);
     const Part part = part_of(row, piece, pieces);
     const float w = g.d_loss ? g.d_loss[r] : 1.f;
-    const float lse = g.in_lse[r], rest = g.tail ? g.in_rest[r] : 0.f;
-    if (w == 0.f || lse == kNegInf) {
+    if (w == 0.f || g.in_lse[r] == kNegInf) {
       if (!teacher) zero_part<NT>(out, piece, pieces);
       continue;
     }
-    Student st{lse * g.v.t, 0.f, 0.f, rest, false, 0.f, 0.f};
-    st.lse_low = fmaf(lse, g.v.t, -st.lse_ref);
-    if (rest != kNegInf) {
-      const float sum = lse + rest, b = sum - lse;
-      st.rest_ref = sum * g.v.t;
-      st.rest_low = fmaf(sum, g.v.t, -st.rest_ref) + ((lse - (sum - b)) + (rest - b)) * g.v.t;
-    }
+    const Student st = student_from(g, r);
     Entries e;
     if (teacher) {
       load_entries(e, g, r);
@@ -1519,6 +1546,137 @@ __global__ void __launch_bounds__(NT + 32) k_distill_backward(const DistillArgs 
   }
 }
 
+// ---------------------------------------------------------------- short rows
+
+// A warp per row, the row in its registers: N vectors per lane at most.  Forward, forward and
+// backward, or the backward pass alone; for rows so short that a block's barriers and its
+// threads' own fixed work would cost more than the row.
+constexpr int kShortWarps = 4;
+enum ShortMode { kShortForward, kShortBoth, kShortBackward };
+
+template <typename T, typename Args, bool ENT, int MODE, int N>
+__global__ void __launch_bounds__(32 * kShortWarps) k_short(const Args g, int* status) {
+  constexpr bool DISTILL = std::is_same<Args, DistillArgs>::value;
+  constexpr int kVec = Elem<T>::kVec;
+  constexpr int kKernel = DISTILL ? NSM_KERNEL_DISTILL : NSM_KERNEL_LOGPROBS;
+  __shared__ uint32_t members[kShortWarps][DISTILL ? 32 * N / 4 : 1];  // a byte per vector, a bit per element
+  grid_dependency_sync();
+  release_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int vocab = g.v.vocab;
+  const float c = g.v.c, inv_t = g.v.inv_t;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kShortWarps + warp; r < g.v.rows;
+       r += static_cast<int64_t>(gridDim.x) * kShortWarps) {
+    const Row<T> row(static_cast<T*>(const_cast<void*>(g.v.logits)) + r * g.v.ld, vocab, status, kKernel);
+    const Part part = part_of(row, 0, 1);
+    uint4 raw[N];
+    uint4 none = make_uint4(0, 0, 0, 0);
+    vec_mask<T>(none, 0xffu);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int i = lane + 32 * u;
+      raw[u] = i >= part.begin && i < part.end ? row.load_whole(i) : none;
+    }
+    if (part.head == 0 && lane == 0) raw[0] = row.load(0);
+    if (part.tail >= 0 && (part.tail & 31) == lane) {
+      const uint4 tail = row.load(part.tail);
+#pragma unroll
+      for (int u = 0; u < N; ++u)
+        if (part.tail == lane + 32 * u) raw[u] = tail;
+    }
+    auto store = [&](bool zero, auto&& value) {  // the lane's vectors of the gradient
+      const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, kKernel);
+      const bool same = row.lead == out.lead;
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const int i = lane + 32 * u;
+        if (i >= row.nvec) continue;
+        uint4 grad = make_uint4(0, 0, 0, 0);
+        if (!zero) grad = value(raw[u]);
+        if (same && i >= part.begin && i < part.end) out.store_whole(i, grad);
+        else out.store(row.first(i), grad);
+      }
+    };
+    if constexpr (DISTILL) {
+      Entries e;
+      load_entries(e, g, r);
+      load_logits(e, row);
+      TeacherStats t = teacher_stats(e, g);
+      t.inside = inside_totals(e, c);
+      const float w = MODE == kShortForward || !g.d_loss ? 1.f : g.d_loss[r];
+      EntryGradient k;
+      Student st;
+      if constexpr (MODE == kShortBackward) {
+        st = student_from(g, r);
+        k = entry_gradient(t, st, w, g.tail, c, inv_t);
+      } else {
+        // the row outside the entries
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j) members[warp][lane + 32 * j] = 0;
+        if (N < 4 && lane < 32 * N / 4) members[warp][lane] = 0;
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kLaneEntries; ++u) {
+          const int at = e.v[u] + row.lead, i = at / kVec;
+          if (e.v[u] >= 0) atomicOr(&members[warp][i / 4], 1u << (8 * (i & 3) + at % kVec));
+        }
+        __syncwarp();
+        Sums a;
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+          if (32 * u >= row.nvec) continue;
+          uint4 v = raw[u];
+          const uint32_t bits = reinterpret_cast<const uint8_t*>(members[warp])[lane + 32 * u];
+          if (bits) vec_mask<T>(v, bits);
+          add_vec<T, false>(a, v, c);
+        }
+        const Totals outside = warp_totals<false>(a, c);
+        st = student_of(t, outside, c, inv_t);
+        write_loss(g, r, e, t, st);
+        k = entry_gradient(t, outside, w, g.tail, c, inv_t);
+      }
+      if constexpr (MODE != kShortForward) {
+        store(k.zero, [&](const uint4& v) { return gradient_vec<T, false>(v, k.ref, c, k.log2_s, k.scale, 0.f); });
+        __syncwarp();  // the entries' own values go over what was written there
+        if (!k.zero) {
+          const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, kKernel);
+          store_entries(row, out, part, e, st, k, inv_t);
+        }
+      }
+    } else {
+      const int64_t token64 = g.tokens ? load_index(g.tokens, g.tokens_wide, r) : -1;
+      const int token = token64 < 0 || token64 >= vocab ? -1 : static_cast<int>(token64);
+      const float x_token = token >= 0 ? Elem<T>::to_float(row.p[token]) : kNegInf;
+      RowLogprob s;
+      float low = 0.f;
+      if constexpr (MODE == kShortBackward) {
+        const float lse = g.in_lse[r];
+        s = RowLogprob{lse * g.v.t, 0.f, 0.f, ENT && g.d_entropy ? g.in_entropy[r] : 0.f, lse == kNegInf};
+        low = fmaf(lse, g.v.t, -s.ref);
+      } else {
+        Sums a;
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+          if (32 * u < row.nvec) add_vec<T, ENT>(a, raw[u], c);
+        s = row_logprob<ENT>(warp_totals<ENT>(a, c), inv_t);
+        if (lane == 0) write_logprob<ENT>(g, r, s, token, x_token, inv_t);
+      }
+      if constexpr (MODE != kShortForward) {
+        const float w = g.d_logprob && token >= 0 ? g.d_logprob[r] : 0.f;
+        const float h = ENT && g.d_entropy ? g.d_entropy[r] : 0.f;
+        const TokenGradient k = token_gradient(w, h, s, low, c, inv_t);
+        __syncwarp();  // in place: every lane has read the token's logit
+        store(k.zero, [&](const uint4& v) { return gradient_vec<T, ENT>(v, k.ref, c, k.log2_s, k.ca, k.cb); });
+        if (!k.zero && token >= 0 && ((token + row.lead) / kVec & 31) == lane) {
+          const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, kKernel);
+          if (bounds_ok(token < vocab, status, kKernel, 0, NSM_SITE_GRADIENT))
+            out.p[token] = Elem<T>::from_float(gradient_at_token(w, h, s, low, x_token, inv_t));
+        }
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------- launches
 
 // CTAs per row: where there are fewer rows than the GPU takes blocks at a time, a cluster
@@ -1536,16 +1694,8 @@ int pieces_for(int64_t rows, int nvec, int most, int least) {
   return (nvec + each - 1) / each;
 }
 
-#ifndef NSM_SLAB
-#define NSM_SLAB 76
-#endif
-#ifndef NSM_RT
-#define NSM_RT 0
-#endif
-#ifndef NSM_PER
-#define NSM_PER 8
-#endif
-constexpr size_t kSlabBytes = NSM_SLAB << 10, kSlabMost = 216 << 10;
+constexpr size_t kSlabBytes = 76 << 10, kSlabAlone = 112 << 10, kSlabMost = 216 << 10;
+constexpr size_t kMembersMost = 160 << 10;  // of k_distill's bits per block
 
 size_t slab_bytes(int nvec, int ctas) { return (static_cast<size_t>((nvec + ctas - 1) / ctas) + 2) * 16; }
 
@@ -1553,13 +1703,17 @@ size_t slab_bytes(int nvec, int ctas) { return (static_cast<size_t>((nvec + ctas
 struct Resident {
   int threads, ctas;
 };
+// Measured on a GB300, loss and gradient in bf16: slabs of 64 KB, three blocks a SM, 32768
+// columns 162 us for 8192 rows (98% of the copy rate); the same row over two blocks of a cluster
+// 208 us, so a row stays in one block up to 112 KB (50257 columns 281 us in one, 302 in two) where
+// rows are many; beyond, clusters of 76 KB slabs (131072 columns 777 us in four, 822 in eight).
+// Eight vectors a thread: 8000 columns 47 us with 128 threads, 62 with 256.
 Resident resident_for(int64_t rows, int nvec) {
   Resident r{256, 1};
-  while (r.ctas < kMaxCluster && slab_bytes(nvec, r.ctas) > kSlabBytes) r.ctas *= 2;
+  if (rows < 2048 || slab_bytes(nvec, 1) > kSlabAlone)
+    while (r.ctas < kMaxCluster && slab_bytes(nvec, r.ctas) > kSlabBytes) r.ctas *= 2;
   if (slab_bytes(nvec, r.ctas) > kSlabMost) return Resident{0, 0};
-  if (NSM_RT) r.threads = NSM_RT;
-  else
-    while (r.threads > 64 && nvec < r.threads * NSM_PER) r.threads /= 2;
+  while (r.threads > 64 && nvec < r.threads * 8) r.threads /= 2;
   while (r.ctas < kMaxCluster && rows * r.ctas * r.threads < 1024 * 152 && nvec >= r.ctas * 4 * r.threads) r.ctas *= 2;
   return r;
 }
@@ -1597,9 +1751,36 @@ cudaError_t launch_clusters(void (*kernel)(K...), int threads, int64_t grid, int
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<K>(args)...);
 }
 
+// Vectors per lane of a warp per row, 0 where rows are too long for that.  Measured on a GB300
+// against blocks of 64 to 256 threads per row, 16384 rows: 259 columns bf16, distillation's loss
+// and gradient 23 us for 60, log probabilities 10 for 24; 2000 columns 45 for 64 and 14 for 30; for
+// 8 rows the two are alike.
+int short_for(int nvec) {
+  if (nvec > 32 * 8) return 0;
+  return nvec <= 64 ? 2 : nvec <= 128 ? 4 : 8;
+}
+
+template <typename T, typename Args, bool ENT, int MODE>
+cudaError_t launch_short(int n, const Args& a, int* status, cudaStream_t stream) {
+  auto* kernel = n == 2 ? k_short<T, Args, ENT, MODE, 2> : n == 4 ? k_short<T, Args, ENT, MODE, 4> : k_short<T, Args, ENT, MODE, 8>;
+  const int64_t blocks = std::min<int64_t>((a.v.rows + kShortWarps - 1) / kShortWarps, 1 << 16);
+  return launch_clusters(kernel, 32 * kShortWarps, blocks, 1, 0, stream, a, status);
+}
+
 template <typename T>
 cudaError_t launch_logprobs_t(const LogprobArgs& a, int* status, cudaStream_t stream) {
-  const int nvec = vectors_of<T>(a.v.vocab);
+  const int nvec = vectors_of<T>(a.v.vocab), n = short_for(nvec);
+  if (n > 0 && a.k == 0) {
+    const bool ent = a.d_entropy || a.entropy;
+    if (a.in_lse)
+      return ent ? launch_short<T, LogprobArgs, true, kShortBackward>(n, a, status, stream)
+                 : launch_short<T, LogprobArgs, false, kShortBackward>(n, a, status, stream);
+    if (a.v.d_logits)
+      return ent ? launch_short<T, LogprobArgs, true, kShortBoth>(n, a, status, stream)
+                 : launch_short<T, LogprobArgs, false, kShortBoth>(n, a, status, stream);
+    return ent ? launch_short<T, LogprobArgs, true, kShortForward>(n, a, status, stream)
+               : launch_short<T, LogprobArgs, false, kShortForward>(n, a, status, stream);
+  }
   if (a.in_lse) {
     constexpr int kThreads = 256;
     const int pieces = pieces_for(a.v.rows, nvec, 4 * kThreads, kThreads);
@@ -1638,6 +1819,11 @@ cudaError_t launch_logprobs_t(const LogprobArgs& a, int* status, cudaStream_t st
 template <typename T>
 cudaError_t launch_distill_t(const DistillArgs& a, int* status, cudaStream_t stream) {
   const int nvec = vectors_of<T>(a.v.vocab);
+  if (const int n = short_for(nvec)) {
+    if (a.in_lse) return launch_short<T, DistillArgs, false, kShortBackward>(n, a, status, stream);
+    if (a.v.d_logits) return launch_short<T, DistillArgs, false, kShortBoth>(n, a, status, stream);
+    return launch_short<T, DistillArgs, false, kShortForward>(n, a, status, stream);
+  }
   if (a.in_lse) {
     constexpr int kThreads = 256;
     const int pieces = pieces_for(a.v.rows, nvec, 16 * kThreads, kThreads);
@@ -1655,10 +1841,11 @@ cudaError_t launch_distill_t(const DistillArgs& a, int* status, cudaStream_t str
   }
   constexpr int kThreads = 128, kGradThreads = 256;
   const int threads = a.v.d_logits ? kGradThreads : kThreads;
-  const int ctas = cluster_for(a.v.rows, nvec, threads);
-  const size_t smem = (static_cast<size_t>((nvec + ctas - 1) / ctas) + 2 + 15) / 16 * 16;
-  return launch_clusters(a.v.d_logits ? k_distill<T, true, kGradThreads> : k_distill<T, false, kThreads>, threads + 32,
-                         a.v.rows * ctas, ctas, smem, stream, a, status);
+  int ctas = cluster_for(a.v.rows, nvec, threads);
+  auto members = [&] { return (static_cast<size_t>((nvec + ctas - 1) / ctas) + 2 + 15) / 16 * 16; };
+  while (members() > kMembersMost && ctas < kMaxCluster) ctas *= 2;
+  auto* kernel = a.v.d_logits ? k_distill<T, true, kGradThreads> : k_distill<T, false, kThreads>;
+  return launch_clusters(kernel, threads + 32, a.v.rows * ctas, ctas, members(), stream, a, status);
 }
 
 }  // namespace

@@ -383,79 +383,93 @@ def gemm(a, b, out, aux=None, b_mn_major: bool = False, alpha: float = 1.0, beta
 
 TOP_MAX_K = 128
 DISTILL_MAX_K = 128
-_torch_codes: Optional[Tuple[dict, dict]] = None
+_LOGITS_TYPES: dict = {}
+_INDEX_TYPES: dict = {}
+_FLOAT32 = _INT32 = None
+_raw_stream = None
 
 
-def _codes() -> Tuple[dict, dict]:
-    """torch's names of the logits' types and of the index types, as the library's codes."""
-    global _torch_codes
-    if _torch_codes is None:
-        import torch
-        _torch_codes = ({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}, {torch.int32: 0, torch.int64: 1})
-    return _torch_codes
+def _torch_types() -> None:
+    """torch's types as the library's codes, once torch is there."""
+    global _FLOAT32, _INT32, _raw_stream
+    import torch
+    _LOGITS_TYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    _INDEX_TYPES.update({torch.int32: 0, torch.int64: 1})
+    _FLOAT32, _INT32 = torch.float32, torch.int32
+    # the current stream's handle without a Stream object: a third of a short call's time
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _matrix(name: str, t, codes, rows: int, cols: int, device) -> Tuple[int, int, int]:
+def _loss_stream(stream, device: int) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _stream_ptr(stream)
+
+
+def _matrix(name: str, t, codes, rows: int, cols: int, device: int) -> Tuple[int, int, int]:
     """(pointer, type code, row stride) of a rows x cols tensor with unit column stride."""
     if t is None:
         raise ValueError(f"{name} is missing")
     code = codes.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} has type {t.dtype}: one of {[str(c) for c in codes]} is wanted")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
-        raise ValueError(f"{name} has shape {tuple(shape)}: ({rows}, {cols}) is wanted")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}: ({rows}, {cols}) is wanted")
+    stride = t.stride()
     if cols > 1 and stride[1] != 1:
         raise ValueError(f"{name} has column stride {stride[1]}: 1 is wanted")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}: {device} is wanted")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on the logits' device")
     return t.data_ptr(), code, (stride[0] if rows > 1 else max(stride[0], cols))
 
 
-def _numbers(name: str, t, shape: Tuple[int, ...], device, dtype=None) -> int:
-    """Pointer of a contiguous tensor of that shape, float32 unless `dtype` says otherwise; 0 for None."""
+def _numbers(name: str, t, shape: Tuple[int, ...], device: int, dtype) -> int:
+    """Pointer of a contiguous tensor of that shape and type; 0 for None."""
     if t is None:
         return 0
-    import torch
-    if t.dtype != (dtype or torch.float32):
-        raise ValueError(f"{name} has type {t.dtype}: {dtype or torch.float32} is wanted")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has type {t.dtype}: {dtype} is wanted")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} is not a contiguous tensor of shape {shape}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}: {device} is wanted")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on the logits' device")
     return t.data_ptr()
 
 
-def _logits(logits) -> Tuple[int, int, int, int, int]:
+def _logits(logits) -> Tuple[int, int, int, int, int, int]:
+    """(pointer, type code, rows, vocab, row stride, device)."""
+    if _FLOAT32 is None:
+        _torch_types()
     if logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits is not a matrix of rows x vocab in device memory")
     rows, vocab = logits.shape
-    ptr, code, ld = _matrix("logits", logits, _codes()[0], rows, vocab, logits.device)
-    return ptr, code, rows, vocab, ld
+    device = logits.get_device()
+    ptr, code, ld = _matrix("logits", logits, _LOGITS_TYPES, rows, vocab, device)
+    return ptr, code, rows, vocab, ld, device
 
 
-def _tokens(tokens, rows: int, device) -> Tuple[int, int]:
+def _tokens(tokens, rows: int, device: int) -> Tuple[int, int]:
     if tokens is None:
         return 0, 0
-    code = _codes()[1].get(tokens.dtype)
+    code = _INDEX_TYPES.get(tokens.dtype)
     if code is None:
         raise ValueError(f"tokens has type {tokens.dtype}: torch.int32 or torch.int64 is wanted")
     return _numbers("tokens", tokens, (rows,), device, tokens.dtype), code
 
 
-def _gradient(name: str, t, logits) -> Tuple[int, int]:
+def _gradient(name: str, t, logits, device: int) -> Tuple[int, int]:
     if t is not None and t.dtype != logits.dtype:
         raise ValueError(f"{name} has type {t.dtype}: the logits' {logits.dtype} is wanted")
-    ptr, _, ld = _matrix(name, t, _codes()[0], logits.shape[0], logits.shape[1], logits.device)
+    ptr, _, ld = _matrix(name, t, _LOGITS_TYPES, logits.shape[0], logits.shape[1], device)
     return ptr, ld
 
 
-def _entries(teacher, index, rows: int, device) -> Tuple[int, int, int, int, int, int, int]:
+def _entries(teacher, index, rows: int, device: int) -> Tuple[int, int, int, int, int, int, int]:
     if teacher is None or teacher.dim() != 2:
         raise ValueError("teacher is not a matrix of rows x k")
     k = teacher.shape[1]
-    t_ptr, t_code, ldt = _matrix("teacher", teacher, _codes()[0], rows, k, device)
-    i_ptr, wide, ldi = _matrix("index", index, _codes()[1], rows, k, device)
+    t_ptr, t_code, ldt = _matrix("teacher", teacher, _LOGITS_TYPES, rows, k, device)
+    i_ptr, wide, ldi = _matrix("index", index, _INDEX_TYPES, rows, k, device)
     return t_ptr, t_code, ldt, i_ptr, wide, ldi, k
 
 
@@ -469,22 +483,21 @@ def logprobs(logits, tokens, logprob=None, entropy=None, lse=None, top_logprob=N
     and ``lse`` (float32, one per row), and the k largest logits as log probabilities
     ``top_logprob`` (float32, rows x k) with their indexes ``top_index`` (int32, rows x k),
     ties by ascending index."""
-    ptr, code, rows, vocab, ld = _logits(logits)
-    dev = logits.device
+    ptr, code, rows, vocab, ld, dev = _logits(logits)
+    row = (rows,)
     t_ptr, wide = _tokens(tokens, rows, dev)
     k = 0
     if top_logprob is not None or top_index is not None:
         if top_logprob is None or top_index is None or top_logprob.dim() != 2:
             raise ValueError("top_logprob and top_index go together, as matrices of rows x k")
-        import torch
         k = top_logprob.shape[1]
-        top_l = _numbers("top_logprob", top_logprob, (rows, k), dev)
-        top_i = _numbers("top_index", top_index, (rows, k), dev, torch.int32)
+        top_l = _numbers("top_logprob", top_logprob, (rows, k), dev, _FLOAT32)
+        top_i = _numbers("top_index", top_index, (rows, k), dev, _INT32)
     else:
         top_l = top_i = 0
     _check(lib().nsm_logprobs(ptr, code, rows, vocab, ld, t_ptr, wide, float(temperature), k,
-                              _numbers("logprob", logprob, (rows,), dev), _numbers("entropy", entropy, (rows,), dev),
-                              _numbers("lse", lse, (rows,), dev), top_l, top_i, _stream_ptr(stream)))
+                              _numbers("logprob", logprob, row, dev, _FLOAT32), _numbers("entropy", entropy, row, dev, _FLOAT32),
+                              _numbers("lse", lse, row, dev, _FLOAT32), top_l, top_i, _loss_stream(stream, dev)))
 
 
 def logprobs_grad(logits, tokens, d_logprob, d_entropy, d_logits, logprob=None, entropy=None, lse=None,
@@ -492,31 +505,31 @@ def logprobs_grad(logits, tokens, d_logprob, d_entropy, d_logits, logprob=None, 
     """:func:`logprobs` with the gradient in the same pass, for weights known beforehand:
     writes ``d_logits``, the gradient of sum(d_logprob * logprob + d_entropy * entropy)
     (one of the two weights may be None), in the logits' type; it may be ``logits`` itself."""
-    ptr, code, rows, vocab, ld = _logits(logits)
-    dev = logits.device
+    ptr, code, rows, vocab, ld, dev = _logits(logits)
+    row = (rows,)
     t_ptr, wide = _tokens(tokens, rows, dev)
-    g_ptr, ldd = _gradient("d_logits", d_logits, logits)
+    g_ptr, ldd = _gradient("d_logits", d_logits, logits, dev)
     _check(lib().nsm_logprobs_grad(ptr, code, rows, vocab, ld, t_ptr, wide, float(temperature),
-                                   _numbers("d_logprob", d_logprob, (rows,), dev),
-                                   _numbers("d_entropy", d_entropy, (rows,), dev), g_ptr, ldd,
-                                   _numbers("logprob", logprob, (rows,), dev),
-                                   _numbers("entropy", entropy, (rows,), dev), _numbers("lse", lse, (rows,), dev),
-                                   _stream_ptr(stream)))
+                                   _numbers("d_logprob", d_logprob, row, dev, _FLOAT32),
+                                   _numbers("d_entropy", d_entropy, row, dev, _FLOAT32), g_ptr, ldd,
+                                   _numbers("logprob", logprob, row, dev, _FLOAT32),
+                                   _numbers("entropy", entropy, row, dev, _FLOAT32), _numbers("lse", lse, row, dev, _FLOAT32),
+                                   _loss_stream(stream, dev)))
 
 
 def logprobs_backward(logits, tokens, lse, entropy, d_logprob, d_entropy, d_logits, temperature: float = 1.0,
                       stream=None) -> None:
     """The backward pass of :func:`logprobs` alone, from its ``lse`` (and ``entropy``, needed
     with ``d_entropy``)."""
-    ptr, code, rows, vocab, ld = _logits(logits)
-    dev = logits.device
+    ptr, code, rows, vocab, ld, dev = _logits(logits)
+    row = (rows,)
     t_ptr, wide = _tokens(tokens, rows, dev)
-    g_ptr, ldd = _gradient("d_logits", d_logits, logits)
+    g_ptr, ldd = _gradient("d_logits", d_logits, logits, dev)
     _check(lib().nsm_logprobs_backward(ptr, code, rows, vocab, ld, t_ptr, wide, float(temperature),
-                                       _numbers("lse", lse, (rows,), dev), _numbers("entropy", entropy, (rows,), dev),
-                                       _numbers("d_logprob", d_logprob, (rows,), dev),
-                                       _numbers("d_entropy", d_entropy, (rows,), dev), g_ptr, ldd,
-                                       _stream_ptr(stream)))
+                                       _numbers("lse", lse, row, dev, _FLOAT32), _numbers("entropy", entropy, row, dev, _FLOAT32),
+                                       _numbers("d_logprob", d_logprob, row, dev, _FLOAT32),
+                                       _numbers("d_entropy", d_entropy, row, dev, _FLOAT32), g_ptr, ldd,
+                                       _loss_stream(stream, dev)))
 
 
 def distill(logits, teacher, index, loss, lse=None, rest=None, temperature: float = 1.0, tail: bool = False,
@@ -529,38 +542,38 @@ def distill(logits, teacher, index, loss, lse=None, rest=None, temperature: floa
     :func:`logprobs`) and the rest of the row is one bucket.  An index outside the
     vocabulary, or given before in its row, does not count.  Writes ``loss`` and, where
     given, the student's ``lse`` and ``rest`` (log of its mass outside the entries)."""
-    ptr, code, rows, vocab, ld = _logits(logits)
-    dev = logits.device
+    ptr, code, rows, vocab, ld, dev = _logits(logits)
+    row = (rows,)
     e = _entries(teacher, index, rows, dev)
     _check(lib().nsm_distill(ptr, code, rows, vocab, ld, *e, float(temperature), 1 if tail else 0,
-                             _numbers("loss", loss, (rows,), dev), _numbers("lse", lse, (rows,), dev),
-                             _numbers("rest", rest, (rows,), dev), _stream_ptr(stream)))
+                             _numbers("loss", loss, row, dev, _FLOAT32), _numbers("lse", lse, row, dev, _FLOAT32),
+                             _numbers("rest", rest, row, dev, _FLOAT32), _loss_stream(stream, dev)))
 
 
 def distill_grad(logits, teacher, index, d_loss, d_logits, loss=None, lse=None, rest=None,
                  temperature: float = 1.0, tail: bool = False, stream=None) -> None:
     """:func:`distill` with the gradient of sum(d_loss * loss) in the same pass (``d_loss``
     None: weights 1); ``d_logits`` has the logits' type and may be ``logits`` itself."""
-    ptr, code, rows, vocab, ld = _logits(logits)
-    dev = logits.device
+    ptr, code, rows, vocab, ld, dev = _logits(logits)
+    row = (rows,)
     e = _entries(teacher, index, rows, dev)
-    g_ptr, ldd = _gradient("d_logits", d_logits, logits)
+    g_ptr, ldd = _gradient("d_logits", d_logits, logits, dev)
     _check(lib().nsm_distill_grad(ptr, code, rows, vocab, ld, *e, float(temperature), 1 if tail else 0,
-                                  _numbers("d_loss", d_loss, (rows,), dev), g_ptr, ldd,
-                                  _numbers("loss", loss, (rows,), dev), _numbers("lse", lse, (rows,), dev),
-                                  _numbers("rest", rest, (rows,), dev), _stream_ptr(stream)))
+                                  _numbers("d_loss", d_loss, row, dev, _FLOAT32), g_ptr, ldd,
+                                  _numbers("loss", loss, row, dev, _FLOAT32), _numbers("lse", lse, row, dev, _FLOAT32),
+                                  _numbers("rest", rest, row, dev, _FLOAT32), _loss_stream(stream, dev)))
 
 
 def distill_backward(logits, teacher, index, lse, rest, d_loss, d_logits, temperature: float = 1.0,
                      tail: bool = False, stream=None) -> None:
     """The backward pass of :func:`distill` alone, from its ``lse`` and (with ``tail``) ``rest``."""
-    ptr, code, rows, vocab, ld = _logits(logits)
-    dev = logits.device
+    ptr, code, rows, vocab, ld, dev = _logits(logits)
+    row = (rows,)
     e = _entries(teacher, index, rows, dev)
-    g_ptr, ldd = _gradient("d_logits", d_logits, logits)
+    g_ptr, ldd = _gradient("d_logits", d_logits, logits, dev)
     _check(lib().nsm_distill_backward(ptr, code, rows, vocab, ld, *e, float(temperature), 1 if tail else 0,
-                                      _numbers("lse", lse, (rows,), dev), _numbers("rest", rest, (rows,), dev),
-                                      _numbers("d_loss", d_loss, (rows,), dev), g_ptr, ldd, _stream_ptr(stream)))
+                                      _numbers("lse", lse, row, dev, _FLOAT32), _numbers("rest", rest, row, dev, _FLOAT32),
+                                      _numbers("d_loss", d_loss, row, dev, _FLOAT32), g_ptr, ldd, _loss_stream(stream, dev)))
 
 
 def device_status(stream=None) -> int:

@@ -180,6 +180,27 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// A vector that begins at element e0 of a row, element by element, for the ragged ends of rows.
+// Out of line: rare, and long beside the loops of the forward kernels (in line where a call would
+// take registers from a kernel that has few: the top alternatives').
+template <typename T>
+__device__ __forceinline__ uint4 load_elements_here(const T* p, int vocab, int e0) {
+  uint4 raw = make_uint4(0, 0, 0, 0);
+  T* h = reinterpret_cast<T*>(&raw);
+  uint32_t none = 0;  // -inf outside the row
+#pragma unroll
+  for (int e = 0; e < Elem<T>::kVec; ++e) {
+    const int v = e0 + e;
+    if (v >= 0 && v < vocab) h[e] = p[v]; else none |= 1u << e;
+  }
+  vec_mask<T>(raw, none);
+  return raw;
+}
+template <typename T>
+__device__ __noinline__ uint4 load_elements(const T* p, int vocab, int e0) {
+  return load_elements_here<T>(p, vocab, e0);
+}
+
 // One row of logits (or gradients) as 16-byte vectors on the address grid: vector i holds
 // elements i kVec - lead ... + kVec, of which those in [0, vocab) exist.
 template <typename T>
@@ -205,17 +226,10 @@ struct Row {
   // vector i of the row, with -inf outside it
   __device__ __forceinline__ uint4 load(int i) const {
     const int e0 = first(i);
-    if (whole(i)) return load_whole(i);
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    T* h = reinterpret_cast<T*>(&raw);
-    uint32_t none = 0;
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      const int v = e0 + e;
-      if (v >= 0 && v < vocab) h[e] = p[v]; else none |= 1u << e;
-    }
-    vec_mask<T>(raw, none);
-    return raw;
+    return whole(i) ? load_whole(i) : load_elements<T>(p, vocab, e0);
+  }
+  __device__ __forceinline__ uint4 load_here(int i) const {
+    return whole(i) ? load_whole(i) : load_elements_here<T>(p, vocab, first(i));
   }
   // writes vector i, which is whole
   __device__ __forceinline__ void store_whole(int i, const uint4& raw) const {
@@ -262,7 +276,7 @@ __device__ __forceinline__ Part part_of(const Row<T>& row, int piece, int pieces
 
 // use(i, vector, whole) for every vector of the part that this thread has, four loads in flight;
 // done(n) after the n-th four of them (the ragged ones come last and are not counted).
-template <int NT, typename T, typename F, typename D>
+template <int NT, bool HERE, typename T, typename F, typename D>
 __device__ __forceinline__ void for_batches(const Row<T>& row, const Part& part, F&& use, D&& done) {
   int i = part.begin + static_cast<int>(threadIdx.x), n = 0;
   for (; i + 3 * NT < part.end; i += 4 * NT, ++n) {
@@ -283,13 +297,41 @@ __device__ __forceinline__ void for_batches(const Row<T>& row, const Part& part,
       if (i + u * NT < part.end) use(i + u * NT, raw[u], true);
     done(n);
   }
-  if (part.head >= 0 && threadIdx.x == kHeadThread) use(part.head, row.load(part.head), false);
-  if (part.tail >= 0 && threadIdx.x == kTailThread) use(part.tail, row.load(part.tail), false);
+  if (part.head >= 0 && threadIdx.x == kHeadThread) use(part.head, HERE ? row.load_here(part.head) : row.load(part.head), false);
+  if (part.tail >= 0 && threadIdx.x == kTailThread) use(part.tail, HERE ? row.load_here(part.tail) : row.load(part.tail), false);
 }
 
-template <int NT, typename T, typename F>
+// A thread's first four vectors of a part, loaded ahead of what their use waits for.
+template <int NT, typename T>
+struct FirstFour {
+  uint4 raw[4];
+  __device__ __forceinline__ void load(const Row<T>& row, const Part& part) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = part.begin + static_cast<int>(threadIdx.x) + u * NT;
+      if (i < part.end) raw[u] = row.load_whole(i);
+    }
+  }
+  // use(i, vector, whole) for those, and what follows them in the part
+  template <typename F>
+  __device__ __forceinline__ void use_all(const Row<T>& row, Part part, F&& use) const;
+};
+
+template <int NT, bool HERE = false, typename T, typename F>
 __device__ __forceinline__ void for_vectors(const Row<T>& row, const Part& part, F&& use) {
-  for_batches<NT>(row, part, use, [](int) {});
+  for_batches<NT, HERE>(row, part, use, [](int) {});
+}
+
+template <int NT, typename T>
+template <typename F>
+__device__ __forceinline__ void FirstFour<NT, T>::use_all(const Row<T>& row, Part part, F&& use) const {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int i = part.begin + static_cast<int>(threadIdx.x) + u * NT;
+    if (i < part.end) use(i, raw[u], true);
+  }
+  part.begin = min(part.end, part.begin + 4 * NT);
+  for_vectors<NT>(row, part, use);
 }
 
 template <int NT, typename T>
@@ -467,6 +509,13 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
 static_assert(kTopCandidates >= kMaxCluster * kTopMaxK, "every CTA's k largest fit");
 
+// What one of the k largest logits reaches: keys from `key` on, and of those up to tie_top only
+// in vectors up to `vec`.
+struct TopBound {
+  uint32_t key, tie_top;
+  int vec;
+};
+
 constexpr int kTopThreads = 256, kTopWarps = kTopThreads / 32;
 constexpr int kTopGroups = 32;   // groups of batches per thread at most
 constexpr int kTopList = 1024;
@@ -476,8 +525,8 @@ struct TopShared {
   uint32_t list[kTopList];                    // group * kTopThreads + thread
   uint64_t cand[kTopCandidates];
   uint64_t best[kTopWarps];
-  uint32_t bound_key, bound_tie_top;
-  int32_t bound_vec, nlist, ncand;
+  TopBound bound;
+  int32_t nlist, ncand;
   uint32_t taken[kMaxCluster];                // how many keys each CTA gave
 };
 
@@ -519,90 +568,73 @@ __device__ __forceinline__ uint64_t full_key(float f, int v) {
   return (static_cast<uint64_t>(order_key(f)) << 32) | (0xffffffffu - static_cast<uint32_t>(v));
 }
 
-// The first warp finds a bound that at least k threads' largest logits reach, and few more:
-// the k-th largest of them, bit by bit until that holds (bits below kKeyLowBit do not tell two
-// values apart), and where too many are equal to it, the vector number up to which they are
-// needed.
-template <typename T>
-__device__ __forceinline__ void top_bound(TopShared& sh, int k) {
+// From the largest logits of groups of vectors (PER keys of each lane of a warp, with the vector
+// where each was met first): a bound that at least k groups reach and at most `enough` do.  The
+// k-th largest key, bit by bit until that holds (bits below kKeyLowBit do not tell two values
+// apart), and where too many are equal to it, the vector number up to which they are needed.
+template <typename T, int PER>
+__device__ __forceinline__ TopBound top_bound(const uint32_t (&key)[PER], const int (&vec)[PER], int k, int enough) {
   constexpr int kLow = Elem<T>::kKeyLowBit;
-  constexpr int kPer = kTopThreads / 32;
-  const int lane = threadIdx.x;
-  uint32_t key[kPer];
-  int vec[kPer];
+  static_assert(32 * PER < 1 << 10, "ten bits hold a count");
   int valid = 0;
   uint32_t high = 0, low = ~0u;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    key[j] = sh.key[j * 32 + lane];
-    vec[j] = sh.vec[j * 32 + lane];
+  for (int j = 0; j < PER; ++j) {
     valid += key[j] > kKeyNegInf;
     high = max(high, key[j]);
     low = min(low, key[j]);
   }
   valid = __reduce_add_sync(~0u, valid);
-  uint32_t bound = kKeyNegInf + 1, tie_top = kKeyNegInf;
-  int bound_vec = 0x7fffffff;
-  if (valid > k) {
-    high = __reduce_max_sync(~0u, high);
-    low = __reduce_min_sync(~0u, low);
-    // bits above the first in which the keys differ are common to all
-    int b = high == low ? kLow - 1 : 31 - __clz(high ^ low);
-    bound = b >= 31 ? 0 : high >> (b + 1) << (b + 1);
-    if (b < kLow) bound = high >> kLow << kLow;
-    int reach = kTopThreads;
-    // a few more threads than k cost less than the steps that would tell them apart
-    const int enough = k + 4 + k / 4;
-    // two bits at a time: the counts of three thresholds side by side in one sum
-    static_assert(kTopThreads < 1 << 10, "ten bits hold a count");
-    for (; b >= kLow && reach > enough; b -= 2) {
-      const uint32_t half = b > kLow ? 1u << (b - 1) : 0u, one = 1u << b;  // the last bit alone: half 0
-      uint32_t n = 0;
+  TopBound t{kKeyNegInf + 1, kKeyNegInf, 0x7fffffff};
+  if (valid <= k) return t;
+  high = __reduce_max_sync(~0u, high);
+  low = __reduce_min_sync(~0u, low);
+  // bits above the first in which the keys differ are common to all
+  int b = high == low ? kLow - 1 : 31 - __clz(high ^ low);
+  uint32_t bound = b < kLow ? high >> kLow << kLow : (b >= 31 ? 0 : high >> (b + 1) << (b + 1));
+  int reach = 32 * PER;
+  // two bits at a time: the counts of three thresholds side by side in one sum
+  for (; b >= kLow && reach > enough; b -= 2) {
+    const uint32_t half = b > kLow ? 1u << (b - 1) : 0u, one = 1u << b;  // the last bit alone: half 0
+    uint32_t n = 0;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        n += (key[j] >= (bound | half) ? 1u : 0u) + (key[j] >= (bound | one) ? 1u << 10 : 0u) +
-             (key[j] >= (bound | one | half) ? 1u << 20 : 0u);
-      n = __reduce_add_sync(~0u, n);
-      const int n1 = n & 1023, n2 = n >> 10 & 1023, n3 = n >> 20;
-      if (n3 >= k) {
-        bound |= one | half;
-        reach = n3;
-      } else if (n2 >= k) {
-        bound |= one;
-        reach = n2;
-      } else if (n1 >= k) {
-        bound |= half;
-        reach = n1;
-      }
-    }
-    if (bound <= kKeyNegInf) bound = kKeyNegInf + 1;
-    if (reach > enough) {  // every bit is fixed: the threads that tie differ below kLow at most
-      tie_top = bound | ((1u << kLow) - 1u);
-      int above = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) above += key[j] > tie_top;
-      above = __reduce_add_sync(~0u, above);
-      int most = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) most = max(most, vec[j]);
-      most = __reduce_max_sync(~0u, most);
-      bound_vec = 0;
-      for (int b = 31 - __clz(most | 1); b >= 0; --b) {
-        const int test = bound_vec | ((1 << b) - 1);
-        int n = 0;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) n += key[j] >= bound && key[j] <= tie_top && vec[j] <= test;
-        if (__reduce_add_sync(~0u, n) < k - above) bound_vec |= 1 << b;
-      }
+    for (int j = 0; j < PER; ++j)
+      n += (key[j] >= (bound | half) ? 1u : 0u) + (key[j] >= (bound | one) ? 1u << 10 : 0u) +
+           (key[j] >= (bound | one | half) ? 1u << 20 : 0u);
+    n = __reduce_add_sync(~0u, n);
+    const int n1 = n & 1023, n2 = n >> 10 & 1023, n3 = n >> 20;
+    if (n3 >= k) {
+      bound |= one | half;
+      reach = n3;
+    } else if (n2 >= k) {
+      bound |= one;
+      reach = n2;
+    } else if (n1 >= k) {
+      bound |= half;
+      reach = n1;
     }
   }
-  if (lane == 0) {
-    sh.bound_key = bound;
-    sh.bound_tie_top = tie_top;
-    sh.bound_vec = bound_vec;
-    sh.nlist = 0;
-    sh.ncand = 0;
+  t.key = max(bound, kKeyNegInf + 1);
+  if (reach > enough) {  // every bit is fixed: the groups that tie differ below kLow at most
+    t.tie_top = bound | ((1u << kLow) - 1u);
+    int above = 0, most = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      above += key[j] > t.tie_top;
+      most = max(most, vec[j]);
+    }
+    above = __reduce_add_sync(~0u, above);
+    most = __reduce_max_sync(~0u, most);
+    t.vec = 0;
+    for (int c = 31 - __clz(most | 1); c >= 0; --c) {
+      const int test = t.vec | ((1 << c) - 1);
+      int n = 0;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) n += key[j] >= t.key && key[j] <= t.tie_top && vec[j] <= test;
+      if (__reduce_add_sync(~0u, n) < k - above) t.vec |= 1 << c;
+    }
   }
+  return t;
 }
 
 // Places `n` distinct keys in descending order: put(place, key) for the first k.
@@ -627,10 +659,24 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
   sh.key[tid] = order_key(a.max);
   sh.vec[tid] = a.max_vec;
   __syncthreads();
-  if (tid < 32) top_bound<T>(sh, k);
+  if (tid < 32) {
+    uint32_t key[kTopThreads / 32];
+    int vec[kTopThreads / 32];
+#pragma unroll
+    for (int j = 0; j < kTopThreads / 32; ++j) {
+      key[j] = sh.key[j * 32 + tid];
+      vec[j] = sh.vec[j * 32 + tid];
+    }
+    // a few more threads than k cost less than the steps that would tell them apart
+    const TopBound t = top_bound<T>(key, vec, k, 2 * k + 8);
+    if (tid == 0) {
+      sh.bound = t;
+      sh.nlist = sh.ncand = 0;
+    }
+  }
   __syncthreads();
-  const uint32_t bound = sh.bound_key, tie_top = sh.bound_tie_top;
-  const int bound_vec = sh.bound_vec;
+  const uint32_t bound = sh.bound.key, tie_top = sh.bound.tie_top;
+  const int bound_vec = sh.bound.vec;
   const int per = 4 << groups.shift;  // vectors of a group
   if (sh.key[tid] >= bound) {
     for (int j = 0; part.begin + tid + j * per * kTopThreads < part.end; ++j) {
@@ -644,7 +690,7 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
   __syncthreads();
   const int nlist = sh.nlist;
   auto offer = [&](int i) {
-    const uint4 raw = row.load(i);
+    const uint4 raw = row.load_here(i);
     uint32_t hits = 0;  // a bit per element that reaches the bound
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
@@ -677,7 +723,7 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
   uint64_t last = ~0ull;
   for (int j = 0; j < k; ++j) {
     uint64_t best = 0;
-    for_vectors<kTopThreads>(row, part, [&](int i, const uint4& raw, bool) {
+    for_vectors<kTopThreads, true>(row, part, [&](int i, const uint4& raw, bool) {
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
         const uint64_t fk = full_key(vec_get<T>(raw, e), row.first(i) + e);
@@ -911,7 +957,7 @@ __device__ __forceinline__ bool owns(const Row<T>& row, const Part& part, int v)
 
 // A cluster of CTAs per row (one CTA where there are rows enough).  TOP: dynamic shared
 // memory holds rank 0's gathered keys (ctas k of them where ctas > 1), then the groups' tops.
-template <typename T, bool ENT, bool TOP, bool GRAD, int NT = TOP ? kTopThreads : GRAD ? 256 : 128>
+template <typename T, bool ENT, bool TOP, bool GRAD, int NT>
 __global__ void __launch_bounds__(NT, TOP ? 6 : 1280 / NT) k_logprobs(const LogprobArgs g, int group_shift, int* status) {
   extern __shared__ __align__(16) uint8_t dynamic[];
   __shared__ TotalsShared totals;
@@ -932,7 +978,7 @@ __global__ void __launch_bounds__(NT, TOP ? 6 : 1280 / NT) k_logprobs(const Logp
   TopGroups<T> groups{reinterpret_cast<typename TopGroups<T>::Key*>(gathered + (ctas > 1 ? ctas * g.k : 0)), group_shift, kNegInf};
   Sums a;
   TopMax<T> seen;
-  for_batches<NT>(row, part,
+  for_batches<NT, TOP>(row, part,
               [&](int i, const uint4& raw, bool) {
                 const float m = add_vec<T, ENT>(a, raw, c);
                 if (TOP) {
@@ -1020,8 +1066,8 @@ __global__ void __launch_bounds__(NT) k_logprobs_resident(const LogprobArgs g, i
 }
 
 // The backward pass alone: pieces of rows, every element on its own.
-template <typename T, bool ENT, int NT = 256>
-__global__ void __launch_bounds__(NT, 6) k_logprobs_backward(const LogprobArgs g, int pieces, int* status) {
+template <typename T, bool ENT, int NT>
+__global__ void __launch_bounds__(NT, 1536 / NT) k_logprobs_backward(const LogprobArgs g, int pieces, int* status) {
   grid_dependency_sync();
   release_dependents();
   const int vocab = g.v.vocab;
@@ -1504,7 +1550,7 @@ __global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs 
 
 // The backward pass alone, in pieces of rows.
 template <typename T, int NT>
-__global__ void __launch_bounds__(NT + 32) k_distill_backward(const DistillArgs g, int pieces, int* status) {
+__global__ void __launch_bounds__(NT + 32, 1280 / (NT + 32)) k_distill_backward(const DistillArgs g, int pieces, int* status) {
   __shared__ TeacherStats shared_stats;
   grid_dependency_sync();
   release_dependents();
@@ -1531,15 +1577,14 @@ __global__ void __launch_bounds__(NT + 32) k_distill_backward(const DistillArgs 
       load_logits(e, row);  // of entries that count, in time for store_entries
       if (threadIdx.x == NT) shared_stats = t;
     }
+    FirstFour<NT, T> first;
+    if (!teacher) first.load(row, part);
     __syncthreads();
     const TeacherStats t = shared_stats;
     const EntryGradient k = entry_gradient(t, st, w, g.tail, c, inv_t);
     if (!teacher) {
       if (k.zero) zero_part<NT>(out, piece, pieces);
-      else
-        for_vectors<NT>(row, part, [&](int i, const uint4& raw, bool whole) {
-          store_dense(row, out, i, raw, whole, k, c);
-        });
+      else first.use_all(row, part, [&](int i, const uint4& raw, bool whole) { store_dense(row, out, i, raw, whole, k, c); });
     }
     __syncthreads();  // and shared_stats is free again
     if (teacher && !k.zero) store_entries(row, out, part, e, st, k, inv_t);
@@ -1552,7 +1597,64 @@ __global__ void __launch_bounds__(NT + 32) k_distill_backward(const DistillArgs 
 // backward, or the backward pass alone; for rows so short that a block's barriers and its
 // threads' own fixed work would cost more than the row.
 constexpr int kShortWarps = 4;
-enum ShortMode { kShortForward, kShortBoth, kShortBackward };
+enum ShortMode { kShortForward, kShortTop, kShortBoth, kShortBackward };  // kShortTop: forward with alternatives
+
+// The k largest logits of a row that a warp has in its registers.
+template <typename T, int N>
+__device__ __forceinline__ void short_top(const Row<T>& row, const uint4 (&raw)[N], int k, const RowLogprob& s, float inv_t,
+                                          float* value, int32_t* index, uint64_t* cand, int* count) {
+  constexpr int kVec = Elem<T>::kVec;
+  const int lane = threadIdx.x & 31;
+  if (s.log_s != s.log_s) {  // NaN or +inf in the row
+    for (int j = lane; j < k; j += 32) {
+      value[j] = s.log_s;
+      index[j] = -1;
+    }
+    return;
+  }
+  uint32_t key[N];
+  int vec[N];
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    vec[u] = lane + 32 * u;
+    key[u] = order_key(Elem<T>::largest(raw[u]));
+  }
+  // at most max(k, 128) vectors reach the bound: their elements fit the candidates
+  const TopBound t = top_bound<T>(key, vec, k, max(k, min(2 * k + 8, kTopMaxK)));
+  if (lane == 0) *count = 0;
+  __syncwarp();
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    if (key[u] < t.key || (key[u] <= t.tie_top && vec[u] > t.vec)) continue;
+    uint32_t hits = 0;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      const uint32_t ek = order_key(vec_get<T>(raw[u], e));
+      if (ek >= t.key && (ek > t.tie_top || vec[u] <= t.vec)) hits |= 1u << e;
+    }
+    int at = atomicAdd(count, __popc(hits));
+#pragma unroll
+    for (int e = 0; e < kVec; ++e)
+      if (hits >> e & 1) cand[at++] = full_key(vec_get<T>(raw[u], e), row.first(vec[u]) + e);
+  }
+  __syncwarp();
+  const int n = *count;
+  for (int j = lane; j < n; j += 32) {
+    const uint64_t mine = cand[j];
+    int place = 0;
+#pragma unroll 8
+    for (int o = 0; o < n; ++o) place += cand[o] > mine;
+    if (place < k) {
+      index[place] = static_cast<int>(0xffffffffu - static_cast<uint32_t>(mine));
+      value[place] = (key_value(static_cast<uint32_t>(mine >> 32)) - s.ref) * inv_t - s.log_s;
+    }
+  }
+  for (int j = n + lane; j < k; j += 32) {
+    index[j] = -1;
+    value[j] = kNegInf;
+  }
+  __syncwarp();
+}
 
 template <typename T, typename Args, bool ENT, int MODE, int N>
 __global__ void __launch_bounds__(32 * kShortWarps) k_short(const Args g, int* status) {
@@ -1560,6 +1662,8 @@ __global__ void __launch_bounds__(32 * kShortWarps) k_short(const Args g, int* s
   constexpr int kVec = Elem<T>::kVec;
   constexpr int kKernel = DISTILL ? NSM_KERNEL_DISTILL : NSM_KERNEL_LOGPROBS;
   __shared__ uint32_t members[kShortWarps][DISTILL ? 32 * N / 4 : 1];  // a byte per vector, a bit per element
+  __shared__ uint64_t cand[kShortWarps][MODE == kShortTop ? kTopCandidates : 1];
+  __shared__ int ncand[kShortWarps];
   grid_dependency_sync();
   release_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1635,7 +1739,7 @@ __global__ void __launch_bounds__(32 * kShortWarps) k_short(const Args g, int* s
         write_loss(g, r, e, t, st);
         k = entry_gradient(t, outside, w, g.tail, c, inv_t);
       }
-      if constexpr (MODE != kShortForward) {
+      if constexpr (MODE != kShortForward) {  // kShortTop is not distillation's
         store(k.zero, [&](const uint4& v) { return gradient_vec<T, false>(v, k.ref, c, k.log2_s, k.scale, 0.f); });
         __syncwarp();  // the entries' own values go over what was written there
         if (!k.zero) {
@@ -1660,8 +1764,10 @@ __global__ void __launch_bounds__(32 * kShortWarps) k_short(const Args g, int* s
           if (32 * u < row.nvec) add_vec<T, ENT>(a, raw[u], c);
         s = row_logprob<ENT>(warp_totals<ENT>(a, c), inv_t);
         if (lane == 0) write_logprob<ENT>(g, r, s, token, x_token, inv_t);
+        if constexpr (MODE == kShortTop)
+          short_top<T, N>(row, raw, g.k, s, inv_t, g.top_logprob + r * g.k, g.top_index + r * g.k, cand[warp], &ncand[warp]);
       }
-      if constexpr (MODE != kShortForward) {
+      if constexpr (MODE == kShortBoth || MODE == kShortBackward) {
         const float w = g.d_logprob && token >= 0 ? g.d_logprob[r] : 0.f;
         const float h = ENT && g.d_entropy ? g.d_entropy[r] : 0.f;
         const TokenGradient k = token_gradient(w, h, s, low, c, inv_t);
@@ -1686,6 +1792,12 @@ int cluster_for(int64_t rows, int nvec, int NT) {
   while (ctas < kMaxCluster && rows * ctas * NT < 1024 * 152 && nvec >= ctas * 4 * NT) ctas *= 2;
   return ctas;
 }
+
+// Threads per row of a forward pass, and per piece of a row of a backward pass.  Measured on a
+// GB300: 16384 x 4000 bf16 forward 29 us with 64 threads, 43 with 128; 8192 x 131072 302 with 128,
+// 354 with 512; 16384 x 2100 backward 37 us with 64 and 58 with 256, 8192 x 131072 677 with 256.
+int forward_threads(int nvec) { return nvec <= 1024 ? 64 : 128; }
+int backward_threads(int nvec) { return nvec <= 1024 ? 64 : 256; }
 
 // Pieces per row of a backward pass: `most` vectors each, less where rows are few.
 int pieces_for(int64_t rows, int nvec, int most, int least) {
@@ -1770,7 +1882,7 @@ cudaError_t launch_short(int n, const Args& a, int* status, cudaStream_t stream)
 template <typename T>
 cudaError_t launch_logprobs_t(const LogprobArgs& a, int* status, cudaStream_t stream) {
   const int nvec = vectors_of<T>(a.v.vocab), n = short_for(nvec);
-  if (n > 0 && a.k == 0) {
+  if (n > 0) {
     const bool ent = a.d_entropy || a.entropy;
     if (a.in_lse)
       return ent ? launch_short<T, LogprobArgs, true, kShortBackward>(n, a, status, stream)
@@ -1778,15 +1890,17 @@ cudaError_t launch_logprobs_t(const LogprobArgs& a, int* status, cudaStream_t st
     if (a.v.d_logits)
       return ent ? launch_short<T, LogprobArgs, true, kShortBoth>(n, a, status, stream)
                  : launch_short<T, LogprobArgs, false, kShortBoth>(n, a, status, stream);
+    if (a.k > 0)
+      return ent ? launch_short<T, LogprobArgs, true, kShortTop>(n, a, status, stream)
+                 : launch_short<T, LogprobArgs, false, kShortTop>(n, a, status, stream);
     return ent ? launch_short<T, LogprobArgs, true, kShortForward>(n, a, status, stream)
                : launch_short<T, LogprobArgs, false, kShortForward>(n, a, status, stream);
   }
   if (a.in_lse) {
-    constexpr int kThreads = 256;
-    const int pieces = pieces_for(a.v.rows, nvec, 4 * kThreads, kThreads);
-    const int64_t grid = std::min<int64_t>(a.v.rows * pieces, 1 << 30);
-    return launch_clusters(a.d_entropy ? k_logprobs_backward<T, true, kThreads> : k_logprobs_backward<T, false, kThreads>,
-                           kThreads, grid, 1, 0, stream, a, pieces, status);
+    const int threads = backward_threads(nvec), pieces = pieces_for(a.v.rows, nvec, 4 * threads, threads);
+    auto* kernel = threads == 64 ? (a.d_entropy ? k_logprobs_backward<T, true, 64> : k_logprobs_backward<T, false, 64>)
+                                 : (a.d_entropy ? k_logprobs_backward<T, true, 256> : k_logprobs_backward<T, false, 256>);
+    return launch_clusters(kernel, threads, std::min<int64_t>(a.v.rows * pieces, 1 << 30), 1, 0, stream, a, pieces, status);
   }
   if (a.v.d_logits) {
     const Resident r = resident_for(a.v.rows, nvec);
@@ -1798,21 +1912,23 @@ cudaError_t launch_logprobs_t(const LogprobArgs& a, int* status, cudaStream_t st
       return launch_clusters(kernel, r.threads, a.v.rows * r.ctas, r.ctas, slab_bytes(nvec, r.ctas), stream, a, status);
     }
   }
-  const int threads = a.v.d_logits || a.k > 0 ? 256 : 128;
+  const int threads = a.v.d_logits || a.k > 0 ? 256 : forward_threads(nvec);
   const int ctas = cluster_for(a.v.rows, nvec, threads);
   const int64_t grid = a.v.rows * ctas;
   if (a.v.d_logits)
-    return launch_clusters(a.d_entropy || a.entropy ? k_logprobs<T, true, false, true> : k_logprobs<T, false, false, true>,
+    return launch_clusters(a.d_entropy || a.entropy ? k_logprobs<T, true, false, true, 256> : k_logprobs<T, false, false, true, 256>,
                            threads, grid, ctas, 0, stream, a, 0, status);
-  if (a.k == 0)
-    return launch_clusters(a.entropy ? k_logprobs<T, true, false, false> : k_logprobs<T, false, false, false>, threads, grid,
-                           ctas, 0, stream, a, 0, status);
+  if (a.k == 0) {
+    auto* kernel = threads == 64 ? (a.entropy ? k_logprobs<T, true, false, false, 64> : k_logprobs<T, false, false, false, 64>)
+                                 : (a.entropy ? k_logprobs<T, true, false, false, 128> : k_logprobs<T, false, false, false, 128>);
+    return launch_clusters(kernel, threads, grid, ctas, 0, stream, a, 0, status);
+  }
   const int batches = ((nvec + ctas - 1) / ctas + 4 * kTopThreads - 1) / (4 * kTopThreads);
   int shift = 0;
   while (((batches + (1 << shift) - 1) >> shift) > kTopGroups) ++shift;
   const size_t smem = (ctas > 1 ? size_t(ctas) * a.k * 8 : 0) +
                       size_t((batches + (1 << shift) - 1) >> shift) * kTopThreads * sizeof(typename TopGroups<T>::Key);
-  return launch_clusters(a.entropy ? k_logprobs<T, true, true, false> : k_logprobs<T, false, true, false>, threads, grid, ctas,
+  return launch_clusters(a.entropy ? k_logprobs<T, true, true, false, kTopThreads> : k_logprobs<T, false, true, false, kTopThreads>, threads, grid, ctas,
                          smem, stream, a, shift, status);
 }
 
@@ -1825,10 +1941,9 @@ cudaError_t launch_distill_t(const DistillArgs& a, int* status, cudaStream_t str
     return launch_short<T, DistillArgs, false, kShortForward>(n, a, status, stream);
   }
   if (a.in_lse) {
-    constexpr int kThreads = 256;
-    const int pieces = pieces_for(a.v.rows, nvec, 16 * kThreads, kThreads);
-    const int64_t grid = std::min<int64_t>(a.v.rows * pieces, 1 << 30);
-    return launch_clusters(k_distill_backward<T, kThreads>, kThreads + 32, grid, 1, 0, stream, a, pieces, status);
+    const int threads = backward_threads(nvec), pieces = pieces_for(a.v.rows, nvec, 16 * threads, threads);
+    auto* kernel = threads == 64 ? k_distill_backward<T, 64> : k_distill_backward<T, 256>;
+    return launch_clusters(kernel, threads + 32, std::min<int64_t>(a.v.rows * pieces, 1 << 30), 1, 0, stream, a, pieces, status);
   }
   if (a.v.d_logits) {
     const Resident r = resident_for(a.v.rows, nvec);
@@ -1839,12 +1954,11 @@ cudaError_t launch_distill_t(const DistillArgs& a, int* status, cudaStream_t str
       return launch_clusters(kernel, r.threads + 32, a.v.rows * r.ctas, r.ctas, slab_bytes(nvec, r.ctas), stream, a, status);
     }
   }
-  constexpr int kThreads = 128, kGradThreads = 256;
-  const int threads = a.v.d_logits ? kGradThreads : kThreads;
+  const int threads = a.v.d_logits ? 256 : forward_threads(nvec);
   int ctas = cluster_for(a.v.rows, nvec, threads);
   auto members = [&] { return (static_cast<size_t>((nvec + ctas - 1) / ctas) + 2 + 15) / 16 * 16; };
   while (members() > kMembersMost && ctas < kMaxCluster) ctas *= 2;
-  auto* kernel = a.v.d_logits ? k_distill<T, true, kGradThreads> : k_distill<T, false, kThreads>;
+  auto* kernel = a.v.d_logits ? k_distill<T, true, 256> : threads == 64 ? k_distill<T, false, 64> : k_distill<T, false, 128>;
   return launch_clusters(kernel, threads + 32, a.v.rows * ctas, ctas, members(), stream, a, status);
 }
 

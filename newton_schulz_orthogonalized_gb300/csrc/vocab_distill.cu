@@ -9,8 +9,8 @@
 //   k_distill            forward: as k_logprobs, S taken out by a bit per element.
 //                        8192 x 131072 bf16 323 us (6.7 TB/s), 1024 x 50257 28.
 //   k_distill_resident   forward and backward in one pass, the row in shared memory, the
-//                        teacher in a warp of its own: 8192 x 32768 bf16, 64 entries 177 us (6.1
-//                        TB/s), 8192 x 131072 (four blocks a row) 870.  Bound by the latency of the
+//                        teacher in a warp of its own: 8192 x 32768 bf16, 64 entries 174 us (6.2
+//                        TB/s), 8192 x 131072 (four blocks a row) 815.  Bound by the latency of the
 //                        entries' loads before the sums and by the cluster's slowest block.
 //   k_distill_backward   pieces of rows from saved statistics: 8192 x 131072 737 us (5.8 TB/s).
 //   k_distill_short      a warp per row of at most 256 vectors: 16384 x 259, loss and gradient 23 us.
@@ -29,10 +29,10 @@ __device__ __forceinline__ V warp_sum(V v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
-  return v;
+__device__ __forceinline__ float warp_max(float v) {  // NaNs aside
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // The teacher of a row lives in one warp (a warp of its own beside the ones that sum the row,
@@ -84,6 +84,13 @@ __device__ __forceinline__ void load_entries(Entries& e, const DistillArgs& g, i
     e.v[u] = v[u] >= 0 && v[u] < g.v.vocab ? static_cast<int>(v[u]) : -1;
     e.x[u] = kNegInf;
   }
+}
+
+// Asks for a later row's entries in L2, sector by sector.
+__device__ __forceinline__ void prefetch_entries(const DistillArgs& g, int64_t r) {
+  const int lane = threadIdx.x & 31, index_size = g.index_wide ? 8 : 4, score_size = g.teacher_dtype == NSM_FP32 ? 4 : 2;
+  if (lane * 32 < g.k * index_size) ptx::prefetch_l2(static_cast<const char*>(g.index) + r * g.ldi * index_size + lane * 32);
+  if (lane * 32 < g.k * score_size) ptx::prefetch_l2(static_cast<const char*>(g.teacher) + r * g.ldt * score_size + lane * 32);
 }
 
 // The student's logits at the entries' tokens, read from the row.
@@ -379,7 +386,7 @@ __global__ void __launch_bounds__(NT + 32) k_distill(const DistillArgs g, int* s
 
 // Forward and backward in one pass over memory, as k_logprobs_resident.
 template <typename T, int NT>
-__global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs g, int* status) {
+__global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs g, int ahead, int* status) {
   extern __shared__ __align__(16) uint8_t dynamic[];
   __shared__ TotalsShared totals;
   __shared__ TeacherStats shared_stats;
@@ -400,10 +407,13 @@ __global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs 
   Slab<T, NT> slab;
   slab.start(row, part, reinterpret_cast<uint4*>(dynamic), &slab_shared);  // ends with a barrier
   const float w = g.d_loss ? g.d_loss[r] : 1.f;
+  if (threadIdx.x == 0 && r + ahead < g.v.rows)
+    slab.prefetch(Row<T>(static_cast<T*>(const_cast<void*>(g.v.logits)) + (r + ahead) * g.v.ld, vocab, status, NSM_KERNEL_DISTILL), rank, ctas);
   Entries e;
   Sums a;
   if (teacher) {
     load_entries(e, g, r);
+    if (rank == 0 && r + ahead < g.v.rows) prefetch_entries(g, r + ahead);
     // What other blocks of the cluster hold of the row comes from memory; of the rest, the chunk
     // it comes with and its place there.
     T elsewhere[kLaneEntries];
@@ -606,7 +616,8 @@ cudaError_t launch_distill_t(const DistillArgs& a, int* status, cudaStream_t str
       auto* kernel = r.threads == 64    ? k_distill_resident<T, 64>
                      : r.threads == 128 ? k_distill_resident<T, 128>
                                         : k_distill_resident<T, 256>;
-      return launch_clusters(kernel, r.threads + 32, a.v.rows * r.ctas, r.ctas, slab_bytes(nvec, r.ctas), stream, a, status);
+      return launch_clusters(kernel, r.threads + 32, a.v.rows * r.ctas, r.ctas, slab_bytes(nvec, r.ctas), stream, a,
+                             rows_ahead(slab_bytes(nvec, r.ctas), r.threads, r.ctas), status);
     }
   }
   const int threads = a.v.d_logits ? 256 : forward_threads(nvec);

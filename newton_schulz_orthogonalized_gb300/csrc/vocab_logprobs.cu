@@ -6,10 +6,10 @@
 //
 //   k_logprobs           forward: a block per row, a cluster of blocks where rows are few; one
 //                        pass, alternatives from groups that can hold one.  Bound by the read:
-//                        8192 x 131072 bf16 297 us (7.2 TB/s), with 64 alternatives 353.
+//                        8192 x 131072 bf16 297 us (7.2 TB/s), with 64 alternatives 359.
 //   k_logprobs_resident  forward and backward in one pass over memory, the row in shared memory:
-//                        8192 x 32768 bf16 160 us (6.7 TB/s read and written), 8192 x 50257 275,
-//                        8192 x 131072 (four blocks a row) 778: the blocks of a cluster wait for
+//                        8192 x 32768 bf16 157 us (6.8 TB/s read and written), 8192 x 50257 262,
+//                        8192 x 131072 (four blocks a row) 692: the blocks of a cluster wait for
 //                        their slowest.
 //   k_logprobs_backward  pieces of rows from saved statistics: 8192 x 131072 677 us (6.3 TB/s).
 //   k_logprobs_short     a warp per row of at most 256 vectors, every direction: 16384 x 1000
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(NT, TOP ? 6 : 1280 / NT) k_logprobs(const Logp
 // Forward and backward in one pass over memory: the row stays in the shared memory of the
 // cluster's blocks between its sums and its gradient.
 template <typename T, bool ENT, int NT>
-__global__ void __launch_bounds__(NT) k_logprobs_resident(const LogprobArgs g, int* status) {
+__global__ void __launch_bounds__(NT) k_logprobs_resident(const LogprobArgs g, int ahead, int* status) {
   extern __shared__ __align__(16) uint8_t dynamic[];
   __shared__ TotalsShared totals;
   __shared__ SlabShared slab_shared;
@@ -476,6 +476,8 @@ __global__ void __launch_bounds__(NT) k_logprobs_resident(const LogprobArgs g, i
   const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, NSM_KERNEL_LOGPROBS);
   Slab<T, NT> slab;
   slab.start(row, part_of(row, rank, ctas), reinterpret_cast<uint4*>(dynamic), &slab_shared);
+  if (threadIdx.x == 0 && r + ahead < g.v.rows)
+    slab.prefetch(Row<T>(static_cast<T*>(const_cast<void*>(g.v.logits)) + (r + ahead) * g.v.ld, vocab, status, NSM_KERNEL_LOGPROBS), rank, ctas);
   const int64_t token64 = g.tokens ? load_index(g.tokens, g.tokens_wide, r) : -1;
   const int token = token64 < 0 || token64 >= vocab ? -1 : static_cast<int>(token64);
   const float x_token = token >= 0 ? Elem<T>::to_float(row.p[token]) : kNegInf;
@@ -684,7 +686,8 @@ cudaError_t launch_logprobs_t(const LogprobArgs& a, int* status, cudaStream_t st
       auto* kernel = r.threads == 64    ? (ent ? k_logprobs_resident<T, true, 64> : k_logprobs_resident<T, false, 64>)
                      : r.threads == 128 ? (ent ? k_logprobs_resident<T, true, 128> : k_logprobs_resident<T, false, 128>)
                                         : (ent ? k_logprobs_resident<T, true, 256> : k_logprobs_resident<T, false, 256>);
-      return launch_clusters(kernel, r.threads, a.v.rows * r.ctas, r.ctas, slab_bytes(nvec, r.ctas), stream, a, status);
+      return launch_clusters(kernel, r.threads, a.v.rows * r.ctas, r.ctas, slab_bytes(nvec, r.ctas), stream, a,
+                             rows_ahead(slab_bytes(nvec, r.ctas), r.threads, r.ctas), status);
     }
   }
   const int threads = a.v.d_logits || a.k > 0 ? 256 : forward_threads(nvec);

@@ -540,6 +540,12 @@ struct Slab {
     if (part.tail >= 0 && threadIdx.x == kTailThread) v[part.tail - base] = row.load(part.tail);
     __syncthreads();  // the barriers are there
   }
+  // Asks for a later row's part in L2.
+  __device__ __forceinline__ void prefetch(const Row<T>& later, int piece, int pieces) const {
+    const Part p = part_of(later, piece, pieces);
+    if (p.end > p.begin && bounds_ok(later.whole(p.begin) && later.whole(p.end - 1), status, kernel, NSM_ROLE_PRODUCER, NSM_SITE_LOGITS))
+      ptx::bulk_prefetch_l2(later.p + later.first(p.begin), (p.end - p.begin) * 16);
+  }
   __device__ __forceinline__ void wait(int q) const { wait_on(&sh->full[q]); }
   // Until a barrier's first phase is over.  After a wait that ran out (recorded) the block goes on with
   // what is there, so that every barrier is still met; drain() then waits once more.
@@ -650,13 +656,23 @@ constexpr size_t kSlabBytes = 76 << 10, kSlabAlone = 112 << 10, kSlabMost = 216 
 
 inline size_t slab_bytes(int nvec, int ctas) { return (static_cast<size_t>((nvec + ctas - 1) / ctas) + 2) * 16; }
 
+// A block keeps memory busy only while its own row is on the way, not in its passes.  So each
+// asks for a part of a later row in L2 when it has asked for its own: of a row half as far on as
+// there are rows on the GPU, whose block starts about when the copy is there.  Measured on a
+// GB300, loss and gradient of 8192 x 131072 bf16: 786 us without, 692 at half as far (and at a
+// quarter), 732 as far as the rows on the GPU, 879 at twice that; 2000 x 151936 fp32 411 and 355.
+inline int rows_ahead(size_t slab, int threads, int ctas) {
+  const int blocks = static_cast<int>(std::min<size_t>((227 << 10) / (slab + 2048), 2048 / threads));
+  return std::max(1, 152 * blocks / 2 / ctas);
+}
+
 // Threads and CTAs per row that keep it in shared memory; ctas 0 where it does not fit.
 struct Resident {
   int threads, ctas;
 };
 // Measured on a GB300, loss and gradient in bf16: slabs of 64 KB, three blocks a SM, 32768
-// columns 162 us for 8192 rows (98% of the copy rate); the same row over two blocks of a cluster
-// 208 us, so a row stays in one block up to 112 KB (50257 columns 281 us in one, 302 in two) where
+// columns 162 us for 8192 rows (98% of the copy rate), the same row over two blocks of a cluster
+// 208 us, both before the copies to L2 of rows_ahead(); so a row stays in one block up to 112 KB (50257 columns 281 us in one, 302 in two) where
 // rows are many; beyond, clusters of 76 KB slabs (131072 columns 777 us in four, 822 in eight).
 // Eight vectors a thread: 8000 columns 47 us with 128 threads, 62 with 256.
 inline Resident resident_for(int64_t rows, int nvec) {

@@ -7,12 +7,12 @@
 //   1 + excess = sum p + p_r.
 //
 //   k_distill            forward: as k_logprobs, S taken out by a bit per element.
-//                        8192 x 131072 bf16 323 us (6.7 TB/s), 1024 x 50257 28.
+//                        8192 x 131072 bf16 321 us (6.7 TB/s), 1024 x 50257 22.
 //   k_distill_resident   forward and backward in one pass, the row in shared memory, the
-//                        teacher in a warp of its own: 8192 x 32768 bf16, 64 entries 174 us (6.2
-//                        TB/s), 8192 x 131072 (four blocks a row) 815.  Bound by the latency of the
+//                        teacher in a warp of its own: 8192 x 32768 bf16, 64 entries 171 us (6.3
+//                        TB/s), 8192 x 131072 (four blocks a row) 714.  Bound by the latency of the
 //                        entries' loads before the sums and by the cluster's slowest block.
-//   k_distill_backward   pieces of rows from saved statistics: 8192 x 131072 737 us (5.8 TB/s).
+//   k_distill_backward   pieces of rows from saved statistics: 8192 x 131072 733 us (5.9 TB/s).
 //   k_distill_short      a warp per row of at most 256 vectors: 16384 x 259, loss and gradient 23 us.
 #include "vocab_rows.cuh"
 
@@ -54,12 +54,16 @@ __device__ __forceinline__ V load_if(bool p, const void* from, int64_t i, V othe
   return p ? static_cast<const V*>(from)[i] : otherwise;
 }
 
-// The entries' tokens and scores (in log_p); equal tokens are still there.  Every load is on its
-// way before the first is looked at: under load each takes microseconds.
-__device__ __forceinline__ void load_entries(Entries& e, const DistillArgs& g, int64_t r) {
+// The entries as they are in memory.  Every load is on its way before the first is looked at:
+// under load each takes microseconds.
+struct RawEntries {
+  int64_t v[kLaneEntries];
+  uint32_t score[kLaneEntries];
+};
+__device__ __forceinline__ void load_raw(RawEntries& raw, const DistillArgs& g, int64_t r) {
   const int lane = threadIdx.x & 31;
   const int64_t at_index = r * g.ldi + lane, at_score = r * g.ldt + lane;
-  int64_t v[kLaneEntries];
+  int64_t* v = raw.v;
   if (g.index_wide) {
 #pragma unroll
     for (int u = 0; u < kLaneEntries; ++u) v[u] = load_if<int64_t>(lane + 32 * u < g.k, g.index, at_index + 32 * u, -1);
@@ -69,21 +73,36 @@ __device__ __forceinline__ void load_entries(Entries& e, const DistillArgs& g, i
   }
   if (g.teacher_dtype == NSM_FP32) {
 #pragma unroll
-    for (int u = 0; u < kLaneEntries; ++u) e.log_p[u] = load_if<float>(lane + 32 * u < g.k, g.teacher, at_score + 32 * u, kNegInf);
+    for (int u = 0; u < kLaneEntries; ++u) raw.score[u] = load_if<uint32_t>(lane + 32 * u < g.k, g.teacher, at_score + 32 * u, 0);
+  } else {
+#pragma unroll
+    for (int u = 0; u < kLaneEntries; ++u) raw.score[u] = load_if<uint16_t>(lane + 32 * u < g.k, g.teacher, at_score + 32 * u, 0);
+  }
+}
+
+// The entries' tokens and scores (in log_p); equal tokens are still there.
+__device__ __forceinline__ void entries_of(Entries& e, const RawEntries& raw, const DistillArgs& g) {
+  if (g.teacher_dtype == NSM_FP32) {
+#pragma unroll
+    for (int u = 0; u < kLaneEntries; ++u) e.log_p[u] = __uint_as_float(raw.score[u]);
   } else {
     const bool bf16 = g.teacher_dtype == NSM_BF16;
-    uint16_t h[kLaneEntries];
 #pragma unroll
-    for (int u = 0; u < kLaneEntries; ++u) h[u] = load_if<uint16_t>(lane + 32 * u < g.k, g.teacher, at_score + 32 * u, 0);
-#pragma unroll
-    for (int u = 0; u < kLaneEntries; ++u)
-      e.log_p[u] = bf16 ? __bfloat162float(__ushort_as_bfloat16(h[u])) : __half2float(__ushort_as_half(h[u]));
+    for (int u = 0; u < kLaneEntries; ++u) {
+      const uint16_t h = static_cast<uint16_t>(raw.score[u]);
+      e.log_p[u] = bf16 ? __bfloat162float(__ushort_as_bfloat16(h)) : __half2float(__ushort_as_half(h));
+    }
   }
 #pragma unroll
   for (int u = 0; u < kLaneEntries; ++u) {
-    e.v[u] = v[u] >= 0 && v[u] < g.v.vocab ? static_cast<int>(v[u]) : -1;
+    e.v[u] = raw.v[u] >= 0 && raw.v[u] < g.v.vocab ? static_cast<int>(raw.v[u]) : -1;
     e.x[u] = kNegInf;
   }
+}
+__device__ __forceinline__ void load_entries(Entries& e, const DistillArgs& g, int64_t r) {
+  RawEntries raw;
+  load_raw(raw, g, r);
+  entries_of(e, raw, g);
 }
 
 // Asks for a later row's entries in L2, sector by sector.
@@ -205,7 +224,11 @@ __device__ __forceinline__ Student student_of(const TeacherStats& t, const Total
   st.lse_ref = st.empty ? 0.f : all.max;
   st.lse_log = st.empty ? 0.f : logf(all.s);
   st.rest_ref = no_rest ? 0.f : outside.max;
-  st.rest = no_rest ? kNegInf : (outside.max - st.lse_ref) * inv_t + (logf(outside.s) - st.lse_log);
+  // where the entries have the smaller part: log (1 - q of the entries), which a difference of
+  // two logs would lose
+  st.rest = no_rest                   ? kNegInf
+            : inside_s < 0.5f * all.s ? log1pf(-inside_s / all.s)
+                                      : (outside.max - st.lse_ref) * inv_t + (logf(outside.s) - st.lse_log);
   return st;
 }
 
@@ -294,22 +317,30 @@ __device__ __forceinline__ void store_dense(const Row<T>& row, const Row<T>& out
   else out.store(row.first(i), grad);
 }
 
-// The teacher's warp writes the gradients at the entries of the block's part, over what the
-// pass over the row wrote there.
+// The gradients at the entries, and their way into the block's part over what the pass over the
+// row wrote there: the teacher's warp has the first done when that pass ends.
 template <typename T>
-__device__ __forceinline__ void store_entries(const Row<T>& row, const Row<T>& out, const Part& part, const Entries& e,
-                                              const Student& s, const EntryGradient& k, float inv_t) {
+__device__ __forceinline__ void entry_gradients(T (&grads)[kLaneEntries], const Entries& e, const Student& s, const EntryGradient& k,
+                                                float inv_t) {
 #pragma unroll
   for (int u = 0; u < kLaneEntries; ++u) {
-    if (e.v[u] < 0 || !in_part(row, part, e.v[u])) continue;
+    if (e.v[u] < 0) continue;
     const float log_q = ((e.x[u] - s.lse_ref) - s.lse_low) * inv_t - s.lse_log, p = e.p[u];
     float grad = 0.f;
     if (log_q != kNegInf) {  // q - p without cancellation
       const float q = expf(log_q);
       grad = k.unit * ((p > 0.f || p != p ? p * expm1f(log_q - e.log_p[u]) : q) + q * k.excess);
     }
-    if (bounds_ok(e.v[u] < out.vocab, out.status, out.kernel, 0, NSM_SITE_GRADIENT)) out.p[e.v[u]] = Elem<T>::from_float(grad);
+    grads[u] = Elem<T>::from_float(grad);
   }
+}
+template <typename T>
+__device__ __forceinline__ void store_entries(const T (&grads)[kLaneEntries], const Row<T>& row, const Row<T>& out, const Part& part,
+                                              const Entries& e) {
+#pragma unroll
+  for (int u = 0; u < kLaneEntries; ++u)
+    if (e.v[u] >= 0 && in_part(row, part, e.v[u]) && bounds_ok(e.v[u] < out.vocab, out.status, out.kernel, 0, NSM_SITE_GRADIENT))
+      out.p[e.v[u]] = grads[u];
 }
 
 // NT threads sum the row (a cluster of blocks per row where rows are few), a warp more has the
@@ -335,6 +366,8 @@ __global__ void __launch_bounds__(NT + 32) k_distill(const DistillArgs g, int* s
   const int bytes = (part.tail >= 0 ? part.tail + 1 : part.end) - base;
   Entries e;
   Sums a;
+  FirstFour<NT, T> first;
+  if (!teacher) first.load(row, part);
   if (teacher) load_entries(e, g, r);
   else
     for (int i = tid; i < (bytes + 15) / 16; i += NT) reinterpret_cast<uint4*>(members)[i] = make_uint4(0, 0, 0, 0);
@@ -355,14 +388,14 @@ __global__ void __launch_bounds__(NT + 32) k_distill(const DistillArgs g, int* s
     t.inside = inside_totals(e, c);
     if (tid == NT) shared_stats = t;
   } else {  // the student outside the entries
-    for_vectors<NT>(row, part, [&](int i, const uint4& raw, bool) {
+    first.use_all(row, part, [&](int i, const uint4& raw, bool) {
       const uint32_t bits = members[i - base];
       uint4 v = raw;
       if (bits) vec_mask<T>(v, bits);
       add_vec<T, false>(a, v, c);
     });
   }
-  const Totals outside = row_totals<false, NT>(a, c, totals, ctas, status, NSM_KERNEL_DISTILL);
+  const Totals outside = row_totals<false, NT>(a, c, totals, ctas, status, NSM_KERNEL_DISTILL, 0.f);
   const TeacherStats t = shared_stats;
   Student st;
   if (teacher) {
@@ -379,8 +412,10 @@ __global__ void __launch_bounds__(NT + 32) k_distill(const DistillArgs g, int* s
           store_dense(row, out, i, raw, whole, k, c);
         });
     }
+    T grads[kLaneEntries];
+    if (teacher) entry_gradients(grads, e, st, k, inv_t);
     __syncthreads();
-    if (teacher && !k.zero) store_entries(row, out, part, e, st, k, inv_t);
+    if (teacher && !k.zero) store_entries(grads, row, out, part, e);
   }
 }
 
@@ -404,6 +439,8 @@ __global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs 
   const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, NSM_KERNEL_DISTILL);
   const Part part = part_of(row, rank, ctas);
   if (tid < kSlabChunks) ptx::mbar_init(ptx::smem_u32(&ready[tid]), 1);
+  RawEntries raw;
+  if (teacher) load_raw(raw, g, r);
   Slab<T, NT> slab;
   slab.start(row, part, reinterpret_cast<uint4*>(dynamic), &slab_shared);  // ends with a barrier
   const float w = g.d_loss ? g.d_loss[r] : 1.f;
@@ -412,7 +449,7 @@ __global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs 
   Entries e;
   Sums a;
   if (teacher) {
-    load_entries(e, g, r);
+    entries_of(e, raw, g);
     if (rank == 0 && r + ahead < g.v.rows) prefetch_entries(g, r + ahead);
     // What other blocks of the cluster hold of the row comes from memory; of the rest, the chunk
     // it comes with and its place there.
@@ -461,7 +498,7 @@ __global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs 
       if (q == 0) slab.ragged(add);
     }
   }
-  const Totals outside = row_totals<false, NT>(a, c, totals, ctas, status, NSM_KERNEL_DISTILL);
+  const Totals outside = row_totals<false, NT>(a, c, totals, ctas, status, NSM_KERNEL_DISTILL, 0.f);
   const TeacherStats t = shared_stats;
   const EntryGradient k = entry_gradient(t, outside, w, g.tail, c, inv_t);
   Student st;
@@ -474,8 +511,10 @@ __global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs 
     slab.all([&](int i, const uint4& raw, bool whole) { store_dense(row, out, i, raw, whole, k, c);
     });
   }
+  T grads[kLaneEntries];
+  if (teacher) entry_gradients(grads, e, st, k, inv_t);
   __syncthreads();
-  if (teacher && !k.zero) store_entries(row, out, part, e, st, k, inv_t);
+  if (teacher && !k.zero) store_entries(grads, row, out, part, e);
   slab.drain();
 }
 
@@ -517,8 +556,10 @@ __global__ void __launch_bounds__(NT + 32, 1280 / (NT + 32)) k_distill_backward(
       if (k.zero) zero_part<NT>(out, piece, pieces);
       else first.use_all(row, part, [&](int i, const uint4& raw, bool whole) { store_dense(row, out, i, raw, whole, k, c); });
     }
+    T grads[kLaneEntries];
+    if (teacher) entry_gradients(grads, e, st, k, inv_t);
     __syncthreads();  // and shared_stats is free again
-    if (teacher && !k.zero) store_entries(row, out, part, e, st, k, inv_t);
+    if (teacher && !k.zero) store_entries(grads, row, out, part, e);
   }
 }
 
@@ -582,7 +623,11 @@ __global__ void __launch_bounds__(32 * kShortWarps) k_distill_short(const Distil
       x.store(row, out, part, k.zero,
               [&](const uint4& v) { return gradient_vec<T, false>(v, k.ref, c, k.log2_s, k.scale, 0.f); });
       __syncwarp();  // the entries' own values go over what was written there
-      if (!k.zero) store_entries(row, out, part, e, st, k, inv_t);
+      if (!k.zero) {
+        T grads[kLaneEntries];
+        entry_gradients(grads, e, st, k, inv_t);
+        store_entries(grads, row, out, part, e);
+      }
     }
   }
 }
@@ -611,7 +656,7 @@ cudaError_t launch_distill_t(const DistillArgs& a, int* status, cudaStream_t str
     return launch_clusters(kernel, threads + 32, std::min<int64_t>(a.v.rows * pieces, 1 << 30), 1, 0, stream, a, pieces, status);
   }
   if (a.v.d_logits) {
-    const Resident r = resident_for(a.v.rows, nvec);
+    const Resident r = resident_for(a.v.rows, nvec, 112 << 10);
     if (r.ctas) {
       auto* kernel = r.threads == 64    ? k_distill_resident<T, 64>
                      : r.threads == 128 ? k_distill_resident<T, 128>

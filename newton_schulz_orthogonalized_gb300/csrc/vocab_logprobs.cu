@@ -6,11 +6,10 @@
 //
 //   k_logprobs           forward: a block per row, a cluster of blocks where rows are few; one
 //                        pass, alternatives from groups that can hold one.  Bound by the read:
-//                        8192 x 131072 bf16 297 us (7.2 TB/s), with 64 alternatives 359.
+//                        8192 x 131072 bf16 297 us (7.2 TB/s), with 64 alternatives 355.
 //   k_logprobs_resident  forward and backward in one pass over memory, the row in shared memory:
-//                        8192 x 32768 bf16 157 us (6.8 TB/s read and written), 8192 x 50257 262,
-//                        8192 x 131072 (four blocks a row) 692: the blocks of a cluster wait for
-//                        their slowest.
+//                        8192 x 32768 bf16 157 us, 8192 x 50257 243, 8192 x 131072 (four blocks
+//                        a row) 620: the rate of a copy, 6.8 TB/s read and written.
 //   k_logprobs_backward  pieces of rows from saved statistics: 8192 x 131072 677 us (6.3 TB/s).
 //   k_logprobs_short     a warp per row of at most 256 vectors, every direction: 16384 x 1000
 //                        forward 8 us, forward and backward 16.
@@ -426,7 +425,7 @@ __global__ void __launch_bounds__(NT, TOP ? 6 : 1280 / NT) k_logprobs(const Logp
               [&](int n) {
                 if (TOP) groups.batch(n);
               });
-  const Totals t = row_totals<ENT, NT>(a, c, totals, ctas, status, NSM_KERNEL_LOGPROBS);
+  const Totals t = row_totals<ENT, NT>(a, c, totals, ctas, status, NSM_KERNEL_LOGPROBS, x_token);
   const RowLogprob s = row_logprob<ENT>(t, inv_t);
   if (rank == 0 && threadIdx.x == 0) write_logprob<ENT>(g, r, s, token, x_token, inv_t);
   if constexpr (GRAD) {
@@ -485,13 +484,13 @@ __global__ void __launch_bounds__(NT) k_logprobs_resident(const LogprobArgs g, i
   const float h = ENT && g.d_entropy ? g.d_entropy[r] : 0.f;
   Sums a;
   auto add = [&](int, const uint4& raw, bool) { add_vec<T, ENT>(a, raw, c); };
-  slab.ragged(add);
 #pragma unroll 1
   for (int q = 0; q < kSlabChunks; ++q) {
     slab.wait(q);
     slab.chunk(q, add);
+    if (q == 0) slab.ragged(add);
   }
-  const Totals t = row_totals<ENT, NT>(a, c, totals, ctas, status, NSM_KERNEL_LOGPROBS);
+  const Totals t = row_totals<ENT, NT>(a, c, totals, ctas, status, NSM_KERNEL_LOGPROBS, x_token);
   const RowLogprob s = row_logprob<ENT>(t, inv_t);
   if (rank == 0 && threadIdx.x == 0) write_logprob<ENT>(g, r, s, token, x_token, inv_t);
   const TokenGradient k = token_gradient(w, h, s, 0.f, c, inv_t);
@@ -680,7 +679,7 @@ cudaError_t launch_logprobs_t(const LogprobArgs& a, int* status, cudaStream_t st
     return launch_clusters(kernel, threads, std::min<int64_t>(a.v.rows * pieces, 1 << 30), 1, 0, stream, a, pieces, status);
   }
   if (a.v.d_logits) {
-    const Resident r = resident_for(a.v.rows, nvec);
+    const Resident r = resident_for(a.v.rows, nvec, 76 << 10);
     if (r.ctas) {
       const bool ent = a.d_entropy || a.entropy;
       auto* kernel = r.threads == 64    ? (ent ? k_logprobs_resident<T, true, 64> : k_logprobs_resident<T, false, 64>)

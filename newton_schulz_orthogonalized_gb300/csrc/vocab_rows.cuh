@@ -416,28 +416,35 @@ __device__ __forceinline__ Totals warp_totals(const Sums& a, float c) {
 
 // The totals of every CTA's threads of a cluster relative to the row's largest logit, the
 // same in every thread: warps, then CTAs, in a fixed order.  Every thread of the block calls
-// this, the sums of the first NT count; the next use of `sh` needs a barrier.  The CTAs
-// exchange theirs through a barrier in shared memory that counts one arrival from each: only
-// the threads that send wait for their stores, not the whole block.  With more than one CTA,
-// start_totals comes first.
+// this, the sums of the first NT count; the next use of `sh` needs a barrier.  With more than
+// one CTA, start_totals comes first.
+// Each CTA stores its totals in the others' shared memory, counted as bytes on a barrier there:
+// one way over the cluster and no wait for it.  With plain stores and a remote arrival behind
+// them, which waits until they are done, loss and gradient of 8192 x 131072 bf16 took 662 us for
+// 617, and a message per warp in place of one per CTA 415 us for 347 with 2000 x 151936 fp32 over
+// eight CTAs (distillation; over four it saves 1%).
+// `read` is what the thread has read of the row and still needs: it goes along, so that its load
+// is over before another CTA can write a gradient there.
 struct TotalsShared {
   Totals warp[kMaxWarps];
-  Totals cta[kMaxCluster];
+  float4 cta[kMaxCluster];
   uint64_t joined;
   int abort;
 };
 __device__ __forceinline__ void start_totals(TotalsShared& sh, int ctas) {
   if (ctas == 1) return;
-  if (threadIdx.x == 0) {
-    ptx::mbar_init(ptx::smem_u32(&sh.joined), ctas);
+  if (threadIdx.x == 32) {  // the first warp starts the row's copies
+    const uint32_t bar = ptx::smem_u32(&sh.joined);
+    ptx::mbar_init(bar, 1);
     sh.abort = 0;
     ptx::fence_mbarrier_init();
+    ptx::mbar_arrive_expect_tx(bar, ctas * sizeof(float4));
   }
   __syncwarp();
   ptx::cluster_arrive();  // the wait is in row_totals: by then every CTA runs
 }
 template <bool ENT, int NT>
-__device__ __forceinline__ Totals row_totals(const Sums& a, float c, TotalsShared& sh, int ctas, int* status, int kernel) {
+__device__ __forceinline__ Totals row_totals(const Sums& a, float c, TotalsShared& sh, int ctas, int* status, int kernel, float read) {
   const Totals w = warp_totals<ENT>(a, c);
   if ((threadIdx.x & 31) == 0 && threadIdx.x < NT) sh.warp[threadIdx.x >> 5] = w;
   if (ctas > 1) ptx::cluster_wait();
@@ -445,26 +452,17 @@ __device__ __forceinline__ Totals row_totals(const Sums& a, float c, TotalsShare
   const Totals v = sh.warp[threadIdx.x & (NT / 32 - 1)];
   const Totals mine = group_totals<ENT, NT / 32>(v.max, v.max, v.s, v.sy, c);
   if (ctas == 1) return mine;
-  if (static_cast<int>(threadIdx.x) < ctas) {
-    const uint32_t to = ptx::mapa_shared(ptx::smem_u32(&sh.cta[ptx::cluster_ctarank()]), threadIdx.x);
-    ptx::st_cluster_f32(to, mine.max);
-    ptx::st_cluster_f32(to + 4, mine.s);
-    ptx::st_cluster_f32(to + 8, mine.sy);
-    ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&sh.joined), threadIdx.x));
-  }
-  if (!ptx::mbar_wait_bounded_cluster(ptx::smem_u32(&sh.joined), 0, &sh.abort, kWaitNs)) {
+  const uint32_t bar = ptx::smem_u32(&sh.joined);
+  if (static_cast<int>(threadIdx.x) < ctas)
+    ptx::st_async_f32x4(ptx::mapa_shared(ptx::smem_u32(&sh.cta[ptx::cluster_ctarank()]), threadIdx.x), mine.max, mine.s, mine.sy, read,
+                        ptx::mapa_shared(bar, threadIdx.x));
+  if (!ptx::mbar_wait_bounded_cluster(bar, 0, &sh.abort, kWaitNs)) {
     record_timeout(status, kernel, NSM_ROLE_EPILOGUE, NSM_SITE_ACC_FULL);
     *static_cast<volatile int*>(&sh.abort) = 1;
   }
-  Totals t{kNegInf, 0.f, 0.f};
-  for (int r = 0; r < ctas; ++r) t.max = fmaxf(t.max, sh.cta[r].max);
-  for (int r = 0; r < ctas; ++r) {
-    Totals o = sh.cta[r];
-    rebase<ENT>(o.s, o.sy, o.max, t.max, c);
-    t.s += o.s;
-    t.sy += o.sy;
-  }
-  return t;
+  const int from = threadIdx.x & (kMaxCluster - 1);
+  const float4 t = from < ctas ? sh.cta[from] : make_float4(kNegInf, 0.f, 0.f, 0.f);
+  return group_totals<ENT, kMaxCluster>(t.x, t.x, t.y, t.z, c);
 }
 
 // One vector of gradients q (ca + cb log2 q), q = 2^((x - ref) c - log2_s).
@@ -519,26 +517,30 @@ struct Slab {
     kernel = row.kernel;
     base = part.head >= 0 ? part.head : part.begin;
     each = max(2, (part.end - part.begin + kSlabChunks * NT - 1) / (kSlabChunks * NT)) * NT;
-    if (threadIdx.x == 0) {
-#pragma unroll
-      for (int q = 0; q < kSlabChunks; ++q) ptx::mbar_init(ptx::smem_u32(&sh->full[q]), 1);
-      sh->abort = 0;
+    // The ragged vectors count as copies of the first chunk: two threads of the second warp load
+    // them and say when they are there.
+    const int ragged = threadIdx.x == 32 ? part.head : threadIdx.x == 33 ? part.tail : -1;
+    uint4 ragged_vec;
+    if (ragged >= 0) ragged_vec = row.load(ragged);
+    if (threadIdx.x < kSlabChunks) {  // a thread per chunk
+      const int q = threadIdx.x;
+      const int b = min(part.end, part.begin + q * each), e = min(part.end, b + each);
+      const uint32_t bar = ptx::smem_u32(&sh->full[q]);
+      ptx::mbar_init(bar, 1 + (q == 0 ? (part.head >= 0) + (part.tail >= 0) : 0));
+      if (q == 0) sh->abort = 0;
       ptx::fence_mbarrier_init();
-#pragma unroll
-      for (int q = 0; q < kSlabChunks; ++q) {
-        const int b = min(part.end, part.begin + q * each), e = min(part.end, b + each);
-        const uint32_t bar = ptx::smem_u32(&sh->full[q]);
-        bool load = e > b;
-        if (load)
-          load = bounds_ok(row.whole(b) && row.whole(e - 1) && (reinterpret_cast<uintptr_t>(row.p + row.first(b)) & 15) == 0,
-                           status, kernel, NSM_ROLE_PRODUCER, NSM_SITE_LOGITS);
-        ptx::mbar_arrive_expect_tx(bar, load ? (e - b) * 16 : 0);
-        if (load) ptx::bulk_load(ptx::smem_u32(v + (b - base)), row.p + row.first(b), (e - b) * 16, bar);
-      }
+      bool load = e > b;
+      if (load)
+        load = bounds_ok(row.whole(b) && row.whole(e - 1) && (reinterpret_cast<uintptr_t>(row.p + row.first(b)) & 15) == 0,
+                         status, kernel, NSM_ROLE_PRODUCER, NSM_SITE_LOGITS);
+      ptx::mbar_arrive_expect_tx(bar, load ? (e - b) * 16 : 0);
+      if (load) ptx::bulk_load(ptx::smem_u32(v + (b - base)), row.p + row.first(b), (e - b) * 16, bar);
     }
-    if (part.head >= 0 && threadIdx.x == kHeadThread) v[part.head - base] = row.load(part.head);
-    if (part.tail >= 0 && threadIdx.x == kTailThread) v[part.tail - base] = row.load(part.tail);
     __syncthreads();  // the barriers are there
+    if (ragged >= 0) {
+      v[ragged - base] = ragged_vec;
+      ptx::mbar_arrive(ptx::smem_u32(&sh->full[0]));
+    }
   }
   // Asks for a later row's part in L2.
   __device__ __forceinline__ void prefetch(const Row<T>& later, int piece, int pieces) const {
@@ -562,6 +564,7 @@ struct Slab {
 #pragma unroll 2
     for (int i = b + static_cast<int>(threadIdx.x); i < e; i += NT) use(i, v[i - base], true);
   }
+  // The same for the ragged vectors, after the wait for the first chunk.
   template <typename F>
   __device__ __forceinline__ void ragged(F&& use) const {
     if (part.head >= 0 && threadIdx.x == kHeadThread) use(part.head, v[part.head - base], false);
@@ -632,10 +635,12 @@ struct ShortRow {
 // ---------------------------------------------------------------- launches
 
 // CTAs per row: where there are fewer rows than the GPU takes blocks at a time, a cluster
-// shares each row, down to two vectors of a thread.
+// shares each row, down to two vectors of a thread, until 256 threads a SM are there.  Measured on
+// a GB300 with 256, 512 and 160 a SM: 600 x 32000 bf16 6.8, 8.1 and 6.7 us, 300 x 131072 19.5, 21.7
+// and 29.1, 64 x 50257 with 20 alternatives 8.6, 13.1 and 9.0.
 inline int cluster_for(int64_t rows, int nvec, int NT) {
   int ctas = 1;
-  while (ctas < kMaxCluster && rows * ctas * NT < 1024 * 152 && nvec >= ctas * 4 * NT) ctas *= 2;
+  while (ctas < kMaxCluster && rows * ctas * NT < 256 * 152 && nvec >= ctas * 4 * NT) ctas *= 2;
   return ctas;
 }
 
@@ -652,7 +657,7 @@ inline int pieces_for(int64_t rows, int nvec, int most, int least) {
   return (nvec + each - 1) / each;
 }
 
-constexpr size_t kSlabBytes = 76 << 10, kSlabAlone = 112 << 10, kSlabMost = 216 << 10;
+constexpr size_t kSlabBytes = 76 << 10, kSlabMost = 216 << 10;
 
 inline size_t slab_bytes(int nvec, int ctas) { return (static_cast<size_t>((nvec + ctas - 1) / ctas) + 2) * 16; }
 
@@ -661,6 +666,8 @@ inline size_t slab_bytes(int nvec, int ctas) { return (static_cast<size_t>((nvec
 // there are rows on the GPU, whose block starts about when the copy is there.  Measured on a
 // GB300, loss and gradient of 8192 x 131072 bf16: 786 us without, 692 at half as far (and at a
 // quarter), 732 as far as the rows on the GPU, 879 at twice that; 2000 x 151936 fp32 411 and 355.
+// The passes that only read, or read and write in pieces, are slower with it: 8192 x 131072 with
+// 64 alternatives 542 us for 359, distillation's backward pass 1072 for 737.
 inline int rows_ahead(size_t slab, int threads, int ctas) {
   const int blocks = static_cast<int>(std::min<size_t>((227 << 10) / (slab + 2048), 2048 / threads));
   return std::max(1, 152 * blocks / 2 / ctas);
@@ -670,14 +677,18 @@ inline int rows_ahead(size_t slab, int threads, int ctas) {
 struct Resident {
   int threads, ctas;
 };
-// Measured on a GB300, loss and gradient in bf16: slabs of 64 KB, three blocks a SM, 32768
-// columns 162 us for 8192 rows (98% of the copy rate), the same row over two blocks of a cluster
-// 208 us, both before the copies to L2 of rows_ahead(); so a row stays in one block up to 112 KB (50257 columns 281 us in one, 302 in two) where
-// rows are many; beyond, clusters of 76 KB slabs (131072 columns 777 us in four, 822 in eight).
+// Measured on a GB300, loss and gradient in bf16: slabs of 64 KB, three blocks a SM, 8192 x 32768
+// 157 us (the rate of a copy), the same row over two blocks of a cluster 171.  Beyond 76 KB a row is
+// shared by a cluster, with 56 KB as the limit 8192 x 131072 takes 688 us for 620; `alone`, the
+// most that a row keeps in one block where rows are many, is 76 KB as well for log probabilities
+// (8192 x 50257 243 us over two blocks, 258 in one of 112 KB) and 112 KB for distillation, whose
+// blocks each wait for the row's entries (291 us over two, 282 in one).
 // Eight vectors a thread: 8000 columns 47 us with 128 threads, 62 with 256.
-inline Resident resident_for(int64_t rows, int nvec) {
+// Where rows are few, clusters grow until 1024 threads a SM are there: 257 x 32003 fp32 16.6 us,
+// 17.5 with half or twice as many.
+inline Resident resident_for(int64_t rows, int nvec, size_t alone) {
   Resident r{256, 1};
-  if (rows < 2048 || slab_bytes(nvec, 1) > kSlabAlone)
+  if (rows < 2048 || slab_bytes(nvec, 1) > alone)
     while (r.ctas < kMaxCluster && slab_bytes(nvec, r.ctas) > kSlabBytes) r.ctas *= 2;
   if (slab_bytes(nvec, r.ctas) > kSlabMost) return Resident{0, 0};
   while (r.threads > 64 && nvec < r.threads * 8) r.threads /= 2;

@@ -6,10 +6,10 @@
 //
 //   k_logprobs           forward: a block per row, a cluster of blocks where rows are few; one
 //                        pass, alternatives from groups that can hold one.  Bound by the read:
-//                        8192 x 131072 bf16 297 us (7.2 TB/s), with 64 alternatives 355.
+//                        8192 x 131072 bf16 297 us (7.2 TB/s), with 64 alternatives 360.
 //   k_logprobs_resident  forward and backward in one pass over memory, the row in shared memory:
-//                        8192 x 32768 bf16 157 us, 8192 x 50257 243, 8192 x 131072 (four blocks
-//                        a row) 620: the rate of a copy, 6.8 TB/s read and written.
+//                        8192 x 32768 bf16 158 us, 8192 x 50257 244, 8192 x 131072 (four blocks
+//                        a row) 625: the rate of a copy, 6.8 TB/s read and written.
 //   k_logprobs_backward  pieces of rows from saved statistics: 8192 x 131072 677 us (6.3 TB/s).
 //   k_logprobs_short     a warp per row of at most 256 vectors, every direction: 16384 x 1000
 //                        forward 8 us, forward and backward 16.
@@ -488,8 +488,8 @@ __global__ void __launch_bounds__(NT) k_logprobs_resident(const LogprobArgs g, i
   for (int q = 0; q < kSlabChunks; ++q) {
     slab.wait(q);
     slab.chunk(q, add);
-    if (q == 0) slab.ragged(add);
   }
+  slab.ragged(add);  // in the loop this costs the first passes more than it is (254 us for 244)
   const Totals t = row_totals<ENT, NT>(a, c, totals, ctas, status, NSM_KERNEL_LOGPROBS, x_token);
   const RowLogprob s = row_logprob<ENT>(t, inv_t);
   if (rank == 0 && threadIdx.x == 0) write_logprob<ENT>(g, r, s, token, x_token, inv_t);

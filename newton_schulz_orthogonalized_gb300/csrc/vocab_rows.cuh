@@ -564,7 +564,7 @@ struct Slab {
 #pragma unroll 2
     for (int i = b + static_cast<int>(threadIdx.x); i < e; i += NT) use(i, v[i - base], true);
   }
-  // The same for the ragged vectors, after the wait for the first chunk.
+  // The same for the ragged vectors, which come with the first chunk.
   template <typename F>
   __device__ __forceinline__ void ragged(F&& use) const {
     if (part.head >= 0 && threadIdx.x == kHeadThread) use(part.head, v[part.head - base], false);

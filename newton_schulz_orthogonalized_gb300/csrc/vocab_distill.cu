@@ -327,9 +327,11 @@ __device__ __forceinline__ void entry_gradients(T (&grads)[kLaneEntries], const 
     if (e.v[u] < 0) continue;
     const float log_q = ((e.x[u] - s.lse_ref) - s.lse_low) * inv_t - s.lse_log, p = e.p[u];
     float grad = 0.f;
-    if (log_q != kNegInf) {  // q - p without cancellation
-      const float q = expf(log_q);
-      grad = k.unit * ((p > 0.f || p != p ? p * expm1f(log_q - e.log_p[u]) : q) + q * k.excess);
+    if (log_q != kNegInf) {
+      // q - p without cancellation where they are near.  Where q is far larger, p may be a subnormal
+      // number with few digits, or 0, and expm1 of the distance infinite: there the difference itself.
+      const float q = expf(log_q), apart = log_q - e.log_p[u];
+      grad = k.unit * ((apart < 1.f ? p * expm1f(apart) : q - p) + q * k.excess);
     }
     grads[u] = Elem<T>::from_float(grad);
   }

@@ -14,6 +14,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "nsm_internal.h"
 
 namespace nsm {
@@ -24,6 +26,24 @@ __device__ __forceinline__ void grid_dependency_sync() {
 
 __device__ __forceinline__ void release_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Raises a kernel's limit of dynamic shared memory to `bytes`, the most that any launch of it
+// asks for, once per device (`done`: a bit each, one variable per kernel).  The default is 48 KB
+// less what the kernel declares.  The limit belongs to the kernel in the whole process: set to
+// what one call needs it could be lowered between another thread's call and its launch.
+template <typename K>
+inline cudaError_t set_smem_once(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+  if (!bit || !(done.load() & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit);
+  }
+  return cudaSuccess;
 }
 
 inline bool pdl_enabled() { return pdl_for_launches(); }

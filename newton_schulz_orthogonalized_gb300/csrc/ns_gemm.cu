@@ -1044,20 +1044,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 
 // ===================================================================== launchers
 
-template <typename K>
-cudaError_t set_smem_once(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
-  if (!bit || !(done.load() & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e != cudaSuccess) return e;
-    done.fetch_or(bit);
-  }
-  return cudaSuccess;
-}
-
 template <bool B_MN, bool FP16, bool HAS_AUX, bool NARROW>
 cudaError_t launch_pair(const GemmLaunch& l, int num_sms, cudaStream_t stream, int* status) {
   static std::atomic<uint64_t> done{0};

@@ -563,20 +563,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename K>
-cudaError_t set_smem_once(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
-  if (!bit || !(done.load() & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e != cudaSuccess) return e;
-    done.fetch_or(bit);
-  }
-  return cudaSuccess;
-}
-
 template <bool FP16>
 cudaError_t launch_typed(const SmallJob* jobs, int njobs, const SmallOp* ops, int nops, int num_sms,
                          cudaStream_t stream) {

@@ -638,10 +638,10 @@ __global__ void __launch_bounds__(32 * kShortWarps) k_distill_short(const Distil
 
 template <typename T, int MODE>
 cudaError_t launch_distill_short(int n, const DistillArgs& a, int* status, cudaStream_t stream) {
-  auto* kernel = n == 2   ? k_distill_short<T, MODE, 2>
-                 : n == 4 ? k_distill_short<T, MODE, 4>
-                          : k_distill_short<T, MODE, 8>;
-  return launch_clusters(kernel, 32 * kShortWarps, short_blocks(a.v.rows), 1, 0, stream, a, status);
+  auto* launch = n == 2   ? Launch<k_distill_short<T, MODE, 2>>::run
+                 : n == 4 ? Launch<k_distill_short<T, MODE, 4>>::run
+                          : Launch<k_distill_short<T, MODE, 8>>::run;
+  return launch(32 * kShortWarps, short_blocks(a.v.rows), 1, 0, 0, stream, a, status);
 }
 
 template <typename T>
@@ -654,25 +654,27 @@ cudaError_t launch_distill_t(const DistillArgs& a, int* status, cudaStream_t str
   }
   if (a.in_lse) {
     const int threads = backward_threads(nvec), pieces = pieces_for(a.v.rows, nvec, 16 * threads, threads);
-    auto* kernel = threads == 64 ? k_distill_backward<T, 64> : k_distill_backward<T, 256>;
-    return launch_clusters(kernel, threads + 32, std::min<int64_t>(a.v.rows * pieces, 1 << 30), 1, 0, stream, a, pieces, status);
+    auto* launch = threads == 64 ? Launch<k_distill_backward<T, 64>>::run : Launch<k_distill_backward<T, 256>>::run;
+    return launch(threads + 32, std::min<int64_t>(a.v.rows * pieces, 1 << 30), 1, 0, 0, stream, a, pieces, status);
   }
   if (a.v.d_logits) {
     const Resident r = resident_for(a.v.rows, nvec, 112 << 10);
     if (r.ctas) {
-      auto* kernel = r.threads == 64    ? k_distill_resident<T, 64>
-                     : r.threads == 128 ? k_distill_resident<T, 128>
-                                        : k_distill_resident<T, 256>;
-      return launch_clusters(kernel, r.threads + 32, a.v.rows * r.ctas, r.ctas, slab_bytes(nvec, r.ctas), stream, a,
-                             rows_ahead(slab_bytes(nvec, r.ctas), r.threads, r.ctas), status);
+      auto* launch = r.threads == 64    ? Launch<k_distill_resident<T, 64>>::run
+                     : r.threads == 128 ? Launch<k_distill_resident<T, 128>>::run
+                                        : Launch<k_distill_resident<T, 256>>::run;
+      const size_t slab = slab_bytes(nvec, r.ctas);
+      return launch(r.threads + 32, a.v.rows * r.ctas, r.ctas, slab, kSlabMost, stream, a, rows_ahead(slab, r.threads, r.ctas), status);
     }
   }
   const int threads = a.v.d_logits ? 256 : forward_threads(nvec);
   int ctas = cluster_for(a.v.rows, nvec, threads);
   auto members = [&] { return (static_cast<size_t>((nvec + ctas - 1) / ctas) + 2 + 15) / 16 * 16; };
   while (members() > kMembersMost && ctas < kMaxCluster) ctas *= 2;
-  auto* kernel = a.v.d_logits ? k_distill<T, true, 256> : threads == 64 ? k_distill<T, false, 64> : k_distill<T, false, 128>;
-  return launch_clusters(kernel, threads + 32, a.v.rows * ctas, ctas, members(), stream, a, status);
+  auto* launch = a.v.d_logits   ? Launch<k_distill<T, true, 256>>::run
+                 : threads == 64 ? Launch<k_distill<T, false, 64>>::run
+                                 : Launch<k_distill<T, false, 128>>::run;
+  return launch(threads + 32, a.v.rows * ctas, ctas, members(), kMembersMost, stream, a, status);
 }
 
 }  // namespace

@@ -649,10 +649,10 @@ __global__ void __launch_bounds__(32 * kShortWarps) k_logprobs_short(const Logpr
 
 template <typename T, bool ENT, int MODE>
 cudaError_t launch_logprobs_short(int n, const LogprobArgs& a, int* status, cudaStream_t stream) {
-  auto* kernel = n == 2   ? k_logprobs_short<T, ENT, MODE, 2>
-                 : n == 4 ? k_logprobs_short<T, ENT, MODE, 4>
-                          : k_logprobs_short<T, ENT, MODE, 8>;
-  return launch_clusters(kernel, 32 * kShortWarps, short_blocks(a.v.rows), 1, 0, stream, a, status);
+  auto* launch = n == 2   ? Launch<k_logprobs_short<T, ENT, MODE, 2>>::run
+                 : n == 4 ? Launch<k_logprobs_short<T, ENT, MODE, 4>>::run
+                          : Launch<k_logprobs_short<T, ENT, MODE, 8>>::run;
+  return launch(32 * kShortWarps, short_blocks(a.v.rows), 1, 0, 0, stream, a, status);
 }
 
 template <typename T>
@@ -674,39 +674,46 @@ cudaError_t launch_logprobs_t(const LogprobArgs& a, int* status, cudaStream_t st
   }
   if (a.in_lse) {
     const int threads = backward_threads(nvec), pieces = pieces_for(a.v.rows, nvec, 4 * threads, threads);
-    auto* kernel = threads == 64 ? (a.d_entropy ? k_logprobs_backward<T, true, 64> : k_logprobs_backward<T, false, 64>)
-                                 : (a.d_entropy ? k_logprobs_backward<T, true, 256> : k_logprobs_backward<T, false, 256>);
-    return launch_clusters(kernel, threads, std::min<int64_t>(a.v.rows * pieces, 1 << 30), 1, 0, stream, a, pieces, status);
+    auto* launch = threads == 64
+                       ? (a.d_entropy ? Launch<k_logprobs_backward<T, true, 64>>::run : Launch<k_logprobs_backward<T, false, 64>>::run)
+                       : (a.d_entropy ? Launch<k_logprobs_backward<T, true, 256>>::run : Launch<k_logprobs_backward<T, false, 256>>::run);
+    return launch(threads, std::min<int64_t>(a.v.rows * pieces, 1 << 30), 1, 0, 0, stream, a, pieces, status);
   }
   if (a.v.d_logits) {
     const Resident r = resident_for(a.v.rows, nvec, 76 << 10);
     if (r.ctas) {
       const bool ent = a.d_entropy || a.entropy;
-      auto* kernel = r.threads == 64    ? (ent ? k_logprobs_resident<T, true, 64> : k_logprobs_resident<T, false, 64>)
-                     : r.threads == 128 ? (ent ? k_logprobs_resident<T, true, 128> : k_logprobs_resident<T, false, 128>)
-                                        : (ent ? k_logprobs_resident<T, true, 256> : k_logprobs_resident<T, false, 256>);
-      return launch_clusters(kernel, r.threads, a.v.rows * r.ctas, r.ctas, slab_bytes(nvec, r.ctas), stream, a,
-                             rows_ahead(slab_bytes(nvec, r.ctas), r.threads, r.ctas), status);
+      auto* launch =
+          r.threads == 64    ? (ent ? Launch<k_logprobs_resident<T, true, 64>>::run : Launch<k_logprobs_resident<T, false, 64>>::run)
+          : r.threads == 128 ? (ent ? Launch<k_logprobs_resident<T, true, 128>>::run : Launch<k_logprobs_resident<T, false, 128>>::run)
+                             : (ent ? Launch<k_logprobs_resident<T, true, 256>>::run : Launch<k_logprobs_resident<T, false, 256>>::run);
+      const size_t slab = slab_bytes(nvec, r.ctas);
+      return launch(r.threads, a.v.rows * r.ctas, r.ctas, slab, kSlabMost, stream, a, rows_ahead(slab, r.threads, r.ctas), status);
     }
   }
   const int threads = a.v.d_logits || a.k > 0 ? 256 : forward_threads(nvec);
   const int ctas = cluster_for(a.v.rows, nvec, threads);
   const int64_t grid = a.v.rows * ctas;
-  if (a.v.d_logits)
-    return launch_clusters(a.d_entropy || a.entropy ? k_logprobs<T, true, false, true, 256> : k_logprobs<T, false, false, true, 256>,
-                           threads, grid, ctas, 0, stream, a, 0, status);
+  if (a.v.d_logits) {
+    auto* launch = a.d_entropy || a.entropy ? Launch<k_logprobs<T, true, false, true, 256>>::run
+                                            : Launch<k_logprobs<T, false, false, true, 256>>::run;
+    return launch(threads, grid, ctas, 0, 0, stream, a, 0, status);
+  }
   if (a.k == 0) {
-    auto* kernel = threads == 64 ? (a.entropy ? k_logprobs<T, true, false, false, 64> : k_logprobs<T, false, false, false, 64>)
-                                 : (a.entropy ? k_logprobs<T, true, false, false, 128> : k_logprobs<T, false, false, false, 128>);
-    return launch_clusters(kernel, threads, grid, ctas, 0, stream, a, 0, status);
+    auto* launch =
+        threads == 64 ? (a.entropy ? Launch<k_logprobs<T, true, false, false, 64>>::run : Launch<k_logprobs<T, false, false, false, 64>>::run)
+                      : (a.entropy ? Launch<k_logprobs<T, true, false, false, 128>>::run : Launch<k_logprobs<T, false, false, false, 128>>::run);
+    return launch(threads, grid, ctas, 0, 0, stream, a, 0, status);
   }
   const int batches = ((nvec + ctas - 1) / ctas + 4 * kTopThreads - 1) / (4 * kTopThreads);
   int shift = 0;
   while (((batches + (1 << shift) - 1) >> shift) > kTopGroups) ++shift;
   const size_t smem = (ctas > 1 ? size_t(ctas) * a.k * 8 : 0) +
                       size_t((batches + (1 << shift) - 1) >> shift) * kTopThreads * sizeof(typename TopGroups<T>::Key);
-  return launch_clusters(a.entropy ? k_logprobs<T, true, true, false, kTopThreads> : k_logprobs<T, false, true, false, kTopThreads>, threads, grid, ctas,
-                         smem, stream, a, shift, status);
+  constexpr size_t kMost = size_t(kMaxCluster) * kTopMaxK * 8 + size_t(kTopGroups) * kTopThreads * sizeof(typename TopGroups<T>::Key);
+  auto* launch = a.entropy ? Launch<k_logprobs<T, true, true, false, kTopThreads>>::run
+                           : Launch<k_logprobs<T, false, true, false, kTopThreads>>::run;
+  return launch(threads, grid, ctas, smem, kMost, stream, a, shift, status);
 }
 
 }  // namespace

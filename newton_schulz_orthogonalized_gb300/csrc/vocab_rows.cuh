@@ -701,33 +701,40 @@ int vectors_of(int vocab) {
   return (vocab + 2 * Elem<T>::kVec - 2) / Elem<T>::kVec;  // at any alignment
 }
 
-template <typename... K, typename... A>
-cudaError_t launch_clusters(void (*kernel)(K...), int threads, int64_t grid, int ctas, size_t smem, cudaStream_t stream, A... args) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+// A kernel's launches: clusters of `ctas` blocks with `smem` bytes of dynamic shared memory each, of
+// which no launch of that kernel asks for more than `most`.
+template <auto KERNEL>
+struct Launch;
+template <typename... K, void (*KERNEL)(K...)>
+struct Launch<KERNEL> {
+  static cudaError_t run(int threads, int64_t grid, int ctas, size_t smem, size_t most, cudaStream_t stream, K... args) {
+    if (most > 0) {
+      static std::atomic<uint64_t> done{0};
+      const cudaError_t e = set_smem_once(KERNEL, most, done);
+      if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (pdl_enabled()) {
+      attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (ctas > 1) {
+      attr[n].id = cudaLaunchAttributeClusterDimension;
+      attr[n].val.clusterDim.x = static_cast<unsigned>(ctas);
+      attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+      ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, KERNEL, args...);
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-  if (pdl_enabled()) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (ctas > 1) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = static_cast<unsigned>(ctas);
-    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-    ++n;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<K>(args)...);
-}
+};
 
 // Vectors per lane of a warp per row, 0 where rows are too long for that.  Measured on a GB300
 // against blocks of 64 to 256 threads per row, 16384 rows: 259 columns bf16, distillation's loss

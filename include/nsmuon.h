@@ -258,6 +258,7 @@ size_t nsm_gemm_scratch_bytes(int M, int N, int flags);
  *     logprob = y_token - lse                 entropy = -sum_v q_v log q_v  (0 log 0 = 0)
  *
  * Conventions of these calls:
+ *   - Buffers marked `device` are memory of the current device, where the kernels run.
  *   - logits: device, rows x vocab elements of `dtype` (NSM_BF16, NSM_FP16 or NSM_FP32) at
  *     row stride ld >= vocab elements, unit column stride, aligned to an element (16-byte
  *     aligned rows are fastest).  1 <= vocab <= 2^20; rows may be 0 (nothing is launched).

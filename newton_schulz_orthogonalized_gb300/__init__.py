@@ -386,13 +386,14 @@ DISTILL_MAX_K = 128
 _LOGITS_TYPES: dict = {}
 _INDEX_TYPES: dict = {}
 _FLOAT32 = _INT32 = None
-_raw_stream = None
+_raw_stream = _current_device = None
 
 
 def _torch_types() -> None:
     """torch's types as the library's codes, once torch is there."""
-    global _FLOAT32, _INT32, _raw_stream
+    global _FLOAT32, _INT32, _raw_stream, _current_device
     import torch
+    _current_device = torch.cuda.current_device
     _LOGITS_TYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
     _INDEX_TYPES.update({torch.int32: 0, torch.int64: 1})
     _FLOAT32, _INT32 = torch.float32, torch.int32
@@ -444,6 +445,8 @@ def _logits(logits) -> Tuple[int, int, int, int, int, int]:
         raise ValueError("logits is not a matrix of rows x vocab in device memory")
     rows, vocab = logits.shape
     device = logits.get_device()
+    if device != _current_device():  # the kernels run there, whatever the logits' device is
+        raise ValueError(f"logits is on {logits.device}, not on the current device")
     ptr, code, ld = _matrix("logits", logits, _LOGITS_TYPES, rows, vocab, device)
     return ptr, code, rows, vocab, ld, device
 
@@ -482,7 +485,8 @@ def logprobs(logits, tokens, logprob=None, entropy=None, lse=None, top_logprob=N
     -100: no token) or None.  Writes the outputs that are given: ``logprob``, ``entropy``
     and ``lse`` (float32, one per row), and the k largest logits as log probabilities
     ``top_logprob`` (float32, rows x k) with their indexes ``top_index`` (int32, rows x k),
-    ties by ascending index."""
+    ties by ascending index.  The tensors are on the current device, here and in the calls
+    below."""
     ptr, code, rows, vocab, ld, dev = _logits(logits)
     row = (rows,)
     t_ptr, wide = _tokens(tokens, rows, dev)

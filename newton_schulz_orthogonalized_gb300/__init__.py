@@ -386,19 +386,21 @@ DISTILL_MAX_K = 128
 _LOGITS_TYPES: dict = {}
 _INDEX_TYPES: dict = {}
 _FLOAT32 = _INT32 = None
-_raw_stream = _current_device = None
+_raw_stream = _current_device = _increment_version = None
 
 
 def _torch_types() -> None:
     """torch's types as the library's codes, once torch is there."""
-    global _FLOAT32, _INT32, _raw_stream, _current_device
+    global _FLOAT32, _INT32, _raw_stream, _current_device, _increment_version
     import torch
-    _current_device = torch.cuda.current_device
     _LOGITS_TYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
     _INDEX_TYPES.update({torch.int32: 0, torch.int64: 1})
     _FLOAT32, _INT32 = torch.float32, torch.int32
-    # the current stream's handle without a Stream object: a third of a short call's time
+    # what torch's public functions call: the current stream's handle without a Stream object is a
+    # third of a short call's time, the other two save a fifth
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _increment_version = getattr(torch._C, "_increment_version", None) or torch.autograd.graph.increment_version
 
 
 def _loss_stream(stream, device: int) -> int:
@@ -416,12 +418,12 @@ def _matrix(name: str, t, codes, rows: int, cols: int, device: int) -> Tuple[int
         raise ValueError(f"{name} has type {t.dtype}: one of {[str(c) for c in codes]} is wanted")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}: ({rows}, {cols}) is wanted")
-    stride = t.stride()
-    if cols > 1 and stride[1] != 1:
-        raise ValueError(f"{name} has column stride {stride[1]}: 1 is wanted")
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name} has column stride {step}: 1 is wanted")
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, not on the logits' device")
-    return t.data_ptr(), code, (stride[0] if rows > 1 else max(stride[0], cols))
+    return t.data_ptr(), code, (ld if rows > 1 else max(ld, cols))
 
 
 def _numbers(name: str, t, shape: Tuple[int, ...], device: int, dtype) -> int:
@@ -437,18 +439,30 @@ def _numbers(name: str, t, shape: Tuple[int, ...], device: int, dtype) -> int:
     return t.data_ptr()
 
 
+def _written(*tensors) -> None:
+    """Tells torch that these were written in place, so that a backward pass that saved one of
+    them raises in place of using what is there now."""
+    _increment_version([t for t in tensors if t is not None])
+
+
 def _logits(logits) -> Tuple[int, int, int, int, int, int]:
     """(pointer, type code, rows, vocab, row stride, device)."""
     if _FLOAT32 is None:
         _torch_types()
-    if logits.dim() != 2 or not logits.is_cuda:
+    device = logits.get_device()  # -1: host memory
+    shape = logits.shape
+    if len(shape) != 2 or device < 0:
         raise ValueError("logits is not a matrix of rows x vocab in device memory")
-    rows, vocab = logits.shape
-    device = logits.get_device()
     if device != _current_device():  # the kernels run there, whatever the logits' device is
         raise ValueError(f"logits is on {logits.device}, not on the current device")
-    ptr, code, ld = _matrix("logits", logits, _LOGITS_TYPES, rows, vocab, device)
-    return ptr, code, rows, vocab, ld, device
+    rows, vocab = shape
+    code = _LOGITS_TYPES.get(logits.dtype)
+    if code is None:
+        raise ValueError(f"logits has type {logits.dtype}: one of {[str(c) for c in _LOGITS_TYPES]} is wanted")
+    ld, step = logits.stride()
+    if vocab > 1 and step != 1:
+        raise ValueError(f"logits has column stride {step}: 1 is wanted")
+    return logits.data_ptr(), code, rows, vocab, (ld if rows > 1 else max(ld, vocab)), device
 
 
 def _tokens(tokens, rows: int, device: int) -> Tuple[int, int]:
@@ -460,17 +474,18 @@ def _tokens(tokens, rows: int, device: int) -> Tuple[int, int]:
     return _numbers("tokens", tokens, (rows,), device, tokens.dtype), code
 
 
-def _gradient(name: str, t, logits, device: int) -> Tuple[int, int]:
-    if t is not None and t.dtype != logits.dtype:
-        raise ValueError(f"{name} has type {t.dtype}: the logits' {logits.dtype} is wanted")
-    ptr, _, ld = _matrix(name, t, _LOGITS_TYPES, logits.shape[0], logits.shape[1], device)
-    return ptr, ld
+def _gradient(t, code: int, rows: int, vocab: int, device: int) -> Tuple[int, int]:
+    ptr, own_code, ldd = _matrix("d_logits", t, _LOGITS_TYPES, rows, vocab, device)
+    if own_code != code:
+        raise ValueError(f"d_logits has type {t.dtype}: the logits' is wanted")
+    return ptr, ldd
 
 
 def _entries(teacher, index, rows: int, device: int) -> Tuple[int, int, int, int, int, int, int]:
-    if teacher is None or teacher.dim() != 2:
+    shape = () if teacher is None else teacher.shape
+    if len(shape) != 2:
         raise ValueError("teacher is not a matrix of rows x k")
-    k = teacher.shape[1]
+    k = shape[1]
     t_ptr, t_code, ldt = _matrix("teacher", teacher, _LOGITS_TYPES, rows, k, device)
     i_ptr, wide, ldi = _matrix("index", index, _INDEX_TYPES, rows, k, device)
     return t_ptr, t_code, ldt, i_ptr, wide, ldi, k
@@ -492,9 +507,10 @@ def logprobs(logits, tokens, logprob=None, entropy=None, lse=None, top_logprob=N
     t_ptr, wide = _tokens(tokens, rows, dev)
     k = 0
     if top_logprob is not None or top_index is not None:
-        if top_logprob is None or top_index is None or top_logprob.dim() != 2:
+        shape = () if top_logprob is None or top_index is None else top_logprob.shape
+        if len(shape) != 2:
             raise ValueError("top_logprob and top_index go together, as matrices of rows x k")
-        k = top_logprob.shape[1]
+        k = shape[1]
         top_l = _numbers("top_logprob", top_logprob, (rows, k), dev, _FLOAT32)
         top_i = _numbers("top_index", top_index, (rows, k), dev, _INT32)
     else:
@@ -502,6 +518,7 @@ def logprobs(logits, tokens, logprob=None, entropy=None, lse=None, top_logprob=N
     _check(lib().nsm_logprobs(ptr, code, rows, vocab, ld, t_ptr, wide, float(temperature), k,
                               _numbers("logprob", logprob, row, dev, _FLOAT32), _numbers("entropy", entropy, row, dev, _FLOAT32),
                               _numbers("lse", lse, row, dev, _FLOAT32), top_l, top_i, _loss_stream(stream, dev)))
+    _written(logprob, entropy, lse, top_logprob, top_index)
 
 
 def logprobs_grad(logits, tokens, d_logprob, d_entropy, d_logits, logprob=None, entropy=None, lse=None,
@@ -512,13 +529,14 @@ def logprobs_grad(logits, tokens, d_logprob, d_entropy, d_logits, logprob=None, 
     ptr, code, rows, vocab, ld, dev = _logits(logits)
     row = (rows,)
     t_ptr, wide = _tokens(tokens, rows, dev)
-    g_ptr, ldd = _gradient("d_logits", d_logits, logits, dev)
+    g_ptr, ldd = _gradient(d_logits, code, rows, vocab, dev)
     _check(lib().nsm_logprobs_grad(ptr, code, rows, vocab, ld, t_ptr, wide, float(temperature),
                                    _numbers("d_logprob", d_logprob, row, dev, _FLOAT32),
                                    _numbers("d_entropy", d_entropy, row, dev, _FLOAT32), g_ptr, ldd,
                                    _numbers("logprob", logprob, row, dev, _FLOAT32),
                                    _numbers("entropy", entropy, row, dev, _FLOAT32), _numbers("lse", lse, row, dev, _FLOAT32),
                                    _loss_stream(stream, dev)))
+    _written(d_logits, logprob, entropy, lse)
 
 
 def logprobs_backward(logits, tokens, lse, entropy, d_logprob, d_entropy, d_logits, temperature: float = 1.0,
@@ -528,12 +546,13 @@ def logprobs_backward(logits, tokens, lse, entropy, d_logprob, d_entropy, d_logi
     ptr, code, rows, vocab, ld, dev = _logits(logits)
     row = (rows,)
     t_ptr, wide = _tokens(tokens, rows, dev)
-    g_ptr, ldd = _gradient("d_logits", d_logits, logits, dev)
+    g_ptr, ldd = _gradient(d_logits, code, rows, vocab, dev)
     _check(lib().nsm_logprobs_backward(ptr, code, rows, vocab, ld, t_ptr, wide, float(temperature),
                                        _numbers("lse", lse, row, dev, _FLOAT32), _numbers("entropy", entropy, row, dev, _FLOAT32),
                                        _numbers("d_logprob", d_logprob, row, dev, _FLOAT32),
                                        _numbers("d_entropy", d_entropy, row, dev, _FLOAT32), g_ptr, ldd,
                                        _loss_stream(stream, dev)))
+    _written(d_logits)
 
 
 def distill(logits, teacher, index, loss, lse=None, rest=None, temperature: float = 1.0, tail: bool = False,
@@ -552,6 +571,7 @@ def distill(logits, teacher, index, loss, lse=None, rest=None, temperature: floa
     _check(lib().nsm_distill(ptr, code, rows, vocab, ld, *e, float(temperature), 1 if tail else 0,
                              _numbers("loss", loss, row, dev, _FLOAT32), _numbers("lse", lse, row, dev, _FLOAT32),
                              _numbers("rest", rest, row, dev, _FLOAT32), _loss_stream(stream, dev)))
+    _written(loss, lse, rest)
 
 
 def distill_grad(logits, teacher, index, d_loss, d_logits, loss=None, lse=None, rest=None,
@@ -561,11 +581,12 @@ def distill_grad(logits, teacher, index, d_loss, d_logits, loss=None, lse=None, 
     ptr, code, rows, vocab, ld, dev = _logits(logits)
     row = (rows,)
     e = _entries(teacher, index, rows, dev)
-    g_ptr, ldd = _gradient("d_logits", d_logits, logits, dev)
+    g_ptr, ldd = _gradient(d_logits, code, rows, vocab, dev)
     _check(lib().nsm_distill_grad(ptr, code, rows, vocab, ld, *e, float(temperature), 1 if tail else 0,
                                   _numbers("d_loss", d_loss, row, dev, _FLOAT32), g_ptr, ldd,
                                   _numbers("loss", loss, row, dev, _FLOAT32), _numbers("lse", lse, row, dev, _FLOAT32),
                                   _numbers("rest", rest, row, dev, _FLOAT32), _loss_stream(stream, dev)))
+    _written(d_logits, loss, lse, rest)
 
 
 def distill_backward(logits, teacher, index, lse, rest, d_loss, d_logits, temperature: float = 1.0,
@@ -574,10 +595,11 @@ def distill_backward(logits, teacher, index, lse, rest, d_loss, d_logits, temper
     ptr, code, rows, vocab, ld, dev = _logits(logits)
     row = (rows,)
     e = _entries(teacher, index, rows, dev)
-    g_ptr, ldd = _gradient("d_logits", d_logits, logits, dev)
+    g_ptr, ldd = _gradient(d_logits, code, rows, vocab, dev)
     _check(lib().nsm_distill_backward(ptr, code, rows, vocab, ld, *e, float(temperature), 1 if tail else 0,
                                       _numbers("lse", lse, row, dev, _FLOAT32), _numbers("rest", rest, row, dev, _FLOAT32),
                                       _numbers("d_loss", d_loss, row, dev, _FLOAT32), g_ptr, ldd, _loss_stream(stream, dev)))
+    _written(d_logits)
 
 
 def device_status(stream=None) -> int:

@@ -1046,18 +1046,28 @@ int device_views(const void* in_bf16, const void* out_bf16, const void** in, con
 // ---- losses over a vocabulary
 
 // A buffer of a call: no written one may overlap another (device memory is not looked at).
+// `stride`: bytes from row to row of a matrix whose rows have `row` bytes, 0 for one piece.
 struct Range {
   const void* p;
   size_t bytes;
   bool written;
+  size_t stride = 0, row = 0;
 };
+
+bool overlap(const Range& a, const Range& b) {
+  if (!ranges_overlap(a.p, a.bytes, b.p, b.bytes)) return false;
+  if (a.stride == 0 || a.stride != b.stride) return true;
+  // rows at one stride, such as columns of one buffer: apart where b's rows lie in a's gaps
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  const size_t from = pb >= pa ? (pb - pa) % a.stride : (a.stride - (pa - pb) % a.stride) % a.stride;
+  return from < a.row || from + b.row > a.stride;
+}
 
 int check_ranges(const Range* ranges, int n) {
   for (int i = 0; i < n; ++i) {
     if (!ranges[i].p) continue;
     for (int j = 0; j < i; ++j) {
-      if (ranges[j].p && (ranges[i].written || ranges[j].written) &&
-          ranges_overlap(ranges[i].p, ranges[i].bytes, ranges[j].p, ranges[j].bytes))
+      if (ranges[j].p && (ranges[i].written || ranges[j].written) && overlap(ranges[i], ranges[j]))
         return fail(NSM_ERR_ARG, "a buffer that the call writes overlaps another one");
     }
   }
@@ -1066,9 +1076,9 @@ int check_ranges(const Range* ranges, int n) {
 
 size_t number_bytes(int dtype) { return dtype == NSM_FP32 ? 4 : 2; }
 
-// Bytes from the first to the last element of rows x cols at row stride ld.
-size_t span_bytes(int64_t rows, int64_t ld, int64_t cols, size_t size) {
-  return (size_t(rows - 1) * size_t(ld) + size_t(cols)) * size;
+// rows x cols elements of `size` bytes at row stride ld, from the first to the last one.
+Range matrix_range(const void* p, int64_t rows, int64_t ld, int64_t cols, size_t size, bool written) {
+  return {p, (size_t(rows - 1) * size_t(ld) + size_t(cols)) * size, written, size_t(ld) * size, size_t(cols) * size};
 }
 
 // rows x cols elements of `size` bytes at row stride ld: non-negative sizes whose span stays
@@ -1110,7 +1120,7 @@ int check_vocab(VocabArgs& v, const void* logits, int dtype, int64_t rows, int64
     if (rc != NSM_OK) return rc;
     // in place, or apart
     if (!(d_logits == logits && ldd == ld) &&
-        ranges_overlap(logits, span_bytes(rows, ld, vocab, size), d_logits, span_bytes(rows, ldd, vocab, size)))
+        overlap(matrix_range(logits, rows, ld, vocab, size, false), matrix_range(d_logits, rows, ldd, vocab, size, true)))
       return fail(NSM_ERR_ARG, "d_logits overlaps logits without being the same rows");
   }
   return NSM_OK;
@@ -1140,8 +1150,8 @@ int run_logprobs(LogprobArgs& a, nsm_stream_t stream_) {
   for (const auto& x : numbers)
     if ((rc = check_numbers(x.what, x.p, x.size)) != NSM_OK) return rc;
   const bool in_place = v.d_logits == v.logits;
-  const Range ranges[] = {{v.logits, span_bytes(v.rows, v.ld, v.vocab, size), in_place},
-                          {in_place ? nullptr : v.d_logits, span_bytes(v.rows, v.ldd, v.vocab, size), true},
+  const Range ranges[] = {matrix_range(v.logits, v.rows, v.ld, v.vocab, size, in_place),
+                          matrix_range(in_place ? nullptr : v.d_logits, v.rows, v.ldd, v.vocab, size, true),
                           {a.tokens, size_t(v.rows) * (a.tokens_wide ? 8 : 4), false},
                           {a.logprob, n, true}, {a.entropy, n, true}, {a.lse, n, true},
                           {a.k ? a.top_logprob : nullptr, n * size_t(a.k), true},
@@ -1180,10 +1190,10 @@ int run_distill(DistillArgs& a, nsm_stream_t stream_) {
   for (const auto& x : numbers)
     if ((rc = check_numbers(x.what, x.p, 4)) != NSM_OK) return rc;
   const bool in_place = v.d_logits == v.logits;
-  const Range ranges[] = {{v.logits, span_bytes(v.rows, v.ld, v.vocab, size), in_place},
-                          {in_place ? nullptr : v.d_logits, span_bytes(v.rows, v.ldd, v.vocab, size), true},
-                          {a.teacher, span_bytes(v.rows, a.ldt, a.k, tsize), false},
-                          {a.index, span_bytes(v.rows, a.ldi, a.k, isize), false},
+  const Range ranges[] = {matrix_range(v.logits, v.rows, v.ld, v.vocab, size, in_place),
+                          matrix_range(in_place ? nullptr : v.d_logits, v.rows, v.ldd, v.vocab, size, true),
+                          matrix_range(a.teacher, v.rows, a.ldt, a.k, tsize, false),
+                          matrix_range(a.index, v.rows, a.ldi, a.k, isize, false),
                           {a.loss, n, true}, {a.lse, n, true}, {a.rest, n, true},
                           {a.d_loss, n, false}, {a.in_lse, n, false}, {a.in_rest, n, false}};
   if ((rc = check_ranges(ranges, int(sizeof ranges / sizeof ranges[0]))) != NSM_OK) return rc;

@@ -273,8 +273,10 @@ size_t nsm_gemm_scratch_bytes(int M, int N, int flags);
  *     -1); a row of weight 0 has a gradient of zeros whatever it holds.
  *   - `*_wide`: index arrays hold int64 (else int32).  An index outside [0, vocab), such
  *     as -100 or -1, stands for no token and no entry.
- *   - Deterministic: identical inputs give bit-identical outputs, and a row's result does
- *     not depend on the other rows. */
+ *   - Deterministic: the same call gives bit-identical outputs, in place or not, and what
+ *     other rows hold does not change a row's bits.  How many rows there are, and where a
+ *     row begins relative to 16 bytes, sets the order of its sums: the last bits of the
+ *     same row's results can change with those. */
 #define NSM_BF16 0
 #define NSM_FP16 1
 #define NSM_FP32 2

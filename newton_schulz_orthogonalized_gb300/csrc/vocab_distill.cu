@@ -117,7 +117,7 @@ template <typename T>
 __device__ __forceinline__ void load_logits(Entries& e, const Row<T>& row) {
 #pragma unroll
   for (int u = 0; u < kLaneEntries; ++u)
-    if (e.v[u] >= 0) e.x[u] = Elem<T>::to_float(row.p[e.v[u]]);
+    if (e.v[u] >= 0) e.x[u] = Elem<T>::to_float(row.at(e.v[u]));
 }
 
 // Of equal tokens the first counts; then the teacher's probabilities (the student is not asked
@@ -341,8 +341,7 @@ __device__ __forceinline__ void store_entries(const T (&grads)[kLaneEntries], co
                                               const Entries& e) {
 #pragma unroll
   for (int u = 0; u < kLaneEntries; ++u)
-    if (e.v[u] >= 0 && in_part(row, part, e.v[u]) && bounds_ok(e.v[u] < out.vocab, out.status, out.kernel, 0, NSM_SITE_GRADIENT))
-      out.p[e.v[u]] = grads[u];
+    if (e.v[u] >= 0 && in_part(row, part, e.v[u])) out.put(e.v[u], grads[u]);
 }
 
 // NT threads sum the row (a cluster of blocks per row where rows are few), a warp more has the
@@ -466,7 +465,7 @@ __global__ void __launch_bounds__(NT + 32) k_distill_resident(const DistillArgs 
       if (e.v[u] < 0) continue;
       if (at >= part.begin && at < part.end) chunk_of[u] = (from >= slab.each) + (from >= 2 * slab.each) + (from >= 3 * slab.each);
       else if (at == part.head || at == part.tail) chunk_of[u] = 0;
-      else elsewhere[u] = row.p[e.v[u]];
+      else elsewhere[u] = row.at(e.v[u]);
     }
     // The entries leave the sums outside them: chunk by chunk as it arrives, their logits are
     // taken and -inf goes in their place.

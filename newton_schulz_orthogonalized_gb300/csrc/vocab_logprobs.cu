@@ -229,7 +229,7 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
     int at = atomicAdd(&sh.ncand, __popc(hits));
     for (; hits; hits &= hits - 1, ++at) {
       const int e = __ffs(hits) - 1;
-      if (at < kTopCandidates) sh.cand[at] = full_key(Elem<T>::to_float(row.p[row.first(i) + e]), row.first(i) + e);
+      if (at < kTopCandidates) sh.cand[at] = full_key(Elem<T>::to_float(row.at(row.first(i) + e)), row.first(i) + e);
     }
   };
   if (nlist <= kTopList) {
@@ -381,8 +381,7 @@ __device__ __forceinline__ void store_token_gradients(const Row<T>& row, const R
     if (whole && same) out.store_whole(i, grad);
     else out.store(row.first(i), grad);
   });
-  if (mine && bounds_ok(token >= 0 && token < out.vocab, out.status, out.kernel, 0, NSM_SITE_GRADIENT))
-    out.p[token] = Elem<T>::from_float(at_token());
+  if (mine) out.put(token, Elem<T>::from_float(at_token()));
 }
 
 // Whether thread `tid` of NT has the vector that holds element v (v < 0: no).
@@ -413,7 +412,7 @@ __global__ void __launch_bounds__(NT, TOP ? 6 : 1280 / NT) k_logprobs(const Logp
   const Part part = part_of(row, rank, ctas);
   int64_t token64 = g.tokens ? load_index(g.tokens, g.tokens_wide, r) : -1;
   const int token = token64 < 0 || token64 >= vocab ? -1 : static_cast<int>(token64);
-  const float x_token = token >= 0 ? Elem<T>::to_float(row.p[token]) : kNegInf;
+  const float x_token = token >= 0 ? Elem<T>::to_float(row.at(token)) : kNegInf;
   uint64_t* gathered = reinterpret_cast<uint64_t*>(dynamic);
   TopGroups<T> groups{reinterpret_cast<typename TopGroups<T>::Key*>(gathered + (ctas > 1 ? ctas * g.k : 0)), group_shift, kNegInf};
   Sums a;
@@ -483,7 +482,7 @@ __global__ void __launch_bounds__(NT) k_logprobs_resident(const LogprobArgs g, i
     slab.prefetch(Row<T>(static_cast<T*>(const_cast<void*>(g.v.logits)) + (r + ahead) * g.v.ld, vocab, status, NSM_KERNEL_LOGPROBS), rank, ctas);
   const int64_t token64 = g.tokens ? load_index(g.tokens, g.tokens_wide, r) : -1;
   const int token = token64 < 0 || token64 >= vocab ? -1 : static_cast<int>(token64);
-  const float x_token = token >= 0 ? Elem<T>::to_float(row.p[token]) : kNegInf;
+  const float x_token = token >= 0 ? Elem<T>::to_float(row.at(token)) : kNegInf;
   const float w = g.d_logprob && token >= 0 ? g.d_logprob[r] : 0.f;
   const float h = ENT && g.d_entropy ? g.d_entropy[r] : 0.f;
   Sums a;
@@ -535,7 +534,7 @@ __global__ void __launch_bounds__(NT, 1536 / NT) k_logprobs_backward(const Logpr
     // thread that has the token's vector reads its logit, before it writes there
     const Part part = part_of(row, piece, pieces);
     const bool mine = owns<NT>(row, part, token);
-    const float x_token = mine ? Elem<T>::to_float(row.p[token]) : kNegInf;
+    const float x_token = mine ? Elem<T>::to_float(row.at(token)) : kNegInf;
     const TokenGradient k = token_gradient(w, h, s, low, c, inv_t);
     store_token_gradients<T, ENT>(row, out, part, k, token, mine, c, [&](auto&& use) { for_vectors<NT>(row, part, use); },
                                   [&] { return gradient_at_token(w, h, s, low, x_token, inv_t); });
@@ -618,7 +617,7 @@ __global__ void __launch_bounds__(32 * kShortWarps) k_logprobs_short(const Logpr
     x.load(row, part);
     const int64_t token64 = g.tokens ? load_index(g.tokens, g.tokens_wide, r) : -1;
     const int token = token64 < 0 || token64 >= vocab ? -1 : static_cast<int>(token64);
-    const float x_token = token >= 0 ? Elem<T>::to_float(row.p[token]) : kNegInf;
+    const float x_token = token >= 0 ? Elem<T>::to_float(row.at(token)) : kNegInf;
     RowLogprob s;
     float low = 0.f;
     if constexpr (MODE == kShortBackward) {
@@ -642,9 +641,8 @@ __global__ void __launch_bounds__(32 * kShortWarps) k_logprobs_short(const Logpr
       const TokenGradient k = token_gradient(w, h, s, low, c, inv_t);
       __syncwarp();  // in place: every lane has read the token's logit
       x.store(row, out, part, k.zero, [&](const uint4& v) { return gradient_vec<T, ENT>(v, k.ref, c, k.log2_s, k.ca, k.cb); });
-      if (!k.zero && token >= 0 && ((token + row.lead) / Elem<T>::kVec & 31) == lane &&
-          bounds_ok(token < vocab, status, NSM_KERNEL_LOGPROBS, 0, NSM_SITE_GRADIENT))
-        out.p[token] = Elem<T>::from_float(gradient_at_token(w, h, s, low, x_token, inv_t));
+      if (!k.zero && token >= 0 && ((token + row.lead) / Elem<T>::kVec & 31) == lane)
+        out.put(token, Elem<T>::from_float(gradient_at_token(w, h, s, low, x_token, inv_t)));
     }
   }
 }

@@ -218,6 +218,13 @@ struct Row {
       return make_uint4(0, 0, 0, 0);
     return *reinterpret_cast<const uint4*>(p + first(i));
   }
+  // element v of the row
+  __device__ __forceinline__ T at(int v) const {
+    return bounds_ok(v >= 0 && v < vocab, status, kernel, 0, NSM_SITE_LOGITS) ? p[v] : Elem<T>::from_float(0.f);
+  }
+  __device__ __forceinline__ void put(int v, T value) const {
+    if (bounds_ok(v >= 0 && v < vocab, status, kernel, 0, NSM_SITE_GRADIENT)) p[v] = value;
+  }
   // vector i of the row, with -inf outside it
   __device__ __forceinline__ uint4 load(int i) const {
     const int e0 = first(i);

@@ -621,6 +621,7 @@ __global__ void __launch_bounds__(32 * kShortWarps) k_distill_short(const Distil
     }
     if constexpr (MODE != kShortForward) {
       const Row<T> out(static_cast<T*>(g.v.d_logits) + r * g.v.ldd, vocab, status, NSM_KERNEL_DISTILL);
+      __syncwarp();  // in place: every lane has read its entries' logits
       x.store(row, out, part, k.zero,
               [&](const uint4& v) { return gradient_vec<T, false>(v, k.ref, c, k.log2_s, k.scale, 0.f); });
       __syncwarp();  // the entries' own values go over what was written there

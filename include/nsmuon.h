@@ -305,7 +305,11 @@ int nsm_logprobs_grad(const void* logits, int dtype, int64_t rows, int64_t vocab
                       float* logprob, float* entropy, float* lse, nsm_stream_t stream);
 
 /* The backward pass alone, from the lse (and, with d_entropy, the entropy) that
- * nsm_logprobs gave for the same logits and temperature. */
+ * nsm_logprobs gave for the same logits and temperature.  lse is an fp32 number: q comes
+ * out with a relative error of |lse| 2^-24 beside the others.  In a row of nothing but a
+ * type's lowest value lse keeps no more than that value (below temperature 1 it leaves
+ * fp32's range): give such a row weight 0, or take nsm_logprobs_grad, which does not pass
+ * through lse.  The same holds for nsm_distill_backward. */
 int nsm_logprobs_backward(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
                           const void* tokens, int tokens_wide, float temperature,
                           const float* lse, const float* entropy, const float* d_logprob,

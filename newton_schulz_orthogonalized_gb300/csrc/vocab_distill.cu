@@ -7,12 +7,14 @@
 //   1 + excess = sum p + p_r.
 //
 //   k_distill            forward: as k_logprobs, S taken out by a bit per element.
-//                        8192 x 131072 bf16 321 us (6.7 TB/s), 1024 x 50257 23.
+//                        8192 x 131072 bf16, 64 entries and the tail 325 us (6.6 TB/s), 1024 x
+//                        50257, 32 entries 22.
 //   k_distill_resident   forward and backward in one pass, the row in shared memory, the
 //                        teacher in a warp of its own: 8192 x 32768 bf16, 64 entries 169 us (6.4
-//                        TB/s), 8192 x 131072 (four blocks a row) 705.  Bound by the latency of the
+//                        TB/s), 8192 x 131072 (four blocks a row) 704.  Bound by the latency of the
 //                        entries' loads before the sums and by the cluster's slowest block.
-//   k_distill_backward   pieces of rows from saved statistics: 8192 x 131072 733 us (5.9 TB/s).
+//   k_distill_backward   pieces of rows from saved statistics: 8192 x 131072, 64 entries and the tail
+//                        762 us (5.6 TB/s).
 //   k_distill_short      a warp per row of at most 256 vectors: 16384 x 259, loss and gradient 25 us.
 #include "vocab_rows.cuh"
 

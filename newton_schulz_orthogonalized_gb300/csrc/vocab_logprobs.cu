@@ -6,13 +6,14 @@
 //
 //   k_logprobs           forward: a block per row, a cluster of blocks where rows are few; one
 //                        pass, alternatives from groups that can hold one.  Bound by the read:
-//                        8192 x 131072 bf16 297 us (7.2 TB/s), with 64 alternatives 360.
+//                        8192 x 131072 bf16 297 us (7.2 TB/s), with 64 alternatives 360, with 128
+//                        495.
 //   k_logprobs_resident  forward and backward in one pass over memory, the row in shared memory:
 //                        8192 x 32768 bf16 158 us, 8192 x 50257 244, 8192 x 131072 (four blocks
-//                        a row) 625: the rate of a copy, 6.8 TB/s read and written.
+//                        a row) 627: the rate of a copy, 6.8 TB/s read and written.
 //   k_logprobs_backward  pieces of rows from saved statistics: 8192 x 131072 677 us (6.3 TB/s).
 //   k_logprobs_short     a warp per row of at most 256 vectors, every direction: 16384 x 1000
-//                        forward 8 us, forward and backward 16.
+//                        forward 8.6 us, forward and backward 19.
 #include "vocab_rows.cuh"
 
 namespace nsm {

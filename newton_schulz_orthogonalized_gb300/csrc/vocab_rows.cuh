@@ -348,7 +348,8 @@ __device__ __forceinline__ void zero_part(const Row<T>& out, int piece, int piec
 // A sum of exponentials s = sum 2^y, y = (x - ref) c, with sum y 2^y (both in two halves, one
 // per element of a pair), and the largest x.  (x - ref) c and not x c - ref c in one fused step:
 // the latter needs a correction for its rounding and a second way for the types' lowest values,
-// which cost more than the step saves (8192 x 8000 bf16, loss and gradient: 75 us for 62).
+// which cost more than the step saves (8192 x 8000 bf16, loss and gradient with 256 threads a row:
+// 75 us for 62).
 struct Sums {
   float ref = 0.f, limit = kNegInf;  // no reference yet: every finite logit exceeds the limit
   Pair s = 0, sy = 0;
@@ -427,8 +428,8 @@ __device__ __forceinline__ Totals warp_totals(const Sums& a, float c) {
 // one CTA, start_totals comes first.
 // Each CTA stores its totals in the others' shared memory, counted as bytes on a barrier there:
 // one way over the cluster and no wait for it.  With plain stores and a remote arrival behind
-// them, which waits until they are done, loss and gradient of 8192 x 131072 bf16 took 662 us for
-// 617, and a message per warp in place of one per CTA 415 us for 347 with 2000 x 151936 fp32 over
+// them, which waits until they are done, loss and gradient of 8192 x 131072 bf16 took 7%
+// longer, and with a message per warp in place of one per CTA 2000 x 151936 fp32 20% longer over
 // eight CTAs (distillation; over four it saves 1%).
 // `read` is what the thread has read of the row and still needs: it goes along, so that its load
 // is over before another CTA can write a gradient there.
@@ -643,8 +644,8 @@ struct ShortRow {
 
 // CTAs per row: where there are fewer rows than the GPU takes blocks at a time, a cluster
 // shares each row, down to two vectors of a thread, until 256 threads a SM are there.  Measured on
-// a GB300 with 256, 512 and 160 a SM: 600 x 32000 bf16 6.8, 8.1 and 6.7 us, 300 x 131072 19.5, 21.7
-// and 29.1, 64 x 50257 with 20 alternatives 8.6, 13.1 and 9.0.
+// a GB300 with 256, 512 and 160 a SM: 600 x 32000 bf16 6.8, 8.2 and 8.0 us, 300 x 131072 19.7, 21.4
+// and 28.8, 64 x 50257 with 20 alternatives 8.6, 13.4 and 8.8.
 inline int cluster_for(int64_t rows, int nvec, int NT) {
   int ctas = 1;
   while (ctas < kMaxCluster && rows * ctas * NT < 256 * 152 && nvec >= ctas * 4 * NT) ctas *= 2;
@@ -652,8 +653,9 @@ inline int cluster_for(int64_t rows, int nvec, int NT) {
 }
 
 // Threads per row of a forward pass, and per piece of a row of a backward pass.  Measured on a
-// GB300: 16384 x 4000 bf16 forward 29 us with 64 threads, 43 with 128; 8192 x 131072 302 with 128,
-// 354 with 512; 16384 x 2100 backward 37 us with 64 and 58 with 256, 8192 x 131072 677 with 256.
+// GB300: 16384 x 4000 bf16 forward 30 us with 64 threads, 38 with 128; 8192 x 131072 297 with 128,
+// a sixth more with 512; 16384 x 2100 backward 37 us with 64 and 57 with 256, 8192 x 131072 677
+// with 256.
 inline int forward_threads(int nvec) { return nvec <= 1024 ? 64 : 128; }
 inline int backward_threads(int nvec) { return nvec <= 1024 ? 64 : 256; }
 
@@ -671,10 +673,10 @@ inline size_t slab_bytes(int nvec, int ctas) { return (static_cast<size_t>((nvec
 // A block keeps memory busy only while its own row is on the way, not in its passes.  So each
 // asks for a part of a later row in L2 when it has asked for its own: of a row half as far on as
 // there are rows on the GPU, whose block starts about when the copy is there.  Measured on a
-// GB300, loss and gradient of 8192 x 131072 bf16: 786 us without, 692 at half as far (and at a
-// quarter), 732 as far as the rows on the GPU, 879 at twice that; 2000 x 151936 fp32 411 and 355.
-// The passes that only read, or read and write in pieces, are slower with it: 8192 x 131072 with
-// 64 alternatives 542 us for 359, distillation's backward pass 1072 for 737.
+// GB300, loss and gradient of 8192 x 131072 bf16: 645 us without, 627 at half as far (and at a
+// quarter), 803 as far as the rows on the GPU, 879 at twice that; 2000 x 151936 fp32 346 without and
+// with, 390 and 496 further on.  The passes that only read, or read and write in pieces, were much
+// slower with it: 8192 x 131072 with 64 alternatives by half, distillation's backward pass by 45%.
 inline int rows_ahead(size_t slab, int threads, int ctas) {
   const int blocks = static_cast<int>(std::min<size_t>((227 << 10) / (slab + 2048), 2048 / threads));
   return std::max(1, 152 * blocks / 2 / ctas);
@@ -685,13 +687,13 @@ struct Resident {
   int threads, ctas;
 };
 // Measured on a GB300, loss and gradient in bf16: slabs of 64 KB, three blocks a SM, 8192 x 32768
-// 157 us (the rate of a copy), the same row over two blocks of a cluster 171.  Beyond 76 KB a row is
-// shared by a cluster, with 56 KB as the limit 8192 x 131072 takes 688 us for 620; `alone`, the
+// 158 us (the rate of a copy), the same row over two blocks of a cluster 170.  Beyond 76 KB a row is
+// shared by a cluster, with 56 KB as the limit 8192 x 131072 takes 680 us for 627; `alone`, the
 // most that a row keeps in one block where rows are many, is 76 KB as well for log probabilities
-// (8192 x 50257 243 us over two blocks, 258 in one of 112 KB) and 112 KB for distillation, whose
-// blocks each wait for the row's entries (291 us over two, 282 in one).
-// Eight vectors a thread: 8000 columns 47 us with 128 threads, 62 with 256.
-// Where rows are few, clusters grow until 1024 threads a SM are there: 257 x 32003 fp32 16.6 us,
+// (8192 x 50257 244 us over two blocks, 266 in one of 112 KB) and 112 KB for distillation, whose
+// blocks each wait for the row's entries (287 us over two, 281 in one).
+// Eight vectors a thread: 8000 columns 44 us with 128 threads, 62 with 256.
+// Where rows are few, clusters grow until 1024 threads a SM are there: 257 x 32003 fp32 16.4 us,
 // 17.5 with half or twice as many.
 inline Resident resident_for(int64_t rows, int nvec, size_t alone) {
   Resident r{256, 1};
@@ -745,7 +747,7 @@ struct Launch<KERNEL> {
 
 // Vectors per lane of a warp per row, 0 where rows are too long for that.  Measured on a GB300
 // against blocks of 64 to 256 threads per row, 16384 rows: 259 columns bf16, distillation's loss
-// and gradient 23 us for 60, log probabilities 10 for 24; 2000 columns 45 for 64 and 14 for 30; for
+// and gradient 25 us for 57, log probabilities 10 for 17; 2000 columns 44 for 62 and 15 for 22; for
 // 8 rows the two are alike.
 inline int short_for(int nvec) {
   if (nvec > 32 * 8) return 0;

@@ -7,7 +7,7 @@
 //   k_logprobs           forward: a block per row, a cluster of blocks where rows are few; one
 //                        pass, alternatives from groups that can hold one.  Bound by the read:
 //                        8192 x 131072 bf16 297 us (7.2 TB/s), with 64 alternatives 360, with 128
-//                        495.
+//                        420.
 //   k_logprobs_resident  forward and backward in one pass over memory, the row in shared memory:
 //                        8192 x 32768 bf16 158 us, 8192 x 50257 244, 8192 x 131072 (four blocks
 //                        a row) 627: the rate of a copy, 6.8 TB/s read and written.
@@ -19,7 +19,9 @@
 namespace nsm {
 namespace {
 
-constexpr int kTopCandidates = 1024;
+// Places for candidates: 128 vectors of eight and a row's ragged first and last one, which two
+// threads have beside the whole vectors that they begin with.
+constexpr int kTopCandidates = 1024 + 16;
 
 // ---------------------------------------------------------------- the k largest
 
@@ -50,6 +52,7 @@ struct TopShared {
   uint32_t list[kTopList];                    // group * kTopThreads + thread
   uint64_t cand[kTopCandidates];
   uint64_t best[kTopWarps];
+  int32_t count[2][kTopWarps];
   TopBound bound;
   int32_t nlist, ncand;
   uint32_t taken[kMaxCluster];                // how many keys each CTA gave
@@ -174,6 +177,41 @@ __device__ __forceinline__ void place_keys(const uint64_t* keys, int n, int k, F
   }
 }
 
+// Leaves of the candidates those that reach a bound on their values: k at least, and few more where
+// the values differ.  Every thread calls it, behind a barrier; the number left.
+template <typename T>
+__device__ __forceinline__ int cut_candidates(TopShared& sh, int n, int k) {
+  constexpr int kOwn = (kTopCandidates + kTopThreads - 1) / kTopThreads;
+  const int tid = threadIdx.x;
+  uint64_t mine[kOwn];  // 0 is no candidate's key
+#pragma unroll
+  for (int u = 0; u < kOwn; ++u) mine[u] = tid + u * kTopThreads < n ? sh.cand[tid + u * kTopThreads] : 0;
+  uint32_t bound = 0;
+  for (int b = 31, reach = n; b >= Elem<T>::kKeyLowBit && reach > k + 32; --b) {
+    const uint32_t test = bound | 1u << b;
+    int c = 0;
+#pragma unroll
+    for (int u = 0; u < kOwn; ++u) c += static_cast<uint32_t>(mine[u] >> 32) >= test;
+    c = __reduce_add_sync(~0u, c);
+    if ((tid & 31) == 0) sh.count[b & 1][tid >> 5] = c;
+    __syncthreads();
+    c = 0;
+#pragma unroll
+    for (int w = 0; w < kTopWarps; ++w) c += sh.count[b & 1][w];
+    if (c >= k) {
+      bound = test;
+      reach = c;
+    }
+  }
+  if (tid == 0) sh.ncand = 0;
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kOwn; ++u)
+    if (mine[u] != 0 && static_cast<uint32_t>(mine[u] >> 32) >= bound) sh.cand[atomicAdd(&sh.ncand, 1)] = mine[u];
+  __syncthreads();
+  return sh.ncand;
+}
+
 // The k largest logits of the block's part of a row, from every thread's largest one and
 // where it met it: put(place, key), and the number of places that were filled.
 template <typename T, typename F>
@@ -192,12 +230,17 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
       key[j] = sh.key[j * 32 + tid];
       vec[j] = sh.vec[j * 32 + tid];
     }
-    // A few more threads than k cost less than the steps that would tell them apart; but three
-    // quarters of the threads at most: a bound that all reach is none, and one that nearly all
-    // reach has more logits above it than the candidates' places (512 x 131072 bf16, 128
-    // alternatives: 6.9 ms with 2 k + 8 alone, where rows were read once per place, 0.05 with this).
-    static_assert(3 * kTopThreads / 4 >= kTopMaxK, "k threads may reach the bound");
-    const TopBound t = top_bound<T>(key, vec, k, min(2 * k + 8, 3 * kTopThreads / 4));
+    // A few more threads than k cost less than the steps that would tell them apart, and up to 32
+    // more less than their logits among the candidates (2048 x 50257 bf16, 64 alternatives: 57 us,
+    // 61 with k + 8 more).  But three quarters of the threads at most: a bound that all reach is
+    // none, and one that nearly all reach has more logits above it than the candidates' places (512
+    // x 131072 bf16, 128 alternatives: 6.9 ms where rows were read once per place, 0.04 with this).
+    // And no more threads than the places hold whole vectors of, as where the logits fall from the
+    // first token on (the same rows falling, 100 alternatives: 5.4 ms and 0.04).
+    constexpr int kVectors = kTopCandidates / kVec - 2, kThreads = 3 * kTopThreads / 4;
+    constexpr int kMost = kVectors < kThreads ? kVectors : kThreads;
+    static_assert(kMost >= kTopMaxK, "k threads may reach the bound");
+    const TopBound t = top_bound<T>(key, vec, k, min(min(2 * k + 8, k + 32), kMost));
     if (tid == 0) {
       sh.bound = t;
       sh.nlist = sh.ncand = 0;
@@ -243,8 +286,12 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
     if (part.tail >= 0 && tid == kTailThread) offer(part.tail);
   }
   __syncthreads();
-  const int ncand = sh.ncand;
+  int ncand = sh.ncand;
   if (nlist <= kTopList && ncand <= kTopCandidates) {
+    // Placing takes n^2 comparisons.  Rows of noise have some 2 k candidates; rows that fall from
+    // token to token have whole vectors of them (608 x 9001 bf16, 128 alternatives: 20 us of noise,
+    // falling 122 without this and 24 with it).
+    if (ncand > 3 * k + 64) ncand = cut_candidates<T>(sh, ncand, k);
     place_keys(sh.cand, ncand, k, put);
     return min(ncand, k);
   }
@@ -296,7 +343,7 @@ __device__ __forceinline__ void row_top(const Row<T>& row, const Part& part, con
     if (threadIdx.x == 0) ptx::st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sh.taken[rank]), 0), mine);
     ptx::cluster_sync();
     if (rank != 0) return;
-    // closed up, in kTopCandidates = kMaxCluster kTopMaxK places
+    // closed up, in kTopCandidates >= kMaxCluster kTopMaxK places
     int total = 0;
     for (int r = 0; r < ctas; ++r) {
       const int n = static_cast<int>(sh.taken[r]);

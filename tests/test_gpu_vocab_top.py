@@ -61,3 +61,28 @@ def test_more_alternatives_cost_little_more(nsm, rows, vocab, dtype):
             best.append(begin.elapsed_time(end))
         times[k] = min(best)
     assert times[123] < 4 * times[32] and times[128] < 4 * times[32], times
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", SHAPES)
+def test_descending_rows_cost_little_more(nsm, rows, vocab, dtype):
+    # whole vectors of the largest logits, as where tokens are ordered by their frequency
+    x = torch.linspace(30.0, -30.0, vocab, device="cuda").to(dtype).repeat(rows, 1)
+    noisy = _rows(rows, vocab, dtype)
+    times = {}
+    for what, logits in (("noisy", noisy), ("descending", x)):
+        for k in (64, 100, 128):
+            value, index, call = _top(nsm, logits, k)
+            best = []
+            for _ in range(4):
+                begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                begin.record()
+                for _ in range(5):
+                    call()
+                end.record()
+                end.synchronize()
+                best.append(begin.elapsed_time(end))
+            times[what, k] = min(best)
+            if logits is x:
+                assert torch.equal(index.long(), torch.arange(k, device="cuda").expand(rows, k))
+    for k in (64, 100, 128):
+        assert times["descending", k] < 4 * times["noisy", k], times

@@ -177,27 +177,39 @@ __device__ __forceinline__ void place_keys(const uint64_t* keys, int n, int k, F
   }
 }
 
-// Leaves of the candidates those that reach a bound on their values: k at least, and few more where
-// the values differ.  Every thread calls it, behind a barrier; the number left.
-template <typename T>
+// Leaves of the candidates the k largest and at most 32 more: a bound on whole keys, which are
+// distinct, by those of their bits that differ at all.  Every thread calls it, behind a barrier, with
+// n > k + 32; the number left.
 __device__ __forceinline__ int cut_candidates(TopShared& sh, int n, int k) {
   constexpr int kOwn = (kTopCandidates + kTopThreads - 1) / kTopThreads;
   const int tid = threadIdx.x;
-  uint64_t mine[kOwn];  // 0 is no candidate's key
+  const uint64_t one = sh.cand[0];
+  uint64_t mine[kOwn], differ = 0;  // 0 is no candidate's key
 #pragma unroll
-  for (int u = 0; u < kOwn; ++u) mine[u] = tid + u * kTopThreads < n ? sh.cand[tid + u * kTopThreads] : 0;
-  uint32_t bound = 0;
-  for (int b = 31, reach = n; b >= Elem<T>::kKeyLowBit && reach > k + 32; --b) {
-    const uint32_t test = bound | 1u << b;
+  for (int u = 0; u < kOwn; ++u) {
+    mine[u] = tid + u * kTopThreads < n ? sh.cand[tid + u * kTopThreads] : 0;
+    if (mine[u] != 0) differ |= mine[u] ^ one;
+  }
+  differ = static_cast<uint64_t>(__reduce_or_sync(~0u, static_cast<uint32_t>(differ >> 32))) << 32 |
+           __reduce_or_sync(~0u, static_cast<uint32_t>(differ));
+  if ((tid & 31) == 0) sh.best[tid >> 5] = differ;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kTopWarps; ++w) differ |= sh.best[w];
+  uint64_t bound = one & ~differ;
+#pragma unroll 1
+  for (int reach = n, step = 0; reach > k + 32 && differ != 0; step ^= 1) {
+    const uint64_t bit = 1ull << (63 - __clzll(differ)), test = bound | bit;
+    differ ^= bit;
     int c = 0;
 #pragma unroll
-    for (int u = 0; u < kOwn; ++u) c += static_cast<uint32_t>(mine[u] >> 32) >= test;
+    for (int u = 0; u < kOwn; ++u) c += mine[u] >= test;
     c = __reduce_add_sync(~0u, c);
-    if ((tid & 31) == 0) sh.count[b & 1][tid >> 5] = c;
+    if ((tid & 31) == 0) sh.count[step][tid >> 5] = c;
     __syncthreads();
     c = 0;
 #pragma unroll
-    for (int w = 0; w < kTopWarps; ++w) c += sh.count[b & 1][w];
+    for (int w = 0; w < kTopWarps; ++w) c += sh.count[step][w];
     if (c >= k) {
       bound = test;
       reach = c;
@@ -207,7 +219,7 @@ __device__ __forceinline__ int cut_candidates(TopShared& sh, int n, int k) {
   __syncthreads();
 #pragma unroll
   for (int u = 0; u < kOwn; ++u)
-    if (mine[u] != 0 && static_cast<uint32_t>(mine[u] >> 32) >= bound) sh.cand[atomicAdd(&sh.ncand, 1)] = mine[u];
+    if (mine[u] != 0 && mine[u] >= bound) sh.cand[atomicAdd(&sh.ncand, 1)] = mine[u];
   __syncthreads();
   return sh.ncand;
 }
@@ -291,7 +303,7 @@ __device__ __forceinline__ int part_top(const Row<T>& row, const Part& part, con
     // Placing takes n^2 comparisons.  Rows of noise have some 2 k candidates; rows that fall from
     // token to token have whole vectors of them (608 x 9001 bf16, 128 alternatives: 20 us of noise,
     // falling 122 without this and 24 with it).
-    if (ncand > 3 * k + 64) ncand = cut_candidates<T>(sh, ncand, k);
+    if (ncand > 3 * k + 64) ncand = cut_candidates(sh, ncand, k);
     place_keys(sh.cand, ncand, k, put);
     return min(ncand, k);
   }

@@ -86,3 +86,28 @@ def test_descending_rows_cost_little_more(nsm, rows, vocab, dtype):
                 assert torch.equal(index.long(), torch.arange(k, device="cuda").expand(rows, k))
     for k in (64, 100, 128):
         assert times["descending", k] < 4 * times["noisy", k], times
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", SHAPES)
+def test_equal_logits_cost_little_more(nsm, rows, vocab, dtype):
+    # as from a head of zeros: every vector holds eight of the largest
+    x = torch.full((rows, vocab), -0.5, device="cuda").to(dtype)
+    noisy = _rows(rows, vocab, dtype)
+    times = {}
+    for what, logits in (("noisy", noisy), ("equal", x)):
+        for k in (64, 100, 128):
+            value, index, call = _top(nsm, logits, k)
+            best = []
+            for _ in range(4):
+                begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                begin.record()
+                for _ in range(5):
+                    call()
+                end.record()
+                end.synchronize()
+                best.append(begin.elapsed_time(end))
+            times[what, k] = min(best)
+            if logits is x:
+                assert torch.equal(index.long(), torch.arange(k, device="cuda").expand(rows, k))
+    for k in (64, 100, 128):
+        assert times["equal", k] < 4 * times["noisy", k], times

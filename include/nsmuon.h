@@ -352,6 +352,126 @@ int nsm_distill_backward(const void* logits, int dtype, int64_t rows, int64_t vo
                          const float* lse, const float* rest, const float* d_loss, void* d_logits,
                          int64_t ldd, nsm_stream_t stream);
 
+/* ---- Penalties, biases and grammar masks on logits ----------------------------------
+ * What stands between a model's logits and the distribution that a token is drawn from (or
+ * scored under: nsm_logprobs takes the result as it is, a masked token is a logit of -inf), and
+ * its backward pass.  The pages have no counterpart.
+ *
+ * For a row x of `vocab` logits whose history holds token v c_v times:
+ *     a_v   = x_v / repetition where x_v > 0, else x_v * repetition      where c_v > 0
+ *     a_v   = x_v                                                        elsewhere
+ *     out_v = a_v - (frequency * c_v + presence * [c_v > 0]) + sum of bias_j over index_j = v
+ *     out_v = -inf                                 where the row's mask has bit v clear
+ *
+ * The conventions are those of the losses over a vocabulary, and:
+ *   - The history of row r is the first length[r] tokens (clamped to [0, history_len]; length
+ *     NULL: all) of row history_row[r] (NULL: r, and then history_rows == rows) of `history`:
+ *     device, history_rows x history_len of int64 (history_wide != 0) or int32, row stride ldh.
+ *     Rows of one sequence can so share its tokens, each up to its own position.  A token
+ *     outside [0, vocab) does not count; a history_row outside [0, history_rows) is no history.
+ *     history may be NULL (no penalties; with history_len 0 its address is not looked at).
+ *   - repetition, frequency, presence: device, fp32, one per row; each may be NULL (1, 0, 0).
+ *     repetition is positive; what it holds is not looked at on the host.
+ *   - bias_index, bias: device, rows x k of int64 (bias_wide != 0) or int32, and of fp32, row
+ *     strides ldbi and ldb; 0 <= k <= 1024.  Biases of an index given several times are added
+ *     in order; an index outside [0, vocab) does not count.
+ *   - mask: device, mask_rows x ceil(vocab / 32) int32 words, row stride ldm; token v is allowed
+ *     in row r when bit v % 32 of word v / 32 of mask row mask_row[r] (NULL: r, and then
+ *     mask_rows == rows) is set.  A mask_row outside [0, mask_rows), such as -1, allows every
+ *     token.  mask may be NULL (every token in every row).
+ *   - A banned token is -inf whatever its logit was, NaN included; other NaN and infinities take
+ *     their course through the formula.  A row whose mask allows nothing is all -inf.
+ *   - Arithmetic is fp32, rounded once to the output's type. */
+
+/* out: device, rows x vocab of the logits' type or NSM_FP32 at row stride ldo; it may be the
+ * logits themselves (same pointer, stride and type: in place, where a row without a penalty, a bias
+ * or a mask is not touched). */
+int nsm_adjust_logits(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld, const void* history,
+                      int history_wide, int64_t history_rows, int64_t history_len, int64_t ldh, const int32_t* length,
+                      const int32_t* history_row, const float* repetition, const float* frequency, const float* presence,
+                      const void* bias_index, int bias_wide, int64_t ldbi, const float* bias, int64_t ldb, int k,
+                      const int32_t* mask, int64_t mask_rows, int64_t ldm, const int32_t* mask_row, void* out, int out_dtype,
+                      int64_t ldo, nsm_stream_t stream);
+
+/* The backward pass: d_logits_v = d_out_v * (1 / repetition or repetition, where c_v > 0), 0 where
+ * the token is banned, whatever d_out holds there.
+ *   logits    the forward call's input, of type dtype at row stride ld; read only with
+ *             repetition, otherwise it may be NULL
+ *   d_out     device, of that type or NSM_FP32, at row stride ldg
+ *   d_logits  device, of type dtype at row stride ldd; may be d_out itself (same pointer, stride
+ *             and type) */
+int nsm_adjust_logits_backward(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld, const void* history,
+                               int history_wide, int64_t history_rows, int64_t history_len, int64_t ldh,
+                               const int32_t* length, const int32_t* history_row, const float* repetition,
+                               const int32_t* mask, int64_t mask_rows, int64_t ldm, const int32_t* mask_row,
+                               const void* d_out, int d_out_dtype, int64_t ldg, void* d_logits, int64_t ldd,
+                               nsm_stream_t stream);
+
+/* ---- The embedding lookup and its gradient --------------------------------------------
+ * The other end of the vocabulary.  The pages have no counterpart; their routing rule sends
+ * embeddings to AdamW, whose bf16 gradient the backward call writes and whose fp32 weights the
+ * lookup reads.
+ *     out_r       = scale * weight[token_r]          (zeros where the token is outside [0, vocab))
+ *     d_weight[v] = scale * sum of d_out_r over the rows r with token_r = v
+ *
+ *   - weight, d_weight: device, vocab x cols of type NSM_BF16, NSM_FP16 or NSM_FP32, row stride
+ *     ldw >= cols; out, d_out: device, rows x cols of any of these types (it need not be the
+ *     weight's), row stride ldo / ldg >= cols.  Aligned to an element; rows on 16-byte
+ *     boundaries are fastest.  tokens: device, one int64 (tokens_wide != 0) or int32 per row.
+ *     1 <= vocab <= 2^30, 1 <= cols <= 2^20; rows may be 0.
+ *   - Elements between the columns and the row stride are left as they are.
+ *   - Sums are fp32 in the order of the rows, the same from call to call; results are rounded once.
+ *   - scale is finite.  No buffer that a call writes may overlap another one. */
+int nsm_embedding(const void* weight, int dtype, int64_t vocab, int64_t cols, int64_t ldw, const void* tokens, int tokens_wide,
+                  int64_t rows, float scale, void* out, int out_dtype, int64_t ldo, nsm_stream_t stream);
+
+/* The gradient.  accumulate == 0: every row of d_weight is written, zeros where no token asks
+ * for it; accumulate != 0: the sums are added to what d_weight holds (in fp32, rounded once), as a
+ * weight that is also the output layer's wants, and rows that no token asks for are neither
+ * read nor written.
+ *   workspace  device, >= nsm_embedding_workspace_bytes(rows, vocab, cols) bytes, 256-byte
+ *              aligned; any content, overwritten.  Calls that share one are ordered by the caller. */
+int nsm_embedding_backward(const void* d_out, int dtype, int64_t rows, int64_t cols, int64_t ldg, const void* tokens,
+                           int tokens_wide, int64_t vocab, float scale, int accumulate, void* d_weight, int weight_dtype,
+                           int64_t ldw, void* workspace, size_t workspace_bytes, nsm_stream_t stream);
+
+/* Bytes of that workspace; 0 when a size is invalid (the reason is in nsm_last_error()).
+ * Host-only. */
+size_t nsm_embedding_workspace_bytes(int64_t rows, int64_t vocab, int64_t cols);
+
+/* ---- The norm of many gradients, and clipping ------------------------------------------
+ *     norm   = sqrt(sum of g^2 over all elements of all tensors), norms[i] that of tensor i
+ *     out    = g * min(1, max_norm / norm)
+ * The pages have no counterpart.
+ *   grads     host array of n device pointers: tensor i has numels[i] >= 0 elements in one piece,
+ *             of type dtypes[i] (NSM_BF16, NSM_FP16 or NSM_FP32), aligned to an element.  The three
+ *             arrays are host memory, read during the call only.  1 <= n <= 2^20.
+ *   norm      device, one fp32; norms: device, n fp32, or NULL
+ *   workspace device, >= nsm_grad_workspace_bytes(numels, n) bytes, 256-byte aligned; any
+ *             content, overwritten.  Calls that share one are ordered by the caller.
+ * The norm has fp32's precision over the whole range of the types: squares neither overflow
+ * nor vanish (it is +inf only where the norm itself is past fp32's largest value).  A tensor with an
+ * infinity or a NaN has that as its norm.  The sums run in a fixed order. */
+int nsm_grad_norm(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int n, float* norm, float* norms,
+                  void* workspace, size_t workspace_bytes, nsm_stream_t stream);
+
+/* Clipping, with the norms of the unclipped gradients.
+ *   out       host array of n device pointers, tensor i of numels[i] elements of type
+ *             out_dtypes[i]: where the clipped gradients go, such as the optimizer's packed slots
+ *             (each may be its grads[i], of the same type); or NULL: in place.  Otherwise no
+ *             buffer that the call writes may overlap another one.
+ *   max_norm  positive and finite
+ *   norm      device, one fp32, or NULL
+ * Each result is g times an fp32 factor, rounded once.  Where the norm is no more than max_norm,
+ * or is infinite or NaN, the factor is 1: in place nothing is written. */
+int nsm_clip_grads(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int n, void* const* out,
+                   const int32_t* out_dtypes, float max_norm, float* norm, float* norms, void* workspace,
+                   size_t workspace_bytes, nsm_stream_t stream);
+
+/* Bytes of their workspace; 0 when a size is invalid (the reason is in nsm_last_error()).
+ * Host-only. */
+size_t nsm_grad_workspace_bytes(const int64_t* numels, int n);
+
 /* Synchronises `stream`, then reads and clears the device status word that kernels set
  * when a bounded wait expires (or, in the checked build, when a bounds check fails).
  * *status_out = NSM_OK, NSM_ERR_TIMEOUT or NSM_ERR_BOUNDS.  Returns NSM_ERR_CUDA if the
@@ -373,6 +493,9 @@ int nsm_device_status(nsm_stream_t stream, int* status_out);
 #define NSM_KERNEL_ADAMW      8  /* k_adamw (bounds checks only) */
 #define NSM_KERNEL_LOGPROBS   9  /* log probabilities of tokens, and their gradient */
 #define NSM_KERNEL_DISTILL   10  /* distillation from top logits, and its gradient */
+#define NSM_KERNEL_ADJUST    11  /* penalties, biases and masks on logits (bounds checks only) */
+#define NSM_KERNEL_EMBEDDING 12  /* the embedding lookup and its gradient (bounds checks only) */
+#define NSM_KERNEL_GRADS     13  /* the norm of many gradients, and clipping (bounds checks only) */
 #define NSM_ROLE_PRODUCER     1  /* the thread issuing TMA loads */
 #define NSM_ROLE_MMA          2  /* the thread issuing tensor-core MMAs */
 #define NSM_ROLE_EPILOGUE     3  /* the epilogue warps draining TMEM */
@@ -407,7 +530,11 @@ int nsm_device_status(nsm_stream_t stream, int* status_out);
 #define NSM_SITE_FLAT           22  /* AdamW's access to its flat group */
 #define NSM_SITE_SELFTEST_BOUNDS 23 /* nsm_bounds_selftest's check of an index past its range */
 #define NSM_SITE_LOGITS         24  /* load of a row of logits */
-#define NSM_SITE_GRADIENT       25  /* store to a row of the logits' gradient */
+#define NSM_SITE_GRADIENT       25  /* store to a row of the logits' gradient, or of adjusted logits */
+#define NSM_SITE_SIDE           26  /* load of a history, a bias or a mask */
+#define NSM_SITE_EMBEDDING      27  /* access to an embedding's rows, or to their gradients */
+#define NSM_SITE_WORKSPACE      28  /* access to the sorted tokens and the sums in the workspace */
+#define NSM_SITE_GRADS          29  /* access to one of many gradients */
 
 /* nsm_device_status with the location: synchronises `stream`, reads and clears the
  * status word.  *status_out = NSM_OK, NSM_ERR_TIMEOUT or NSM_ERR_BOUNDS; then *kernel_out,
@@ -449,7 +576,8 @@ int nsm_copy_to_device(void* dst, const void* src, size_t bytes, int ctas, nsm_s
 
 /* Kernel timing for profiling.  While enabled, every kernel launch of muon_step,
  * muon_orthogonalize, adamw_step, nsm_gemm, nsm_logprobs* and nsm_distill* is bracketed by CUDA events on the
- * caller's stream.  nsm_timing_read_kind synchronises the recorded events and returns,
+ * caller's stream; of nsm_adjust_logits*, nsm_embedding*, nsm_grad_norm and nsm_clip_grads the call
+ * as a whole, as one launch.  nsm_timing_read_kind synchronises the recorded events and returns,
  * summed since the last reset for one kind of kernel: *ms (device time), *launches and
  * *work (the algorithmic work of those launches: flops for NSM_KIND_GEMM, bytes that
  * must cross HBM for the other kinds).  nsm_timing_read is the GEMM kind.  Any output
@@ -468,13 +596,17 @@ int nsm_copy_to_device(void* dst, const void* src, size_t bytes, int ctas, nsm_s
 #define NSM_KIND_GRAD_NORM 7  /* the orthogonalisation's pass: sums of G^2, largest |G| */
 #define NSM_KIND_LOGPROBS  8  /* nsm_logprobs*: logits read, and gradients written */
 #define NSM_KIND_DISTILL   9  /* nsm_distill*: logits read, and gradients written */
+#define NSM_KIND_ADJUST   11  /* nsm_adjust_logits*: rows read and written */
+#define NSM_KIND_EMBEDDING 12 /* nsm_embedding*: rows read and written */
+#define NSM_KIND_GRADS    13  /* nsm_grad_norm, nsm_clip_grads: gradients read (twice) and written */
 int nsm_timing_enable(int enable);
 int nsm_timing_read(double* gemm_ms, int64_t* gemm_launches, double* gemm_flops);
 int nsm_timing_read_kind(int kind, double* ms, int64_t* launches, double* work);
 int nsm_timing_reset(void);
 
 /* Number of kernel launches the last successful muon_step / muon_orthogonalize /
- * adamw_step / nsm_logprobs* / nsm_distill* call made on this host thread. */
+ * adamw_step / nsm_logprobs* / nsm_distill* / nsm_adjust_logits* / nsm_embedding* / nsm_grad_norm /
+ * nsm_clip_grads call made on this host thread. */
 int nsm_last_launch_count(void);
 
 /* Process-wide launch options.  They select between the library's own equivalent paths,

@@ -124,8 +124,23 @@ def lib() -> ctypes.CDLL:
     L.nsm_distill.argtypes = rows_of_logits + entries + [_vp, _vp, _vp, _vp]
     L.nsm_distill_grad.argtypes = rows_of_logits + entries + [_vp, _vp, _i64, _vp, _vp, _vp, _vp]
     L.nsm_distill_backward.argtypes = rows_of_logits + entries + [_vp, _vp, _vp, _vp, _i64, _vp]
+    history = [_vp, _int, _i64, _i64, _i64, _vp, _vp]
+    mask = [_vp, _i64, _i64, _vp]
+    L.nsm_adjust_logits.argtypes = rows_of_logits + history + [_vp, _vp, _vp, _vp, _int, _i64, _vp, _i64, _int] + mask \
+        + [_vp, _int, _i64, _vp]
+    L.nsm_adjust_logits_backward.argtypes = rows_of_logits + history + [_vp] + mask + [_vp, _int, _i64, _vp, _i64, _vp]
+    L.nsm_embedding.argtypes = [_vp, _int, _i64, _i64, _i64, _vp, _int, _i64, _f32, _vp, _int, _i64, _vp]
+    L.nsm_embedding_backward.argtypes = [_vp, _int, _i64, _i64, _i64, _vp, _int, _i64, _f32, _int, _vp, _int, _i64, _vp,
+                                         ctypes.c_size_t, _vp]
+    L.nsm_embedding_workspace_bytes.argtypes = [_i64, _i64, _i64]
+    L.nsm_embedding_workspace_bytes.restype = ctypes.c_size_t
+    L.nsm_grad_norm.argtypes = [_vp, _vp, _vp, _int, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    L.nsm_clip_grads.argtypes = [_vp, _vp, _vp, _int, _vp, _vp, _f32, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    L.nsm_grad_workspace_bytes.argtypes = [_vp, _int]
+    L.nsm_grad_workspace_bytes.restype = ctypes.c_size_t
     for f in (L.nsm_logprobs, L.nsm_logprobs_grad, L.nsm_logprobs_backward, L.nsm_distill, L.nsm_distill_grad,
-              L.nsm_distill_backward):
+              L.nsm_distill_backward, L.nsm_adjust_logits, L.nsm_adjust_logits_backward, L.nsm_embedding,
+              L.nsm_embedding_backward, L.nsm_grad_norm, L.nsm_clip_grads):
         f.restype = ctypes.c_int
     L.nsm_device_status.argtypes = [_vp, ctypes.POINTER(ctypes.c_int)]
     L.nsm_device_status.restype = ctypes.c_int
@@ -385,6 +400,8 @@ TOP_MAX_K = 128
 DISTILL_MAX_K = 128
 _LOGITS_TYPES: dict = {}
 _INDEX_TYPES: dict = {}
+_WORD_TYPES: dict = {}
+_FLOAT_TYPES: dict = {}
 _FLOAT32 = _INT32 = None
 _raw_stream = _current_device = _increment_version = None
 
@@ -395,6 +412,8 @@ def _torch_types() -> None:
     import torch
     _LOGITS_TYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
     _INDEX_TYPES.update({torch.int32: 0, torch.int64: 1})
+    _WORD_TYPES.update({torch.int32: 0})
+    _FLOAT_TYPES.update({torch.float32: 2})
     _FLOAT32, _INT32 = torch.float32, torch.int32
     # what torch's public functions call: the current stream's handle without a Stream object is a
     # third of a short call's time, the other two save a fifth
@@ -602,6 +621,249 @@ def distill_backward(logits, teacher, index, lse, rest, d_loss, d_logits, temper
     _written(d_logits)
 
 
+# ---------------------------------------------------------------- penalties, biases and masks on logits
+
+ADJUST_MAX_K = 1024
+
+
+def _history(history, length, history_row, rows: int, device: int) -> Tuple[int, int, int, int, int, int, int]:
+    if history is None:
+        return 0, 0, 0, 0, 0, _numbers("length", length, (rows,), device, _INT32), \
+            _numbers("history_row", history_row, (rows,), device, _INT32)
+    shape = history.shape
+    if len(shape) != 2:
+        raise ValueError("history is not a matrix of tokens")
+    ptr, wide, ld = _matrix("history", history, _INDEX_TYPES, shape[0], shape[1], device)
+    return ptr, wide, shape[0], shape[1], ld, _numbers("length", length, (rows,), device, _INT32), \
+        _numbers("history_row", history_row, (rows,), device, _INT32)
+
+
+def _mask(mask, mask_row, rows: int, vocab: int, device: int) -> Tuple[int, int, int, int]:
+    row = _numbers("mask_row", mask_row, (rows,), device, _INT32)
+    if mask is None:
+        return 0, 0, 0, row
+    if len(mask.shape) != 2:
+        raise ValueError("mask is not a matrix of words")
+    ptr, _, ld = _matrix("mask", mask, _WORD_TYPES, mask.shape[0], (vocab + 31) // 32, device)
+    return ptr, mask.shape[0], ld, row
+
+
+def _logits_like(name: str, t, code: int, rows: int, vocab: int, device: int) -> Tuple[int, int, int]:
+    """(pointer, type code, row stride) of a rows x vocab tensor of the logits' type or float32."""
+    ptr, own_code, ld = _matrix(name, t, _LOGITS_TYPES, rows, vocab, device)
+    if own_code != code and own_code != 2:
+        raise ValueError(f"{name} has type {t.dtype}: the logits' or torch.float32 is wanted")
+    return ptr, own_code, ld
+
+
+def adjust_logits(logits, out, history=None, length=None, history_row=None, repetition=None, frequency=None,
+                  presence=None, bias_index=None, bias=None, mask=None, mask_row=None, stream=None) -> None:
+    """Penalties for repeated tokens, biases and a grammar's mask on rows of logits.
+
+    ``out`` (rows x vocab, the logits' type or float32; it may be ``logits`` itself) receives
+    each logit, where the row's history holds token v c times: x / ``repetition`` (x *
+    ``repetition`` where x <= 0), less ``frequency`` * c + ``presence``; with the biases that
+    ``bias_index`` gives for v added; and -inf where the row's mask has bit v clear, which is a
+    masked token to :func:`logprobs` and the other losses.
+
+    ``history`` (int32 or int64, history rows x tokens): row r's is the first ``length[r]``
+    (int32, None: all) tokens of row ``history_row[r]`` (int32, None: r).  ``repetition``,
+    ``frequency`` and ``presence`` are float32, one per row.  ``bias_index`` (int32 or int64) and
+    ``bias`` (float32) are rows x k, k <= 1024.  ``mask`` (int32, mask rows x ceil(vocab / 32)) has
+    bit v % 32 of word v // 32 set where v is allowed; row r's is ``mask_row[r]`` (int32, None: r;
+    -1: everything is allowed).  Indexes outside the vocabulary do not count."""
+    ptr, code, rows, vocab, ld, dev = _logits(logits)
+    row = (rows,)
+    o_ptr, o_code, ldo = _logits_like("out", out, code, rows, vocab, dev)
+    k, bi_ptr, b_wide, ldbi, b_ptr, ldb = 0, 0, 0, 0, 0, 0
+    if bias_index is not None or bias is not None:
+        shape = () if bias_index is None or bias is None else bias_index.shape
+        if len(shape) != 2:
+            raise ValueError("bias_index and bias go together, as matrices of rows x k")
+        k = shape[1]
+        bi_ptr, b_wide, ldbi = _matrix("bias_index", bias_index, _INDEX_TYPES, rows, k, dev)
+        b_ptr, _, ldb = _matrix("bias", bias, _FLOAT_TYPES, rows, k, dev)
+    _check(lib().nsm_adjust_logits(ptr, code, rows, vocab, ld, *_history(history, length, history_row, rows, dev),
+                                   _numbers("repetition", repetition, row, dev, _FLOAT32),
+                                   _numbers("frequency", frequency, row, dev, _FLOAT32),
+                                   _numbers("presence", presence, row, dev, _FLOAT32), bi_ptr, b_wide, ldbi, b_ptr, ldb, k,
+                                   *_mask(mask, mask_row, rows, vocab, dev), o_ptr, o_code, ldo, _loss_stream(stream, dev)))
+    _written(out)
+
+
+def adjust_logits_backward(logits, d_out, d_logits, history=None, length=None, history_row=None, repetition=None,
+                           mask=None, mask_row=None, stream=None) -> None:
+    """The backward pass of :func:`adjust_logits`: writes ``d_logits`` (the logits' type) from
+    ``d_out`` (that type or float32; of the logits' type it may be ``d_logits`` itself).  ``logits``
+    are the forward call's input, as they were before it; only ``repetition`` needs them, and
+    without it they may be None.  Frequency, presence and biases change no gradient."""
+    if logits is None and repetition is not None:
+        raise ValueError("repetition needs the logits")
+    like = d_logits if logits is None else logits
+    ptr, code, rows, vocab, ld, dev = _logits(like)
+    g_ptr, ldd = _gradient(d_logits, code, rows, vocab, dev)
+    o_ptr, o_code, ldo = _logits_like("d_out", d_out, code, rows, vocab, dev)
+    _check(lib().nsm_adjust_logits_backward(0 if logits is None else ptr, code, rows, vocab, ld,
+                                            *_history(history, length, history_row, rows, dev),
+                                            _numbers("repetition", repetition, (rows,), dev, _FLOAT32),
+                                            *_mask(mask, mask_row, rows, vocab, dev), o_ptr, o_code, ldo, g_ptr, ldd,
+                                            _loss_stream(stream, dev)))
+    _written(d_logits)
+
+
+# ---------------------------------------------------------------- the embedding lookup and its gradient
+
+
+def _rows_of(name: str, t) -> Tuple[int, int, int, int, int, int]:
+    """(pointer, type code, rows, columns, row stride, device) of a matrix on the current device."""
+    if _FLOAT32 is None:
+        _torch_types()
+    device = t.get_device()
+    shape = t.shape
+    if len(shape) != 2 or device < 0:
+        raise ValueError(f"{name} is not a matrix in device memory")
+    if device != _current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    ptr, code, ld = _matrix(name, t, _LOGITS_TYPES, shape[0], shape[1], device)
+    return ptr, code, shape[0], shape[1], ld, device
+
+
+def embedding(weight, tokens, out, scale: float = 1.0, stream=None) -> None:
+    """out[r] = scale * weight[tokens[r]], zeros where the token (int32 or int64) is outside the
+    vocabulary.  ``weight`` (vocab x cols) and ``out`` (rows x cols) have any of the three types
+    each: an optimizer's fp32 master weights can give bf16 activations."""
+    w_ptr, w_code, vocab, cols, ldw, dev = _rows_of("weight", weight)
+    rows = len(tokens)
+    t_ptr, wide = _tokens(tokens, rows, dev)
+    o_ptr, o_code, ldo = _matrix("out", out, _LOGITS_TYPES, rows, cols, dev)
+    _check(lib().nsm_embedding(w_ptr, w_code, vocab, cols, ldw, t_ptr, wide, rows, float(scale), o_ptr, o_code, ldo,
+                               _loss_stream(stream, dev)))
+    _written(out)
+
+
+def embedding_workspace_bytes(rows: int, vocab: int, cols: int) -> int:
+    """Bytes of :func:`embedding_backward`'s workspace."""
+    b = lib().nsm_embedding_workspace_bytes(int(rows), int(vocab), int(cols))
+    if b == 0:
+        raise NsmError(NSM_ERR_SHAPE, last_error())
+    return int(b)
+
+
+def embedding_backward(d_out, tokens, d_weight, workspace, scale: float = 1.0, accumulate: bool = False,
+                       stream=None) -> None:
+    """The gradient of :func:`embedding`: d_weight[v] = scale * the sum of d_out's rows of token
+    v, zeros in rows without one; with ``accumulate`` the sums are added to what ``d_weight``
+    holds (a weight that is the output layer's too).  ``d_weight`` and ``d_out`` have any of the
+    three types each; ``MuonAdamW.grad(name)`` is such a ``d_weight``.  The order of every sum is that
+    of the rows."""
+    w_ptr, w_code, vocab, cols, ldw, dev = _rows_of("d_weight", d_weight)
+    rows = len(tokens)
+    t_ptr, wide = _tokens(tokens, rows, dev)
+    g_ptr, g_code, ldg = _matrix("d_out", d_out, _LOGITS_TYPES, rows, cols, dev)
+    ws_ptr, ws_size = _workspace(workspace, dev)
+    _check(lib().nsm_embedding_backward(g_ptr, g_code, rows, cols, ldg, t_ptr, wide, vocab, float(scale),
+                                        1 if accumulate else 0, w_ptr, w_code, ldw, ws_ptr, ws_size,
+                                        _loss_stream(stream, dev)))
+    _written(d_weight)
+
+
+def _workspace(workspace, device: int) -> Tuple[int, int]:
+    """(pointer, bytes) of a contiguous tensor of any type."""
+    if workspace is None:
+        return 0, 0
+    if workspace.get_device() != device:
+        raise ValueError(f"workspace is on {workspace.device}, not on the current device")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace is not contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+# ---------------------------------------------------------------- the norm of many gradients, and clipping
+
+class GradTable:
+    """The places of many gradients and, for :func:`clip_grads`, of where the clipped ones go
+    (``out``, None: in place).  A program whose gradients stay where they are keeps one from step to
+    step; it holds the tensors.  Each is contiguous, bf16, fp16 or fp32, all on one device."""
+
+    def __init__(self, grads: Sequence, out: Optional[Sequence] = None):
+        if _FLOAT32 is None:
+            _torch_types()
+        self.grads = list(grads)
+        self.out = None if out is None else list(out)
+        n = len(self.grads)
+        if n == 0:
+            raise ValueError("no gradients are given")
+        if self.out is not None and len(self.out) != n:
+            raise ValueError(f"{n} gradients and {len(self.out)} places for them")
+        self.device = self.grads[0].get_device()
+        self.numels = np.zeros(n, dtype=np.int64)
+        self._places, self._types = self._table("gradient", self.grads)
+        for i, t in enumerate(self.grads):
+            self.numels[i] = t.numel()
+        self._out_places = self._out_types = None
+        if self.out is not None:
+            self._out_places, self._out_types = self._table("out", self.out)
+            for i, t in enumerate(self.out):
+                if t.numel() != self.numels[i]:
+                    raise ValueError(f"out {i} has {t.numel()} elements, its gradient {self.numels[i]}")
+        b = lib().nsm_grad_workspace_bytes(self.numels.ctypes.data, n)
+        if b == 0:
+            raise NsmError(NSM_ERR_SHAPE, last_error())
+        self.workspace_bytes = int(b)
+        # for the calls: arrays as the library takes them
+        self._in_args = (self._places.ctypes.data, self.numels.ctypes.data, self._types.ctypes.data, n)
+        self._out_args = (0, 0) if self.out is None else (self._out_places.ctypes.data, self._out_types.ctypes.data)
+
+    def __len__(self) -> int:
+        return len(self.grads)
+
+    def _table(self, name: str, tensors) -> Tuple[np.ndarray, np.ndarray]:
+        places = np.zeros(len(tensors), dtype=np.uint64)
+        types = np.zeros(len(tensors), dtype=np.int32)
+        for i, t in enumerate(tensors):
+            code = _LOGITS_TYPES.get(t.dtype)
+            if code is None:
+                raise ValueError(f"{name} {i} has type {t.dtype}: one of {[str(c) for c in _LOGITS_TYPES]} is wanted")
+            device = t.get_device()
+            if device < 0 or device != self.device:
+                raise ValueError(f"{name} {i} is on {t.device}: all are wanted on one device")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} {i} is not contiguous")
+            places[i], types[i] = t.data_ptr(), code
+        return places, types
+
+    def _checked(self, norm, norms, workspace, stream):
+        """What both calls check; (norm, norms, workspace, its bytes, stream) as the library takes them."""
+        device = self.device
+        if device != _current_device():
+            raise ValueError("the gradients are not on the current device")
+        if norm is not None and norm.shape != ():
+            norm_ptr = _numbers("norm", norm, (1,), device, _FLOAT32)
+        else:
+            norm_ptr = _numbers("norm", norm, (), device, _FLOAT32)
+        norms_ptr = _numbers("norms", norms, (len(self.grads),), device, _FLOAT32)
+        return (norm_ptr, norms_ptr, *_workspace(workspace, device), _loss_stream(stream, device))
+
+
+def grad_norm(grads, norm, norms=None, workspace=None, stream=None) -> None:
+    """Writes the norm of all gradients together to ``norm`` (float32, one element) and each
+    one's to ``norms`` (float32, one per gradient, or None).  ``grads`` is a :class:`GradTable` or a
+    list of tensors; ``workspace`` has the table's ``workspace_bytes``."""
+    table = grads if isinstance(grads, GradTable) else GradTable(grads)
+    _check(lib().nsm_grad_norm(*table._in_args, *table._checked(norm, norms, workspace, stream)))
+    _written(norm, norms)
+
+
+def clip_grads(grads, max_norm: float, norm=None, norms=None, workspace=None, stream=None) -> None:
+    """Scales the gradients by min(1, max_norm / norm), in place or to the table's ``out``
+    (converted to its types), and writes the norms before clipping as :func:`grad_norm` does.
+    A norm that is infinite or NaN leaves the gradients as they are."""
+    table = grads if isinstance(grads, GradTable) else GradTable(grads)
+    _check(lib().nsm_clip_grads(*table._in_args, *table._out_args, float(max_norm),
+                                *table._checked(norm, norms, workspace, stream)))
+    _written(norm, norms, *(table.grads if table.out is None else table.out))
+
+
 def device_status(stream=None) -> int:
     """Synchronises the stream; returns NSM_OK, NSM_ERR_TIMEOUT or (checked build)
     NSM_ERR_BOUNDS, and clears the record."""
@@ -676,10 +938,12 @@ def timing_reset() -> None:
 
 KIND_GEMM, KIND_MOMENTUM, KIND_NORM, KIND_LAYOUT, KIND_APPLY, KIND_ADAMW, KIND_SMALL, KIND_GRAD_NORM, \
     KIND_LOGPROBS, KIND_DISTILL = range(10)
+KIND_ADJUST, KIND_EMBEDDING, KIND_GRADS = 11, 12, 13
 KIND_NAMES = {KIND_GEMM: "k_ns_gemm", KIND_MOMENTUM: "k_momentum_class", KIND_NORM: "k_scale_finalize",
               KIND_LAYOUT: "k_to_class", KIND_APPLY: "k_from_class", KIND_ADAMW: "k_adamw",
               KIND_SMALL: "k_ns_small", KIND_GRAD_NORM: "k_grad_norm",
-              KIND_LOGPROBS: "k_logprobs", KIND_DISTILL: "k_distill"}
+              KIND_LOGPROBS: "k_logprobs", KIND_DISTILL: "k_distill", KIND_ADJUST: "k_adjust",
+              KIND_EMBEDDING: "k_embed", KIND_GRADS: "k_grad_clip"}
 
 
 def timing_read(kind: int = KIND_GEMM) -> Tuple[float, int, float]:
@@ -766,6 +1030,8 @@ class MuonAdamW:
         self.adam_exp_avg = torch.zeros(n_adam, dtype=torch.float32, device=dev)
         self.adam_exp_avg_sq = torch.zeros(n_adam, dtype=torch.float32, device=dev)
         self.adam_grads = torch.zeros(n_adam, dtype=torch.bfloat16, device=dev)
+        self._clip = None  # the slots' table, norm and workspace, made by the first clip
+        self.grad_norms = None
 
     def _view(self, name: str, muon_buf, adam_buf):
         shape = self._shape_of[name]
@@ -788,7 +1054,39 @@ class MuonAdamW:
         """The bf16 gradient slot of a parameter (a view; write each step's gradient here)."""
         return self._view(name, getattr(self, "muon_grads", None), self.adam_grads)
 
-    def step(self, stream=None) -> None:
+    def clip(self, max_norm: float, grads=None, stream=None):
+        """Scales all gradient slots together by min(1, max_norm / their norm); with ``grads`` (a
+        mapping of every parameter's name to its gradient, bf16, fp16 or fp32) those are clipped
+        into the slots, which takes the place of copying them there.  Returns the norm before
+        clipping (float32, one element on the device); ``grad_norms`` then holds each
+        parameter's, Muon's first, in the order of ``muon_names`` and ``adam_names``."""
+        import torch
+        names = self.muon_names + self.adam_names
+        buffers = (getattr(self, "muon_grads", None), self.adam_grads)
+        if self._clip is None or any(a is not b for a, b in zip(self._clip[4], buffers)):
+            slots = [self.grad(n) for n in names]
+            table = GradTable(slots)
+            dev = self.adam_params.device
+            self.grad_norms = torch.zeros(len(names), dtype=torch.float32, device=dev)
+            self._clip = (slots, table, torch.zeros(1, dtype=torch.float32, device=dev),
+                          torch.empty(table.workspace_bytes, dtype=torch.uint8, device=dev), buffers)
+        slots, table, norm, workspace, _ = self._clip
+        if grads is not None:
+            lacking = [n for n in names if grads.get(n) is None]
+            if lacking or len(grads) != len(names):
+                raise ValueError(f"grads names other parameters than the optimizer's (without {lacking})")
+            for n in names:
+                if tuple(grads[n].shape) != self._shape_of[n]:
+                    raise ValueError(f"the gradient of {n!r} has shape {tuple(grads[n].shape)}: {self._shape_of[n]} is wanted")
+            table = GradTable([grads[n] for n in names], slots)
+        clip_grads(table, max_norm, norm, self.grad_norms, workspace=workspace, stream=stream)
+        return norm
+
+    def step(self, stream=None, max_norm: Optional[float] = None) -> None:
+        """One step of both groups on the slots' gradients, clipped to ``max_norm`` together
+        first where it is given."""
+        if max_norm is not None:
+            self.clip(max_norm, stream=stream)
         self.step_count += 1
         if self.muon_shapes:
             muon_step(self.muon_grads, self.muon_params, self.muon_momentum, self.offsets,

@@ -17,6 +17,7 @@
 #include <map>
 #include <memory>
 #include <mutex>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -911,7 +912,8 @@ Plan* get_plan(const int32_t* shapes, const int64_t* offsets, int n, int method,
 // ---------------------------------------------------------------- timing
 
 // Kernel kinds the timing hooks distinguish (NSM_KIND_* in the header).
-constexpr int kKinds = 10;
+constexpr int kKinds = 14;  // 10 is none
+bool known_kind(int kind) { return kind >= 0 && kind < kKinds && kind != 10; }
 
 struct Timing {
   std::mutex mu;
@@ -1213,6 +1215,276 @@ int check_workspace(void* ws, size_t ws_bytes, size_t need) {
   if (!ws) return fail(NSM_ERR_WORKSPACE, "workspace is NULL");
   if (!aligned(ws, 256)) return fail(NSM_ERR_ALIGN, "workspace is not 256-byte aligned");
   if (ws_bytes < need) return fail(NSM_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", ws_bytes, need);
+  return NSM_OK;
+}
+
+// ---- penalties, biases and masks on logits
+
+bool known_dtype(int dtype) { return dtype == NSM_BF16 || dtype == NSM_FP16 || dtype == NSM_FP32; }
+
+// The arguments that both directions have, and the launch.
+int run_adjust(AdjustArgs& a, nsm_stream_t stream_) {
+  const char* in_name = a.backward ? "d_out" : "logits";
+  const char* out_name = a.backward ? "d_logits" : "out";
+  const int dtype = a.backward ? a.out_dtype : a.in_dtype, other = a.backward ? a.in_dtype : a.out_dtype;
+  if (!known_dtype(dtype)) return fail(NSM_ERR_ARG, "unknown logits type %d", dtype);
+  if (other != dtype && other != NSM_FP32)
+    return fail(NSM_ERR_ARG, "%s has type %d: the logits' or NSM_FP32 is wanted", a.backward ? in_name : out_name, other);
+  if (a.rows < 0 || a.rows > INT32_MAX)
+    return fail(NSM_ERR_SHAPE, "rows = %lld not in [0, 2^31 - 1]", static_cast<long long>(a.rows));
+  if (a.vocab < 1 || a.vocab > kVocabMax) return fail(NSM_ERR_SHAPE, "vocab = %d not in [1, %d]", a.vocab, kVocabMax);
+  if (a.k < 0 || a.k > kBiasMaxK) return fail(NSM_ERR_ARG, "k = %d not in [0, %d]", a.k, kBiasMaxK);
+  if (a.rows == 0) {
+    t_last_launches = 0;
+    return NSM_OK;
+  }
+  const size_t in_size = number_bytes(a.in_dtype), out_size = number_bytes(a.out_dtype), size = number_bytes(dtype);
+  const size_t hsize = a.history_wide ? 8 : 4, bsize = a.bias_wide ? 8 : 4;
+  const int64_t words = (a.vocab + 31) / 32;
+  int rc = check_matrix(in_name, a.in, a.rows, a.ld_in, a.vocab, in_size);
+  if (rc != NSM_OK) return rc;
+  if ((rc = check_matrix(out_name, a.out, a.rows, a.ld_out, a.vocab, out_size)) != NSM_OK) return rc;
+  if (a.backward && a.repetition && (rc = check_matrix("logits", a.logits, a.rows, a.ld_logits, a.vocab, size)) != NSM_OK) return rc;
+  if (a.history || (a.history_rows > 0 && a.history_len == 0)) {  // no token has no place
+    if (a.history_rows < 1 || a.history_rows > INT32_MAX || a.history_len < 0 || a.history_len > INT32_MAX)
+      return fail(NSM_ERR_SHAPE, "history has %lld rows of %lld tokens", static_cast<long long>(a.history_rows),
+                  static_cast<long long>(a.history_len));
+    if (a.history_len > 0 && (rc = check_matrix("history", a.history, a.history_rows, a.ldh, a.history_len, hsize)) != NSM_OK) return rc;
+    if (!a.history_row && a.history_rows != a.rows)
+      return fail(NSM_ERR_SHAPE, "history has %lld rows for %lld rows of logits, and no history_row",
+                  static_cast<long long>(a.history_rows), static_cast<long long>(a.rows));
+  } else if (a.length || a.history_row) {
+    return fail(NSM_ERR_NULL, "length or history_row is given without history");
+  } else if (a.repetition || a.frequency || a.presence) {
+    return fail(NSM_ERR_NULL, "a penalty is given without history");
+  }
+  if (a.k > 0) {
+    if ((rc = check_matrix("bias_index", a.bias_index, a.rows, a.ldbi, a.k, bsize)) != NSM_OK) return rc;
+    if ((rc = check_matrix("bias", a.bias, a.rows, a.ldb, a.k, 4)) != NSM_OK) return rc;
+  }
+  if (a.mask) {
+    if (a.mask_rows < 1 || a.mask_rows > INT32_MAX)
+      return fail(NSM_ERR_SHAPE, "mask has %lld rows", static_cast<long long>(a.mask_rows));
+    if ((rc = check_matrix("mask", a.mask, a.mask_rows, a.ldm, words, 4)) != NSM_OK) return rc;
+    if (!a.mask_row && a.mask_rows != a.rows)
+      return fail(NSM_ERR_SHAPE, "mask has %lld rows for %lld rows of logits, and no mask_row",
+                  static_cast<long long>(a.mask_rows), static_cast<long long>(a.rows));
+  } else if (a.mask_row) {
+    return fail(NSM_ERR_NULL, "mask_row is given without mask");
+  }
+  const struct { const char* what; const void* p; } numbers[] = {{"length", a.length}, {"history_row", a.history_row},
+                                                                 {"repetition", a.repetition}, {"frequency", a.frequency},
+                                                                 {"presence", a.presence}, {"mask_row", a.mask_row}};
+  for (const auto& x : numbers)
+    if ((rc = check_numbers(x.what, x.p, 4)) != NSM_OK) return rc;
+  a.in_place = a.in == a.out && a.ld_in == a.ld_out && in_size == out_size;
+  const size_t n = size_t(a.rows) * 4;
+  const Range ranges[] = {
+      matrix_range(a.in, a.rows, a.ld_in, a.vocab, in_size, a.in_place != 0),
+      matrix_range(a.in_place ? nullptr : a.out, a.rows, a.ld_out, a.vocab, out_size, true),
+      matrix_range(a.backward && a.repetition ? a.logits : nullptr, a.rows, a.ld_logits, a.vocab, size, false),
+      matrix_range(a.history_len > 0 ? a.history : nullptr, std::max<int64_t>(a.history_rows, 1), a.ldh, a.history_len, hsize, false),
+      matrix_range(a.k ? a.bias_index : nullptr, a.rows, a.ldbi, a.k, bsize, false),
+      matrix_range(a.k ? a.bias : nullptr, a.rows, a.ldb, a.k, 4, false),
+      matrix_range(a.mask, a.mask ? a.mask_rows : 1, a.ldm, words, 4, false),
+      {a.length, n, false}, {a.history_row, n, false}, {a.repetition, n, false}, {a.frequency, n, false},
+      {a.presence, n, false}, {a.mask_row, n, false}};
+  if ((rc = check_ranges(ranges, int(sizeof ranges / sizeof ranges[0]))) != NSM_OK) return rc;
+  if (a.history_len == 0 || (a.backward && !a.repetition)) a.history = nullptr;  // nothing that it could change
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const PdlScope pdl(a.rows * a.vocab);
+  cudaError_t e;
+  {
+    TimedLaunch t(stream, NSM_KIND_ADJUST, double(a.rows) * a.vocab * double(in_size + out_size));
+    e = launch_adjust(a, stream);
+  }
+  if (e != cudaSuccess) return fail_cuda(e, "launch of the logits' adjustment");
+  t_last_launches = 1;
+  return NSM_OK;
+}
+
+// ---- the embedding lookup and its gradient
+
+constexpr int64_t kEmbeddingMaxVocab = int64_t(1) << 30, kEmbeddingMaxCols = int64_t(1) << 20;
+
+int check_embedding_sizes(int64_t rows, int64_t vocab, int64_t cols) {
+  if (rows < 0 || rows > INT32_MAX) return fail(NSM_ERR_SHAPE, "rows = %lld not in [0, 2^31 - 1]", static_cast<long long>(rows));
+  if (vocab < 1 || vocab > kEmbeddingMaxVocab)
+    return fail(NSM_ERR_SHAPE, "vocab = %lld not in [1, 2^30]", static_cast<long long>(vocab));
+  if (cols < 1 || cols > kEmbeddingMaxCols) return fail(NSM_ERR_SHAPE, "cols = %lld not in [1, 2^20]", static_cast<long long>(cols));
+  return NSM_OK;
+}
+
+// What both directions check: sizes, types, tokens, the two matrices and their overlaps.
+int check_embedding(const EmbeddingArgs& a, const void* workspace, size_t workspace_bytes) {
+  const bool backward = a.d_weight != nullptr;
+  const void *weight = backward ? a.d_weight : a.weight, *rows = backward ? a.rows_in : a.rows_out;
+  const char *weight_name = backward ? "d_weight" : "weight", *rows_name = backward ? "d_out" : "out";
+  if (!known_dtype(a.weight_dtype)) return fail(NSM_ERR_ARG, "%s has the unknown type %d", weight_name, a.weight_dtype);
+  if (!known_dtype(a.rows_dtype)) return fail(NSM_ERR_ARG, "%s has the unknown type %d", rows_name, a.rows_dtype);
+  if (!std::isfinite(a.scale)) return fail(NSM_ERR_ARG, "scale must be finite");
+  const size_t wsize = number_bytes(a.weight_dtype), rsize = number_bytes(a.rows_dtype), tsize = a.tokens_wide ? 8 : 4;
+  int rc = check_matrix(weight_name, weight, a.vocab, a.ld_weight, a.cols, wsize);
+  if (rc != NSM_OK) return rc;
+  if (a.rows > 0) {
+    if (!a.tokens) return fail(NSM_ERR_NULL, "tokens is NULL");
+    if ((rc = check_numbers("tokens", a.tokens, tsize)) != NSM_OK) return rc;
+    if ((rc = check_matrix(rows_name, rows, a.rows, a.ld_rows, a.cols, rsize)) != NSM_OK) return rc;
+  }
+  const Range ranges[] = {matrix_range(weight, a.vocab, a.ld_weight, a.cols, wsize, backward),
+                          matrix_range(a.rows > 0 ? rows : nullptr, std::max<int64_t>(a.rows, 1), a.ld_rows, a.cols, rsize, !backward),
+                          {a.rows > 0 ? a.tokens : nullptr, size_t(a.rows) * tsize, false},
+                          {workspace, workspace_bytes, true}};
+  return check_ranges(ranges, int(sizeof ranges / sizeof ranges[0]));
+}
+
+int current_sms(int* num_sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? NSM_OK : fail_cuda(e, "device query");
+}
+
+// ---- the norm of many gradients, and clipping
+
+constexpr int kGradMaxTensors = 1 << 20;
+constexpr int64_t kGradMaxNumel = int64_t(1) << 44;
+
+// Chunks of all tensors together.
+int check_grad_sizes(const int64_t* numels, int n, int64_t* chunks) {
+  if (!numels) return fail(NSM_ERR_NULL, "numels is NULL");
+  if (n < 1 || n > kGradMaxTensors) return fail(NSM_ERR_SHAPE, "n = %d not in [1, %d]", n, kGradMaxTensors);
+  int64_t all = 0;
+  for (int i = 0; i < n; ++i) {
+    if (numels[i] < 0 || numels[i] > kGradMaxNumel)
+      return fail(NSM_ERR_SHAPE, "tensor %d has %lld elements", i, static_cast<long long>(numels[i]));
+    all += (numels[i] + kGradChunk - 1) / kGradChunk;
+  }
+  if (all > INT32_MAX) return fail(NSM_ERR_SHAPE, "the tensors have too many elements together");
+  *chunks = all;
+  return NSM_OK;
+}
+
+size_t grad_bytes(int64_t chunks, int n) { return align_up(size_t(chunks) * 8, 256) + align_up(size_t(n) * 8, 256); }
+
+struct Span {
+  uintptr_t from, to;
+  bool written;
+};
+
+// No written span may overlap another one.  Sorts them.
+int check_spans(Span* spans, int n) {
+  const auto before = [](const Span& x, const Span& y) { return x.from < y.from; };
+  if (!std::is_sorted(spans, spans + n, before)) std::sort(spans, spans + n, before);
+  uintptr_t any = 0, written = 0;  // where those so far end
+  for (int i = 0; i < n; ++i) {
+    if (spans[i].from == spans[i].to) continue;
+    if (spans[i].from < (spans[i].written ? any : written))
+      return fail(NSM_ERR_ARG, "a buffer that the call writes overlaps another one");
+    any = std::max(any, spans[i].to);
+    if (spans[i].written) written = std::max(written, spans[i].to);
+  }
+  return NSM_OK;
+}
+
+// clip: out is where the clipped gradients go (NULL: in place); else nothing but norms.
+int run_grads(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int n, bool clip, void* const* out,
+              const int32_t* out_dtypes, float max_norm, float* norm, float* norms, void* workspace, size_t workspace_bytes,
+              nsm_stream_t stream_) {
+  int64_t chunks = 0;
+  int rc = check_grad_sizes(numels, n, &chunks);
+  if (rc != NSM_OK) return rc;
+  if (!grads || !dtypes) return fail(NSM_ERR_NULL, "grads or dtypes is NULL");
+  if (out && !out_dtypes) return fail(NSM_ERR_NULL, "out_dtypes is NULL");
+  const std::unique_ptr<GradTensor[]> tensors(new (std::nothrow) GradTensor[size_t(n)]);
+  const std::unique_ptr<Span[]> spans(new (std::nothrow) Span[size_t(n) * 2 + 3]);
+  if (!tensors || !spans) return fail(NSM_ERR_ARG, "no host memory for a table of %d tensors", n);
+  int count = 0;
+  const auto add = [&](const void* p, size_t bytes, bool written) {
+    if (p) spans[count++] = {reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, written};
+  };
+  double bytes = 0;
+  for (int i = 0; i < n; ++i) {
+    GradTensor& t = tensors[i];
+    t = GradTensor{grads[i], out ? out[i] : const_cast<void*>(grads[i]), numels[i], 0, 0, 0};
+    const int out_dtype = out ? out_dtypes[i] : dtypes[i];
+    if (!known_dtype(dtypes[i]) || !known_dtype(out_dtype))
+      return fail(NSM_ERR_ARG, "tensor %d has the unknown type %d", i, known_dtype(dtypes[i]) ? out_dtype : dtypes[i]);
+    t.in_dtype = static_cast<int16_t>(dtypes[i]);
+    t.out_dtype = static_cast<int16_t>(out_dtype);
+    if (numels[i] == 0) continue;
+    const size_t in_size = number_bytes(dtypes[i]), out_size = number_bytes(out_dtype);
+    if (!t.in || !t.out) return fail(NSM_ERR_NULL, "tensor %d is NULL", i);
+    if (!aligned(t.in, in_size) || !aligned(t.out, out_size))
+      return fail(NSM_ERR_ALIGN, "tensor %d is not aligned to its elements", i);
+    const bool same = t.out == t.in && out_dtype == dtypes[i];
+    add(t.in, size_t(numels[i]) * in_size, clip && same);
+    if (clip && !same) add(t.out, size_t(numels[i]) * out_size, true);
+    bytes += double(numels[i]) * double(clip ? 2 * in_size + out_size : in_size);
+  }
+  if ((rc = check_workspace(workspace, workspace_bytes, grad_bytes(chunks, n))) != NSM_OK) return rc;
+  if ((rc = check_numbers("norm", norm, 4)) != NSM_OK) return rc;
+  if ((rc = check_numbers("norms", norms, 4)) != NSM_OK) return rc;
+  add(workspace, workspace_bytes, true);
+  add(norm, 4, true);
+  add(norms, size_t(n) * 4, true);
+  if ((rc = check_spans(spans.get(), count)) != NSM_OK) return rc;
+  int num_sms = 0;
+  if ((rc = current_sms(&num_sms)) != NSM_OK) return rc;
+
+  double* partials = static_cast<double*>(workspace);
+  double* sums = reinterpret_cast<double*>(static_cast<char*>(workspace) + align_up(size_t(chunks) * 8, 256));
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const PdlScope pdl(0);  // several kernels of which all but the largest tables' are short
+  int launches = 0;
+  cudaError_t e = cudaSuccess;
+  // the tensors of one launch from first on, their chunks counted from 0
+  const auto part = [&](int first, int* total) {
+    const int m = std::min(n - first, kGradTable);
+    int64_t all = 0;
+    for (int i = first; i < first + m; ++i) {
+      tensors[i].chunk_begin = static_cast<int32_t>(all);
+      all += (numels[i] + kGradChunk - 1) / kGradChunk;
+    }
+    *total = static_cast<int>(all);
+    return m;
+  };
+  {
+    TimedLaunch t(stream, NSM_KIND_GRADS, bytes);
+    int64_t done = 0;
+    for (int first = 0; first < n && e == cudaSuccess; first += kGradTable) {
+      int total = 0;
+      const int m = part(first, &total);
+      if (total > 0) {
+        e = launch_grad_chunks(&tensors[first], m, total, partials + done, stream);
+        ++launches;
+      }
+      if (e == cudaSuccess) e = launch_grad_sums(&tensors[first], m, total, partials + done, sums + first, norms ? norms + first : nullptr, stream);
+      ++launches;
+      done += total;
+    }
+    if (!clip) {
+      if (e == cudaSuccess) e = launch_grad_total(sums, n, norm, stream);
+      ++launches;
+    }
+    bool said = false;
+    for (int first = 0; clip && first < n && e == cudaSuccess; first += kGradTable) {
+      int total = 0;
+      const int m = part(first, &total);
+      if (total == 0) continue;
+      bool in_place = true;
+      for (int i = first; i < first + m; ++i) in_place &= numels[i] == 0 || (tensors[i].out == tensors[i].in && tensors[i].out_dtype == tensors[i].in_dtype);
+      e = launch_grad_clip(&tensors[first], m, total, sums, n, max_norm, said ? nullptr : norm, in_place, num_sms, stream);
+      said = true;
+      ++launches;
+    }
+    if (clip && !said && norm && e == cudaSuccess) {  // nothing but empty tensors
+      e = launch_grad_total(sums, n, norm, stream);
+      ++launches;
+    }
+  }
+  if (e != cudaSuccess) return fail_cuda(e, "launch of the gradients' norm");
+  t_last_launches = launches;
   return NSM_OK;
 }
 
@@ -1947,6 +2219,180 @@ int nsm_distill_backward(const void* logits, int dtype, int64_t rows, int64_t vo
   return run_distill(a, stream);
 }
 
+int nsm_adjust_logits(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld, const void* history,
+                      int history_wide, int64_t history_rows, int64_t history_len, int64_t ldh, const int32_t* length,
+                      const int32_t* history_row, const float* repetition, const float* frequency, const float* presence,
+                      const void* bias_index, int bias_wide, int64_t ldbi, const float* bias, int64_t ldb, int k,
+                      const int32_t* mask, int64_t mask_rows, int64_t ldm, const int32_t* mask_row, void* out, int out_dtype,
+                      int64_t ldo, nsm_stream_t stream) {
+  if (vocab < 1 || vocab > kVocabMax) return fail(NSM_ERR_SHAPE, "vocab = %lld not in [1, %d]", static_cast<long long>(vocab), kVocabMax);
+  AdjustArgs a{};
+  a.in = logits;
+  a.in_dtype = dtype;
+  a.rows = rows;
+  a.vocab = static_cast<int32_t>(vocab);
+  a.ld_in = ld;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.ld_out = ldo;
+  a.history = history;
+  a.history_wide = history_wide != 0;
+  a.history_rows = history_rows;
+  a.history_len = history_len;
+  a.ldh = ldh;
+  a.length = length;
+  a.history_row = history_row;
+  a.repetition = repetition;
+  a.frequency = frequency;
+  a.presence = presence;
+  a.bias_index = bias_index;
+  a.bias_wide = bias_wide != 0;
+  a.ldbi = ldbi;
+  a.bias = bias;
+  a.ldb = ldb;
+  a.k = k;
+  a.mask = mask;
+  a.mask_rows = mask_rows;
+  a.ldm = ldm;
+  a.mask_row = mask_row;
+  return run_adjust(a, stream);
+}
+
+int nsm_adjust_logits_backward(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld, const void* history,
+                               int history_wide, int64_t history_rows, int64_t history_len, int64_t ldh,
+                               const int32_t* length, const int32_t* history_row, const float* repetition,
+                               const int32_t* mask, int64_t mask_rows, int64_t ldm, const int32_t* mask_row,
+                               const void* d_out, int d_out_dtype, int64_t ldg, void* d_logits, int64_t ldd,
+                               nsm_stream_t stream) {
+  if (vocab < 1 || vocab > kVocabMax) return fail(NSM_ERR_SHAPE, "vocab = %lld not in [1, %d]", static_cast<long long>(vocab), kVocabMax);
+  AdjustArgs a{};
+  a.backward = 1;
+  a.logits = repetition ? logits : nullptr;
+  a.ld_logits = ld;
+  a.in = d_out;
+  a.in_dtype = d_out_dtype;
+  a.rows = rows;
+  a.vocab = static_cast<int32_t>(vocab);
+  a.ld_in = ldg;
+  a.out = d_logits;
+  a.out_dtype = dtype;
+  a.ld_out = ldd;
+  a.history = history;
+  a.history_wide = history_wide != 0;
+  a.history_rows = history_rows;
+  a.history_len = history_len;
+  a.ldh = ldh;
+  a.length = length;
+  a.history_row = history_row;
+  a.repetition = repetition;
+  a.mask = mask;
+  a.mask_rows = mask_rows;
+  a.ldm = ldm;
+  a.mask_row = mask_row;
+  return run_adjust(a, stream);
+}
+
+int nsm_embedding(const void* weight, int dtype, int64_t vocab, int64_t cols, int64_t ldw, const void* tokens, int tokens_wide,
+                  int64_t rows, float scale, void* out, int out_dtype, int64_t ldo, nsm_stream_t stream_) {
+  int rc = check_embedding_sizes(rows, vocab, cols);
+  if (rc != NSM_OK) return rc;
+  EmbeddingArgs a{};
+  a.weight = weight;
+  a.weight_dtype = dtype;
+  a.vocab = vocab;
+  a.cols = cols;
+  a.ld_weight = ldw;
+  a.tokens = tokens;
+  a.tokens_wide = tokens_wide != 0;
+  a.rows = rows;
+  a.scale = scale;
+  a.rows_out = out;
+  a.rows_dtype = out_dtype;
+  a.ld_rows = ldo;
+  if ((rc = check_embedding(a, nullptr, 0)) != NSM_OK) return rc;
+  if (rows == 0) {
+    t_last_launches = 0;
+    return NSM_OK;
+  }
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const PdlScope pdl(rows * cols);
+  cudaError_t e;
+  {
+    TimedLaunch t(stream, NSM_KIND_EMBEDDING, double(rows) * double(cols) * double(number_bytes(dtype) + number_bytes(out_dtype)));
+    e = launch_embedding(a, stream);
+  }
+  if (e != cudaSuccess) return fail_cuda(e, "embedding launch");
+  t_last_launches = 1;
+  return NSM_OK;
+}
+
+size_t nsm_embedding_workspace_bytes(int64_t rows, int64_t vocab, int64_t cols) {
+  if (check_embedding_sizes(rows, vocab, cols) != NSM_OK) return 0;
+  return embedding_plan(rows, vocab, cols).bytes;
+}
+
+int nsm_embedding_backward(const void* d_out, int dtype, int64_t rows, int64_t cols, int64_t ldg, const void* tokens,
+                           int tokens_wide, int64_t vocab, float scale, int accumulate, void* d_weight, int weight_dtype,
+                           int64_t ldw, void* workspace, size_t workspace_bytes, nsm_stream_t stream_) {
+  int rc = check_embedding_sizes(rows, vocab, cols);
+  if (rc != NSM_OK) return rc;
+  if (!d_weight) return fail(NSM_ERR_NULL, "d_weight is NULL");
+  EmbeddingArgs a{};
+  a.d_weight = d_weight;
+  a.weight_dtype = weight_dtype;
+  a.vocab = vocab;
+  a.cols = cols;
+  a.ld_weight = ldw;
+  a.tokens = tokens;
+  a.tokens_wide = tokens_wide != 0;
+  a.rows = rows;
+  a.scale = scale;
+  a.accumulate = accumulate != 0;
+  a.rows_in = d_out;
+  a.rows_dtype = dtype;
+  a.ld_rows = ldg;
+  if ((rc = check_workspace(workspace, workspace_bytes, embedding_plan(rows, vocab, cols).bytes)) != NSM_OK) return rc;
+  if ((rc = check_embedding(a, workspace, workspace_bytes)) != NSM_OK) return rc;
+  if (rows == 0 && accumulate) {
+    t_last_launches = 0;
+    return NSM_OK;
+  }
+  int num_sms = 0;
+  if ((rc = current_sms(&num_sms)) != NSM_OK) return rc;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const PdlScope pdl(0);  // the sort's kernels are short whatever the sizes
+  int launches = 0;
+  cudaError_t e;
+  {
+    const double written = accumulate ? 2.0 * double(std::min(rows, vocab)) : double(vocab);
+    TimedLaunch t(stream, NSM_KIND_EMBEDDING,
+                  double(cols) * (double(rows) * double(number_bytes(dtype)) + written * double(number_bytes(weight_dtype))));
+    e = launch_embedding_backward(a, workspace, num_sms, &launches, stream);
+  }
+  if (e != cudaSuccess) return fail_cuda(e, "launch of the embedding's gradient");
+  t_last_launches = launches;
+  return NSM_OK;
+}
+
+size_t nsm_grad_workspace_bytes(const int64_t* numels, int n) {
+  int64_t chunks = 0;
+  if (check_grad_sizes(numels, n, &chunks) != NSM_OK) return 0;
+  return grad_bytes(chunks, n);
+}
+
+int nsm_grad_norm(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int n, float* norm, float* norms,
+                  void* workspace, size_t workspace_bytes, nsm_stream_t stream) {
+  if (!norm) return fail(NSM_ERR_NULL, "norm is NULL");
+  return run_grads(grads, numels, dtypes, n, false, nullptr, nullptr, 0.f, norm, norms, workspace, workspace_bytes, stream);
+}
+
+int nsm_clip_grads(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int n, void* const* out,
+                   const int32_t* out_dtypes, float max_norm, float* norm, float* norms, void* workspace,
+                   size_t workspace_bytes, nsm_stream_t stream) {
+  if (!(max_norm > 0.f) || !std::isfinite(max_norm)) return fail(NSM_ERR_ARG, "max_norm must be positive and finite");
+  return run_grads(grads, numels, dtypes, n, true, out, out_dtypes, max_norm, norm, norms, workspace, workspace_bytes, stream);
+}
+
 int nsm_device_status(nsm_stream_t stream, int* status_out) {
   return nsm_device_status_detail(stream, status_out, nullptr, nullptr, nullptr);
 }
@@ -2038,7 +2484,7 @@ int nsm_timing_read(double* gemm_ms, int64_t* gemm_launches, double* gemm_flops)
 }
 
 int nsm_timing_read_kind(int kind, double* ms, int64_t* launches, double* work) {
-  if (kind < 0 || kind >= kKinds) return fail(NSM_ERR_ARG, "unknown timing kind %d", kind);
+  if (!known_kind(kind)) return fail(NSM_ERR_ARG, "unknown timing kind %d", kind);
   Timing& T = timing();
   std::lock_guard<std::mutex> lock(T.mu);
   T.collect();

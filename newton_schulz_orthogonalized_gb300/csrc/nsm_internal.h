@@ -255,6 +255,67 @@ struct DistillArgs {
   const float *in_lse, *in_rest;  // in_lse != NULL: the backward pass alone
 };
 
+// ---- penalties, biases and masks on logits
+
+constexpr int kBiasMaxK = 1024;  // biases per row at most
+
+struct AdjustArgs {
+  const void* in;      // logits, or the gradient of what the forward call wrote
+  void* out;           // adjusted logits, or the gradient of the logits
+  const void* logits;  // backward with repetition: the logits, of out's type (else NULL)
+  int64_t rows, ld_in, ld_out, ld_logits;
+  int32_t vocab, in_dtype, out_dtype;
+  int32_t backward, in_place;
+  const void* history;  // NULL: none counts
+  int64_t history_rows, history_len, ldh;
+  const int32_t *length, *history_row;
+  int32_t history_wide, bias_wide, k;
+  const float *repetition, *frequency, *presence;
+  const void* bias_index;
+  const float* bias;
+  int64_t ldbi, ldb;
+  const int32_t* mask;  // NULL: no row has one
+  int64_t mask_rows, ldm;
+  const int32_t* mask_row;
+};
+
+// ---- the embedding lookup and its gradient
+
+struct EmbeddingArgs {
+  const void* weight;  // forward
+  void* d_weight;      // backward
+  const void* rows_in; // backward: d_out
+  void* rows_out;      // forward: out
+  const void* tokens;
+  int64_t rows, vocab, cols, ld_weight, ld_rows;
+  int32_t weight_dtype, rows_dtype, tokens_wide, accumulate;
+  float scale;
+};
+
+// What nsm_embedding_backward keeps in its workspace, for rows x cols gradients of a vocabulary.
+struct EmbeddingPlan {
+  int32_t bits, passes;      // of a sorting pass's digit; passes
+  int32_t tiles, tile;       // blocks of a pass, and their entries
+  int32_t units;             // pieces of the sorted entries
+  int64_t cols;              // of a unit's sums: cols rounded up to 8
+  size_t off_pairs[2], off_counts, off_last, off_sums, bytes;
+};
+EmbeddingPlan embedding_plan(int64_t rows, int64_t vocab, int64_t cols);
+
+// ---- the norm of many gradients, and clipping
+
+constexpr int kGradChunk = 16384;  // elements that one block sums at a time
+constexpr int kGradTable = 512;    // tensors of one launch at most
+
+struct GradTensor {
+  const void* in;
+  void* out;
+  int64_t numel;
+  int32_t chunk_begin;  // within its launch
+  int16_t in_dtype, out_dtype;
+};
+static_assert(sizeof(GradTensor) == 32, "GradTensor layout");
+
 // ---- launchers (defined in the .cu files) ---------------------------------------
 
 // Runs `ops` for every job; the final pass stores O into its X buffer.
@@ -306,6 +367,23 @@ cudaError_t launch_copy_h2d(void* dst, const void* src_mapped, size_t bytes, int
 
 cudaError_t launch_logprobs(const LogprobArgs& args, cudaStream_t stream);
 cudaError_t launch_distill(const DistillArgs& args, cudaStream_t stream);
+
+cudaError_t launch_adjust(const AdjustArgs& args, cudaStream_t stream);
+cudaError_t launch_embedding(const EmbeddingArgs& args, cudaStream_t stream);
+// *launches: how many kernels it took
+cudaError_t launch_embedding_backward(const EmbeddingArgs& args, void* workspace, int num_sms, int* launches,
+                                      cudaStream_t stream);
+// Sums of squares of `n` tensors (of one launch: n <= kGradTable), one per chunk from partials[0]
+cudaError_t launch_grad_chunks(const GradTensor* tensors, int n, int total_chunks, double* partials, cudaStream_t stream);
+// Their sums: sums[i] per tensor, and its root to norms[i] where norms is not NULL
+cudaError_t launch_grad_sums(const GradTensor* tensors, int n, int total_chunks, const double* partials, double* sums,
+                             float* norms, cudaStream_t stream);
+// *norm = sqrt(sum of sums[0 ... n - 1])
+cudaError_t launch_grad_total(const double* sums, int n, float* norm, cudaStream_t stream);
+// out = in min(1, max_norm / norm) for the tensors of one launch, the norm from all_sums[0 ... all_n - 1],
+// written to *norm where that is not NULL
+cudaError_t launch_grad_clip(const GradTensor* tensors, int n, int total_chunks, const double* all_sums, int all_n,
+                             float max_norm, float* norm, int in_place, int num_sms, cudaStream_t stream);
 
 int* device_status_ptr();
 // One CTA whose bounded wait expires after limit_ns and records kDevTimeout.

@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "elem.cuh"
 #include "launch.cuh"
 #include "nsm_internal.h"
 #include "ptx.cuh"
@@ -32,119 +33,6 @@ constexpr float kRefSlack = 16.f;
 constexpr float kLog2Floor = -200.f;
 constexpr int kMaxCluster = 8;
 constexpr uint64_t kWaitNs = 2000000000ull;  // a wait's limit
-
-// Two fp32 values in one 64-bit register: add, multiply and fused multiply-add of both are
-// one instruction each.
-using Pair = uint64_t;
-__device__ __forceinline__ Pair make_pair(float lo, float hi) {
-  Pair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void split_pair(Pair p, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
-}
-__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
-  Pair r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ Pair pair_mul(Pair a, Pair b) {
-  Pair r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ Pair pair_fma(Pair a, Pair b, Pair c) {
-  Pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
-// A 16-byte vector of one of the logits' types.
-template <typename T>
-struct Elem;
-template <>
-struct Elem<float> {
-  static constexpr int kVec = 4;
-  static constexpr int kKeyLowBit = 0;  // lowest bit in which two values' keys can differ
-  static constexpr uint32_t kNegInfBits = 0xff800000u;
-  static __device__ __forceinline__ float to_float(float v) { return v; }
-  static __device__ __forceinline__ float from_float(float v) { return v; }
-  static __device__ __forceinline__ void unpack(const uint4& r, Pair (&x)[2]) {
-    x[0] = (static_cast<Pair>(r.y) << 32) | r.x;
-    x[1] = (static_cast<Pair>(r.w) << 32) | r.z;
-  }
-  static __device__ __forceinline__ uint4 pack(const Pair (&x)[2]) {
-    return make_uint4(static_cast<uint32_t>(x[0]), static_cast<uint32_t>(x[0] >> 32), static_cast<uint32_t>(x[1]),
-                      static_cast<uint32_t>(x[1] >> 32));
-  }
-  static __device__ __forceinline__ float largest(const uint4& r) {  // NaNs aside
-    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
-  }
-};
-template <>
-struct Elem<__nv_bfloat16> {
-  static constexpr int kVec = 8;
-  static constexpr int kKeyLowBit = 16;
-  static constexpr uint32_t kNegInfBits = 0xff80u;
-  static __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-  static __device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
-  static __device__ __forceinline__ Pair widen(uint32_t w) {
-    return (static_cast<Pair>(w & 0xffff0000u) << 32) | (w << 16);
-  }
-  static __device__ __forceinline__ uint32_t narrow(Pair p) {
-    float lo, hi;
-    split_pair(p, lo, hi);
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  static __device__ __forceinline__ void unpack(const uint4& r, Pair (&x)[4]) {
-    x[0] = widen(r.x);
-    x[1] = widen(r.y);
-    x[2] = widen(r.z);
-    x[3] = widen(r.w);
-  }
-  static __device__ __forceinline__ uint4 pack(const Pair (&x)[4]) {
-    return make_uint4(narrow(x[0]), narrow(x[1]), narrow(x[2]), narrow(x[3]));
-  }
-  static __device__ __forceinline__ float largest(const uint4& r) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r);
-    const float2 m = __bfloat1622float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
-    return fmaxf(m.x, m.y);
-  }
-};
-template <>
-struct Elem<__half> {
-  static constexpr int kVec = 8;
-  static constexpr int kKeyLowBit = 13;
-  static constexpr uint32_t kNegInfBits = 0xfc00u;
-  static __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
-  static __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
-  static __device__ __forceinline__ Pair widen(uint32_t w) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-    return make_pair(f.x, f.y);
-  }
-  static __device__ __forceinline__ uint32_t narrow(Pair p) {
-    float lo, hi;
-    split_pair(p, lo, hi);
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  static __device__ __forceinline__ void unpack(const uint4& r, Pair (&x)[4]) {
-    x[0] = widen(r.x);
-    x[1] = widen(r.y);
-    x[2] = widen(r.z);
-    x[3] = widen(r.w);
-  }
-  static __device__ __forceinline__ uint4 pack(const Pair (&x)[4]) {
-    return make_uint4(narrow(x[0]), narrow(x[1]), narrow(x[2]), narrow(x[3]));
-  }
-  static __device__ __forceinline__ float largest(const uint4& r) {
-    const __half2* h = reinterpret_cast<const __half2*>(&r);
-    const float2 m = __half22float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
-    return fmaxf(m.x, m.y);
-  }
-};
 
 // Element e of a vector, and the vector with element e replaced (e may vary at run time).
 template <typename T>

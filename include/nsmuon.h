@@ -366,8 +366,8 @@ int nsm_distill_backward(const void* logits, int dtype, int64_t rows, int64_t vo
  * The conventions are those of the losses over a vocabulary, and:
  *   - The history of row r is the first length[r] tokens (clamped to [0, history_len]; length
  *     NULL: all) of row history_row[r] (NULL: r, and then history_rows == rows) of `history`:
- *     device, history_rows x history_len of int64 (history_wide != 0) or int32, row stride ldh.
- *     Rows of one sequence can so share its tokens, each up to its own position.  A token
+ *     device, history_rows x history_len of int64 (history_wide != 0) or int32, row stride ldh,
+ *     history_len <= 2^30.  Rows of one sequence can so share its tokens, each up to its own position.  A token
  *     outside [0, vocab) does not count; a history_row outside [0, history_rows) is no history.
  *     history may be NULL (no penalties; with history_len 0 its address is not looked at).
  *   - repetition, frequency, presence: device, fp32, one per row; each may be NULL (1, 0, 0).

@@ -1222,6 +1222,15 @@ int check_workspace(void* ws, size_t ws_bytes, size_t need) {
 
 bool known_dtype(int dtype) { return dtype == NSM_BF16 || dtype == NSM_FP16 || dtype == NSM_FP32; }
 
+int current_sms(int* num_sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? NSM_OK : fail_cuda(e, "device query");
+}
+
+constexpr int64_t kHistoryMax = int64_t(1) << 30;
+
 // The arguments that both directions have, and the launch.
 int run_adjust(AdjustArgs& a, nsm_stream_t stream_) {
   const char* in_name = a.backward ? "d_out" : "logits";
@@ -1246,7 +1255,7 @@ int run_adjust(AdjustArgs& a, nsm_stream_t stream_) {
   if ((rc = check_matrix(out_name, a.out, a.rows, a.ld_out, a.vocab, out_size)) != NSM_OK) return rc;
   if (a.backward && a.repetition && (rc = check_matrix("logits", a.logits, a.rows, a.ld_logits, a.vocab, size)) != NSM_OK) return rc;
   if (a.history || (a.history_rows > 0 && a.history_len == 0)) {  // no token has no place
-    if (a.history_rows < 1 || a.history_rows > INT32_MAX || a.history_len < 0 || a.history_len > INT32_MAX)
+    if (a.history_rows < 1 || a.history_rows > INT32_MAX || a.history_len < 0 || a.history_len > kHistoryMax)
       return fail(NSM_ERR_SHAPE, "history has %lld rows of %lld tokens", static_cast<long long>(a.history_rows),
                   static_cast<long long>(a.history_len));
     if (a.history_len > 0 && (rc = check_matrix("history", a.history, a.history_rows, a.ldh, a.history_len, hsize)) != NSM_OK) return rc;
@@ -1291,6 +1300,7 @@ int run_adjust(AdjustArgs& a, nsm_stream_t stream_) {
       {a.presence, n, false}, {a.mask_row, n, false}};
   if ((rc = check_ranges(ranges, int(sizeof ranges / sizeof ranges[0]))) != NSM_OK) return rc;
   if (a.history_len == 0 || (a.backward && !a.repetition)) a.history = nullptr;  // nothing that it could change
+  if ((rc = current_sms(&a.num_sms)) != NSM_OK) return rc;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   const PdlScope pdl(a.rows * a.vocab);
   cudaError_t e;
@@ -1336,13 +1346,6 @@ int check_embedding(const EmbeddingArgs& a, const void* workspace, size_t worksp
                           {a.rows > 0 ? a.tokens : nullptr, size_t(a.rows) * tsize, false},
                           {workspace, workspace_bytes, true}};
   return check_ranges(ranges, int(sizeof ranges / sizeof ranges[0]));
-}
-
-int current_sms(int* num_sms) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, dev);
-  return e == cudaSuccess ? NSM_OK : fail_cuda(e, "device query");
 }
 
 // ---- the norm of many gradients, and clipping

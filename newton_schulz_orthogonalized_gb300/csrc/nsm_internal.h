@@ -265,7 +265,7 @@ struct AdjustArgs {
   const void* logits;  // backward with repetition: the logits, of out's type (else NULL)
   int64_t rows, ld_in, ld_out, ld_logits;
   int32_t vocab, in_dtype, out_dtype;
-  int32_t backward, in_place;
+  int32_t backward, in_place, num_sms;
   const void* history;  // NULL: none counts
   int64_t history_rows, history_len, ldh;
   const int32_t *length, *history_row;

@@ -6,196 +6,328 @@
 //   out_v = a_v - (frequency c_v + presence [c_v > 0]) + sum of the biases at v; -inf where banned
 //   d x_v = d out_v (d a_v / d x_v); 0 where banned
 //
-// A block takes 8192 logits of a row.  It counts the history's tokens among them in shared memory
-// (whole numbers: their order does not matter), while its logits are on their way to
-// registers.  Every slice of a row reads the row's history again, from L2: 4 or 8 bytes per token
-// against 16 KB of logits and as many written.
+// A block takes a slice of 4096 (fp32: 2048) logits of one row after another.  It counts the history's
+// tokens among them in shared memory (whole numbers: their order does not matter), writes the
+// slice as it was read, with the mask applied, and then settles the tokens that a penalty or a
+// bias is for, one thread each.  Rows that share a history, as the positions of one sequence
+// do, follow one another in a block, which counts only the tokens that a row has more.  The next
+// slice's logits are asked for before a slice is settled.
 #include "elem.cuh"
 #include "launch.cuh"
 #include "nsm_internal.h"
 
+#include <algorithm>
+#include <type_traits>
+
 namespace nsm {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnits = 4;                        // of eight logits, per thread
-constexpr int kSlice = kThreads * kUnits * 8;    // logits of a block
+constexpr int kThreads = 128;
 constexpr uint32_t kHasBias = 0x80000000u;       // in a count: some bias is for this token
-
-struct Rows {  // of one matrix: where row r begins
-  template <typename T>
-  static __device__ __forceinline__ T* at(T* p, int64_t r, int64_t ld) {
-    return p + r * ld;
-  }
-};
 
 __device__ __forceinline__ int64_t index_at(const void* p, int wide, int64_t i) {
   return wide ? static_cast<const int64_t*>(p)[i] : static_cast<const int32_t*>(p)[i];
 }
 
-// The eight bits of a row's mask from element e0 on (bit set: allowed); what lies outside is 0.
+// The eight bits of a row's mask from element e0 on (bit set: allowed); all eight exist.
 __device__ __forceinline__ uint32_t mask_bits(const int32_t* words, int nwords, int e0, int* status) {
   const int w = e0 >> 5, bit = e0 & 31;
-  const auto word = [&](int i) {
-    return i >= 0 && i < nwords && bounds_ok(i < nwords, status, NSM_KERNEL_ADJUST, 0, NSM_SITE_SIDE)
-               ? static_cast<uint32_t>(__ldg(words + i)) : 0u;
+  if (!bounds_ok(w >= 0 && (e0 + 7) >> 5 < nwords, status, NSM_KERNEL_ADJUST, 0, NSM_SITE_SIDE)) return 0;
+  const uint32_t low = static_cast<uint32_t>(__ldg(words + w));
+  return __funnelshift_r(low, bit > 24 ? static_cast<uint32_t>(__ldg(words + w + 1)) : 0u, bit) & 0xffu;
+}
+
+// A vector with -inf (0 in the backward pass) where a bit of `allowed` is clear.
+template <typename T, bool kBackward>
+__device__ __forceinline__ void ban(Eight<T>& r, uint32_t allowed) {
+  constexpr uint32_t kGone = kBackward ? 0u : Elem<T>::kNegInfBits;
+  uint32_t* w = reinterpret_cast<uint32_t*>(r.w);
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (!(allowed >> e & 1)) w[e] = kGone;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t keep = (allowed >> (2 * i) & 1) * 0xffffu | (allowed >> (2 * i + 1) & 1) * 0xffff0000u;
+      w[i] = (w[i] & keep) | (~keep & (kGone * 0x10001u));
+    }
+  }
+}
+
+template <typename A, typename B>
+__device__ __forceinline__ void convert(const Eight<A>& from, Eight<B>& to) {
+  if constexpr (std::is_same<A, B>::value) {
+#pragma unroll
+    for (int i = 0; i < Eight<A>::kWords; ++i) to.w[i] = from.w[i];
+  } else {
+    float f[8];
+    from.get(f);
+    to.set(f);
+  }
+}
+
+// Units of eight logits per thread, and logits of a block: 16 KB in either size of type.
+template <typename A>
+constexpr int kUnitsOf = sizeof(A) == 4 ? 2 : 4;
+template <typename A>
+constexpr int kSliceOf = kThreads * kUnitsOf<A> * 8;
+// Resident blocks of an SM: as many as their registers and shared memory let in.
+constexpr int kBlocks = 8;
+
+constexpr int kRun = 16;  // rows at most whose slices a block takes after one another
+
+// Calls f with every token of a row's history, in no order.
+template <typename I, typename F>
+__device__ __forceinline__ void for_history(const I* p, int tokens, F f) {
+  constexpr int kPer = 16 / sizeof(I);
+  const int head = min(static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) % 16 / sizeof(I)), tokens);
+  const int vecs = (tokens - head) / kPer;
+  const int4* v = reinterpret_cast<const int4*>(p + head);
+  const auto all = [&](const int4& q) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) f(static_cast<int64_t>(reinterpret_cast<const I*>(&q)[e]));
   };
-  return __funnelshift_r(word(w), bit > 24 ? word(w + 1) : 0u, bit) & 0xffu;
+  for (int i = threadIdx.x; i < vecs; i += 2 * kThreads) {
+    const bool two = i + kThreads < vecs;
+    const int4 q = v[i];
+    const int4 r = two ? v[i + kThreads] : q;
+    all(q);
+    if (two) all(r);
+  }
+  const int rest = head + vecs * kPer + threadIdx.x;
+  if (static_cast<int>(threadIdx.x) < head) f(static_cast<int64_t>(p[threadIdx.x]));
+  if (rest < tokens) f(static_cast<int64_t>(p[rest]));
 }
 
 // A: type of what is read, B: of what is written.
 template <typename A, typename B, bool kBackward>
-__global__ void __launch_bounds__(kThreads)
-    k_adjust(const AdjustArgs a, int slices, int* status) {
+__global__ void __launch_bounds__(kThreads, kBlocks) k_adjust(const AdjustArgs a, int slices, int run, int* status) {
+  constexpr int kUnits = kUnitsOf<A>, kSlice = kSliceOf<A>, kPlaces = kSlice + 8;
   extern __shared__ __align__(16) uint32_t shared[];
-  uint32_t* count = shared;                                        // kSlice
-  float* bias = reinterpret_cast<float*>(shared + kSlice);         // a.k
-  int32_t* bias_index = reinterpret_cast<int32_t*>(bias + a.k);    // a.k
+  uint32_t* count = shared;                                              // kPlaces
+  uint16_t* list = reinterpret_cast<uint16_t*>(shared + kPlaces);        // kPlaces: those with a count
+  float* bias = reinterpret_cast<float*>(list + kPlaces);                // a.k
+  int32_t* bias_index = reinterpret_cast<int32_t*>(bias + a.k);          // a.k
+  __shared__ int listed[2];
+  const int tid = threadIdx.x, vocab = a.vocab;
+  const bool counts = a.history || a.k;
+  if (counts) {  // once: every count goes back to 0 with the last row that wants it
+    for (int i = tid; i < kPlaces / 4; i += kThreads) reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
+    if (tid < 2) listed[tid] = 0;
+    __syncthreads();
+  }
   grid_dependency_sync();
   release_dependents();
-  const int tid = threadIdx.x, vocab = a.vocab;
   const int nwords = (vocab + 31) / 32;
-  const int64_t items = a.rows * slices;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t row = item / slices;
-    const A* in = Rows::at(static_cast<const A*>(a.in), row, a.ld_in);
-    B* out = Rows::at(static_cast<B*>(a.out), row, a.ld_out);
-    // units of eight on the 16-byte grid of what is read: unit u begins at element 8 u - lead
-    const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(in) & 15) / sizeof(A));
-    const int v0 = static_cast<int>(item % slices) * kSlice - lead;
-    if (v0 >= vocab) continue;
-    const int v1 = min(v0 + kSlice, vocab);
+  // A block takes one slice of `run` rows after one another, then of other rows.
+  const int run_step = gridDim.x / slices, slice_step = gridDim.x % slices;
 
-    const int32_t* mask = nullptr;
+  // One slice of a row: units of eight on the 16-byte grid of what is read, unit u from element
+  // v0 + 8 u on.  v0 may lie before the row, by less than a vector.
+  struct Place {
+    int64_t row, line;
+    int slice, v0, tokens;
+    const A* in;
+    const int32_t* mask;
+  };
+  const auto place = [&](Place& p) {
+    p.in = static_cast<const A*>(a.in) + p.row * a.ld_in;
+    p.v0 = p.slice * kSlice - static_cast<int>((reinterpret_cast<uintptr_t>(p.in) & 15) / sizeof(A));
+    p.mask = nullptr;
     if (a.mask) {
-      const int64_t m = a.mask_row ? a.mask_row[row] : row;
-      if (m >= 0 && m < a.mask_rows) mask = a.mask + m * a.ldm;
+      const int64_t m = a.mask_row ? a.mask_row[p.row] : p.row;
+      if (m >= 0 && m < a.mask_rows) p.mask = a.mask + m * a.ldm;
     }
-    int64_t tokens = 0, line = 0;
+    p.tokens = 0;
+    p.line = -1;
     if (a.history) {
-      line = a.history_row ? a.history_row[row] : row;
-      tokens = a.length ? a.length[row] : a.history_len;
-      tokens = line >= 0 && line < a.history_rows ? min(max(tokens, int64_t(0)), a.history_len) : 0;
+      p.line = a.history_row ? a.history_row[p.row] : p.row;
+      const int most = static_cast<int>(a.history_len);
+      if (p.line >= 0 && p.line < a.history_rows) p.tokens = a.length ? min(max(a.length[p.row], 0), most) : most;
     }
-
-    // what the mask allows of each unit, of the elements that exist
-    uint32_t exists[kUnits], allowed[kUnits];
-    Eight<A> raw[kUnits];
-    const auto load = [&](int i, int e0) {
-      if (exists[i] == 0xffu) {
-        if (bounds_ok(e0 >= 0 && e0 + 8 <= vocab && on_16_bytes(in + e0), status, NSM_KERNEL_ADJUST, 0, NSM_SITE_LOGITS))
-          raw[i].load_written(in + e0);
-      } else {
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = exists[i] >> e & 1 ? Elem<A>::to_float(in[e0 + e]) : 0.f;
-        raw[i].set(f);
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int e0 = v0 + (tid + i * kThreads) * 8;
-      const uint32_t low = e0 < 0 ? 0xffu << -e0 : 0xffu;
-      const uint32_t high = e0 + 8 <= vocab ? 0xffu : e0 < vocab ? 0xffu >> (e0 + 8 - vocab) : 0u;
-      exists[i] = low & high & 0xffu;
-      allowed[i] = mask && exists[i] ? mask_bits(mask, nwords, e0, status) & exists[i] : exists[i];
-#pragma unroll
-      for (int w = 0; w < Eight<A>::kWords; ++w) raw[i].w[w] = make_uint4(0, 0, 0, 0);
-    }
-    if (!a.in_place) {
+  };
+  // Most slices lie inside their row with all their units.
+  const auto inside = [&](int v0) { return v0 >= 0 && v0 + kSlice <= vocab; };
+  const auto whole = [&](int e0) { return e0 >= 0 && e0 + 8 <= vocab; };
+  uint32_t allowed = 0;  // with a mask, a byte per unit: the elements that it allows
+  Eight<A> raw[kUnits];
+  // What a row has before its first whole unit and behind its last one: threads 0 to 7 and 8 to
+  // 15 of the block that has them take an element each.
+  A edge = Elem<A>::from_float(0.f);
+  const auto edge_at = [&](int v0) {  // -1: none
+    if (tid >= 16) return -1;
+    const int tail = v0 + (vocab - v0) / 8 * 8;
+    const int e = tid < 8 ? v0 + tid : tail + tid - 8;
+    const bool mine = tid < 8 ? v0 < 0 : tail < v0 + kSlice && !(v0 < 0 && tail == v0);
+    return mine && e >= 0 && e < vocab ? e : -1;
+  };
+  const auto load = [&](const A* from, int i) {
+    if (bounds_ok(on_16_bytes(from + i * kThreads * 8), status, NSM_KERNEL_ADJUST, 0, NSM_SITE_LOGITS)) raw[i].load_written(from + i * kThreads * 8);
+  };
+  const auto fetch_units = [&](const Place& p, auto all) {
+    const int first = p.v0 + tid * 8;
+    const A* from = p.in + first;
+    if (!p.mask) {
 #pragma unroll
       for (int i = 0; i < kUnits; ++i)
-        if (allowed[i]) load(i, v0 + (tid + i * kThreads) * 8);
+        if (decltype(all)::value || whole(first + i * kThreads * 8)) load(from, i);
+      return;
     }
-
-    const bool counted = tokens > 0 || a.k > 0;
-    if (counted) {
-#pragma unroll
-      for (int i = 0; i < kSlice / 4 / kThreads; ++i)
-        reinterpret_cast<uint4*>(count)[tid + i * kThreads] = make_uint4(0, 0, 0, 0);
-      for (int j = tid; j < a.k; j += kThreads) {
-        const int64_t v = index_at(a.bias_index, a.bias_wide, row * a.ldbi + j);
-        bias_index[j] = v >= v0 && v < v1 && v >= 0 ? static_cast<int32_t>(v) : -1;
-        bias[j] = a.bias[row * a.ldb + j];
-      }
-      __syncthreads();
-      for (int64_t j = tid; j < tokens; j += kThreads) {
-        if (!bounds_ok(line >= 0 && line < a.history_rows && j < a.history_len, status, NSM_KERNEL_ADJUST, 0, NSM_SITE_SIDE)) break;
-        const int64_t v = index_at(a.history, a.history_wide, line * a.ldh + j);
-        if (v >= v0 && v < v1 && v >= 0) atomicAdd(&count[v - v0], 1u);
-      }
-      for (int j = tid; j < a.k; j += kThreads)
-        if (bias_index[j] >= 0) atomicOr(&count[bias_index[j] - v0], kHasBias);
-      __syncthreads();
-    }
-    const float theta = a.repetition ? a.repetition[row] : 1.f;
-    const float frequency = a.frequency ? a.frequency[row] : 0.f;
-    const float presence = a.presence ? a.presence[row] : 0.f;
-    const B* logits = kBackward && a.logits ? Rows::at(static_cast<const B*>(a.logits), row, a.ld_logits) : nullptr;
-    const bool aligned_out = on_16_bytes(out + v0);
-
+    allowed = 0;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int u = tid + i * kThreads;
-      const int e0 = v0 + u * 8;
-      if (!exists[i]) continue;
-      uint32_t c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      uint32_t any = 0;
-      if (counted) {
-        *reinterpret_cast<uint4*>(c) = reinterpret_cast<const uint4*>(count)[2 * u];
-        *reinterpret_cast<uint4*>(c + 4) = reinterpret_cast<const uint4*>(count)[2 * u + 1];
-        any = c[0] | c[1] | c[2] | c[3] | c[4] | c[5] | c[6] | c[7];
-      }
-      if (a.in_place) {
-        if (!any && allowed[i] == exists[i]) continue;  // stays as it is
-        if (allowed[i]) load(i, e0);
-      }
-      float f[8];
-      raw[i].get(f);
-      if (any) {
+      const int e0 = first + i * kThreads * 8;
+      if (decltype(all)::value || whole(e0)) allowed |= mask_bits(p.mask, nwords, e0, status) << (8 * i);
+    }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t n = c[e] & ~kHasBias;
-          if (!c[e] || !(allowed[i] >> e & 1)) continue;
-          if (n && a.repetition) {
-            const float sign = kBackward ? Elem<B>::to_float(logits[e0 + e]) : f[e];
-            f[e] = sign > 0.f ? f[e] / theta : f[e] * theta;
-          }
-          if (!kBackward) {
-            if (n) f[e] -= fmaf(frequency, static_cast<float>(n), presence);
-            if (c[e] & kHasBias)
-              for (int j = 0; j < a.k; ++j)
-                if (bias_index[j] == e0 + e) f[e] += bias[j];
-          }
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (!(allowed[i] >> e & 1)) f[e] = kBackward ? 0.f : -__builtin_huge_valf();
-      if (exists[i] == 0xffu && aligned_out) {
-        Eight<B> r;
-        r.set(f);
-        if (bounds_ok(e0 >= 0 && e0 + 8 <= vocab && on_16_bytes(out + e0), status, NSM_KERNEL_ADJUST, 0, NSM_SITE_GRADIENT))
-          r.store(out + e0);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (exists[i] >> e & 1) out[e0 + e] = Elem<B>::from_float(f[e]);
+    for (int i = 0; i < kUnits; ++i) {
+      const uint32_t may = allowed >> (8 * i) & 0xffu;
+      if (may && !(a.in_place && may == 0xffu)) load(from, i);
+    }
+  };
+  const auto fetch = [&](const Place& p) {
+    if (a.in_place && !p.mask) return;
+    if (inside(p.v0)) {
+      fetch_units(p, std::true_type());
+    } else {
+      fetch_units(p, std::false_type());
+      const int e = edge_at(p.v0);
+      if (e >= 0) {
+        edge = p.in[e];
+        if (p.mask && !(static_cast<uint32_t>(p.mask[e >> 5]) >> (e & 31) & 1)) edge = Elem<A>::from_float(kBackward ? 0.f : -__builtin_huge_valf());
       }
     }
-    if (item + gridDim.x < items) __syncthreads();  // the counts have been read
+  };
+
+  Place now{};
+  int64_t first = int64_t(blockIdx.x / slices) * run;  // of the rows that it takes after one another
+  now.row = first;
+  now.slice = blockIdx.x % slices;
+  if (now.row >= a.rows) return;
+  place(now);
+  fetch(now);
+  int parity = 0, held = 0;  // tokens of this row's history that are counted already
+  for (;;) {
+    // counts are kept of all tokens that may be in this slice of some row, whatever its v0
+    const int v0 = now.v0, base = now.slice * kSlice - 7;
+    const int low = max(base, 0), span = min(base + 7 + kSlice, vocab) - low;  // span <= 0: nothing is left
+    if (now.tokens > held && span > 0) {
+      const auto bump = [&](int64_t v) {
+        if (static_cast<uint64_t>(v - low) >= static_cast<uint64_t>(span)) return;
+        if (atomicAdd(&count[v - base], 1u) == 0) list[atomicAdd(&listed[parity], 1)] = static_cast<uint16_t>(v - base);
+      };
+      if (a.history_wide) for_history(static_cast<const int64_t*>(a.history) + now.line * a.ldh + held, now.tokens - held, bump);
+      else for_history(static_cast<const int32_t*>(a.history) + now.line * a.ldh + held, now.tokens - held, bump);
+    }
+    for (int j = tid; j < a.k; j += kThreads) {
+      const int64_t v = index_at(a.bias_index, a.bias_wide, now.row * a.ldbi + j);
+      const bool here = span > 0 && static_cast<uint64_t>(v - low) < static_cast<uint64_t>(span);
+      bias_index[j] = here ? static_cast<int32_t>(v) : -1;
+      bias[j] = a.bias[now.row * a.ldb + j];
+      if (here && atomicOr(&count[v - base], kHasBias) == 0) list[atomicAdd(&listed[parity], 1)] = static_cast<uint16_t>(v - base);
+    }
+
+    B* out = static_cast<B*>(a.out) + now.row * a.ld_out;
+    const bool aligned_out = on_16_bytes(out + v0);
+    const auto store_units = [&](auto all) {
+      const int first_unit = v0 + tid * 8;
+      B* to = out + first_unit;
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const uint32_t may = now.mask ? allowed >> (8 * i) & 0xffu : 0xffu;
+        if (!(decltype(all)::value || whole(first_unit + i * kThreads * 8)) || (a.in_place && may == 0xffu)) continue;
+        Eight<B> r;
+        convert(raw[i], r);
+        if (may != 0xffu) ban<B, kBackward>(r, may);
+        if (aligned_out) {
+          if (bounds_ok(on_16_bytes(to + i * kThreads * 8), status, NSM_KERNEL_ADJUST, 0, NSM_SITE_GRADIENT)) r.store(to + i * kThreads * 8);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) to[i * kThreads * 8 + e] = reinterpret_cast<const B*>(r.w)[e];
+        }
+      }
+    };
+    if (!a.in_place || now.mask) {
+      if (inside(v0)) {
+        store_units(std::true_type());
+      } else {
+        store_units(std::false_type());
+        const int e = edge_at(v0);
+        if (e >= 0) out[e] = Elem<B>::from_float(Elem<A>::to_float(edge));
+      }
+    }
+
+    // the next slice's logits are asked for before this one's tokens are settled
+    const Place last = now;
+    if (++now.row >= min(first + run, a.rows)) {
+      const int carry = now.slice + slice_step >= slices;
+      first += int64_t(run_step + carry) * run;
+      now.row = first;
+      now.slice += slice_step - (carry ? slices : 0);
+    }
+    const bool more = now.row < a.rows;
+    if (more) {
+      place(now);
+      fetch(now);
+    }
+
+    // what a penalty or a bias is for, one token at a time, over what was just written
+    held = 0;
+    if (last.tokens > 0 || a.k > 0) {
+      // positions of one sequence: the next row's history is this one's and some tokens more
+      const bool keep = more && a.k == 0 && now.slice == last.slice && now.line == last.line && now.tokens >= last.tokens;
+      if (keep) held = last.tokens;
+      __syncthreads();
+      const int n_listed = listed[parity];
+      if (tid == 0) listed[parity ^ 1] = 0;
+      const float theta = a.repetition ? a.repetition[last.row] : 1.f;
+      const float frequency = a.frequency ? a.frequency[last.row] : 0.f;
+      const float presence = a.presence ? a.presence[last.row] : 0.f;
+      for (int i = tid; i < n_listed; i += kThreads) {
+        const int at = list[i], v = base + at;
+        const uint32_t c = count[at], n = c & ~kHasBias;
+        if (!keep) count[at] = 0;
+        if (v < v0 || v >= v0 + kSlice) continue;  // another slice's of this row
+        if (last.mask && !(static_cast<uint32_t>(last.mask[v >> 5]) >> (v & 31) & 1)) continue;
+        if (!bounds_ok(v >= 0 && v < vocab, status, NSM_KERNEL_ADJUST, 0, NSM_SITE_LOGITS)) continue;
+        float f = Elem<A>::to_float(last.in[v]);
+        if (n && a.repetition) {
+          const float sign = kBackward ? Elem<B>::to_float(static_cast<const B*>(a.logits)[last.row * a.ld_logits + v]) : f;
+          f = sign > 0.f ? f / theta : f * theta;
+        }
+        if (!kBackward) {
+          if (n) f -= fmaf(frequency, static_cast<float>(n), presence);
+          if (c & kHasBias)
+            for (int j = 0; j < a.k; ++j)
+              if (bias_index[j] == v) f += bias[j];
+        }
+        out[v] = Elem<B>::from_float(f);
+      }
+      __syncthreads();  // the next row counts in the same places
+      if (!keep) parity ^= 1;
+    }
+    if (!more) return;
   }
 }
 
 template <typename A, typename B, bool kBackward>
 cudaError_t launch_as(const AdjustArgs& a, int* status, cudaStream_t stream) {
+  constexpr int kSlice = kSliceOf<A>;
   const int units = (a.vocab + 7 + 7) / 8;  // the lead is at most seven
   const int slices = (units + kSlice / 8 - 1) / (kSlice / 8);
-  const bool counted = a.history || a.k;
-  const size_t smem = counted ? size_t(kSlice) * 4 + size_t(a.k) * 8 : 0;
-  const int64_t items = a.rows * slices;
-  const int grid = static_cast<int>(std::min<int64_t>(items, INT32_MAX));
-  return launch_pdl(k_adjust<A, B, kBackward>, dim3(grid), dim3(kThreads), smem, stream, a, slices, status);
+  const bool counts = a.history || a.k;
+  const size_t places = kSlice + 8, smem = counts ? places * 6 + size_t(a.k) * 8 : 0;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = set_smem_once(k_adjust<A, B, kBackward>, places * 6 + size_t(kBiasMaxK) * 8, done);
+  if (e != cudaSuccess) return e;
+  // Rows that share histories are taken in runs, so that a history is counted once per run; a
+  // block still gets four of them, of different slices.
+  const int64_t resident = int64_t(a.num_sms) * kBlocks;
+  const int run = a.history_row ? static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kRun, a.rows * slices / (4 * resident)))) : 1;
+  const int64_t items = (a.rows + run - 1) / run * slices;
+  const int grid = static_cast<int>(std::min<int64_t>(items, resident));
+  return launch_pdl(k_adjust<A, B, kBackward>, dim3(grid), dim3(kThreads), smem, stream, a, slices, run, status);
 }
 
 template <typename T>

@@ -141,6 +141,11 @@ struct Eight {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
   }
+  // what is not read again soon
+  __device__ __forceinline__ void store_streaming(T* p) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) __stcs(reinterpret_cast<uint4*>(p) + i, w[i]);
+  }
   __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {

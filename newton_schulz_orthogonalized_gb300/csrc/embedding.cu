@@ -5,16 +5,18 @@
 //
 //   k_embed        a group of lanes per row: reads and writes, nothing else.
 //   k_sort_count, k_sort_place
-//                  one pass of a stable radix sort of (token, row) by a digit of the token: a
-//                  block per tile counts its digits; every block then adds up the counts of
-//                  the tiles before its own and places its pairs in order.  Rows without a token
-//                  sort behind the others.
-//   k_embed_sums   pieces of kPiece sorted entries: a group of lanes adds the rows of equal
-//                  tokens in ascending order and writes each sum; the sums of a token that lies
-//                  in several pieces go to the workspace.  Blocks behind those clear the rows
-//                  of the gradient that no token asks for.
-//   k_embed_join   adds up such tokens' sums, piece after piece.
-// No atomic adds a floating-point number: the order of every sum is that of the rows.
+//                  a stable radix sort of (token, row) by digits of the token: a block per tile
+//                  counts its first digits; in each pass every block adds up the counts of
+//                  the tiles before its own, places its pairs in order, and counts where their next
+//                  digits come to lie.  Rows without a token sort behind the others.
+//   k_sort_block   the same for few rows, by one block in shared memory.
+//   k_embed_sums   pieces of the sorted entries: a group of lanes adds the rows of equal tokens
+//                  in ascending order and writes each sum.  It goes on into the next piece for a
+//                  token that ends there; of one that reaches further every piece leaves its
+//                  sum in the workspace.  Blocks behind those clear the rows of the gradient that no token
+//                  asks for.
+//   k_embed_join   adds up such tokens' sums.
+// No atomic adds a floating-point number: the order of every sum is set by the tokens alone.
 #include "elem.cuh"
 #include "launch.cuh"
 #include "nsm_internal.h"
@@ -27,10 +29,21 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnits = 4;      // of eight columns, per lane of k_embed
-constexpr int kMaxBits = 10;   // of a sorting pass's digit
+constexpr int kMaxBits = 9;    // of a sorting pass's digit
+constexpr int kMaxBins = 1 << kMaxBits;
 constexpr int kMaxTiles = 64;
-constexpr int kPiece = 32;     // sorted entries of a group of lanes
-constexpr int kClear = 64;     // rows of the gradient that a block looks at
+constexpr int kPlaceThreads = 512;
+constexpr int kPlaceWarps = kPlaceThreads / 32;
+constexpr int kBlockThreads = 1024;  // of k_sort_block
+constexpr int kBlockRows = 4096;     // that it takes at most
+constexpr int kMaxPiece = 32, kMinPiece = 4;  // sorted entries of a piece
+constexpr int kWantedWarps = 152 * 16;
+constexpr int kEmbedBlocks = 152 * 16;
+constexpr int kJoinThreads = 256;
+constexpr int kJoinPieces = 8;  // that a block of k_embed_join looks at
+// Bytes of rows without a token that a sorting pass clears on the side.
+constexpr int64_t kClearBytes = 24 << 20;
+constexpr int kClear = 8;      // rows of the gradient that a warp looks at
 
 __device__ __forceinline__ int64_t token_at(const EmbeddingArgs& a, int64_t r) {
   return a.tokens_wide ? static_cast<const int64_t*>(a.tokens)[r] : static_cast<const int32_t*>(a.tokens)[r];
@@ -45,177 +58,150 @@ __device__ __forceinline__ bool row_ok(bool ok, int* status, int site) {
   return bounds_ok(ok, status, NSM_KERNEL_EMBEDDING, 0, site);
 }
 
-// Eight columns from c0 on: the next eight where kVec (16-byte accesses), else every lanes-th.
-template <bool kVec>
-__device__ __forceinline__ int64_t column(int64_t slice, int lanes, int lane, int e) {
-  return kVec ? (slice * lanes + lane) * 8 + e : slice * lanes * 8 + lane + int64_t(e) * lanes;
+// Rows are cut into units of eight columns on the 16-byte grid of where results go: unit u holds
+// columns 8 u - lead ... + 8, of which those in [0, cols) exist.
+template <typename T>
+__device__ __forceinline__ int lead_of(const T* row) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
 }
 
-template <typename T, bool kVec>
-__device__ __forceinline__ void load_columns(const T* row, int64_t cols, int64_t slice, int lanes, int lane, Eight<T>& r,
-                                             int* status, int site) {
-  const int64_t c0 = column<kVec>(slice, lanes, lane, 0);
-  if (kVec && c0 + 8 <= cols) {
-    if (row_ok(on_16_bytes(row + c0), status, site)) r.load(row + c0);
+// The columns c0 ... c0 + 7 of a row, zeros outside it, whatever their alignment: whole vectors around
+// them, shifted into place, where those lie within the row.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int cols, int c0, Eight<T>& r, int* status, int site) {
+  constexpr int kPer = 16 / sizeof(T);
+  const T* at = row + c0;
+  const int s = lead_of(at);
+  if (s == 0 && c0 >= 0 && c0 + 8 <= cols) {
+    if (row_ok(on_16_bytes(at), status, site)) r.load_written(at);
     return;
   }
-  float f[8];
+  if (c0 - s >= 0 && c0 - s + 8 + kPer <= cols) {
+    uint32_t w[4 * (Eight<T>::kWords + 1)];
+    const uint4* from = reinterpret_cast<const uint4*>(at - s);
+    if (!row_ok(on_16_bytes(from), status, site)) return;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int64_t c = column<kVec>(slice, lanes, lane, e);
-    f[e] = c < cols ? Elem<T>::to_float(row[c]) : 0.f;
+    for (int i = 0; i <= Eight<T>::kWords; ++i) *reinterpret_cast<uint4*>(w + 4 * i) = from[i];
+    constexpr int kNeed = 4 * Eight<T>::kWords;  // words that are wanted
+    const int words = sizeof(T) == 4 ? s : s >> 1;
+    if (words & 2) {
+#pragma unroll
+      for (int i = 0; i < kNeed + 2; ++i) w[i] = w[i + 2];
+    }
+    if (words & 1) {
+#pragma unroll
+      for (int i = 0; i < kNeed + 1; ++i) w[i] = w[i + 1];
+    }
+    if (sizeof(T) == 2 && (s & 1)) {
+#pragma unroll
+      for (int i = 0; i < kNeed; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+#pragma unroll
+    for (int i = 0; i < Eight<T>::kWords; ++i) r.w[i] = *reinterpret_cast<const uint4*>(w + 4 * i);
+    return;
   }
+  T e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = c0 + i >= 0 && c0 + i < cols ? at[i] : Elem<T>::from_float(0.f);
+#pragma unroll
+  for (int i = 0; i < Eight<T>::kWords; ++i) r.w[i] = reinterpret_cast<const uint4*>(e)[i];
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* row, int cols, int c0, const float (&f)[8], int* status, int site) {
+  T* at = row + c0;
+  Eight<T> r;
   r.set(f);
-}
-
-template <typename T, bool kVec>
-__device__ __forceinline__ void store_columns(T* row, int64_t cols, int64_t slice, int lanes, int lane, const float (&f)[8],
-                                              int* status, int site) {
-  const int64_t c0 = column<kVec>(slice, lanes, lane, 0);
-  if (kVec && c0 + 8 <= cols && on_16_bytes(row + c0)) {
-    Eight<T> r;
-    r.set(f);
-    r.store(row + c0);
+  if (c0 >= 0 && c0 + 8 <= cols && on_16_bytes(at)) {
+    if (row_ok(on_16_bytes(at), status, site)) r.store(at);
     return;
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int64_t c = column<kVec>(slice, lanes, lane, e);
-    if (c < cols) row[c] = Elem<T>::from_float(f[e]);
-  }
+  for (int i = 0; i < 8; ++i)
+    if (c0 + i >= 0 && c0 + i < cols) at[i] = reinterpret_cast<const T*>(r.w)[i];
 }
 
 // ---------------------------------------------------------------- lookup
 
-template <typename W, typename O, bool kVec>
-__global__ void __launch_bounds__(kThreads) k_embed(const EmbeddingArgs a, int lanes, int chunks, int* status) {
+// Units of eight columns per lane, one row's after the other's: a group takes kUnits of them at a
+// time, and asks for the tokens of its next ones before.
+template <typename W, typename O>
+__global__ void __launch_bounds__(kThreads) k_embed(const EmbeddingArgs a, int lanes, int slices, int* status) {
   grid_dependency_sync();
   release_dependents();
-  const int lane = threadIdx.x & (lanes - 1), groups = kThreads / lanes;
-  const int64_t items = a.rows * chunks;
-  const int64_t slices = (a.cols + lanes * 8 - 1) / (lanes * 8);
-  for (int64_t item = int64_t(blockIdx.x) * groups + threadIdx.x / lanes; item < items; item += int64_t(gridDim.x) * groups) {
-    const int64_t row = item / chunks, first = item % chunks * kUnits;
-    const int64_t token = token_at(a, row);
-    const bool has = token >= 0 && token < a.vocab;
-    const W* from = static_cast<const W*>(a.weight) + (has ? token : 0) * a.ld_weight;
-    O* to = static_cast<O*>(a.rows_out) + row * a.ld_rows;
-    Eight<W> raw[kUnits];
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i)
-      if (has && first + i < slices)
-        load_columns<W, kVec>(from, a.cols, first + i, lanes, lane, raw[i], status, NSM_SITE_EMBEDDING);
+  const int lane = threadIdx.x & (lanes - 1), groups = kThreads / lanes, cols = static_cast<int>(a.cols);
+  const int64_t units = a.rows * slices, step = int64_t(gridDim.x) * groups * kUnits;
+  int64_t unit = (int64_t(blockIdx.x) * groups + threadIdx.x / lanes) * kUnits;
+  // the row and slice of `unit`, and how far they move with a step
+  int row = static_cast<int>(unit / slices), slice = static_cast<int>(unit % slices);
+  const int64_t row_step = step / slices;
+  const int slice_step = static_cast<int>(step % slices), rows = static_cast<int>(a.rows);
+  const auto tokens_of = [&](int r, int s, int (&t)[kUnits]) {  // -1: none
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      if (first + i >= slices) break;
-      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (has) {
-        raw[i].get(f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= a.scale;
+      t[i] = -1;
+      if (r < rows) {
+        const int64_t v = token_at(a, r);
+        if (v >= 0 && v < a.vocab) t[i] = static_cast<int>(v);
       }
-      store_columns<O, kVec>(to, a.cols, first + i, lanes, lane, f, status, NSM_SITE_EMBEDDING);
+      if (++s == slices) {
+        s = 0;
+        ++r;
+      }
     }
-  }
-}
-
-// ---------------------------------------------------------------- sorting tokens
-
-// The pair of entry i: from the tokens in the first pass, from the pass before later on.
-__device__ __forceinline__ uint2 pair_at(const EmbeddingArgs& a, const uint2* pairs, int64_t i) {
-  return pairs ? pairs[i] : make_uint2(key_at(a, i), static_cast<uint32_t>(i));
-}
-
-__global__ void __launch_bounds__(kThreads)
-    k_sort_count(const EmbeddingArgs a, const EmbeddingPlan p, const uint2* pairs, int shift, uint32_t* counts,
-                 int32_t* last, int* status) {
-  __shared__ uint32_t hist[1 << kMaxBits];
-  const int bins = 1 << p.bits;
-  for (int b = threadIdx.x; b < bins; b += kThreads) hist[b] = 0;
-  __syncthreads();
-  grid_dependency_sync();
-  release_dependents();
-  const int64_t first = int64_t(blockIdx.x) * p.tile, end = min(first + p.tile, a.rows);
-  for (int64_t i = first + threadIdx.x; i < end; i += kThreads) {
-    if (!row_ok(i < a.rows, status, NSM_SITE_WORKSPACE)) break;
-    const uint32_t key = pair_at(a, pairs, i).x;
-    atomicAdd(&hist[key >> shift & (bins - 1)], 1u);
-    // some row that asks for this token, whichever thread comes last: see k_embed_sums
-    if (last && key < a.vocab) asm volatile("st.relaxed.gpu.global.s32 [%0], %1;" ::"l"(last + key), "r"(static_cast<int32_t>(i)) : "memory");
-  }
-  __syncthreads();
-  for (int b = threadIdx.x; b < bins; b += kThreads) counts[int64_t(blockIdx.x) * bins + b] = hist[b];
-}
-
-__global__ void __launch_bounds__(kThreads)
-    k_sort_place(const EmbeddingArgs a, const EmbeddingPlan p, const uint2* pairs, int shift, const uint32_t* counts,
-                 uint2* placed, int* status) {
-  __shared__ uint32_t place[kWarps][1 << kMaxBits];  // of each warp's next pair with a digit
-  __shared__ uint32_t warp_total[kWarps];
-  const int bins = 1 << p.bits, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  for (int w = 0; w < kWarps; ++w)
-    for (int b = threadIdx.x; b < bins; b += kThreads) place[w][b] = 0;
-  __syncthreads();
-  grid_dependency_sync();
-  release_dependents();
-  const int64_t tile0 = int64_t(blockIdx.x) * p.tile, tile1 = min(tile0 + p.tile, a.rows);
-  const int64_t part = p.tile / kWarps;  // whole groups of 32
-  const int64_t first = min(tile0 + warp * part, tile1), end = min(first + part, tile1);
-  for (int64_t i = first + lane; i < end; i += 32) atomicAdd(&place[warp][pair_at(a, pairs, i).x >> shift & (bins - 1)], 1u);
-
-  // digits 4 tid ... 4 tid + 3: all pairs with a digit, and those of the tiles before this one
-  uint32_t all[4] = {0, 0, 0, 0}, before[4] = {0, 0, 0, 0};
-  const int b0 = threadIdx.x * 4;
-  for (int t = 0; t < p.tiles; ++t) {
+  };
+  int token[kUnits];
+  if (unit < units) tokens_of(row, slice, token);
+  while (unit < units) {
+    Eight<W> raw[kUnits];
+    int r = row, s = slice;
+    uint32_t has = 0;
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      if (b0 + d >= bins) break;
-      const uint32_t n = counts[int64_t(t) * bins + b0 + d];
-      all[d] += n;
-      if (t < blockIdx.x) before[d] += n;
+    for (int i = 0; i < kUnits; ++i) {
+      O* to = static_cast<O*>(a.rows_out) + r * a.ld_rows;
+      if (r < rows && token[i] >= 0) {
+        has |= 1u << i;
+        load8(static_cast<const W*>(a.weight) + token[i] * a.ld_weight, cols, (s * lanes + lane) * 8 - lead_of(to), raw[i], status,
+              NSM_SITE_EMBEDDING);
+      }
+      if (++s == slices) {
+        s = 0;
+        ++r;
+      }
     }
-  }
-  const uint32_t own = all[0] + all[1] + all[2] + all[3];
-  uint32_t scan = own;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const uint32_t n = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += n;
-  }
-  if (lane == 31) warp_total[warp] = scan;
-  __syncthreads();
-  uint32_t base = scan - own;
-  for (int w = 0; w < warp; ++w) base += warp_total[w];
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    if (b0 + d >= bins) break;
-    uint32_t at = base + before[d];
-    for (int w = 0; w < kWarps; ++w) {
-      const uint32_t n = place[w][b0 + d];
-      place[w][b0 + d] = at;
-      at += n;
+    r = row;
+    s = slice;
+    unit += step;
+    if (unit < units) {
+      row += static_cast<int>(row_step);
+      slice += slice_step;
+      if (slice >= slices) {
+        slice -= slices;
+        ++row;
+      }
+      tokens_of(row, slice, token);
     }
-    base += all[d];
-  }
-  __syncthreads();
-  for (int64_t i0 = first; i0 < end; i0 += 32) {
-    const int64_t i = i0 + lane;
-    const uint32_t live = __ballot_sync(0xffffffffu, i < end);
-    if (i < end) {
-      const uint2 pair = pair_at(a, pairs, i);
-      const uint32_t digit = pair.x >> shift & (bins - 1);
-      const uint32_t same = __match_any_sync(live, digit);
-      const uint32_t rank = __popc(same & ((1u << lane) - 1));
-      const uint32_t at = place[warp][digit] + rank;
-      __syncwarp(live);
-      if (rank == 0) place[warp][digit] += __popc(same);
-      __syncwarp(live);
-      if (row_ok(at < a.rows, status, NSM_SITE_WORKSPACE)) placed[at] = pair;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      if (r < rows) {
+        O* to = static_cast<O*>(a.rows_out) + r * a.ld_rows;
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (has >> i & 1) {
+          raw[i].get(f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] *= a.scale;
+        }
+        store8(to, cols, (s * lanes + lane) * 8 - lead_of(to), f, status, NSM_SITE_EMBEDDING);
+      }
+      if (++s == slices) {
+        s = 0;
+        ++r;
+      }
     }
   }
 }
 
-// ---------------------------------------------------------------- sums
+// ---------------------------------------------------------------- rows without a token
 
 // Whether some row asks for token v: last[v], which nothing ever clears, is then one of them.
 __device__ __forceinline__ bool asked_for(const EmbeddingArgs& a, const int32_t* last, int64_t v) {
@@ -236,134 +222,432 @@ __device__ __forceinline__ void clear_row(W* row, int64_t cols, int lane, int* s
   if (c < cols) row[c] = Elem<W>::from_float(0.f);
 }
 
-template <typename W, bool kVec>
-__device__ __forceinline__ void write_sum(const EmbeddingArgs& a, uint32_t token, int64_t slice, int lanes, int lane,
-                                          const float (&sum)[8], int* status) {
+// Clears those of the rows from v0 on, kClear per warp, that no token asks for.
+template <typename W>
+__device__ __forceinline__ void clear_rows(const EmbeddingArgs& a, const int32_t* last, int64_t v0, int64_t end, int* status) {
+  const int lane = threadIdx.x & 31;
+  const int64_t first = v0 + threadIdx.x / 32 * kClear, v = first + lane;
+  const bool none = lane < kClear && v < end && !asked_for(a, last, v);
+  for (uint32_t rows = __ballot_sync(0xffffffffu, none); rows; rows &= rows - 1)
+    clear_row(static_cast<W*>(a.d_weight) + (first + __ffs(rows) - 1) * a.ld_weight, a.cols, lane, status);
+}
+
+// ---------------------------------------------------------------- sorting tokens
+
+// The pair of entry i: from the tokens in the first pass, from the pass before later on.
+__device__ __forceinline__ uint2 pair_at(const EmbeddingArgs& a, const uint2* pairs, int64_t i) {
+  return pairs ? pairs[i] : make_uint2(key_at(a, i), static_cast<uint32_t>(i));
+}
+
+// Notes some row that asks for the token, whichever comes last: see asked_for.
+__device__ __forceinline__ void note_row(const EmbeddingArgs& a, int32_t* last, uint32_t key, int64_t row) {
+  if (key < a.vocab)
+    asm volatile("st.relaxed.gpu.global.s32 [%0], %1;" ::"l"(last + key), "r"(static_cast<int32_t>(row)) : "memory");
+}
+
+// counts: of every pass one after the other, tiles x bins each.
+__global__ void __launch_bounds__(kThreads)
+    k_sort_count(const EmbeddingArgs a, const EmbeddingPlan p, uint32_t* counts, int32_t* last, int* status) {
+  __shared__ uint32_t hist[kMaxBins];
+  const int bins = 1 << p.bits;
+  for (int b = threadIdx.x; b < bins; b += kThreads) hist[b] = 0;
+  __syncthreads();
+  grid_dependency_sync();
+  release_dependents();
+  const int64_t first = int64_t(blockIdx.x) * p.tile, end = min(first + p.tile, a.rows);
+  for (int64_t i = first + threadIdx.x; i < end; i += kThreads) {
+    if (!row_ok(i < a.rows, status, NSM_SITE_WORKSPACE)) break;
+    const uint32_t key = key_at(a, i);
+    atomicAdd(&hist[key & (bins - 1)], 1u);
+    if (last) note_row(a, last, key, i);
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < bins; b += kThreads) {
+    counts[int64_t(blockIdx.x) * bins + b] = hist[b];
+    for (int pass = 1; pass < p.passes; ++pass) counts[(int64_t(pass) * p.tiles + blockIdx.x) * bins + b] = 0;
+  }
+}
+
+// Exclusive sums over kMaxBins numbers, four to each of the first 128 threads of a block.
+__device__ __forceinline__ void scan_bins(uint32_t (&n)[4], uint32_t* warp_total) {
+  const uint32_t own = n[0] + n[1] + n[2] + n[3];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  uint32_t scan = own;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const uint32_t m = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += m;
+  }
+  if (lane == 31 && warp < 4) warp_total[warp] = scan;
+  __syncthreads();
+  uint32_t base = scan - own;
+  for (int w = 0; w < min(warp, 4); ++w) base += warp_total[w];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const uint32_t m = n[d];
+    n[d] = base;
+    base += m;
+  }
+}
+
+// Hands out places in order: each warp's entries [first, end) one group of 32 after the other,
+// from next[digit] on.
+template <typename Get, typename Put>
+__device__ __forceinline__ void place_in_order(uint32_t* next, int64_t first, int64_t end, int shift, int bins, Get get, Put put) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t i0 = first; i0 < end; i0 += 32) {
+    const int64_t i = i0 + lane;
+    const uint32_t live = __ballot_sync(0xffffffffu, i < end);
+    if (i < end) {
+      const uint2 pair = get(i);
+      const uint32_t digit = pair.x >> shift & (bins - 1);
+      const uint32_t same = __match_any_sync(live, digit);
+      const uint32_t rank = __popc(same & ((1u << lane) - 1));
+      const uint32_t at = next[digit] + rank;
+      __syncwarp(live);
+      if (rank == 0) next[digit] += __popc(same);
+      __syncwarp(live);
+      put(at, pair);
+    }
+  }
+}
+
+// Blocks behind the tiles' clear a part of the rows that no token asks for, on the SMs that the
+// sort leaves idle.  W: type of the weight's gradient.
+template <typename W>
+__global__ void __launch_bounds__(kPlaceThreads)
+    k_sort_place(const EmbeddingArgs a, const EmbeddingPlan p, const uint2* pairs, int pass, uint32_t* counts, uint2* placed,
+                 const int32_t* last, int* status) {
+  __shared__ uint32_t next[kPlaceWarps][kMaxBins];  // each warp's next place for a digit
+  __shared__ __align__(16) uint32_t part[4][kMaxBins];
+  __shared__ uint32_t warp_total[4];
+  const int bins = 1 << p.bits, shift = pass * p.bits, tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+  for (int b = tid; b < kPlaceWarps * kMaxBins; b += kPlaceThreads) next[0][b] = 0;
+  __syncthreads();
+  grid_dependency_sync();
+  release_dependents();
+  if (blockIdx.x >= p.tiles) {
+    const int64_t v0 = p.clear_rows * pass;
+    clear_rows<W>(a, last, v0 + int64_t(blockIdx.x - p.tiles) * kPlaceWarps * kClear, min(v0 + p.clear_rows, a.vocab), status);
+    return;
+  }
+  // the counts of all tiles and of those before this one: four digits and every fourth tile per thread
+  const int b0 = (tid & 127) * 4, group = tid / 128;
+  const uint32_t* of_pass = counts + int64_t(pass) * p.tiles * bins;
+  uint4 all = make_uint4(0, 0, 0, 0), before = all;
+  if (b0 < bins) {
+#pragma unroll 8
+    for (int t = group; t < p.tiles; t += 4) {
+      const uint4 n = *reinterpret_cast<const uint4*>(of_pass + int64_t(t) * bins + b0);
+      all = make_uint4(all.x + n.x, all.y + n.y, all.z + n.z, all.w + n.w);
+      if (t < static_cast<int>(blockIdx.x)) before = make_uint4(before.x + n.x, before.y + n.y, before.z + n.z, before.w + n.w);
+    }
+  }
+  const int64_t tile0 = int64_t(blockIdx.x) * p.tile, tile1 = min(tile0 + p.tile, a.rows);
+  const int64_t per_warp = p.tile / kPlaceWarps;  // whole groups of 32
+  const int64_t first = min(tile0 + warp * per_warp, tile1), end = min(first + per_warp, tile1);
+  for (int64_t i = first + lane; i < end; i += 32) atomicAdd(&next[warp][pair_at(a, pairs, i).x >> shift & (bins - 1)], 1u);
+  *reinterpret_cast<uint4*>(&part[group][b0]) = all;
+  __syncthreads();
+  uint32_t base[4];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) base[d] = part[0][b0 + d] + part[1][b0 + d] + part[2][b0 + d] + part[3][b0 + d];
+  scan_bins(base, warp_total);
+  __syncthreads();  // the parts have been read
+  *reinterpret_cast<uint4*>(&part[group][b0]) = before;
+  __syncthreads();
+#pragma unroll
+  for (int d = 0; d < 4; ++d) base[d] += part[0][b0 + d] + part[1][b0 + d] + part[2][b0 + d] + part[3][b0 + d];
+  __syncthreads();
+  if (group == 0) *reinterpret_cast<uint4*>(&part[0][b0]) = make_uint4(base[0], base[1], base[2], base[3]);
+  __syncthreads();
+  if (tid < bins) {  // a digit per thread: where each warp's own begin
+    uint32_t at = part[0][tid];
+    for (int w = 0; w < kPlaceWarps; ++w) {
+      const uint32_t n = next[w][tid];
+      next[w][tid] = at;
+      at += n;
+    }
+  }
+  __syncthreads();
+  uint32_t* of_next = pass + 1 < p.passes ? counts + int64_t(pass + 1) * p.tiles * bins : nullptr;
+  place_in_order(
+      next[warp], first, end, shift, bins, [&](int64_t i) { return pair_at(a, pairs, i); },
+      [&](uint32_t at, const uint2& pair) {
+        if (!row_ok(at < a.rows, status, NSM_SITE_WORKSPACE)) return;
+        placed[at] = pair;
+        if (of_next) atomicAdd(&of_next[int64_t(at / p.tile) * bins + (pair.x >> (shift + p.bits) & (bins - 1))], 1u);
+      });
+}
+
+constexpr size_t kBlockSmem = size_t(kBlockRows) * 16 + size_t(kBlockThreads / 32) * kMaxBins * 4;
+
+// All passes for at most kBlockRows rows.
+__global__ void __launch_bounds__(kBlockThreads)
+    k_sort_block(const EmbeddingArgs a, const EmbeddingPlan p, uint2* sorted, int32_t* last, int* status) {
+  extern __shared__ __align__(16) uint2 block_pairs[];  // two times kBlockRows, then the warps' counts
+  uint2* from = block_pairs;
+  uint2* to = block_pairs + kBlockRows;
+  constexpr int kAllWarps = kBlockThreads / 32;
+  uint32_t* next = reinterpret_cast<uint32_t*>(block_pairs + 2 * kBlockRows);
+  __shared__ __align__(16) uint32_t total[kMaxBins];
+  __shared__ uint32_t warp_total[4];
+  const int bins = 1 << p.bits, tid = threadIdx.x, warp = tid / 32, lane = tid & 31, rows = static_cast<int>(a.rows);
+  grid_dependency_sync();
+  release_dependents();
+  for (int i = tid; i < rows; i += kBlockThreads) {
+    const uint32_t key = key_at(a, i);
+    from[i] = make_uint2(key, i);
+    if (last) note_row(a, last, key, i);
+  }
+  const int warps = min((rows + 31) / 32, kAllWarps);  // that have entries
+  const int per_warp = (rows + warps * 32 - 1) / (warps * 32) * 32;
+  const int first = min(warp * per_warp, rows), end = min(first + per_warp, rows);
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * p.bits;
+    for (int i = tid; i < warps * kMaxBins; i += kBlockThreads) next[i] = 0;
+    __syncthreads();
+    for (int i = first + lane; i < end; i += 32) atomicAdd(&next[warp * kMaxBins + (from[i].x >> shift & (bins - 1))], 1u);
+    __syncthreads();
+    if (tid < kMaxBins) {  // a digit per thread: what the warps before each have of it
+      uint32_t at = 0;
+      for (int w = 0; w < warps; ++w) {
+        const uint32_t n = next[w * kMaxBins + tid];
+        next[w * kMaxBins + tid] = at;
+        at += n;
+      }
+      total[tid] = at;
+    }
+    __syncthreads();
+    uint32_t n[4] = {0, 0, 0, 0};
+    if (tid < kMaxBins / 4) *reinterpret_cast<uint4*>(n) = reinterpret_cast<const uint4*>(total)[tid];
+    scan_bins(n, warp_total);
+    if (tid < kMaxBins / 4) reinterpret_cast<uint4*>(total)[tid] = make_uint4(n[0], n[1], n[2], n[3]);
+    __syncthreads();
+    const bool done = pass + 1 == p.passes;
+    place_in_order(
+        next + warp * kMaxBins, first, end, shift, bins, [&](int64_t i) { return from[i]; },
+        [&](uint32_t at, const uint2& pair) {
+          at += total[pair.x >> shift & (bins - 1)];
+          if (!row_ok(at < a.rows, status, NSM_SITE_WORKSPACE)) return;
+          (done ? sorted : to)[at] = pair;
+        });
+    __syncthreads();
+    uint2* other = from;
+    from = to;
+    to = other;
+  }
+}
+
+// ---------------------------------------------------------------- sums
+
+template <typename W>
+__device__ __forceinline__ W* weight_row(const EmbeddingArgs& a, uint32_t token) {
+  return static_cast<W*>(a.d_weight) + int64_t(token) * a.ld_weight;
+}
+
+// Unit u of a token's row: its first column.
+template <typename W>
+__device__ __forceinline__ int unit_column(const EmbeddingArgs& a, uint32_t token, int u) {
+  return u * 8 - lead_of(weight_row<W>(a, token));
+}
+
+// The columns that the gradient holds already, where the sums are added to them.
+template <typename W>
+__device__ __forceinline__ void load_old(const EmbeddingArgs& a, uint32_t token, int u, Eight<W>& old, int* status) {
+  if (row_ok(token < a.vocab, status, NSM_SITE_EMBEDDING))
+    load8(static_cast<const W*>(weight_row<W>(a, token)), static_cast<int>(a.cols), unit_column<W>(a, token, u), old, status, NSM_SITE_EMBEDDING);
+}
+
+template <typename W, bool kAccumulate>
+__device__ __forceinline__ void write_sum(const EmbeddingArgs& a, uint32_t token, int u, const float (&sum)[8], const Eight<W>& old,
+                                          int* status) {
   if (!row_ok(token < a.vocab, status, NSM_SITE_EMBEDDING)) return;
-  W* row = static_cast<W*>(a.d_weight) + int64_t(token) * a.ld_weight;
   float f[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[e] = a.scale * sum[e];
-  if (a.accumulate) {
+  if (kAccumulate) {
+    float g[8];
+    old.get(g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int64_t c = column<kVec>(slice, lanes, lane, e);
-      if (c < a.cols) f[e] += Elem<W>::to_float(row[c]);
-    }
+    for (int e = 0; e < 8; ++e) f[e] += g[e];
   }
-  store_columns<W, kVec>(row, a.cols, slice, lanes, lane, f, status, NSM_SITE_EMBEDDING);
+  store8(weight_row<W>(a, token), static_cast<int>(a.cols), unit_column<W>(a, token, u), f, status, NSM_SITE_EMBEDDING);
 }
 
-// A piece's two sums in the workspace: of a token that began in an earlier piece and ends in
-// this one, and of one that goes on in the next.
+// A piece's two sums in the workspace, unit after unit, of tokens in more than two pieces: of the
+// one that ends here, and of the one that goes on behind this piece.
 __device__ __forceinline__ float* piece_sum(const EmbeddingPlan& p, float* sums, int64_t piece, int which) {
   return sums + (piece * 2 + which) * p.cols;
 }
 
-// G: type of the rows' gradients, W: of the weight's.
-template <typename G, typename W, bool kVec>
-__global__ void __launch_bounds__(kThreads)
+__device__ __forceinline__ void keep_sum(float* sums, int u, const float (&sum)[8], int* status) {
+  Eight<float> r;
+  r.set(sum);
+  if (row_ok(on_16_bytes(sums), status, NSM_SITE_WORKSPACE)) r.store(sums + u * 8);
+}
+
+__device__ __forceinline__ bool token_is(const uint2* pairs, int64_t i, int64_t rows, uint32_t token) {
+  return i >= 0 && i < rows && pairs[i].x == token;
+}
+
+// G: type of the rows' gradients, W: of the weight's.  The block's groups take pieces that follow
+// one another, of one slice of the columns; their pairs, with those of a piece and an entry more on
+// either side, are read to shared memory first.
+template <typename G, typename W, bool kAccumulate>
+__global__ void __launch_bounds__(kThreads, !kAccumulate && sizeof(G) == 2 ? 4 : 2)
     k_embed_sums(const EmbeddingArgs a, const EmbeddingPlan p, const uint2* pairs, const int32_t* last, float* sums,
-                 int lanes, int slices, int64_t sum_blocks, int* status) {
+                 int lanes, int64_t sum_blocks, int blocks_per_slice, int* status) {
+  extern __shared__ __align__(16) uint2 near[];
   grid_dependency_sync();
   release_dependents();
-  if (blockIdx.x >= sum_blocks) {  // rows of the gradient that no token asks for
-    const int64_t v0 = (blockIdx.x - sum_blocks) * kClear + threadIdx.x / 32 * (kClear / kWarps);
-    const int lane = threadIdx.x & 31;
-    const int64_t v = v0 + lane;
-    const bool none = lane < kClear / kWarps && v < a.vocab && !asked_for(a, last, v);
-    uint32_t rows = __ballot_sync(0xffffffffu, none);
-    for (; rows; rows &= rows - 1)
-      clear_row(static_cast<W*>(a.d_weight) + (v0 + __ffs(rows) - 1) * a.ld_weight, a.cols, lane, status);
+  if (blockIdx.x >= sum_blocks) {
+    clear_rows<W>(a, last, p.clear_rows * p.passes + (blockIdx.x - sum_blocks) * kWarps * kClear, a.vocab, status);
     return;
   }
-  const int lane = threadIdx.x & (lanes - 1), groups = kThreads / lanes;
-  const int64_t item = blockIdx.x * int64_t(groups) + threadIdx.x / lanes;
-  const int64_t piece = item % p.units, slice = item / p.units;
-  if (slice >= slices) return;
-  const int64_t first = piece * kPiece, end = min(first + kPiece, a.rows);
-  uint32_t token = pairs[first].x;
-  if (token >= a.vocab) return;
-  bool joined = first > 0 && pairs[first - 1].x == token;  // the token began in an earlier piece
+  const int lane = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = kThreads / lanes;
+  const int64_t piece0 = int64_t(blockIdx.x % blocks_per_slice) * groups;
+  const int u = static_cast<int>(blockIdx.x / blocks_per_slice) * lanes + lane;
+  const int halo = p.piece + 1, total = groups * p.piece + 2 * halo;
+  const int64_t near0 = piece0 * p.piece - halo;
+  const uint32_t none = static_cast<uint32_t>(a.vocab);
+  for (int i = threadIdx.x; i < total; i += kThreads) {
+    const int64_t j = near0 + i;
+    near[i] = j >= 0 && j < a.rows ? pairs[j] : make_uint2(none, 0);
+  }
+  __syncthreads();
+  const int64_t piece = piece0 + group;
+  const int first = halo + group * p.piece, end = first + p.piece;
+  const uint32_t first_token = near[first].x, last_token = near[end - 1].x;
+  if (first_token >= none) return;
+  // a token of the piece before that ends here is that piece's, unless it began further back
+  const bool from_before = near[first - 1].x == first_token;
+  const bool joined = from_before && (near[first - halo].x == first_token || near[end].x == first_token);
+  int j = first;
+  if (from_before && !joined)
+    while (j < end && near[j].x == first_token) ++j;
+  // a token that begins here and ends in the next piece is added up whole
+  int until = end;
+  const bool goes_on = last_token < none && near[end].x == last_token;
+  const bool whole = goes_on && !(from_before && last_token == first_token) && near[end + p.piece].x != last_token;
+  if (whole)
+    while (near[until].x == last_token) ++until;
+
+  constexpr int kAhead = kAccumulate || sizeof(G) == 4 ? 4 : 8;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const auto keep = [&](int which) {
-    float* to = piece_sum(p, sums, piece, which);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int64_t c = column<kVec>(slice, lanes, lane, e);
-      if (c < p.cols) to[c] = sum[e];
-    }
-  };
-  const auto finish = [&]() {
-    if (joined) keep(0); else write_sum<W, kVec>(a, token, slice, lanes, lane, sum, status);
-  };
-  constexpr int kAhead = 4;
-  for (int64_t j0 = first; j0 < end; j0 += kAhead) {
-    uint2 pair[kAhead];
+  bool of_before = joined;  // the sum is of a token that began before this piece
+  for (; j < until; j += kAhead) {
+    if (near[j].x >= none) break;
     Eight<G> raw[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) pair[i] = j0 + i < end ? pairs[j0 + i] : make_uint2(static_cast<uint32_t>(a.vocab), 0);
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (pair[i].x < a.vocab && row_ok(pair[i].y < a.rows, status, NSM_SITE_EMBEDDING))
-        load_columns<G, kVec>(static_cast<const G*>(a.rows_in) + int64_t(pair[i].y) * a.ld_rows, a.cols, slice, lanes, lane,
-                              raw[i], status, NSM_SITE_EMBEDDING);
+    Eight<W> old[kAccumulate ? kAhead : 1];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      if (pair[i].x >= a.vocab) break;
-      if (pair[i].x != token) {
-        finish();
-        token = pair[i].x;
-        joined = false;
+      const uint2 pair = near[min(j + i, until - 1)];
+      if (j + i >= until || pair.x >= none || !row_ok(pair.y < a.rows, status, NSM_SITE_EMBEDDING)) continue;
+      load8(static_cast<const G*>(a.rows_in) + int64_t(pair.y) * a.ld_rows, static_cast<int>(a.cols), unit_column<W>(a, pair.x, u),
+            raw[i], status, NSM_SITE_EMBEDDING);
+      if (kAccumulate && near[j + i + 1].x != pair.x) load_old<W>(a, pair.x, u, old[i], status);
+    }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] = 0.f;
-      }
+    for (int i = 0; i < kAhead; ++i) {
+      if (j + i >= until) break;
+      const uint32_t token = near[j + i].x;
+      if (token >= none) break;
       float f[8];
       raw[i].get(f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] += f[e];
+      if (near[j + i + 1].x == token) continue;
+      if (of_before) keep_sum(piece_sum(p, sums, piece, 0), u, sum, status);
+      else write_sum<W, kAccumulate>(a, token, u, sum, old[kAccumulate ? i : 0], status);
+      of_before = false;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] = 0.f;
     }
   }
-  if (end < a.rows && pairs[end].x == token) keep(1); else finish();
+  if (goes_on && !whole) keep_sum(piece_sum(p, sums, piece, 1), u, sum, status);
 }
 
-// For every piece in which a token of earlier pieces ends: their sums in order.
-template <typename W, bool kVec>
-__global__ void __launch_bounds__(kThreads)
-    k_embed_join(const EmbeddingArgs a, const EmbeddingPlan p, const uint2* pairs, const float* sums, int lanes, int slices,
-                 int* status) {
+// Tokens of more than two pieces that begin in one of the block's: their sums, the block's groups
+// a part of the pieces each, then the groups' in order.  A block looks at every `blocks`-th piece, so
+// that the pieces of frequent tokens, which follow one another, are different blocks'.
+template <typename W, bool kAccumulate>
+__global__ void __launch_bounds__(kJoinThreads)
+    k_embed_join(const EmbeddingArgs a, const EmbeddingPlan p, const uint2* pairs, float* sums, int lanes, int slices,
+                 int blocks, int* status) {
+  __shared__ __align__(16) float part[kJoinThreads * 8], total[256];
   grid_dependency_sync();
   release_dependents();
-  const int lane = threadIdx.x & (lanes - 1), groups = kThreads / lanes;
-  const int64_t item = blockIdx.x * int64_t(groups) + threadIdx.x / lanes;
-  const int64_t piece = item % p.units, slice = item / p.units;
-  if (slice >= slices || piece == 0) return;
-  const int64_t first = piece * kPiece, end = min(first + kPiece, a.rows);
-  const uint32_t token = pairs[first].x;
-  if (token >= a.vocab || pairs[first - 1].x != token) return;
-  if (end < a.rows && pairs[end].x == token) return;  // goes on
-  int64_t low = 0, high = first - 1;  // where the token's entries begin
-  while (low < high) {
-    const int64_t mid = (low + high) / 2;
-    if (pairs[mid].x < token) low = mid + 1; else high = mid;
+  const int lane = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = kJoinThreads / lanes;
+  const int64_t piece0 = blockIdx.x / slices;
+  const int u = static_cast<int>(blockIdx.x % slices) * lanes + lane;
+  const int64_t rows = a.rows;
+  // every warp finds the same ones
+  const int64_t mine = piece0 + int64_t(threadIdx.x & 31) * blocks, end = (mine + 1) * p.piece;
+  bool begins = false;
+  if ((threadIdx.x & 31) < kJoinPieces && end + p.piece < rows) {
+    const uint32_t token = pairs[end - 1].x, next = pairs[end].x, far = pairs[end + p.piece].x;
+    const uint32_t back = mine > 0 ? pairs[end - p.piece - 1].x : static_cast<uint32_t>(a.vocab);
+    begins = (token < a.vocab) & (next == token) & (far == token) & (back != token);
   }
-  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int64_t w = low / kPiece; w <= piece; ++w) {
-    const float* from = piece_sum(p, const_cast<float*>(sums), w, w < piece ? 1 : 0);
+  for (uint32_t some = __ballot_sync(0xffffffffu, begins); some; some &= some - 1) {
+    const int64_t begin = piece0 + int64_t(__ffs(some) - 1) * blocks;
+    const uint32_t token = pairs[(begin + 1) * p.piece - 1].x;
+    // it fills whole pieces from begin + 1 on, and ends in the one behind them
+    int64_t last = begin + 1;
+    for (int full = kJoinThreads; full == kJoinThreads; last += full)
+      full = __syncthreads_count(token_is(pairs, (last + 1 + threadIdx.x) * p.piece, rows, token));
+    const int64_t count = last + 1 - begin;
+    const int64_t from = begin + count * group / groups, to = begin + count * (group + 1) / groups;
+    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    constexpr int kAhead = 4;
+    for (int64_t w0 = from; w0 < to; w0 += kAhead) {
+      Eight<float> f[kAhead];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int64_t c = column<kVec>(slice, lanes, lane, e);
-      if (c < p.cols) sum[e] += from[c];
+      for (int i = 0; i < kAhead; ++i)
+        if (w0 + i < to && row_ok(u * 8 + 8 <= p.cols, status, NSM_SITE_WORKSPACE)) f[i].load_written(piece_sum(p, sums, w0 + i, w0 + i < last ? 1 : 0) + u * 8);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (w0 + i >= to) break;
+        float g[8];
+        f[i].get(g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += g[e];
+      }
     }
+    // a column per thread over the groups
+    float* own = part + (group * lanes + lane) * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) own[e] = sum[e];
+    __syncthreads();
+    if (threadIdx.x < lanes * 8) {
+      float s = 0.f;
+      for (int g = 0; g < groups; ++g) s += part[g * lanes * 8 + threadIdx.x];
+      total[threadIdx.x] = s;
+    }
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] = total[lane * 8 + e];
+      Eight<W> old;
+      if (kAccumulate) load_old<W>(a, token, u, old, status);
+      write_sum<W, kAccumulate>(a, token, u, sum, old, status);
+    }
+    __syncthreads();
   }
-  write_sum<W, kVec>(a, token, slice, lanes, lane, sum, status);
 }
 
-// Lanes that share a row: as many as its eights of columns ask for, a power of two, a warp at most.
-int lanes_for(int64_t cols) {
+// How a row of `cols` columns is cut: lanes that share it, a power of two up to a warp, each with a
+// unit at a time, and slices of so many units.  Rows that do not begin on 16-byte boundaries have up
+// to seven columns' room more.
+struct Cut {
+  int lanes, slices;
+};
+Cut cut_rows(int64_t cols, bool aligned) {
+  const int64_t room = cols + (aligned ? 0 : 7);
   int lanes = 1;
-  while (lanes < 32 && lanes * 8 < cols) lanes *= 2;
-  return lanes;
+  while (lanes < 32 && lanes * 8 < room) lanes *= 2;
+  return {lanes, static_cast<int>((room + lanes * 8 - 1) / (lanes * 8))};
 }
 
 bool rows_aligned(const void* p, int64_t ld, int dtype) {
@@ -375,36 +659,33 @@ int blocks(int64_t n) { return static_cast<int>(std::min<int64_t>(std::max<int64
 
 template <typename W, typename O>
 cudaError_t launch_embed(const EmbeddingArgs& a, int* status, cudaStream_t stream) {
-  const int lanes = lanes_for(a.cols);
-  const int64_t slices = (a.cols + lanes * 8 - 1) / (lanes * 8);
-  const int chunks = static_cast<int>((slices + kUnits - 1) / kUnits);
-  const dim3 grid(blocks((a.rows * chunks + kThreads / lanes - 1) / (kThreads / lanes)));
-  const bool vec = rows_aligned(a.weight, a.ld_weight, a.weight_dtype) && rows_aligned(a.rows_out, a.ld_rows, a.rows_dtype);
-  return launch_pdl(vec ? k_embed<W, O, true> : k_embed<W, O, false>, grid, dim3(kThreads), 0, stream, a, lanes, chunks, status);
+  const Cut cut = cut_rows(a.cols, rows_aligned(a.rows_out, a.ld_rows, a.rows_dtype));
+  const int64_t per_block = int64_t(kThreads / cut.lanes) * kUnits;
+  const dim3 grid(blocks(std::min<int64_t>((a.rows * cut.slices + per_block - 1) / per_block, kEmbedBlocks)));
+  return launch_pdl(k_embed<W, O>, grid, dim3(kThreads), 0, stream, a, cut.lanes, cut.slices, status);
 }
 
-template <typename G, typename W, bool kVec>
+template <typename G, typename W, bool kAccumulate>
 cudaError_t launch_sums(const EmbeddingArgs& a, const EmbeddingPlan& p, const uint2* pairs, const int32_t* last, float* sums,
                         int* launches, int* status, cudaStream_t stream) {
-  const int lanes = lanes_for(a.cols);
-  const int64_t slices = (a.cols + lanes * 8 - 1) / (lanes * 8);
-  const int64_t groups = kThreads / lanes, sum_blocks = (p.units * slices + groups - 1) / groups;
-  const int64_t clear = a.accumulate ? 0 : (a.vocab + kClear - 1) / kClear;
-  cudaError_t e = launch_pdl(k_embed_sums<G, W, kVec>, dim3(blocks(sum_blocks + clear)), dim3(kThreads), 0, stream, a, p, pairs,
-                             last, sums, lanes, static_cast<int>(slices), sum_blocks, status);
+  const Cut cut = cut_rows(a.cols, rows_aligned(a.d_weight, a.ld_weight, a.weight_dtype));
+  const int groups = kThreads / cut.lanes;
+  const int per_slice = (p.units + groups - 1) / groups;
+  const int64_t sum_blocks = int64_t(per_slice) * cut.slices;
+  const int64_t left = kAccumulate ? 0 : std::max<int64_t>(a.vocab - p.clear_rows * p.passes, 0);
+  const int64_t clear = (left + kWarps * kClear - 1) / (kWarps * kClear);
+  const size_t smem = size_t(groups * p.piece + 2 * (p.piece + 1)) * sizeof(uint2);
+  if (sum_blocks + clear > 0) {
+    const cudaError_t e = launch_pdl(k_embed_sums<G, W, kAccumulate>, dim3(blocks(sum_blocks + clear)), dim3(kThreads), smem,
+                                     stream, a, p, pairs, last, sums, cut.lanes, sum_blocks, per_slice, status);
+    ++*launches;
+    if (e != cudaSuccess) return e;
+  }
+  if (p.units <= 2) return cudaSuccess;
   ++*launches;
-  if (e != cudaSuccess || p.units <= 1) return e;
-  ++*launches;
-  return launch_pdl(k_embed_join<W, kVec>, dim3(blocks(sum_blocks)), dim3(kThreads), 0, stream, a, p, pairs,
-                    static_cast<const float*>(sums), lanes, static_cast<int>(slices), status);
-}
-
-template <typename G, typename W>
-cudaError_t launch_gradient(const EmbeddingArgs& a, const EmbeddingPlan& p, const uint2* pairs, const int32_t* last,
-                            float* sums, int* launches, int* status, cudaStream_t stream) {
-  return rows_aligned(a.rows_in, a.ld_rows, a.rows_dtype)
-             ? launch_sums<G, W, true>(a, p, pairs, last, sums, launches, status, stream)
-             : launch_sums<G, W, false>(a, p, pairs, last, sums, launches, status, stream);
+  const int join = (p.units + kJoinPieces - 1) / kJoinPieces;
+  return launch_pdl(k_embed_join<W, kAccumulate>, dim3(blocks(int64_t(join) * cut.slices)), dim3(kJoinThreads), 0, stream, a, p, pairs,
+                    sums, cut.lanes, cut.slices, join, status);
 }
 
 // f with a value of each of the two types
@@ -425,19 +706,23 @@ cudaError_t for_types(int first, int second, F f) {
 EmbeddingPlan embedding_plan(int64_t rows, int64_t vocab, int64_t cols) {
   const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   EmbeddingPlan p{};
-  int bits = 1;
+  int bits = 2;
   while (bits < 62 && vocab >> bits) ++bits;  // keys 0 ... vocab
   p.passes = (bits + kMaxBits - 1) / kMaxBits;
   p.bits = (bits + p.passes - 1) / p.passes;
-  const int64_t step = 32 * kWarps;
+  const int64_t step = 32 * kPlaceWarps;
   p.tile = static_cast<int32_t>(std::max<int64_t>(1024, ((rows + kMaxTiles - 1) / kMaxTiles + step - 1) / step * step));
   p.tiles = static_cast<int32_t>((rows + p.tile - 1) / p.tile);
-  p.units = static_cast<int32_t>((rows + kPiece - 1) / kPiece);
-  p.cols = (cols + 7) / 8 * 8;
+  // the longest pieces that still make some 16 warps for each SM
+  const Cut cut = cut_rows(cols, true), wide = cut_rows(cols, false);
+  p.piece = std::min(kMaxPiece, 8 * cut.lanes);  // a block's pairs are 16 KB and little more at most
+  while (p.piece > kMinPiece && (rows + p.piece - 1) / p.piece * cut.slices * cut.lanes < int64_t(kWantedWarps) * 32) p.piece /= 2;
+  p.units = static_cast<int32_t>((rows + p.piece - 1) / p.piece);
+  p.cols = std::max(int64_t(cut.lanes) * cut.slices, int64_t(wide.lanes) * wide.slices) * 8;
   p.off_pairs[0] = 0;
   p.off_pairs[1] = p.off_pairs[0] + up(size_t(rows) * 8);
   p.off_counts = p.off_pairs[1] + up(p.passes > 1 ? size_t(rows) * 8 : 0);
-  p.off_last = p.off_counts + up(size_t(p.tiles) * 4 << p.bits);
+  p.off_last = p.off_counts + up(size_t(p.passes) * size_t(p.tiles) * 4 << p.bits);
   p.off_sums = p.off_last + up(size_t(vocab) * 4);
   p.bytes = p.off_sums + up(size_t(p.units) * 2 * size_t(p.cols) * 4);
   return p;
@@ -450,31 +735,43 @@ cudaError_t launch_embedding(const EmbeddingArgs& a, cudaStream_t stream) {
                    [&](auto w, auto o) { return launch_embed<decltype(w), decltype(o)>(a, status, stream); });
 }
 
-cudaError_t launch_embedding_backward(const EmbeddingArgs& a, void* workspace, int num_sms, int* launches, cudaStream_t stream) {
-  (void)num_sms;
+cudaError_t launch_embedding_backward(const EmbeddingArgs& a, void* workspace, int* launches, cudaStream_t stream) {
   int* status = device_status_ptr();
   if (!status) return cudaErrorInvalidSymbol;
-  const EmbeddingPlan p = embedding_plan(a.rows, a.vocab, a.cols);
+  EmbeddingPlan p = embedding_plan(a.rows, a.vocab, a.cols);
   char* ws = static_cast<char*>(workspace);
   uint2* pairs[2] = {reinterpret_cast<uint2*>(ws + p.off_pairs[0]), reinterpret_cast<uint2*>(ws + p.off_pairs[1])};
   uint32_t* counts = reinterpret_cast<uint32_t*>(ws + p.off_counts);
   int32_t* last = reinterpret_cast<int32_t*>(ws + p.off_last);
   const uint2* sorted = nullptr;
   *launches = 0;
-  for (int pass = 0; pass < p.passes && a.rows > 0; ++pass) {
-    const int shift = pass * p.bits;
-    cudaError_t e = launch_pdl(k_sort_count, dim3(p.tiles), dim3(kThreads), 0, stream, a, p, sorted, shift, counts,
-                               pass == 0 && !a.accumulate ? last : static_cast<int32_t*>(nullptr), status);
+  int32_t* noted = a.accumulate ? nullptr : last;
+  if (a.rows > 0 && a.rows <= kBlockRows) {
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = set_smem_once(k_sort_block, kBlockSmem, done);
+    if (e == cudaSuccess) e = launch_pdl(k_sort_block, dim3(1), dim3(kBlockThreads), kBlockSmem, stream, a, p, pairs[0], noted, status);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(k_sort_place, dim3(p.tiles), dim3(kThreads), 0, stream, a, p, sorted, shift,
-                   static_cast<const uint32_t*>(counts), pairs[pass & 1], status);
+    *launches = 1;
+    sorted = pairs[0];
+  } else if (a.rows > 0) {
+    cudaError_t e = launch_pdl(k_sort_count, dim3(p.tiles), dim3(kThreads), 0, stream, a, p, counts, noted, status);
+    if (!a.accumulate) p.clear_rows = std::max<int64_t>(kClearBytes / (a.cols * (a.weight_dtype == NSM_FP32 ? 4 : 2)), 1);
+    for (int pass = 0; pass < p.passes && e == cudaSuccess; ++pass) {
+      const int64_t clear = std::min(std::max<int64_t>(a.vocab - p.clear_rows * pass, 0), p.clear_rows);
+      const dim3 grid(p.tiles + blocks((clear + kPlaceWarps * kClear - 1) / (kPlaceWarps * kClear) + 1) - 1);
+      e = for_types(a.weight_dtype, NSM_FP32, [&](auto w, auto) {
+        return launch_pdl(k_sort_place<decltype(w)>, grid, dim3(kPlaceThreads), 0, stream, a, p, sorted, pass, counts, pairs[pass & 1],
+                          static_cast<const int32_t*>(last), status);
+      });
+      sorted = pairs[pass & 1];
+    }
     if (e != cudaSuccess) return e;
-    *launches += 2;
-    sorted = pairs[pass & 1];
+    *launches = 1 + p.passes;
   }
   return for_types(a.rows_dtype, a.weight_dtype, [&](auto g, auto w) {
-    return launch_gradient<decltype(g), decltype(w)>(a, p, sorted, last, reinterpret_cast<float*>(ws + p.off_sums), launches,
-                                                     status, stream);
+    float* sums = reinterpret_cast<float*>(ws + p.off_sums);
+    return a.accumulate ? launch_sums<decltype(g), decltype(w), true>(a, p, sorted, last, sums, launches, status, stream)
+                        : launch_sums<decltype(g), decltype(w), false>(a, p, sorted, last, sums, launches, status, stream);
   });
 }
 

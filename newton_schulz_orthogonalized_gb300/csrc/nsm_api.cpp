@@ -1315,10 +1315,10 @@ int run_adjust(AdjustArgs& a, nsm_stream_t stream_) {
 
 // ---- the embedding lookup and its gradient
 
-constexpr int64_t kEmbeddingMaxVocab = int64_t(1) << 30, kEmbeddingMaxCols = int64_t(1) << 20;
+constexpr int64_t kEmbeddingMaxRows = int64_t(1) << 30, kEmbeddingMaxVocab = int64_t(1) << 30, kEmbeddingMaxCols = int64_t(1) << 20;
 
 int check_embedding_sizes(int64_t rows, int64_t vocab, int64_t cols) {
-  if (rows < 0 || rows > INT32_MAX) return fail(NSM_ERR_SHAPE, "rows = %lld not in [0, 2^31 - 1]", static_cast<long long>(rows));
+  if (rows < 0 || rows > kEmbeddingMaxRows) return fail(NSM_ERR_SHAPE, "rows = %lld not in [0, 2^30]", static_cast<long long>(rows));
   if (vocab < 1 || vocab > kEmbeddingMaxVocab)
     return fail(NSM_ERR_SHAPE, "vocab = %lld not in [1, 2^30]", static_cast<long long>(vocab));
   if (cols < 1 || cols > kEmbeddingMaxCols) return fail(NSM_ERR_SHAPE, "cols = %lld not in [1, 2^20]", static_cast<long long>(cols));
@@ -2360,8 +2360,6 @@ int nsm_embedding_backward(const void* d_out, int dtype, int64_t rows, int64_t c
     t_last_launches = 0;
     return NSM_OK;
   }
-  int num_sms = 0;
-  if ((rc = current_sms(&num_sms)) != NSM_OK) return rc;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   const PdlScope pdl(0);  // the sort's kernels are short whatever the sizes
   int launches = 0;
@@ -2370,7 +2368,7 @@ int nsm_embedding_backward(const void* d_out, int dtype, int64_t rows, int64_t c
     const double written = accumulate ? 2.0 * double(std::min(rows, vocab)) : double(vocab);
     TimedLaunch t(stream, NSM_KIND_EMBEDDING,
                   double(cols) * (double(rows) * double(number_bytes(dtype)) + written * double(number_bytes(weight_dtype))));
-    e = launch_embedding_backward(a, workspace, num_sms, &launches, stream);
+    e = launch_embedding_backward(a, workspace, &launches, stream);
   }
   if (e != cudaSuccess) return fail_cuda(e, "launch of the embedding's gradient");
   t_last_launches = launches;

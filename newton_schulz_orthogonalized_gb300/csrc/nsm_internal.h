@@ -296,8 +296,9 @@ struct EmbeddingArgs {
 struct EmbeddingPlan {
   int32_t bits, passes;      // of a sorting pass's digit; passes
   int32_t tiles, tile;       // blocks of a pass, and their entries
-  int32_t units;             // pieces of the sorted entries
-  int64_t cols;              // of a unit's sums: cols rounded up to 8
+  int32_t piece, units;      // sorted entries that a group of lanes adds up, and how many such pieces
+  int64_t cols;              // of a piece's sums: columns with room for any alignment
+  int64_t clear_rows;        // of the gradient, that a sorting pass clears on the side (set by the call)
   size_t off_pairs[2], off_counts, off_last, off_sums, bytes;
 };
 EmbeddingPlan embedding_plan(int64_t rows, int64_t vocab, int64_t cols);
@@ -371,8 +372,7 @@ cudaError_t launch_distill(const DistillArgs& args, cudaStream_t stream);
 cudaError_t launch_adjust(const AdjustArgs& args, cudaStream_t stream);
 cudaError_t launch_embedding(const EmbeddingArgs& args, cudaStream_t stream);
 // *launches: how many kernels it took
-cudaError_t launch_embedding_backward(const EmbeddingArgs& args, void* workspace, int num_sms, int* launches,
-                                      cudaStream_t stream);
+cudaError_t launch_embedding_backward(const EmbeddingArgs& args, void* workspace, int* launches, cudaStream_t stream);
 // Sums of squares of `n` tensors (of one launch: n <= kGradTable), one per chunk from partials[0]
 cudaError_t launch_grad_chunks(const GradTensor* tensors, int n, int total_chunks, double* partials, cudaStream_t stream);
 // Their sums: sums[i] per tensor, and its root to norms[i] where norms is not NULL

@@ -416,7 +416,8 @@ int nsm_adjust_logits_backward(const void* logits, int dtype, int64_t rows, int6
  *
  *   - weight, d_weight: device, vocab x cols of type NSM_BF16, NSM_FP16 or NSM_FP32, row stride
  *     ldw >= cols; out, d_out: device, rows x cols of any of these types (it need not be the
- *     weight's), row stride ldo / ldg >= cols.  Aligned to an element.  tokens: device, one int64 (tokens_wide != 0) or int32 per row.
+ *     weight's), row stride ldo / ldg >= cols.  Aligned to an element.  tokens: device, one int64
+ *     (tokens_wide != 0) or int32 per row.
  *     1 <= vocab <= 2^30, 1 <= cols <= 2^20, 0 <= rows <= 2^30.
  *   - Elements between the columns and the row stride are left as they are.
  *   - Sums are fp32 in the order of the rows, the same from call to call; results are rounded once.

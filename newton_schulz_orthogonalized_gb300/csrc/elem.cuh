@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "nsm_internal.h"
+
 namespace nsm {
 namespace {
 
@@ -167,6 +169,68 @@ struct Eight {
 };
 
 __device__ __forceinline__ bool on_16_bytes(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// How many elements past a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ int lead_of(const T* row) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+}
+
+// The elements c0 ... c0 + 7 of a row that has [low, high), zeros outside it, whatever their
+// alignment: whole vectors around them, shifted into place, where those lie within the row.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int low, int high, int c0, Eight<T>& r, int* status, int kernel, int site) {
+  constexpr int kPer = 16 / sizeof(T);
+  const T* at = row + c0;
+  const int s = lead_of(at);
+  if (s == 0 && c0 >= low && c0 + 8 <= high) {
+    if (bounds_ok(on_16_bytes(at), status, kernel, 0, site)) r.load_written(at);
+    return;
+  }
+  if (c0 - s >= low && c0 - s + 8 + kPer <= high) {
+    uint32_t w[4 * (Eight<T>::kWords + 1)];
+    const uint4* from = reinterpret_cast<const uint4*>(at - s);
+    if (!bounds_ok(on_16_bytes(from), status, kernel, 0, site)) return;
+#pragma unroll
+    for (int i = 0; i <= Eight<T>::kWords; ++i) *reinterpret_cast<uint4*>(w + 4 * i) = from[i];
+    constexpr int kNeed = 4 * Eight<T>::kWords;  // words that are wanted
+    const int words = sizeof(T) == 4 ? s : s >> 1;
+    if (words & 2) {
+#pragma unroll
+      for (int i = 0; i < kNeed + 2; ++i) w[i] = w[i + 2];
+    }
+    if (words & 1) {
+#pragma unroll
+      for (int i = 0; i < kNeed + 1; ++i) w[i] = w[i + 1];
+    }
+    if (sizeof(T) == 2 && (s & 1)) {
+#pragma unroll
+      for (int i = 0; i < kNeed; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+#pragma unroll
+    for (int i = 0; i < Eight<T>::kWords; ++i) r.w[i] = *reinterpret_cast<const uint4*>(w + 4 * i);
+    return;
+  }
+  T e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = c0 + i >= low && c0 + i < high ? at[i] : Elem<T>::from_float(0.f);
+#pragma unroll
+  for (int i = 0; i < Eight<T>::kWords; ++i) r.w[i] = reinterpret_cast<const uint4*>(e)[i];
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* row, int low, int high, int c0, const float (&f)[8], int* status, int kernel, int site) {
+  T* at = row + c0;
+  Eight<T> r;
+  r.set(f);
+  if (c0 >= low && c0 + 8 <= high && on_16_bytes(at)) {
+    if (bounds_ok(on_16_bytes(at), status, kernel, 0, site)) r.store(at);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c0 + i >= low && c0 + i < high) at[i] = reinterpret_cast<const T*>(r.w)[i];
+}
 
 }  // namespace
 }  // namespace nsm

@@ -31,6 +31,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kUnits = 4;      // of eight columns, per lane of k_embed
 constexpr int kMaxBits = 9;    // of a sorting pass's digit
 constexpr int kMaxBins = 1 << kMaxBits;
+static_assert(kMaxBins == 4 * 128, "scan_bins gives four digits to each of 128 threads");
 constexpr int kMaxTiles = 64;
 constexpr int kPlaceThreads = 512;
 constexpr int kPlaceWarps = kPlaceThreads / 32;
@@ -43,6 +44,7 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinPieces = 8;  // that a block of k_embed_join looks at
 // Bytes of rows without a token that a sorting pass clears on the side.
 constexpr int64_t kClearBytes = 24 << 20;
+constexpr int kClearBlocks = 150;  // that clear beside k_sort_block's first
 constexpr int kClear = 8;      // rows of the gradient that a warp looks at
 
 __device__ __forceinline__ int64_t token_at(const EmbeddingArgs& a, int64_t r) {
@@ -61,64 +63,12 @@ __device__ __forceinline__ bool row_ok(bool ok, int* status, int site) {
 // Rows are cut into units of eight columns on the 16-byte grid of where results go: unit u holds
 // columns 8 u - lead ... + 8, of which those in [0, cols) exist.
 template <typename T>
-__device__ __forceinline__ int lead_of(const T* row) {
-  return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+__device__ __forceinline__ void load_unit(const T* row, int cols, int c0, Eight<T>& r, int* status) {
+  load8(row, 0, cols, c0, r, status, NSM_KERNEL_EMBEDDING, NSM_SITE_EMBEDDING);
 }
-
-// The columns c0 ... c0 + 7 of a row, zeros outside it, whatever their alignment: whole vectors around
-// them, shifted into place, where those lie within the row.
 template <typename T>
-__device__ __forceinline__ void load8(const T* row, int cols, int c0, Eight<T>& r, int* status, int site) {
-  constexpr int kPer = 16 / sizeof(T);
-  const T* at = row + c0;
-  const int s = lead_of(at);
-  if (s == 0 && c0 >= 0 && c0 + 8 <= cols) {
-    if (row_ok(on_16_bytes(at), status, site)) r.load_written(at);
-    return;
-  }
-  if (c0 - s >= 0 && c0 - s + 8 + kPer <= cols) {
-    uint32_t w[4 * (Eight<T>::kWords + 1)];
-    const uint4* from = reinterpret_cast<const uint4*>(at - s);
-    if (!row_ok(on_16_bytes(from), status, site)) return;
-#pragma unroll
-    for (int i = 0; i <= Eight<T>::kWords; ++i) *reinterpret_cast<uint4*>(w + 4 * i) = from[i];
-    constexpr int kNeed = 4 * Eight<T>::kWords;  // words that are wanted
-    const int words = sizeof(T) == 4 ? s : s >> 1;
-    if (words & 2) {
-#pragma unroll
-      for (int i = 0; i < kNeed + 2; ++i) w[i] = w[i + 2];
-    }
-    if (words & 1) {
-#pragma unroll
-      for (int i = 0; i < kNeed + 1; ++i) w[i] = w[i + 1];
-    }
-    if (sizeof(T) == 2 && (s & 1)) {
-#pragma unroll
-      for (int i = 0; i < kNeed; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-    }
-#pragma unroll
-    for (int i = 0; i < Eight<T>::kWords; ++i) r.w[i] = *reinterpret_cast<const uint4*>(w + 4 * i);
-    return;
-  }
-  T e[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) e[i] = c0 + i >= 0 && c0 + i < cols ? at[i] : Elem<T>::from_float(0.f);
-#pragma unroll
-  for (int i = 0; i < Eight<T>::kWords; ++i) r.w[i] = reinterpret_cast<const uint4*>(e)[i];
-}
-
-template <typename T>
-__device__ __forceinline__ void store8(T* row, int cols, int c0, const float (&f)[8], int* status, int site) {
-  T* at = row + c0;
-  Eight<T> r;
-  r.set(f);
-  if (c0 >= 0 && c0 + 8 <= cols && on_16_bytes(at)) {
-    if (row_ok(on_16_bytes(at), status, site)) r.store(at);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c0 + i >= 0 && c0 + i < cols) at[i] = reinterpret_cast<const T*>(r.w)[i];
+__device__ __forceinline__ void store_unit(T* row, int cols, int c0, const float (&f)[8], int* status) {
+  store8(row, 0, cols, c0, f, status, NSM_KERNEL_EMBEDDING, NSM_SITE_EMBEDDING);
 }
 
 // ---------------------------------------------------------------- lookup
@@ -161,8 +111,7 @@ __global__ void __launch_bounds__(kThreads) k_embed(const EmbeddingArgs a, int l
       O* to = static_cast<O*>(a.rows_out) + r * a.ld_rows;
       if (r < rows && token[i] >= 0) {
         has |= 1u << i;
-        load8(static_cast<const W*>(a.weight) + token[i] * a.ld_weight, cols, (s * lanes + lane) * 8 - lead_of(to), raw[i], status,
-              NSM_SITE_EMBEDDING);
+        load_unit(static_cast<const W*>(a.weight) + token[i] * a.ld_weight, cols, (s * lanes + lane) * 8 - lead_of(to), raw[i], status);
       }
       if (++s == slices) {
         s = 0;
@@ -191,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) k_embed(const EmbeddingArgs a, int l
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] *= a.scale;
         }
-        store8(to, cols, (s * lanes + lane) * 8 - lead_of(to), f, status, NSM_SITE_EMBEDDING);
+        store_unit(to, cols, (s * lanes + lane) * 8 - lead_of(to), f, status);
       }
       if (++s == slices) {
         s = 0;
@@ -290,18 +239,29 @@ __device__ __forceinline__ void scan_bins(uint32_t (&n)[4], uint32_t* warp_total
   }
 }
 
+// The lanes of `live` whose digit is this lane's: a vote per bit (with a match instruction one block
+// sorted 16384 rows in 46 us, with votes in 34).
+__device__ __forceinline__ uint32_t same_digit(uint32_t live, uint32_t digit, int bits) {
+  uint32_t same = live;
+  for (int b = 0; b < bits; ++b) {
+    const uint32_t set = __ballot_sync(live, digit >> b & 1);
+    same &= digit >> b & 1 ? set : ~set;
+  }
+  return same;
+}
+
 // Hands out places in order: each warp's entries [first, end) one group of 32 after the other,
 // from next[digit] on.
 template <typename Get, typename Put>
-__device__ __forceinline__ void place_in_order(uint32_t* next, int64_t first, int64_t end, int shift, int bins, Get get, Put put) {
+__device__ __forceinline__ void place_in_order(uint32_t* next, int first, int end, int shift, int bits, Get get, Put put) {
   const int lane = threadIdx.x & 31;
-  for (int64_t i0 = first; i0 < end; i0 += 32) {
-    const int64_t i = i0 + lane;
+  for (int i0 = first; i0 < end; i0 += 32) {
+    const int i = i0 + lane;
     const uint32_t live = __ballot_sync(0xffffffffu, i < end);
     if (i < end) {
       const uint2 pair = get(i);
-      const uint32_t digit = pair.x >> shift & (bins - 1);
-      const uint32_t same = __match_any_sync(live, digit);
+      const uint32_t digit = pair.x >> shift & ((1u << bits) - 1);
+      const uint32_t same = same_digit(live, digit, bits);
       const uint32_t rank = __popc(same & ((1u << lane) - 1));
       const uint32_t at = next[digit] + rank;
       __syncwarp(live);
@@ -327,8 +287,7 @@ __global__ void __launch_bounds__(kPlaceThreads)
   grid_dependency_sync();
   release_dependents();
   if (blockIdx.x >= p.tiles) {
-    const int64_t v0 = p.clear_rows * pass;
-    clear_rows<W>(a, last, v0 + int64_t(blockIdx.x - p.tiles) * kPlaceWarps * kClear, min(v0 + p.clear_rows, a.vocab), status);
+    clear_rows<W>(a, last, p.clear_first + int64_t(blockIdx.x - p.tiles) * kPlaceWarps * kClear, p.clear_end, status);
     return;
   }
   // the counts of all tiles and of those before this one: four digits and every fourth tile per thread
@@ -372,7 +331,7 @@ __global__ void __launch_bounds__(kPlaceThreads)
   __syncthreads();
   uint32_t* of_next = pass + 1 < p.passes ? counts + int64_t(pass + 1) * p.tiles * bins : nullptr;
   place_in_order(
-      next[warp], first, end, shift, bins, [&](int64_t i) { return pair_at(a, pairs, i); },
+      next[warp], static_cast<int>(first), static_cast<int>(end), shift, p.bits, [&](int i) { return pair_at(a, pairs, i); },
       [&](uint32_t at, const uint2& pair) {
         if (!row_ok(at < a.rows, status, NSM_SITE_WORKSPACE)) return;
         placed[at] = pair;
@@ -380,34 +339,44 @@ __global__ void __launch_bounds__(kPlaceThreads)
       });
 }
 
-constexpr size_t kBlockSmem = size_t(kBlockRows) * 16 + size_t(kBlockThreads / 32) * kMaxBins * 4;
+constexpr size_t kBlockSmem = size_t(kBlockRows) * 8 + size_t(kBlockThreads / 32) * kMaxBins * 4;
 
-// All passes for at most kBlockRows rows.
+// All passes for at most kBlockRows rows (one block's instructions bound it: the whole gradient of
+// 4096 x 768 takes 27 us with it and 29 with the kernels above, of 16384 x 768 49 and 36), whose token and row fit 32 bits together, by the first
+// block.  The others (none where the sums are added to the gradient) note the rows and clear those
+// of the gradient from p.clear_end on, asked for or not: k_embed_sums writes later.
+template <typename W>
 __global__ void __launch_bounds__(kBlockThreads)
     k_sort_block(const EmbeddingArgs a, const EmbeddingPlan p, uint2* sorted, int32_t* last, int* status) {
-  extern __shared__ __align__(16) uint2 block_pairs[];  // two times kBlockRows, then the warps' counts
-  uint2* from = block_pairs;
-  uint2* to = block_pairs + kBlockRows;
+  extern __shared__ __align__(16) uint32_t block_pairs[];  // two times kBlockRows, then the warps' counts
+  uint32_t* from = block_pairs;
+  uint32_t* to = block_pairs + kBlockRows;
   constexpr int kAllWarps = kBlockThreads / 32;
-  uint32_t* next = reinterpret_cast<uint32_t*>(block_pairs + 2 * kBlockRows);
+  uint32_t* next = block_pairs + 2 * kBlockRows;
   __shared__ __align__(16) uint32_t total[kMaxBins];
   __shared__ uint32_t warp_total[4];
   const int bins = 1 << p.bits, tid = threadIdx.x, warp = tid / 32, lane = tid & 31, rows = static_cast<int>(a.rows);
   grid_dependency_sync();
   release_dependents();
+  if (blockIdx.x > 0) {
+    for (int i = (blockIdx.x - 1) * kBlockThreads + tid; i < rows; i += (gridDim.x - 1) * kBlockThreads) note_row(a, last, key_at(a, i), i);
+    for (int64_t v = p.clear_end + int64_t(blockIdx.x - 1) * kAllWarps + warp; v < a.vocab; v += int64_t(gridDim.x - 1) * kAllWarps)
+      clear_row(static_cast<W*>(a.d_weight) + v * a.ld_weight, a.cols, lane, status);
+    return;
+  }
+  const int row_bits = p.row_bits;
+  const uint32_t row_mask = (1u << row_bits) - 1;
   for (int i = tid; i < rows; i += kBlockThreads) {
-    const uint32_t key = key_at(a, i);
-    from[i] = make_uint2(key, i);
-    if (last) note_row(a, last, key, i);
+    from[i] = key_at(a, i) << row_bits | i;
   }
   const int warps = min((rows + 31) / 32, kAllWarps);  // that have entries
   const int per_warp = (rows + warps * 32 - 1) / (warps * 32) * 32;
   const int first = min(warp * per_warp, rows), end = min(first + per_warp, rows);
   for (int pass = 0; pass < p.passes; ++pass) {
-    const int shift = pass * p.bits;
+    const int shift = pass * p.bits + row_bits;
     for (int i = tid; i < warps * kMaxBins; i += kBlockThreads) next[i] = 0;
     __syncthreads();
-    for (int i = first + lane; i < end; i += 32) atomicAdd(&next[warp * kMaxBins + (from[i].x >> shift & (bins - 1))], 1u);
+    for (int i = first + lane; i < end; i += 32) atomicAdd(&next[warp * kMaxBins + (from[i] >> shift & (bins - 1))], 1u);
     __syncthreads();
     if (tid < kMaxBins) {  // a digit per thread: what the warps before each have of it
       uint32_t at = 0;
@@ -424,19 +393,19 @@ __global__ void __launch_bounds__(kBlockThreads)
     scan_bins(n, warp_total);
     if (tid < kMaxBins / 4) reinterpret_cast<uint4*>(total)[tid] = make_uint4(n[0], n[1], n[2], n[3]);
     __syncthreads();
-    const bool done = pass + 1 == p.passes;
     place_in_order(
-        next + warp * kMaxBins, first, end, shift, bins, [&](int64_t i) { return from[i]; },
+        next + warp * kMaxBins, first, end, shift, p.bits, [&](int i) { return make_uint2(from[i], 0); },
         [&](uint32_t at, const uint2& pair) {
           at += total[pair.x >> shift & (bins - 1)];
           if (!row_ok(at < a.rows, status, NSM_SITE_WORKSPACE)) return;
-          (done ? sorted : to)[at] = pair;
+          to[at] = pair.x;
         });
     __syncthreads();
-    uint2* other = from;
+    uint32_t* other = from;
     from = to;
     to = other;
   }
+  for (int i = tid; i < rows; i += kBlockThreads) sorted[i] = make_uint2(from[i] >> row_bits, from[i] & row_mask);
 }
 
 // ---------------------------------------------------------------- sums
@@ -456,7 +425,7 @@ __device__ __forceinline__ int unit_column(const EmbeddingArgs& a, uint32_t toke
 template <typename W>
 __device__ __forceinline__ void load_old(const EmbeddingArgs& a, uint32_t token, int u, Eight<W>& old, int* status) {
   if (row_ok(token < a.vocab, status, NSM_SITE_EMBEDDING))
-    load8(static_cast<const W*>(weight_row<W>(a, token)), static_cast<int>(a.cols), unit_column<W>(a, token, u), old, status, NSM_SITE_EMBEDDING);
+    load_unit(static_cast<const W*>(weight_row<W>(a, token)), static_cast<int>(a.cols), unit_column<W>(a, token, u), old, status);
 }
 
 template <typename W, bool kAccumulate>
@@ -472,7 +441,7 @@ __device__ __forceinline__ void write_sum(const EmbeddingArgs& a, uint32_t token
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] += g[e];
   }
-  store8(weight_row<W>(a, token), static_cast<int>(a.cols), unit_column<W>(a, token, u), f, status, NSM_SITE_EMBEDDING);
+  store_unit(weight_row<W>(a, token), static_cast<int>(a.cols), unit_column<W>(a, token, u), f, status);
 }
 
 // A piece's two sums in the workspace, unit after unit, of tokens in more than two pieces: of the
@@ -502,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, !kAccumulate && sizeof(G) == 2 ? 4 :
   grid_dependency_sync();
   release_dependents();
   if (blockIdx.x >= sum_blocks) {
-    clear_rows<W>(a, last, p.clear_rows * p.passes + (blockIdx.x - sum_blocks) * kWarps * kClear, a.vocab, status);
+    clear_rows<W>(a, last, p.clear_first + (blockIdx.x - sum_blocks) * kWarps * kClear, p.clear_end, status);
     return;
   }
   const int lane = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = kThreads / lanes;
@@ -544,8 +513,7 @@ __global__ void __launch_bounds__(kThreads, !kAccumulate && sizeof(G) == 2 ? 4 :
     for (int i = 0; i < kAhead; ++i) {
       const uint2 pair = near[min(j + i, until - 1)];
       if (j + i >= until || pair.x >= none || !row_ok(pair.y < a.rows, status, NSM_SITE_EMBEDDING)) continue;
-      load8(static_cast<const G*>(a.rows_in) + int64_t(pair.y) * a.ld_rows, static_cast<int>(a.cols), unit_column<W>(a, pair.x, u),
-            raw[i], status, NSM_SITE_EMBEDDING);
+      load_unit(static_cast<const G*>(a.rows_in) + int64_t(pair.y) * a.ld_rows, static_cast<int>(a.cols), unit_column<W>(a, pair.x, u), raw[i], status);
       if (kAccumulate && near[j + i + 1].x != pair.x) load_old<W>(a, pair.x, u, old[i], status);
     }
 #pragma unroll
@@ -672,7 +640,7 @@ cudaError_t launch_sums(const EmbeddingArgs& a, const EmbeddingPlan& p, const ui
   const int groups = kThreads / cut.lanes;
   const int per_slice = (p.units + groups - 1) / groups;
   const int64_t sum_blocks = int64_t(per_slice) * cut.slices;
-  const int64_t left = kAccumulate ? 0 : std::max<int64_t>(a.vocab - p.clear_rows * p.passes, 0);
+  const int64_t left = kAccumulate ? 0 : std::max<int64_t>(p.clear_end - p.clear_first, 0);
   const int64_t clear = (left + kWarps * kClear - 1) / (kWarps * kClear);
   const size_t smem = size_t(groups * p.piece + 2 * (p.piece + 1)) * sizeof(uint2);
   if (sum_blocks + clear > 0) {
@@ -746,28 +714,43 @@ cudaError_t launch_embedding_backward(const EmbeddingArgs& a, void* workspace, i
   const uint2* sorted = nullptr;
   *launches = 0;
   int32_t* noted = a.accumulate ? nullptr : last;
-  if (a.rows > 0 && a.rows <= kBlockRows) {
-    static std::atomic<uint64_t> done{0};
-    cudaError_t e = set_smem_once(k_sort_block, kBlockSmem, done);
-    if (e == cudaSuccess) e = launch_pdl(k_sort_block, dim3(1), dim3(kBlockThreads), kBlockSmem, stream, a, p, pairs[0], noted, status);
-    if (e != cudaSuccess) return e;
+  // rows of the gradient whose writing takes about as long as one of the sort's kernels
+  const int64_t aside = a.accumulate ? 0 : std::min<int64_t>(kClearBytes / (a.cols * (a.weight_dtype == NSM_FP32 ? 4 : 2)) + 1, a.vocab);
+  p.clear_first = 0;
+  p.clear_end = a.vocab;
+  int key_bits = 1;
+  while (a.vocab >> key_bits) ++key_bits;
+  p.row_bits = std::min(32 - key_bits, 12);
+  static_assert(kBlockRows == 1 << 12, "row_bits");
+  cudaError_t e = cudaSuccess;
+  if (a.rows > 0 && a.rows <= int64_t(1) << p.row_bits) {
+    p.clear_end = a.vocab - aside;
+    const int clear = static_cast<int>(std::min<int64_t>((aside + kBlockThreads / 32 - 1) / (kBlockThreads / 32), kClearBlocks));
+    e = for_types(a.weight_dtype, NSM_FP32, [&](auto w, auto) {
+      static std::atomic<uint64_t> done{0};
+      const cudaError_t set = set_smem_once(k_sort_block<decltype(w)>, kBlockSmem, done);
+      if (set != cudaSuccess) return set;
+      return launch_pdl(k_sort_block<decltype(w)>, dim3(1 + clear), dim3(kBlockThreads), kBlockSmem, stream, a, p, pairs[0], noted, status);
+    });
     *launches = 1;
     sorted = pairs[0];
   } else if (a.rows > 0) {
-    cudaError_t e = launch_pdl(k_sort_count, dim3(p.tiles), dim3(kThreads), 0, stream, a, p, counts, noted, status);
-    if (!a.accumulate) p.clear_rows = std::max<int64_t>(kClearBytes / (a.cols * (a.weight_dtype == NSM_FP32 ? 4 : 2)), 1);
+    e = launch_pdl(k_sort_count, dim3(p.tiles), dim3(kThreads), 0, stream, a, p, counts, noted, status);
     for (int pass = 0; pass < p.passes && e == cudaSuccess; ++pass) {
-      const int64_t clear = std::min(std::max<int64_t>(a.vocab - p.clear_rows * pass, 0), p.clear_rows);
-      const dim3 grid(p.tiles + blocks((clear + kPlaceWarps * kClear - 1) / (kPlaceWarps * kClear) + 1) - 1);
+      p.clear_end = std::min(p.clear_first + aside, a.vocab);
+      const int64_t clear = p.clear_end - p.clear_first;
+      const dim3 grid(p.tiles + static_cast<int>((clear + kPlaceWarps * kClear - 1) / (kPlaceWarps * kClear)));
       e = for_types(a.weight_dtype, NSM_FP32, [&](auto w, auto) {
         return launch_pdl(k_sort_place<decltype(w)>, grid, dim3(kPlaceThreads), 0, stream, a, p, sorted, pass, counts, pairs[pass & 1],
                           static_cast<const int32_t*>(last), status);
       });
       sorted = pairs[pass & 1];
+      p.clear_first = p.clear_end;
     }
-    if (e != cudaSuccess) return e;
+    p.clear_end = a.vocab;
     *launches = 1 + p.passes;
   }
+  if (e != cudaSuccess) return e;
   return for_types(a.rows_dtype, a.weight_dtype, [&](auto g, auto w) {
     float* sums = reinterpret_cast<float*>(ws + p.off_sums);
     return a.accumulate ? launch_sums<decltype(g), decltype(w), true>(a, p, sorted, last, sums, launches, status, stream)

@@ -46,16 +46,29 @@ __device__ __forceinline__ const GradTensor& tensor_of(const Table<kMost>& table
   return table.t[low];
 }
 
-// Every element of a chunk once: whole vectors of eight (sixteen bytes of a 16-bit type, two
-// times sixteen of fp32) on the 16-byte grid, what lies beside them one by one.
+constexpr int kAhead = 4;  // vectors of eight under way per thread
+
+// Every element of a chunk once: whole vectors of eight on the 16-byte grid, several under way
+// together, and what lies beside them one by one.
 template <typename T, typename F8, typename F1>
 __device__ __forceinline__ void for_chunk(const T* p, int n, int* status, F8 eight, F1 one) {
-  const int head = min(static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) % 16 / sizeof(T)), n);
+  const int head = min((16 / static_cast<int>(sizeof(T)) - lead_of(p)) % (16 / static_cast<int>(sizeof(T))), n);
   const int vecs = (n - head) / 8;
-  for (int i = threadIdx.x; i < vecs; i += kThreads) eight(head + i * 8);
-  if (static_cast<int>(threadIdx.x) < head) one(static_cast<int>(threadIdx.x));
+  for (int i0 = threadIdx.x; i0 < vecs; i0 += kAhead * kThreads) {
+    Eight<T> r[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = head + (i0 + k * kThreads) * 8;
+      if (i0 + k * kThreads < vecs && bounds_ok(i >= 0 && i + 8 <= n && on_16_bytes(p + i), status, NSM_KERNEL_GRADS, 0, NSM_SITE_GRADS))
+        r[k].load_written(p + i);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (i0 + k * kThreads < vecs) eight(r[k]);
+  }
+  if (static_cast<int>(threadIdx.x) < head) one(p[threadIdx.x]);
   const int rest = head + vecs * 8 + threadIdx.x;
-  if (rest < n) one(rest);
+  if (rest < n) one(p[rest]);
 }
 
 __device__ __forceinline__ float block_sum(float v, float* shared) {
@@ -102,17 +115,14 @@ __device__ double chunk_sum(const T* p, int n, int* status) {
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for_chunk(
         p, n, status,
-        [&](int i) {
-          Eight<T> r;
-          if (!bounds_ok(i >= 0 && i + 8 <= n && on_16_bytes(p + i), status, NSM_KERNEL_GRADS, 0, NSM_SITE_GRADS)) return;
-          r.load_written(p + i);
+        [&](const Eight<T>& r) {
           float f[8];
           r.get(f);
 #pragma unroll
           for (int e = 0; e < 8; ++e) s[e] = fmaf(f[e] * scale, f[e] * scale, s[e]);
         },
-        [&](int i) {
-          const float f = Elem<T>::to_float(p[i]) * scale;
+        [&](T v) {
+          const float f = Elem<T>::to_float(v) * scale;
           s[0] = fmaf(f, f, s[0]);
         });
     return block_sum(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])), shared);
@@ -123,15 +133,13 @@ __device__ double chunk_sum(const T* p, int n, int* status) {
   const auto take = [&](float f) { most = f != f || most != most ? most + f : fmaxf(most, fabsf(f)); };
   for_chunk(
       p, n, status,
-      [&](int i) {
-        Eight<T> r;
-        r.load_written(p + i);
+      [&](const Eight<T>& r) {
         float f[8];
         r.get(f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) take(f[e]);
       },
-      [&](int i) { take(Elem<T>::to_float(p[i])); });
+      [&](T v) { take(Elem<T>::to_float(v)); });
   most = block_max(most, shared);
   if (!(most > 0.f) || most > kFltMax) return most;  // nothing but zeros; an infinity or NaN
   // the largest element to [1, 2) (a subnormal one no further than fp32's exponents reach)
@@ -188,36 +196,38 @@ __global__ void __launch_bounds__(kThreads) k_grad_total(const double* sums, int
   if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(sum));
 }
 
+// A chunk's elements, in units of eight on the 16-byte grid of where they go.  Around it the tensor
+// goes on for `before` and `after` elements.
 template <typename T, typename O>
-__device__ void scale_chunk(const T* p, O* out, int n, float factor, float more, int* status) {
-  for_chunk(
-      p, n, status,
-      [&](int i) {
-        if (!bounds_ok(i >= 0 && i + 8 <= n && on_16_bytes(p + i), status, NSM_KERNEL_GRADS, 0, NSM_SITE_GRADS)) return;
-        Eight<T> r;
-        r.load_written(p + i);
-        float f[8];
-        r.get(f);
+__device__ void scale_chunk(const T* p, O* out, int n, int before, int after, float factor, float more, int* status) {
+  const int lead = lead_of(out), units = (n + lead + 7) / 8;
+  for (int u0 = threadIdx.x; u0 < units; u0 += kAhead * kThreads) {
+    Eight<T> r[kAhead];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = f[e] * factor * more;
-        if (on_16_bytes(out + i)) {
-          Eight<O> w;
-          w.set(f);
-          w.store(out + i);
-        } else {
+    for (int k = 0; k < kAhead; ++k) {
+      const int u = u0 + k * kThreads;
+      if (u < units) load8(p, -before, n + after, u * 8 - lead, r[k], status, NSM_KERNEL_GRADS, NSM_SITE_GRADS);
+    }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) out[i + e] = Elem<O>::from_float(f[e]);
-        }
-      },
-      [&](int i) { out[i] = Elem<O>::from_float(Elem<T>::to_float(p[i]) * factor * more); });
+    for (int k = 0; k < kAhead; ++k) {
+      const int u = u0 + k * kThreads;
+      if (u >= units) break;
+      float f[8];
+      r[k].get(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = f[e] * factor * more;
+      store8(out, 0, n, u * 8 - lead, f, status, NSM_KERNEL_GRADS, NSM_SITE_GRADS);
+    }
+  }
 }
 
 template <typename T>
-__device__ __forceinline__ void scale_chunk_to(const T* p, const GradTensor& t, int64_t first, int n, float factor, float more,
-                                               int* status) {
-  if (t.out_dtype == NSM_BF16) scale_chunk(p, static_cast<__nv_bfloat16*>(t.out) + first, n, factor, more, status);
-  else if (t.out_dtype == NSM_FP16) scale_chunk(p, static_cast<__half*>(t.out) + first, n, factor, more, status);
-  else scale_chunk(p, static_cast<float*>(t.out) + first, n, factor, more, status);
+__device__ __forceinline__ void scale_chunk_to(const GradTensor& t, int64_t first, int n, float factor, float more, int* status) {
+  const T* p = static_cast<const T*>(t.in) + first;
+  const int before = static_cast<int>(min(first, int64_t(8))), after = static_cast<int>(min(t.numel - first - n, int64_t(8)));
+  if (t.out_dtype == NSM_BF16) scale_chunk(p, static_cast<__nv_bfloat16*>(t.out) + first, n, before, after, factor, more, status);
+  else if (t.out_dtype == NSM_FP16) scale_chunk(p, static_cast<__half*>(t.out) + first, n, before, after, factor, more, status);
+  else scale_chunk(p, static_cast<float*>(t.out) + first, n, before, after, factor, more, status);
 }
 
 template <int kMost>
@@ -240,9 +250,9 @@ __global__ void __launch_bounds__(kThreads)
     const GradTensor& t = tensor_of(table, c);
     const int64_t first = int64_t(c - t.chunk_begin) * kGradChunk;
     const int n = static_cast<int>(min(t.numel - first, int64_t(kGradChunk)));
-    if (t.in_dtype == NSM_BF16) scale_chunk_to(static_cast<const __nv_bfloat16*>(t.in) + first, t, first, n, first_factor, more, status);
-    else if (t.in_dtype == NSM_FP16) scale_chunk_to(static_cast<const __half*>(t.in) + first, t, first, n, first_factor, more, status);
-    else scale_chunk_to(static_cast<const float*>(t.in) + first, t, first, n, first_factor, more, status);
+    if (t.in_dtype == NSM_BF16) scale_chunk_to<__nv_bfloat16>(t, first, n, first_factor, more, status);
+    else if (t.in_dtype == NSM_FP16) scale_chunk_to<__half>(t, first, n, first_factor, more, status);
+    else scale_chunk_to<float>(t, first, n, first_factor, more, status);
   }
 }
 

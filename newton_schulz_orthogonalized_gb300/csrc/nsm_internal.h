@@ -298,7 +298,10 @@ struct EmbeddingPlan {
   int32_t tiles, tile;       // blocks of a pass, and their entries
   int32_t piece, units;      // sorted entries that a group of lanes adds up, and how many such pieces
   int64_t cols;              // of a piece's sums: columns with room for any alignment
-  int64_t clear_rows;        // of the gradient, that a sorting pass clears on the side (set by the call)
+  // set by the call: rows of the gradient that a launch clears, and the bits of a row's number
+  // beside its token's
+  int64_t clear_first, clear_end;
+  int32_t row_bits;
   size_t off_pairs[2], off_counts, off_last, off_sums, bytes;
 };
 EmbeddingPlan embedding_plan(int64_t rows, int64_t vocab, int64_t cols);

@@ -1368,7 +1368,39 @@ int check_grad_sizes(const int64_t* numels, int n, int64_t* chunks) {
   return NSM_OK;
 }
 
-size_t grad_bytes(int64_t chunks, int n) { return align_up(size_t(chunks) * 8, 256) + align_up(size_t(n) * 8, 256); }
+// One launch's tensors: chunks, and where its sums lie in the workspace (numbers of 64 bits).
+struct GradPart {
+  int first, n, chunks;
+  int64_t totals, parts;
+};
+
+// Calls f with each launch's part; n_totals: the blocks' sums of all of them, which come first.
+// Returns how many numbers the workspace holds (one more than those for the sum of many launches').
+template <typename F>
+int64_t grad_parts(const int64_t* numels, int n, int64_t* n_totals, F f) {
+  int64_t totals = 0, parts = 0;
+  for (int pass = 0; pass < 2; ++pass) {  // the sums' number sets where the parts begin
+    int64_t t = 0, p = totals + 1;
+    for (int first = 0; first < n; first += kGradTable) {
+      const int m = std::min(n - first, kGradTable);
+      int64_t chunks = 0;
+      for (int i = first; i < first + m; ++i) chunks += (numels[i] + kGradChunk - 1) / kGradChunk;
+      const int blocks = grad_blocks(static_cast<int>(chunks));
+      if (pass == 1) f(GradPart{first, m, static_cast<int>(chunks), t, p});
+      t += blocks;
+      p += blocks + m;
+    }
+    totals = t;
+    parts = p;
+  }
+  *n_totals = totals;
+  return parts;
+}
+
+size_t grad_bytes(const int64_t* numels, int n) {
+  int64_t n_totals = 0;
+  return align_up(size_t(grad_parts(numels, n, &n_totals, [](const GradPart&) {})) * 8, 256);
+}
 
 struct Span {
   uintptr_t from, to;
@@ -1425,66 +1457,70 @@ int run_grads(const void* const* grads, const int64_t* numels, const int32_t* dt
     if (clip && !same) add(t.out, size_t(numels[i]) * out_size, true);
     bytes += double(numels[i]) * double(clip ? 2 * in_size + out_size : in_size);
   }
-  if ((rc = check_workspace(workspace, workspace_bytes, grad_bytes(chunks, n))) != NSM_OK) return rc;
+  if ((rc = check_workspace(workspace, workspace_bytes, grad_bytes(numels, n))) != NSM_OK) return rc;
   if ((rc = check_numbers("norm", norm, 4)) != NSM_OK) return rc;
   if ((rc = check_numbers("norms", norms, 4)) != NSM_OK) return rc;
   add(workspace, workspace_bytes, true);
   add(norm, 4, true);
   add(norms, size_t(n) * 4, true);
   if ((rc = check_spans(spans.get(), count)) != NSM_OK) return rc;
-  int num_sms = 0;
-  if ((rc = current_sms(&num_sms)) != NSM_OK) return rc;
 
-  double* partials = static_cast<double*>(workspace);
-  double* sums = reinterpret_cast<double*>(static_cast<char*>(workspace) + align_up(size_t(chunks) * 8, 256));
+  double* sums = static_cast<double*>(workspace);
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  const PdlScope pdl(0);  // several kernels of which all but the largest tables' are short
+  const PdlScope pdl(0);  // a pass over the gradients and what follows it: their launches overlap
   int launches = 0;
   cudaError_t e = cudaSuccess;
-  // the tensors of one launch from first on, their chunks counted from 0
-  const auto part = [&](int first, int* total) {
-    const int m = std::min(n - first, kGradTable);
-    int64_t all = 0;
-    for (int i = first; i < first + m; ++i) {
-      tensors[i].chunk_begin = static_cast<int32_t>(all);
-      all += (numels[i] + kGradChunk - 1) / kGradChunk;
+  int64_t n_totals = 0;
+  const auto prefix = [&](const GradPart& part) {  // the chunks of a launch's tensors, from 0
+    int64_t at = 0;
+    for (int i = part.first; i < part.first + part.n; ++i) {
+      tensors[i].chunk_begin = static_cast<int32_t>(at);
+      at += (numels[i] + kGradChunk - 1) / kGradChunk;
     }
-    *total = static_cast<int>(all);
-    return m;
   };
-  {
-    TimedLaunch t(stream, NSM_KIND_GRADS, bytes);
-    int64_t done = 0;
-    for (int first = 0; first < n && e == cudaSuccess; first += kGradTable) {
-      int total = 0;
-      const int m = part(first, &total);
-      if (total > 0) {
-        e = launch_grad_chunks(&tensors[first], m, total, partials + done, stream);
-        ++launches;
+  const auto all_in_place = [&](const GradPart& part) {
+    for (int i = part.first; i < part.first + part.n; ++i)
+      if (numels[i] > 0 && (tensors[i].out != tensors[i].in || tensors[i].out_dtype != tensors[i].in_dtype)) return false;
+    return true;
+  };
+  if (chunks <= kGradSmall && n <= kGradTable) {
+    const GradPart all{0, n, static_cast<int>(chunks), 0, 0};
+    TimedLaunch timed(stream, NSM_KIND_GRADS, bytes);
+    prefix(all);
+    e = launch_grad_small(&tensors[0], n, all.chunks, clip, max_norm, norm, norms, all_in_place(all), stream);
+    launches = 1;
+  } else {
+    TimedLaunch timed(stream, NSM_KIND_GRADS, bytes);
+    grad_parts(numels, n, &n_totals, [&](const GradPart& part) {
+      prefix(part);
+      if (part.chunks == 0 || e != cudaSuccess) return;
+      e = launch_grad_squares(&tensors[part.first], part.n, part.chunks, sums + part.totals, sums + part.parts, stream);
+      launches += 2;
+    });
+    const double* totals = sums;
+    if (n_totals > kGradTotals && e == cudaSuccess) {
+      e = launch_grad_total(sums, static_cast<int>(n_totals), sums + n_totals, stream);
+      ++launches;
+      totals = sums + n_totals;
+      n_totals = 1;
+    }
+    const int count_totals = static_cast<int>(n_totals);
+    float* norm_left = norm;
+    int64_t unused = 0;
+    grad_parts(numels, n, &unused, [&](const GradPart& part) {
+      if (e != cudaSuccess) return;
+      const GradTensor* t = &tensors[part.first];
+      float* own = norms ? norms + part.first : nullptr;
+      if (clip && part.chunks > 0) {
+        e = launch_grad_clip(t, part.n, part.chunks, sums + part.parts, own, totals, count_totals, max_norm, norm_left, all_in_place(part), stream);
+      } else if (own || norm_left) {
+        e = launch_grad_norms(t, part.n, part.chunks, sums + part.parts, own, totals, count_totals, norm_left, stream);
+      } else {
+        return;
       }
-      if (e == cudaSuccess) e = launch_grad_sums(&tensors[first], m, total, partials + done, sums + first, norms ? norms + first : nullptr, stream);
+      norm_left = nullptr;
       ++launches;
-      done += total;
-    }
-    if (!clip) {
-      if (e == cudaSuccess) e = launch_grad_total(sums, n, norm, stream);
-      ++launches;
-    }
-    bool said = false;
-    for (int first = 0; clip && first < n && e == cudaSuccess; first += kGradTable) {
-      int total = 0;
-      const int m = part(first, &total);
-      if (total == 0) continue;
-      bool in_place = true;
-      for (int i = first; i < first + m; ++i) in_place &= numels[i] == 0 || (tensors[i].out == tensors[i].in && tensors[i].out_dtype == tensors[i].in_dtype);
-      e = launch_grad_clip(&tensors[first], m, total, sums, n, max_norm, said ? nullptr : norm, in_place, num_sms, stream);
-      said = true;
-      ++launches;
-    }
-    if (clip && !said && norm && e == cudaSuccess) {  // nothing but empty tensors
-      e = launch_grad_total(sums, n, norm, stream);
-      ++launches;
-    }
+    });
   }
   if (e != cudaSuccess) return fail_cuda(e, "launch of the gradients' norm");
   t_last_launches = launches;
@@ -2378,7 +2414,7 @@ int nsm_embedding_backward(const void* d_out, int dtype, int64_t rows, int64_t c
 size_t nsm_grad_workspace_bytes(const int64_t* numels, int n) {
   int64_t chunks = 0;
   if (check_grad_sizes(numels, n, &chunks) != NSM_OK) return 0;
-  return grad_bytes(chunks, n);
+  return grad_bytes(numels, n);
 }
 
 int nsm_grad_norm(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int n, float* norm, float* norms,

@@ -310,6 +310,9 @@ EmbeddingPlan embedding_plan(int64_t rows, int64_t vocab, int64_t cols);
 
 constexpr int kGradChunk = 16384;  // elements that one block sums at a time
 constexpr int kGradTable = 512;    // tensors of one launch at most
+constexpr int kGradBlocks = 152 * 4;  // blocks of one launch at most
+constexpr int kGradSmall = 32;     // chunks of a table that one cluster takes
+constexpr int kGradTotals = 8192;  // blocks' sums that every clipping block adds for itself, at most
 
 struct GradTensor {
   const void* in;
@@ -376,17 +379,22 @@ cudaError_t launch_adjust(const AdjustArgs& args, cudaStream_t stream);
 cudaError_t launch_embedding(const EmbeddingArgs& args, cudaStream_t stream);
 // *launches: how many kernels it took
 cudaError_t launch_embedding_backward(const EmbeddingArgs& args, void* workspace, int* launches, cudaStream_t stream);
-// Sums of squares of `n` tensors (of one launch: n <= kGradTable), one per chunk from partials[0]
-cudaError_t launch_grad_chunks(const GradTensor* tensors, int n, int total_chunks, double* partials, cudaStream_t stream);
-// Their sums: sums[i] per tensor, and its root to norms[i] where norms is not NULL
-cudaError_t launch_grad_sums(const GradTensor* tensors, int n, int total_chunks, const double* partials, double* sums,
-                             float* norms, cudaStream_t stream);
-// *norm = sqrt(sum of sums[0 ... n - 1])
-cudaError_t launch_grad_total(const double* sums, int n, float* norm, cudaStream_t stream);
-// out = in min(1, max_norm / norm) for the tensors of one launch, the norm from all_sums[0 ... all_n - 1],
-// written to *norm where that is not NULL
-cudaError_t launch_grad_clip(const GradTensor* tensors, int n, int total_chunks, const double* all_sums, int all_n,
-                             float max_norm, float* norm, int in_place, int num_sms, cudaStream_t stream);
+// Blocks that a launch of so many chunks has.
+int grad_blocks(int chunks);
+// Sums of squares of the `n` <= kGradTable tensors of one launch: totals, one per block, and parts, the
+// blocks' of each tensor (grad_blocks + n)
+cudaError_t launch_grad_squares(const GradTensor* tensors, int n, int chunks, double* totals, double* parts, cudaStream_t stream);
+// Roots of the tensors' sums to norms, and of that of all n_totals to *norm (each may be NULL)
+cudaError_t launch_grad_norms(const GradTensor* tensors, int n, int chunks, const double* parts, float* norms, const double* totals,
+                              int n_totals, float* norm, cudaStream_t stream);
+cudaError_t launch_grad_total(const double* totals, int n, double* total, cudaStream_t stream);
+// launch_grad_norms, and out = in min(1, max_norm / norm) for the tensors of one launch
+cudaError_t launch_grad_clip(const GradTensor* tensors, int n, int chunks, const double* parts, float* norms, const double* totals,
+                             int n_totals, float max_norm, float* norm, int in_place, cudaStream_t stream);
+
+// All of it for n <= kGradTable tensors of at most kGradSmall chunks (clip == 0: the norms alone)
+cudaError_t launch_grad_small(const GradTensor* tensors, int n, int chunks, int clip, float max_norm, float* norm, float* norms,
+                              int in_place, cudaStream_t stream);
 
 int* device_status_ptr();
 // One CTA whose bounded wait expires after limit_ns and records kDevTimeout.

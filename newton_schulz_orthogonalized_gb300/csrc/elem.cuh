@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "nsm_internal.h"
 
 namespace nsm {
@@ -169,6 +171,30 @@ struct Eight {
 };
 
 __device__ __forceinline__ bool on_16_bytes(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+struct Bytes32 {
+  uint4 low, high;
+};
+
+// kPer elements side by side: 8, 16 or 32 bytes.
+template <typename T, int kPer>
+struct Side {
+  static constexpr int kBytes = kPer * sizeof(T);
+  using Word = typename std::conditional<kBytes == 32, Bytes32, typename std::conditional<kBytes == 16, uint4, uint2>::type>::type;
+  Word w;
+  __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const Word*>(p); }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Word*>(p) = w; }
+  __device__ __forceinline__ void get(float (&f)[kPer]) const {
+    const T* e = reinterpret_cast<const T*>(&w);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) f[i] = Elem<T>::to_float(e[i]);
+  }
+  __device__ __forceinline__ void set(const float (&f)[kPer]) {
+    T* e = reinterpret_cast<T*>(&w);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) e[i] = Elem<T>::from_float(f[i]);
+  }
+};
 
 // How many elements past a 16-byte boundary.
 template <typename T>

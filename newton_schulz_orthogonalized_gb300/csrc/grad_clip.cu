@@ -339,26 +339,6 @@ __global__ void __launch_bounds__(32) k_grad_total(const double* totals, int n, 
 
 constexpr int kBatch = 1;  // vectors under way per thread
 
-// kPer elements side by side: 8 or 16 bytes.
-template <typename T, int kPer>
-struct Part {
-  static constexpr int kBytes = kPer * sizeof(T);
-  using Word = typename std::conditional<kBytes == 16, uint4, uint2>::type;
-  Word w;
-  __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const Word*>(p); }
-  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Word*>(p) = w; }
-  __device__ __forceinline__ void get(float (&f)[kPer]) const {
-    const T* e = reinterpret_cast<const T*>(&w);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) f[i] = Elem<T>::to_float(e[i]);
-  }
-  __device__ __forceinline__ void set(const float (&f)[kPer]) {
-    T* e = reinterpret_cast<T*>(&w);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) e[i] = Elem<T>::from_float(f[i]);
-  }
-};
-
 // A chunk's elements, in units of eight on the 16-byte grid of where they go.  Around it the tensor
 // goes on for `before` and `after` elements.
 template <int NT, typename T, typename O>
@@ -388,7 +368,7 @@ __device__ __noinline__ void scale_chunk(const T* p, O* out, int n, int before, 
   const int from = low * 8 - lead, count = (high - low) * (8 / kPer);
 #pragma unroll 1
   for (int v0 = threadIdx.x; v0 < count; v0 += kBatch * NT) {
-    Part<T, kPer> r[kBatch];
+    Side<T, kPer> r[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int v = v0 + k * NT;
@@ -403,7 +383,7 @@ __device__ __noinline__ void scale_chunk(const T* p, O* out, int n, int before, 
         r[k].get(f);
 #pragma unroll
         for (int e = 0; e < kPer; ++e) f[e] = f[e] * factor * more;
-        Part<O, kPer> w;
+        Side<O, kPer> w;
         w.set(f);
         w.store(out + from + v * kPer);
       }

@@ -11,7 +11,11 @@
 // slice as it was read, with the mask applied, and then settles the tokens that a penalty or a
 // bias is for, one thread each.  Rows that share a history, as the positions of one sequence
 // do, follow one another in a block, which counts only the tokens that a row has more.  The next
-// slice's logits are asked for before a slice is settled.
+// slice's logits are asked for before a slice is settled, and which history it has a row earlier.
+//
+// Without penalties bound by memory (8192 x 50257 bf16 256 us, 6.4 TB/s read and written); with them by
+// the two barriers of a slice and the accesses to single tokens between them: 281 us with a sequence's
+// growing history of 1024 tokens, 256 x 131072 to fp32 with 4096 tokens and masks 55 us.
 #include "elem.cuh"
 #include "launch.cuh"
 #include "nsm_internal.h"
@@ -25,57 +29,65 @@ namespace {
 constexpr int kThreads = 128;
 constexpr uint32_t kHasBias = 0x80000000u;       // in a count: some bias is for this token
 
+__device__ __forceinline__ bool on_bytes(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
 __device__ __forceinline__ int64_t index_at(const void* p, int wide, int64_t i) {
   return wide ? static_cast<const int64_t*>(p)[i] : static_cast<const int32_t*>(p)[i];
 }
 
-// The eight bits of a row's mask from element e0 on (bit set: allowed); all eight exist.
+// The bits of a row's mask for the unit of kE elements from e0 on (bit set: allowed); all of them exist.
+template <int kE>
 __device__ __forceinline__ uint32_t mask_bits(const int32_t* words, int nwords, int e0, int* status) {
   const int w = e0 >> 5, bit = e0 & 31;
-  if (!bounds_ok(w >= 0 && (e0 + 7) >> 5 < nwords, status, NSM_KERNEL_ADJUST, 0, NSM_SITE_SIDE)) return 0;
+  if (!bounds_ok(w >= 0 && (e0 + kE - 1) >> 5 < nwords, status, NSM_KERNEL_ADJUST, 0, NSM_SITE_SIDE)) return 0;
   const uint32_t low = static_cast<uint32_t>(__ldg(words + w));
-  return __funnelshift_r(low, bit > 24 ? static_cast<uint32_t>(__ldg(words + w + 1)) : 0u, bit) & 0xffu;
+  return __funnelshift_r(low, bit > 32 - kE ? static_cast<uint32_t>(__ldg(words + w + 1)) : 0u, bit) & ((1u << kE) - 1);
 }
 
-// A vector with -inf (0 in the backward pass) where a bit of `allowed` is clear.
-template <typename T, bool kBackward>
-__device__ __forceinline__ void ban(Eight<T>& r, uint32_t allowed) {
+// A unit with -inf (0 in the backward pass) where a bit of `allowed` is clear.
+template <typename T, int kE, bool kBackward>
+__device__ __forceinline__ void ban(Side<T, kE>& r, uint32_t allowed) {
   constexpr uint32_t kGone = kBackward ? 0u : Elem<T>::kNegInfBits;
-  uint32_t* w = reinterpret_cast<uint32_t*>(r.w);
+  uint32_t* w = reinterpret_cast<uint32_t*>(&r.w);
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < kE; ++e)
       if (!(allowed >> e & 1)) w[e] = kGone;
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kE / 2; ++i) {
       const uint32_t keep = (allowed >> (2 * i) & 1) * 0xffffu | (allowed >> (2 * i + 1) & 1) * 0xffff0000u;
       w[i] = (w[i] & keep) | (~keep & (kGone * 0x10001u));
     }
   }
 }
 
-template <typename A, typename B>
-__device__ __forceinline__ void convert(const Eight<A>& from, Eight<B>& to) {
+template <typename A, typename B, int kE>
+__device__ __forceinline__ void convert(const Side<A, kE>& from, Side<B, kE>& to) {
   if constexpr (std::is_same<A, B>::value) {
-#pragma unroll
-    for (int i = 0; i < Eight<A>::kWords; ++i) to.w[i] = from.w[i];
+    to.w = from.w;
   } else {
-    float f[8];
+    float f[kE];
     from.get(f);
     to.set(f);
   }
 }
 
-// Units of eight logits per thread, and logits of a block: 16 KB in either size of type.
+// Logits of a unit: 16 bytes of what is read, so that a warp's loads lie side by side (fp32 in units of
+// eight, 32 bytes apart: 2049 x 65537 copied in 212 us for 177).  Units per thread, and logits of a
+// block: 8 KB.
 template <typename A>
-constexpr int kUnitsOf = sizeof(A) == 4 ? 2 : 4;
+constexpr int kUnitOf = 16 / sizeof(A);
 template <typename A>
-constexpr int kSliceOf = kThreads * kUnitsOf<A> * 8;
-// Resident blocks of an SM: as many as their registers and shared memory let in.
-constexpr int kBlocks = 8;
+constexpr int kSliceOf = kThreads * (sizeof(A) == 4 ? 16 : 32);
+// Resident blocks of an SM.  8192 x 50257 bf16 with histories takes 281 us with 7, 341 with 8 (whose 64
+// registers a thread are too few) and 295 with 6; 2049 x 65537 fp32 203 with 8, 380 with 9, 214 with 7.
+template <typename A>
+constexpr int kBlocks = sizeof(A) == 4 ? 8 : 7;
 
-constexpr int kRun = 16;  // rows at most whose slices a block takes after one another
+// Rows at most whose slices a block takes after one another: the two cases above take 302 and 227 us with
+// 16, 281 and 203 with 4, 288 and 203 with 2.
+constexpr int kRun = 4;
 
 // Calls f with every token of a row's history, in no order.
 template <typename I, typename F>
@@ -102,8 +114,11 @@ __device__ __forceinline__ void for_history(const I* p, int tokens, F f) {
 
 // A: type of what is read, B: of what is written.
 template <typename A, typename B, bool kBackward>
-__global__ void __launch_bounds__(kThreads, kBlocks) k_adjust(const AdjustArgs a, int slices, int run, int* status) {
-  constexpr int kUnits = kUnitsOf<A>, kSlice = kSliceOf<A>, kPlaces = kSlice + 8;
+__global__ void __launch_bounds__(kThreads, kBlocks<A>) k_adjust(const AdjustArgs a, int slices, int run, int* status) {
+  constexpr int kE = kUnitOf<A>, kSlice = kSliceOf<A>, kUnits = kSlice / kThreads / kE, kPlaces = kSlice + 8;
+  constexpr uint32_t kAll = (1u << kE) - 1;
+  constexpr size_t kStore = kE * sizeof(B) < 16 ? kE * sizeof(B) : 16;  // what a unit's stores are aligned to
+  static_assert(kUnits * kE <= 32, "a bit per element");
   extern __shared__ __align__(16) uint32_t shared[];
   uint32_t* count = shared;                                              // kPlaces
   uint16_t* list = reinterpret_cast<uint16_t*>(shared + kPlaces);        // kPlaces: those with a count
@@ -120,70 +135,79 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_adjust(const AdjustArgs a
   grid_dependency_sync();
   release_dependents();
   const int nwords = (vocab + 31) / 32;
+  const uint32_t rows = static_cast<uint32_t>(a.rows);
   // A block takes one slice of `run` rows after one another, then of other rows.
   const int run_step = gridDim.x / slices, slice_step = gridDim.x % slices;
 
-  // One slice of a row: units of eight on the 16-byte grid of what is read, unit u from element
-  // v0 + 8 u on.  v0 may lie before the row, by less than a vector.
+  // One slice of a row: units on the grid that their loads want, unit u from element v0 + kE u on.  v0 may lie before the row, by less than a vector.
   struct Place {
-    int64_t row, line;
-    int slice, v0, tokens;
+    uint32_t row;
+    int line, slice, v0, tokens;
     const A* in;
     const int32_t* mask;
   };
   const auto place = [&](Place& p) {
-    p.in = static_cast<const A*>(a.in) + p.row * a.ld_in;
-    p.v0 = p.slice * kSlice - static_cast<int>((reinterpret_cast<uintptr_t>(p.in) & 15) / sizeof(A));
+    p.in = static_cast<const A*>(a.in) + int64_t(p.row) * a.ld_in;
+    p.v0 = p.slice * kSlice - static_cast<int>((reinterpret_cast<uintptr_t>(p.in) & (kE * sizeof(A) - 1)) / sizeof(A));
     p.mask = nullptr;
     if (a.mask) {
-      const int64_t m = a.mask_row ? a.mask_row[p.row] : p.row;
+      const int m = a.mask_row ? a.mask_row[p.row] : static_cast<int>(p.row);
       if (m >= 0 && m < a.mask_rows) p.mask = a.mask + m * a.ldm;
     }
-    p.tokens = 0;
-    p.line = -1;
-    if (a.history) {
-      p.line = a.history_row ? a.history_row[p.row] : p.row;
-      const int most = static_cast<int>(a.history_len);
-      if (p.line >= 0 && p.line < a.history_rows) p.tokens = a.length ? min(max(a.length[p.row], 0), most) : most;
+  };
+  // Which history a row has, as the tables hold it: asked for a row ahead, looked at when its turn comes.
+  struct Held {
+    int line, length;
+  };
+  const auto look = [&](uint32_t row) {
+    Held h{0, 0};
+    if (a.history && row < rows) {
+      h.line = a.history_row ? a.history_row[row] : static_cast<int>(row);
+      h.length = a.length ? a.length[row] : static_cast<int>(a.history_len);
     }
+    return h;
+  };
+  const auto take = [&](Place& p, const Held& h) {
+    p.line = h.line;
+    p.tokens = h.line >= 0 && h.line < a.history_rows ? min(max(h.length, 0), static_cast<int>(a.history_len)) : 0;
   };
   // Most slices lie inside their row with all their units.
   const auto inside = [&](int v0) { return v0 >= 0 && v0 + kSlice <= vocab; };
-  const auto whole = [&](int e0) { return e0 >= 0 && e0 + 8 <= vocab; };
-  uint32_t allowed = 0;  // with a mask, a byte per unit: the elements that it allows
-  Eight<A> raw[kUnits];
+  const auto whole = [&](int e0) { return e0 >= 0 && e0 + kE <= vocab; };
+  uint32_t allowed = 0;  // with a mask, kE bits per unit: the elements that it allows
+  Side<A, kE> raw[kUnits];
   // What a row has before its first whole unit and behind its last one: threads 0 to 7 and 8 to
   // 15 of the block that has them take an element each.
   A edge = Elem<A>::from_float(0.f);
   const auto edge_at = [&](int v0) {  // -1: none
     if (tid >= 16) return -1;
-    const int tail = v0 + (vocab - v0) / 8 * 8;
+    const int tail = v0 + (vocab - v0) / kE * kE;
     const int e = tid < 8 ? v0 + tid : tail + tid - 8;
-    const bool mine = tid < 8 ? v0 < 0 : tail < v0 + kSlice && !(v0 < 0 && tail == v0);
+    const bool mine = (tid & 7) < kE && (tid < 8 ? v0 < 0 : tail < v0 + kSlice && !(v0 < 0 && tail == v0));
     return mine && e >= 0 && e < vocab ? e : -1;
   };
   const auto load = [&](const A* from, int i) {
-    if (bounds_ok(on_16_bytes(from + i * kThreads * 8), status, NSM_KERNEL_ADJUST, 0, NSM_SITE_LOGITS)) raw[i].load_written(from + i * kThreads * 8);
+    if (bounds_ok(on_bytes(from + i * kThreads * kE, kE * sizeof(A)), status, NSM_KERNEL_ADJUST, 0, NSM_SITE_LOGITS)) raw[i].load(from + i * kThreads * kE);
   };
   const auto fetch_units = [&](const Place& p, auto all) {
-    const int first = p.v0 + tid * 8;
+    const int first = p.v0 + tid * kE;
     const A* from = p.in + first;
     if (!p.mask) {
 #pragma unroll
       for (int i = 0; i < kUnits; ++i)
-        if (decltype(all)::value || whole(first + i * kThreads * 8)) load(from, i);
+        if (decltype(all)::value || whole(first + i * kThreads * kE)) load(from, i);
       return;
     }
     allowed = 0;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int e0 = first + i * kThreads * 8;
-      if (decltype(all)::value || whole(e0)) allowed |= mask_bits(p.mask, nwords, e0, status) << (8 * i);
+      const int e0 = first + i * kThreads * kE;
+      if (decltype(all)::value || whole(e0)) allowed |= mask_bits<kE>(p.mask, nwords, e0, status) << (kE * i);
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const uint32_t may = allowed >> (8 * i) & 0xffu;
-      if (may && !(a.in_place && may == 0xffu)) load(from, i);
+      const uint32_t may = allowed >> (kE * i) & kAll;
+      if (may && !(a.in_place && may == kAll)) load(from, i);
     }
   };
   const auto fetch = [&](const Place& p) {
@@ -201,12 +225,26 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_adjust(const AdjustArgs a
   };
 
   Place now{};
-  int64_t first = int64_t(blockIdx.x / slices) * run;  // of the rows that it takes after one another
+  uint32_t first = blockIdx.x / slices * run;  // of the rows that it takes after one another
   now.row = first;
   now.slice = blockIdx.x % slices;
-  if (now.row >= a.rows) return;
+  if (now.row >= rows) return;
   place(now);
   fetch(now);
+  take(now, look(now.row));
+  // the row and slice after one
+  const auto advance = [&](uint32_t& row, int& slice, uint32_t& of_run) {
+    if (++row >= min(of_run + run, rows)) {
+      const int carry = slice + slice_step >= slices;
+      of_run += (run_step + carry) * run;
+      row = of_run;
+      slice += slice_step - (carry ? slices : 0);
+    }
+  };
+  uint32_t next_row = now.row;
+  int next_slice = now.slice;
+  advance(next_row, next_slice, first);
+  Held next_held = look(next_row);
   int parity = 0, held = 0;  // tokens of this row's history that are counted already
   for (;;) {
     // counts are kept of all tokens that may be in this slice of some row, whatever its v0
@@ -217,34 +255,34 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_adjust(const AdjustArgs a
         if (static_cast<uint64_t>(v - low) >= static_cast<uint64_t>(span)) return;
         if (atomicAdd(&count[v - base], 1u) == 0) list[atomicAdd(&listed[parity], 1)] = static_cast<uint16_t>(v - base);
       };
-      if (a.history_wide) for_history(static_cast<const int64_t*>(a.history) + now.line * a.ldh + held, now.tokens - held, bump);
-      else for_history(static_cast<const int32_t*>(a.history) + now.line * a.ldh + held, now.tokens - held, bump);
+      if (a.history_wide) for_history(static_cast<const int64_t*>(a.history) + int64_t(now.line) * a.ldh + held, now.tokens - held, bump);
+      else for_history(static_cast<const int32_t*>(a.history) + int64_t(now.line) * a.ldh + held, now.tokens - held, bump);
     }
     for (int j = tid; j < a.k; j += kThreads) {
-      const int64_t v = index_at(a.bias_index, a.bias_wide, now.row * a.ldbi + j);
+      const int64_t v = index_at(a.bias_index, a.bias_wide, int64_t(now.row) * a.ldbi + j);
       const bool here = span > 0 && static_cast<uint64_t>(v - low) < static_cast<uint64_t>(span);
       bias_index[j] = here ? static_cast<int32_t>(v) : -1;
-      bias[j] = a.bias[now.row * a.ldb + j];
+      bias[j] = a.bias[int64_t(now.row) * a.ldb + j];
       if (here && atomicOr(&count[v - base], kHasBias) == 0) list[atomicAdd(&listed[parity], 1)] = static_cast<uint16_t>(v - base);
     }
 
-    B* out = static_cast<B*>(a.out) + now.row * a.ld_out;
-    const bool aligned_out = on_16_bytes(out + v0);
+    B* out = static_cast<B*>(a.out) + int64_t(now.row) * a.ld_out;
+    const bool aligned_out = on_bytes(out + v0, kStore);
     const auto store_units = [&](auto all) {
-      const int first_unit = v0 + tid * 8;
+      const int first_unit = v0 + tid * kE;
       B* to = out + first_unit;
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
-        const uint32_t may = now.mask ? allowed >> (8 * i) & 0xffu : 0xffu;
-        if (!(decltype(all)::value || whole(first_unit + i * kThreads * 8)) || (a.in_place && may == 0xffu)) continue;
-        Eight<B> r;
+        const uint32_t may = now.mask ? allowed >> (kE * i) & kAll : kAll;
+        if (!(decltype(all)::value || whole(first_unit + i * kThreads * kE)) || (a.in_place && may == kAll)) continue;
+        Side<B, kE> r;
         convert(raw[i], r);
-        if (may != 0xffu) ban<B, kBackward>(r, may);
+        if (may != kAll) ban<B, kE, kBackward>(r, may);
         if (aligned_out) {
-          if (bounds_ok(on_16_bytes(to + i * kThreads * 8), status, NSM_KERNEL_ADJUST, 0, NSM_SITE_GRADIENT)) r.store(to + i * kThreads * 8);
+          if (bounds_ok(on_bytes(to + i * kThreads * kE, kStore), status, NSM_KERNEL_ADJUST, 0, NSM_SITE_GRADIENT)) r.store(to + i * kThreads * kE);
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) to[i * kThreads * 8 + e] = reinterpret_cast<const B*>(r.w)[e];
+          for (int e = 0; e < kE; ++e) to[i * kThreads * kE + e] = reinterpret_cast<const B*>(&r.w)[e];
         }
       }
     };
@@ -260,16 +298,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_adjust(const AdjustArgs a
 
     // the next slice's logits are asked for before this one's tokens are settled
     const Place last = now;
-    if (++now.row >= min(first + run, a.rows)) {
-      const int carry = now.slice + slice_step >= slices;
-      first += int64_t(run_step + carry) * run;
-      now.row = first;
-      now.slice += slice_step - (carry ? slices : 0);
-    }
-    const bool more = now.row < a.rows;
+    const float theta = a.repetition ? a.repetition[last.row] : 1.f;
+    const float frequency = a.frequency ? a.frequency[last.row] : 0.f;
+    const float presence = a.presence ? a.presence[last.row] : 0.f;
+    now.row = next_row;
+    now.slice = next_slice;
+    const bool more = now.row < rows;
     if (more) {
       place(now);
       fetch(now);
+      take(now, next_held);
+      advance(next_row, next_slice, first);
+      next_held = look(next_row);
     }
 
     // what a penalty or a bias is for, one token at a time, over what was just written
@@ -281,9 +321,6 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_adjust(const AdjustArgs a
       __syncthreads();
       const int n_listed = listed[parity];
       if (tid == 0) listed[parity ^ 1] = 0;
-      const float theta = a.repetition ? a.repetition[last.row] : 1.f;
-      const float frequency = a.frequency ? a.frequency[last.row] : 0.f;
-      const float presence = a.presence ? a.presence[last.row] : 0.f;
       for (int i = tid; i < n_listed; i += kThreads) {
         const int at = list[i], v = base + at;
         const uint32_t c = count[at], n = c & ~kHasBias;
@@ -293,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_adjust(const AdjustArgs a
         if (!bounds_ok(v >= 0 && v < vocab, status, NSM_KERNEL_ADJUST, 0, NSM_SITE_LOGITS)) continue;
         float f = Elem<A>::to_float(last.in[v]);
         if (n && a.repetition) {
-          const float sign = kBackward ? Elem<B>::to_float(static_cast<const B*>(a.logits)[last.row * a.ld_logits + v]) : f;
+          const float sign = kBackward ? Elem<B>::to_float(static_cast<const B*>(a.logits)[int64_t(last.row) * a.ld_logits + v]) : f;
           f = sign > 0.f ? f / theta : f * theta;
         }
         if (!kBackward) {
@@ -314,8 +351,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_adjust(const AdjustArgs a
 template <typename A, typename B, bool kBackward>
 cudaError_t launch_as(const AdjustArgs& a, int* status, cudaStream_t stream) {
   constexpr int kSlice = kSliceOf<A>;
-  const int units = (a.vocab + 7 + 7) / 8;  // the lead is at most seven
-  const int slices = (units + kSlice / 8 - 1) / (kSlice / 8);
+  const int slices = (a.vocab + 7 + kSlice - 1) / kSlice;  // the lead is at most seven
   const bool counts = a.history || a.k;
   const size_t places = kSlice + 8, smem = counts ? places * 6 + size_t(a.k) * 8 : 0;
   static std::atomic<uint64_t> done{0};
@@ -323,7 +359,7 @@ cudaError_t launch_as(const AdjustArgs& a, int* status, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // Rows that share histories are taken in runs, so that a history is counted once per run; a
   // block still gets four of them, of different slices.
-  const int64_t resident = int64_t(a.num_sms) * kBlocks;
+  const int64_t resident = int64_t(a.num_sms) * kBlocks<A>;
   const int run = a.history_row ? static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kRun, a.rows * slices / (4 * resident)))) : 1;
   const int64_t items = (a.rows + run - 1) / run * slices;
   const int grid = static_cast<int>(std::min<int64_t>(items, resident));

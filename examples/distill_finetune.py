@@ -1,6 +1,7 @@
 """Distils a small language model head from a teacher, with this library from the logits on:
 the teacher's top log probabilities (logprobs), the student's loss and gradient in one pass
-(distill_grad, or logprobs_grad for the plain cross-entropy), and the optimizer step
+(distill_grad, or logprobs_grad for the plain cross-entropy), the embedding and its gradient
+(embedding, embedding_backward), and the optimizer step on gradients clipped into its slots
 (MuonAdamW: Muon for the hidden matrices, AdamW for the embedding and the head).
 
     python examples/distill_finetune.py [--steps 40] [--loss distill|ce] [--vocab 5003]
@@ -20,6 +21,26 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import newton_schulz_orthogonalized_gb300 as nsm  # noqa: E402
 
 
+class Lookup(torch.autograd.Function):
+    """The library's embedding as a function that torch can differentiate."""
+
+    @staticmethod
+    def forward(ctx, weight, tokens):
+        out = torch.empty(len(tokens), weight.shape[1], dtype=weight.dtype, device=weight.device)
+        nsm.embedding(weight, tokens, out)
+        ctx.save_for_backward(tokens)
+        ctx.shape = weight.shape
+        return out
+
+    @staticmethod
+    def backward(ctx, d_out):
+        (tokens,) = ctx.saved_tensors
+        d_weight = torch.empty(ctx.shape, dtype=d_out.dtype, device=d_out.device)
+        workspace = torch.empty(nsm.embedding_workspace_bytes(len(tokens), *ctx.shape), dtype=torch.uint8, device=d_out.device)
+        nsm.embedding_backward(d_out.contiguous(), tokens, d_weight, workspace)
+        return d_weight, None
+
+
 class Model(torch.nn.Module):
     """Two embedded context tokens, a gated hidden layer, a head over the vocabulary."""
 
@@ -37,7 +58,7 @@ class Model(torch.nn.Module):
         self.lm_head = matrix(vocab, width, scale * width ** -0.5)
 
     def forward(self, context):
-        x = torch.nn.functional.embedding(context, self.embed_tokens).flatten(1)
+        x = Lookup.apply(self.embed_tokens, context.flatten()).view(len(context), -1)
         h = (torch.nn.functional.silu(x @ self.gate.T) * (x @ self.up.T)) @ self.down.T
         return torch.nn.functional.layer_norm(h, h.shape[1:]) @ self.lm_head.T
 
@@ -51,6 +72,7 @@ def main(argv=None):
     ap.add_argument("--rows", type=int, default=1024)
     ap.add_argument("--top", type=int, default=32)
     ap.add_argument("--temperature", type=float, default=1.0)
+    ap.add_argument("--max-norm", type=float, default=1.0)
     a = ap.parse_args(argv)
 
     teacher = Model(a.vocab, a.width, seed=1, scale=3.0)
@@ -88,15 +110,15 @@ def main(argv=None):
         logits.backward(d_logits)
         nsm.logprobs(logits.detach(), tokens, logprob, entropy)
         history.append((float(loss.mean()), float(logprob.mean()), float(entropy.mean())))
-        for n, p in named.items():
-            opt.grad(n).copy_(p.grad)
+        norm = opt.clip(a.max_norm, {n: p.grad for n, p in named.items()})
+        for p in named.values():
             p.grad = None
         opt.step()
         for n, p in named.items():
             p.data.copy_(opt.param(n))
         if step % max(1, a.steps // 8) == 0 or step == a.steps - 1:
             print(f"step {step:4d}  {a.loss} {history[-1][0]:8.4f}  log probability of the teacher's tokens "
-                  f"{history[-1][1]:8.4f}  entropy {history[-1][2]:7.4f}")
+                  f"{history[-1][1]:8.4f}  entropy {history[-1][2]:7.4f}  gradient norm {float(norm):7.4f}")
     status = nsm.device_status()
     if status != nsm.NSM_OK:
         raise RuntimeError(f"device status {status}")

@@ -47,6 +47,8 @@ MUON_MOMENTUM_DEFAULT = 0.95
 ADAM_LR_DEFAULT = 3e-4
 ADAM_BETAS_DEFAULT = (0.9, 0.95)
 ADAM_EPS_DEFAULT = 1e-10
+# an exponent that no matrix's entries fit: the step chooses one, as it does where none was left
+EXPONENT_NONE = 120
 
 _c_i32p = ctypes.POINTER(ctypes.c_int32)
 _c_i64p = ctypes.POINTER(ctypes.c_int64)
@@ -1025,6 +1027,9 @@ class MuonAdamW:
             self.muon_grads = torch.zeros(total, dtype=torch.bfloat16, device=dev)
             self.workspace = torch.empty(workspace_bytes(self.muon_shapes, ns_method, ns_steps),
                                          dtype=torch.uint8, device=dev)
+            # the step's exponents (its first 4 bytes per matrix): none yet, where whatever the memory held
+            # could be taken for one and change the last bits of the first step
+            self._exponents().fill_(EXPONENT_NONE)
         n_adam = sum(self.adam_sizes)
         self.adam_params = torch.zeros(n_adam, dtype=torch.float32, device=dev)
         self.adam_exp_avg = torch.zeros(n_adam, dtype=torch.float32, device=dev)
@@ -1032,6 +1037,11 @@ class MuonAdamW:
         self.adam_grads = torch.zeros(n_adam, dtype=torch.bfloat16, device=dev)
         self._clip = None  # the slots' table, norm and workspace, made by the first clip
         self.grad_norms = None
+
+    def _exponents(self):
+        """The exponents that the step keeps in its workspace, one int32 per Muon matrix."""
+        import torch
+        return self.workspace[:4 * len(self.muon_shapes)].view(torch.int32)
 
     def _view(self, name: str, muon_buf, adam_buf):
         shape = self._shape_of[name]
@@ -1058,8 +1068,9 @@ class MuonAdamW:
         """Scales all gradient slots together by min(1, max_norm / their norm); with ``grads`` (a
         mapping of every parameter's name to its gradient, bf16, fp16 or fp32) those are clipped
         into the slots, which takes the place of copying them there.  Returns the norm before
-        clipping (float32, one element on the device); ``grad_norms`` then holds each
-        parameter's, Muon's first, in the order of ``muon_names`` and ``adam_names``."""
+        clipping (float32, one element on the device, the same tensor at every call);
+        ``grad_norms`` then holds each parameter's, Muon's first, in the order of
+        ``muon_names`` and ``adam_names``."""
         import torch
         names = self.muon_names + self.adam_names
         buffers = (getattr(self, "muon_grads", None), self.adam_grads)
@@ -1100,7 +1111,8 @@ class MuonAdamW:
     def state_dict(self) -> Dict[str, object]:
         """The whole optimizer state as plain tensors (the caller saves and restores them):
         the step count, both groups' fp32 master weights, the Muon momentum and the AdamW
-        moments, with the names and shapes they were packed from."""
+        moments, with the names and shapes they were packed from, and the exponents that the
+        next step stores its input with."""
         d: Dict[str, object] = {"step": self.step_count,
                                 "muon_names": list(self.muon_names),
                                 "muon_shapes": list(self.muon_shapes),
@@ -1112,6 +1124,7 @@ class MuonAdamW:
         if self.muon_shapes:
             d["muon_params"] = self.muon_params
             d["muon_momentum"] = self.muon_momentum
+            d["muon_exponents"] = self._exponents()
         return d
 
     def load_state_dict(self, d: Dict[str, object]) -> None:
@@ -1126,3 +1139,7 @@ class MuonAdamW:
         if self.muon_shapes:
             self.muon_params.copy_(d["muon_params"])
             self.muon_momentum.copy_(d["muon_momentum"])
+            if d.get("muon_exponents") is None:  # a checkpoint from before they were carried
+                self._exponents().fill_(EXPONENT_NONE)
+            else:
+                self._exponents().copy_(d["muon_exponents"])

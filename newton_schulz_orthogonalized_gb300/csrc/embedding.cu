@@ -16,7 +16,12 @@
 //                  sum in the workspace.  Blocks behind those clear the rows of the gradient that no token
 //                  asks for.
 //   k_embed_join   adds up such tokens' sums.
-// No atomic adds a floating-point number: the order of every sum is set by the tokens alone.
+// No atomic adds a floating-point number: the order of every sum is set by the sizes and the tokens.
+//
+// Bound by memory where rows are many (the gradient of 65536 x 4096 bf16 rows into 131072: 274 us, of
+// which sums and clearing 235 at 6.7 TB/s; the lookup of 65536 x 2048 from 100003: 79 us), and by
+// its kernels' latencies where they are few (16384 x 768 into 50257: 37 us; 257 x 769 added to
+// 32003 fp32 rows: 12.5 us).
 #include "elem.cuh"
 #include "launch.cuh"
 #include "nsm_internal.h"
@@ -37,12 +42,15 @@ constexpr int kPlaceThreads = 512;
 constexpr int kPlaceWarps = kPlaceThreads / 32;
 constexpr int kBlockThreads = 1024;  // of k_sort_block
 constexpr int kBlockRows = 4096;     // that it takes at most
-constexpr int kMaxPiece = 32, kMinPiece = 4;  // sorted entries of a piece
+// Sorted entries of a piece: the most that still make so many warps, 16 for each SM.  Pieces of 32
+// whatever the sizes took 53 us for 257 x 769 in place of 13.
+constexpr int kMaxPiece = 32, kMinPiece = 4;
 constexpr int kWantedWarps = 152 * 16;
 constexpr int kEmbedBlocks = 152 * 16;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinPieces = 8;  // that a block of k_embed_join looks at
-// Bytes of rows without a token that a sorting pass clears on the side.
+// Bytes of rows without a token that a sorting pass clears on the side: about what its time leaves
+// room for (12 and 40 MB take as long).
 constexpr int64_t kClearBytes = 24 << 20;
 constexpr int kClearBlocks = 150;  // that clear beside k_sort_block's first
 constexpr int kClear = 8;      // rows of the gradient that a warp looks at

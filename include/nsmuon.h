@@ -420,7 +420,8 @@ int nsm_adjust_logits_backward(const void* logits, int dtype, int64_t rows, int6
  *     (tokens_wide != 0) or int32 per row.
  *     1 <= vocab <= 2^30, 1 <= cols <= 2^20, 0 <= rows <= 2^30.
  *   - Elements between the columns and the row stride are left as they are.
- *   - Sums are fp32 in the order of the rows, the same from call to call; results are rounded once.
+ *   - Sums are fp32, in an order that the sizes and the tokens set (a token's rows ascending, in pieces
+ *     whose sums are added in turn): the same from call to call.  Results are rounded once.
  *   - scale is finite.  No buffer that a call writes may overlap another one. */
 int nsm_embedding(const void* weight, int dtype, int64_t vocab, int64_t cols, int64_t ldw, const void* tokens, int tokens_wide,
                   int64_t rows, float scale, void* out, int out_dtype, int64_t ldo, nsm_stream_t stream);

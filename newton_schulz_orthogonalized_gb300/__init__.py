@@ -756,8 +756,8 @@ def embedding_backward(d_out, tokens, d_weight, workspace, scale: float = 1.0, a
     """The gradient of :func:`embedding`: d_weight[v] = scale * the sum of d_out's rows of token
     v, zeros in rows without one; with ``accumulate`` the sums are added to what ``d_weight``
     holds (a weight that is the output layer's too).  ``d_weight`` and ``d_out`` have any of the
-    three types each; ``MuonAdamW.grad(name)`` is such a ``d_weight``.  The order of every sum is that
-    of the rows."""
+    three types each; ``MuonAdamW.grad(name)`` is such a ``d_weight``.  The order of every sum is set
+    by the sizes and the tokens."""
     w_ptr, w_code, vocab, cols, ldw, dev = _rows_of("d_weight", d_weight)
     rows = len(tokens)
     t_ptr, wide = _tokens(tokens, rows, dev)

@@ -88,6 +88,13 @@ def test_clip_refusals(nsm):
     assert _clip(nsm, out=(C, C + 0x1001, 0)) == E.NSM_ERR_ALIGN
 
 
+def test_timing_kinds(nsm):
+    for kind in (nsm.KIND_ADJUST, nsm.KIND_EMBEDDING, nsm.KIND_GRADS):
+        assert nsm.timing_read(kind) == (0.0, 0, 0.0) and kind in nsm.KIND_NAMES
+    with pytest.raises(nsm.NsmError):
+        nsm.timing_read(max(nsm.KIND_NAMES) + 1)
+
+
 def test_workspace_bytes(nsm):
     k = (ctypes.c_int64 * 3)(0, 1, 1 << 30)
     b = nsm.lib().nsm_grad_workspace_bytes(k, 3)

@@ -177,6 +177,32 @@ def test_only_what_is_asked_for(nsm):
     _backward_near(d, x, x, {"mask": kw["mask"]}, "bf16")
 
 
+def test_tables_with_row_strides(nsm):
+    """Histories, biases and masks that are views of wider buffers, and begin anywhere."""
+    torch = _torch()
+    x, kw = _inputs(7, 9001, "bf16", 21, 301, 3, 6, 4)
+
+    def strided(t, first, pad):
+        buf = torch.full((t.shape[0] * (t.shape[1] + pad) + first,), 5, dtype=t.dtype, device="cuda")
+        v = buf[first:].view(t.shape[0], t.shape[1] + pad)[:, :t.shape[1]]
+        v.copy_(t)
+        return v
+
+    want, d_want = torch.empty(7, 9001, device="cuda"), torch.empty_like(x)
+    nsm.adjust_logits(x, want, **kw)
+    nsm.adjust_logits_backward(x, x, d_want, **_back(kw))
+    for first, pad in ((1, 0), (0, 3), (3, 5)):
+        for wide in (True, False):
+            other = dict(kw)
+            for n in ("history", "bias_index"):
+                other[n] = strided(kw[n].long() if wide else kw[n].int(), first, pad)
+            other["bias"], other["mask"] = strided(kw["bias"], first, pad), strided(kw["mask"], first, pad)
+            out, d = torch.empty_like(want), torch.empty_like(x)
+            nsm.adjust_logits(x, out, **other)
+            nsm.adjust_logits_backward(x, x, d, **_back(other))
+            assert torch.equal(out, want) and torch.equal(d, d_want)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 def test_values_that_are_no_numbers(nsm, dtype):
     """A banned token is -inf (its gradient 0) whatever stood there; infinities keep their sign."""

@@ -240,3 +240,24 @@ def test_workspace_refusals(nsm):
         nsm.embedding_backward(d, t, w, torch.zeros(ws.numel(), dtype=torch.uint8))
     with pytest.raises(nsm.NsmError):
         nsm.embedding_backward(d, t, w, w.view(torch.uint8).view(-1))
+
+
+@pytest.mark.parametrize("rows,vocab,cols", [(9000, 300000, 24), (5000, (1 << 28) + 5, 1)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_gradient_of_more_sorting_passes(nsm, rows, vocab, cols, accumulate):
+    """Vocabularies whose tokens take three and four digits."""
+    torch = _torch()
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    tokens = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    tokens[: rows // 3] = tokens[-(rows // 3):] // 4096 * 4096 % vocab  # some tokens several times
+    tokens[::11] = -100
+    d_out = torch.randn(rows, cols, generator=g, device="cuda")
+    w = torch.full((vocab, cols), 0.5, dtype=torch.bfloat16, device="cuda")
+    nsm.embedding_backward(d_out, tokens, w, _workspace(nsm, rows, vocab, cols), accumulate=accumulate)
+    live = tokens >= 0
+    some, place = torch.unique(tokens[live], return_inverse=True)
+    start = 0.5 if accumulate else 0.0
+    got = w[some]
+    _sum_near(got, d_out[live], place, len(some), 1.0, torch.full_like(got, 0.5) if accumulate else None, "bf16")
+    w[some] = start
+    assert bool((w == start).all())

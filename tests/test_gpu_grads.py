@@ -213,6 +213,29 @@ def test_more_than_2_31_elements(nsm):
     assert norm.item() == 13.0 and [float(g[i]) for i in (-1, 0, 1 << 31)] == [1.5, 2.0, 6.0]
 
 
+def test_more_sums_than_a_block_adds(nsm):
+    """Many launches, whose blocks' sums one launch adds first; in place and to slots."""
+    torch = _torch()
+    n, size = 8000, 20000
+    buffer = torch.randn(n * size, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").bfloat16()
+    grads = list(buffer.view(n, size))
+    slots = torch.empty(n, size, dtype=torch.bfloat16, device="cuda")
+    table = nsm.GradTable(grads, list(slots))
+    norm, norms = torch.empty(1, device="cuda"), torch.empty(n, device="cuda")
+    ws = torch.empty(table.workspace_bytes, dtype=torch.uint8, device="cuda")
+    nsm.clip_grads(table, 2.0, norm, norms, workspace=ws)
+    each = torch.linalg.vector_norm(buffer.view(n, size), dim=1, dtype=torch.float64)
+    want = float(torch.linalg.vector_norm(each))
+    _near(norm.item(), want)
+    _near(norms.cpu(), each.cpu())
+    clipped = buffer.view(n, size).double() * (2.0 / want)
+    assert bool(((slots.double() - clipped).abs() <= (NORM_TOL + 2 * 2.0 ** -24 + 2.0 ** -8) * clipped.abs() * 1.0001 + LEAST["bf16"]).all())
+    norm.zero_()
+    nsm.clip_grads(grads, 2.0, norm, workspace=ws)
+    _near(norm.item(), want)
+    assert torch.equal(buffer.view(n, size), slots)
+
+
 def test_refusals(nsm):
     torch = _torch()
     a, b = torch.zeros(100, device="cuda"), torch.zeros(100, device="cuda")

@@ -1035,8 +1035,13 @@ class MuonAdamW:
         self.adam_exp_avg = torch.zeros(n_adam, dtype=torch.float32, device=dev)
         self.adam_exp_avg_sq = torch.zeros(n_adam, dtype=torch.float32, device=dev)
         self.adam_grads = torch.zeros(n_adam, dtype=torch.bfloat16, device=dev)
-        self._clip = None  # the slots' table, norm and workspace, made by the first clip
-        self.grad_norms = None
+        # clip's outputs and workspace: made here, so that a first clip on a stream of its own finds them ready
+        self._clip = None  # the slots' table, made by the first clip
+        numels = np.array([m * n for m, n in self.muon_shapes] + self.adam_sizes, dtype=np.int64)
+        self._clip_norm = torch.zeros(1, dtype=torch.float32, device=dev)
+        self.grad_norms = torch.zeros(len(numels), dtype=torch.float32, device=dev)
+        self._clip_workspace = torch.empty(lib().nsm_grad_workspace_bytes(numels.ctypes.data, len(numels)),
+                                           dtype=torch.uint8, device=dev)
 
     def _exponents(self):
         """The exponents that the step keeps in its workspace, one int32 per Muon matrix."""
@@ -1071,17 +1076,12 @@ class MuonAdamW:
         clipping (float32, one element on the device, the same tensor at every call);
         ``grad_norms`` then holds each parameter's, Muon's first, in the order of
         ``muon_names`` and ``adam_names``."""
-        import torch
         names = self.muon_names + self.adam_names
         buffers = (getattr(self, "muon_grads", None), self.adam_grads)
-        if self._clip is None or any(a is not b for a, b in zip(self._clip[4], buffers)):
+        if self._clip is None or any(a is not b for a, b in zip(self._clip[2], buffers)):
             slots = [self.grad(n) for n in names]
-            table = GradTable(slots)
-            dev = self.adam_params.device
-            self.grad_norms = torch.zeros(len(names), dtype=torch.float32, device=dev)
-            self._clip = (slots, table, torch.zeros(1, dtype=torch.float32, device=dev),
-                          torch.empty(table.workspace_bytes, dtype=torch.uint8, device=dev), buffers)
-        slots, table, norm, workspace, _ = self._clip
+            self._clip = (slots, GradTable(slots), buffers)
+        slots, table, _ = self._clip
         if grads is not None:
             lacking = [n for n in names if grads.get(n) is None]
             if lacking or len(grads) != len(names):
@@ -1090,8 +1090,8 @@ class MuonAdamW:
                 if tuple(grads[n].shape) != self._shape_of[n]:
                     raise ValueError(f"the gradient of {n!r} has shape {tuple(grads[n].shape)}: {self._shape_of[n]} is wanted")
             table = GradTable([grads[n] for n in names], slots)
-        clip_grads(table, max_norm, norm, self.grad_norms, workspace=workspace, stream=stream)
-        return norm
+        clip_grads(table, max_norm, self._clip_norm, self.grad_norms, workspace=self._clip_workspace, stream=stream)
+        return self._clip_norm
 
     def step(self, stream=None, max_norm: Optional[float] = None) -> None:
         """One step of both groups on the slots' gradients, clipped to ``max_norm`` together

@@ -236,6 +236,30 @@ def test_more_sums_than_a_block_adds(nsm):
     assert torch.equal(buffer.view(n, size), slots)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_first_clip_on_a_stream_of_its_own(nsm, captured):
+    """While the current stream is behind: nothing that it still has to do is the clip's."""
+    torch = _torch()
+    opt = nsm.MuonAdamW([("layers.0.proj.weight", (64, 96)), ("norm.bias", (64,))])
+    opt.grad("layers.0.proj.weight").fill_(0.5)
+    opt.grad("norm.bias").fill_(2.0)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            norm = opt.clip(1.0)
+        opt.grad_norms.zero_()
+        norm.zero_()
+        graph.replay()
+    else:
+        torch.cuda._sleep(100_000_000)
+        norm = opt.clip(1.0, stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    _near(norm.item(), (64 * 96 * 0.25 + 64 * 4.0) ** 0.5)
+    _near(opt.grad_norms.cpu(), [(64 * 96 * 0.25) ** 0.5, 16.0])
+
+
 def test_refusals(nsm):
     torch = _torch()
     a, b = torch.zeros(100, device="cuda"), torch.zeros(100, device="cuda")

@@ -1112,7 +1112,8 @@ class MuonAdamW:
         """The whole optimizer state as plain tensors (the caller saves and restores them):
         the step count, both groups' fp32 master weights, the Muon momentum and the AdamW
         moments, with the names and shapes they were packed from, and the exponents that the
-        next step stores its input with."""
+        next step stores its input with (a copy of their own, made on the current stream: a view
+        would save the whole workspace with them)."""
         d: Dict[str, object] = {"step": self.step_count,
                                 "muon_names": list(self.muon_names),
                                 "muon_shapes": list(self.muon_shapes),
@@ -1124,7 +1125,7 @@ class MuonAdamW:
         if self.muon_shapes:
             d["muon_params"] = self.muon_params
             d["muon_momentum"] = self.muon_momentum
-            d["muon_exponents"] = self._exponents()
+            d["muon_exponents"] = self._exponents().clone()
         return d
 
     def load_state_dict(self, d: Dict[str, object]) -> None:

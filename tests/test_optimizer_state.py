@@ -1,0 +1,40 @@
+"""MuonAdamW's state without a GPU: what a checkpoint holds, and calls on optimizers at the edge of
+what they are made for."""
+
+import io
+import os
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def nsm():
+    import newton_schulz_orthogonalized_gb300 as m
+    if not os.path.exists(m.LIB_PATH):
+        from newton_schulz_orthogonalized_gb300 import _build
+        _build.build()
+    m.lib()
+    return m
+
+
+NAMED = [("layers.0.proj.weight", (128, 256)), ("layers.1.proj.weight", (300, 200)), ("norm.weight", (77,))]
+
+
+def test_a_checkpoint_holds_its_tensors_and_no_more(nsm):
+    """Saving a view writes all that its storage holds: none may be of the step's workspace."""
+    import torch
+    opt = nsm.MuonAdamW(NAMED, device="cpu")
+    state = opt.state_dict()
+    own = 0
+    for key, t in state.items():
+        if torch.is_tensor(t):
+            assert t.untyped_storage().nbytes() == t.numel() * t.element_size(), key
+            own += t.numel() * t.element_size()
+    file = io.BytesIO()
+    torch.save(state, file)
+    assert own <= file.tell() < own + (1 << 16)  # and the names, sizes and headers
+    assert state["muon_exponents"].tolist() == [nsm.EXPONENT_NONE] * 2
+    opt._exponents().copy_(torch.tensor([3, -5]))
+    other = nsm.MuonAdamW(NAMED, device="cpu")
+    other.load_state_dict(opt.state_dict())
+    assert other._exponents().tolist() == [3, -5]

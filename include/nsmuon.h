@@ -436,8 +436,8 @@ int nsm_embedding_backward(const void* d_out, int dtype, int64_t rows, int64_t c
                            int tokens_wide, int64_t vocab, float scale, int accumulate, void* d_weight, int weight_dtype,
                            int64_t ldw, void* workspace, size_t workspace_bytes, nsm_stream_t stream);
 
-/* Bytes of that workspace; 0 when a size is invalid (the reason is in nsm_last_error()).
- * Host-only. */
+/* Bytes of that workspace; 0 when a size is invalid (the reason is in nsm_last_error()).  They do
+ * not fall as rows grow: a workspace for the largest batch serves the smaller ones.  Host-only. */
 size_t nsm_embedding_workspace_bytes(int64_t rows, int64_t vocab, int64_t cols);
 
 /* ---- The norm of many gradients, and clipping ------------------------------------------

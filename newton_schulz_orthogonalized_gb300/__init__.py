@@ -744,7 +744,7 @@ def embedding(weight, tokens, out, scale: float = 1.0, stream=None) -> None:
 
 
 def embedding_workspace_bytes(rows: int, vocab: int, cols: int) -> int:
-    """Bytes of :func:`embedding_backward`'s workspace."""
+    """Bytes of :func:`embedding_backward`'s workspace; one for the largest batch serves smaller ones."""
     b = lib().nsm_embedding_workspace_bytes(int(rows), int(vocab), int(cols))
     if b == 0:
         raise NsmError(NSM_ERR_SHAPE, last_error())

@@ -691,16 +691,23 @@ EmbeddingPlan embedding_plan(int64_t rows, int64_t vocab, int64_t cols) {
   p.tiles = static_cast<int32_t>((rows + p.tile - 1) / p.tile);
   // the longest pieces that still make some 16 warps for each SM
   const Cut cut = cut_rows(cols, true), wide = cut_rows(cols, false);
-  p.piece = std::min(kMaxPiece, 8 * cut.lanes);  // a block's pairs are 16 KB and little more at most
+  const int32_t longest = std::min(kMaxPiece, 8 * cut.lanes);  // a block's pairs are 16 KB and little more at most
+  p.piece = longest;
   while (p.piece > kMinPiece && (rows + p.piece - 1) / p.piece * cut.slices * cut.lanes < int64_t(kWantedWarps) * 32) p.piece /= 2;
   p.units = static_cast<int32_t>((rows + p.piece - 1) / p.piece);
   p.cols = std::max(int64_t(cut.lanes) * cut.slices, int64_t(wide.lanes) * wide.slices) * 8;
   p.off_pairs[0] = 0;
   p.off_pairs[1] = p.off_pairs[0] + up(size_t(rows) * 8);
   p.off_counts = p.off_pairs[1] + up(p.passes > 1 ? size_t(rows) * 8 : 0);
-  p.off_last = p.off_counts + up(size_t(p.passes) * size_t(p.tiles) * 4 << p.bits);
+  // Room for the most tiles and pieces that any smaller number of rows has, where their lengths grow there are
+  // fewer: the bytes never fall as rows grow, and a workspace for the largest batch serves all.  A length below
+  // the longest is taken only while pieces of twice that length are too few, `few` at most.
+  const int64_t tiles = std::min<int64_t>(kMaxTiles, (rows + 1023) / 1024);
+  const int64_t few = (int64_t(kWantedWarps) * 32 - 1) / (int64_t(cut.slices) * cut.lanes);
+  const int64_t units = std::max(std::min((rows + kMinPiece - 1) / kMinPiece, 2 * few), (rows + longest - 1) / longest);
+  p.off_last = p.off_counts + up(size_t(p.passes) * size_t(tiles) * 4 << p.bits);
   p.off_sums = p.off_last + up(size_t(vocab) * 4);
-  p.bytes = p.off_sums + up(size_t(p.units) * 2 * size_t(p.cols) * 4);
+  p.bytes = p.off_sums + up(size_t(units) * 2 * size_t(p.cols) * 4);
   return p;
 }
 

@@ -346,6 +346,8 @@ constexpr int kBatch = 1;  // vectors under way per thread of k_grad_clip; 2 too
 // goes on for `before` and `after` elements.
 template <int NT, typename T, typename O>
 __device__ __noinline__ void scale_chunk(const T* p, O* out, int n, int before, int after, float factor, float more, int* status) {
+  if constexpr (std::is_same<T, O>::value)  // in place a factor of 1 writes nothing: the product would give NaNs other bits
+    if (p == out && factor * more == 1.f) return;
   const int lead = lead_of(out), units = (n + lead + 7) / 8;
   const auto put = [&](int u, const Eight<T>& r) {
     float f[8];

@@ -1077,6 +1077,12 @@ class MuonAdamW:
         ``grad_norms`` then holds each parameter's, Muon's first, in the order of
         ``muon_names`` and ``adam_names``."""
         names = self.muon_names + self.adam_names
+        if not names:  # an owner that got none: its norm stays 0
+            if grads:
+                raise ValueError("grads names parameters, and the optimizer has none")
+            if not 0.0 < max_norm < float("inf"):
+                raise NsmError(NSM_ERR_ARG, "max_norm must be positive and finite")
+            return self._clip_norm
         buffers = (getattr(self, "muon_grads", None), self.adam_grads)
         if self._clip is None or any(a is not b for a, b in zip(self._clip[2], buffers)):
             slots = [self.grad(n) for n in names]

@@ -38,3 +38,19 @@ def test_a_checkpoint_holds_its_tensors_and_no_more(nsm):
     other = nsm.MuonAdamW(NAMED, device="cpu")
     other.load_state_dict(opt.state_dict())
     assert other._exponents().tolist() == [3, -5]
+
+
+def test_an_optimizer_without_parameters_clips_nothing(nsm):
+    """An owner that got none: its norm is 0, and a step that clips is a step."""
+    opt = nsm.MuonAdamW([], device="cpu")
+    opt.step()
+    opt.step(max_norm=1.0)
+    assert opt.step_count == 2
+    for grads in (None, {}):
+        norm = opt.clip(2.0, grads)
+        assert norm.tolist() == [0.0] and opt.grad_norms.numel() == 0
+    for bad in (0.0, -1.0, float("nan"), float("inf")):
+        with pytest.raises(nsm.NsmError):
+            opt.clip(bad)
+    with pytest.raises(ValueError):
+        opt.clip(1.0, {"a": None})

@@ -1083,10 +1083,10 @@ class MuonAdamW:
             if not 0.0 < max_norm < float("inf"):
                 raise NsmError(NSM_ERR_ARG, "max_norm must be positive and finite")
             return self._clip_norm
-        buffers = (getattr(self, "muon_grads", None), self.adam_grads)
-        if self._clip is None or any(a is not b for a, b in zip(self._clip[2], buffers)):
+        places = [b.data_ptr() for b in (getattr(self, "muon_grads", None), self.adam_grads) if b is not None]
+        if self._clip is None or self._clip[2] != places:  # its views hold the memory that its places are in
             slots = [self.grad(n) for n in names]
-            self._clip = (slots, GradTable(slots), buffers)
+            self._clip = (slots, GradTable(slots), places)
         slots, table, _ = self._clip
         if grads is not None:
             lacking = [n for n in names if grads.get(n) is None]

@@ -54,3 +54,22 @@ def test_an_optimizer_without_parameters_clips_nothing(nsm):
             opt.clip(bad)
     with pytest.raises(ValueError):
         opt.clip(1.0, {"a": None})
+
+
+def test_clip_finds_slots_that_have_moved(nsm, monkeypatch):
+    """The slots' buffers are plain tensors, whose memory a program may change between two clips, as between
+    two steps: the kept table is of where they are."""
+    import torch
+    opt = nsm.MuonAdamW(NAMED, device="cpu")
+    clipped = []
+    monkeypatch.setattr(nsm, "GradTable", lambda grads, out=None: [t.data_ptr() for t in (out or grads)])
+    monkeypatch.setattr(nsm, "clip_grads", lambda table, *args, **kw: clipped.append(table))
+    grads = {n: torch.zeros(s) for n, s in NAMED}
+    for move in (lambda: None, lambda: setattr(opt.muon_grads, "data", opt.muon_grads.clone()),
+                 lambda: opt.adam_grads.set_(opt.adam_grads.clone()), lambda: setattr(opt, "muon_grads", opt.muon_grads.clone())):
+        move()
+        for given in (None, grads):
+            opt.clip(1.0, given)
+            assert clipped[-1] == [opt.grad(n).data_ptr() for n in opt.muon_names + opt.adam_names]
+    opt.clip(1.0)
+    assert clipped[-1] is clipped[-3]  # made once while they stay

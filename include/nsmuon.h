@@ -370,6 +370,9 @@ int nsm_distill_backward(const void* logits, int dtype, int64_t rows, int64_t vo
  *     history_len <= 2^30.  Rows of one sequence can so share its tokens, each up to its own position.  A token
  *     outside [0, vocab) does not count; a history_row outside [0, history_rows) is no history.
  *     history may be NULL (no penalties; with history_len 0 its address is not looked at).
+ *     All three penalties count over this one history.  Where some are to count other tokens
+ *     (repetition a prompt's too, the others the answer's alone) that takes two calls: one with
+ *     repetition, to fp32, and one with the others and the mask, in place.
  *   - repetition, frequency, presence: device, fp32, one per row; each may be NULL (1, 0, 0).
  *     repetition is positive; what it holds is not looked at on the host.
  *   - bias_index, bias: device, rows x k of int64 (bias_wide != 0) or int32, and of fp32, row
@@ -451,8 +454,12 @@ size_t nsm_embedding_workspace_bytes(int64_t rows, int64_t vocab, int64_t cols);
  *   workspace device, >= nsm_grad_workspace_bytes(numels, n) bytes, 256-byte aligned; any
  *             content, overwritten.  Calls that share one are ordered by the caller.
  * The norm has fp32's precision over the whole range of the types: squares neither overflow
- * nor vanish (it is +inf only where the norm itself is past fp32's largest value).  A tensor with an
- * infinity or a NaN has that as its norm.  The sums run in a fixed order. */
+ * nor vanish (without an infinity among the gradients it is +inf only where the norm itself is past
+ * fp32's largest value).  A tensor with an infinity or a NaN has that as its norm.  The sums run in a
+ * fixed order.
+ * It is the norm of the tensors given and of no others: where the gradients of a model are split
+ * among processes, each gets that of its own part (the whole one's square is the sum of their squares)
+ * and clips by it. */
 int nsm_grad_norm(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int n, float* norm, float* norms,
                   void* workspace, size_t workspace_bytes, nsm_stream_t stream);
 
@@ -464,7 +471,9 @@ int nsm_grad_norm(const void* const* grads, const int64_t* numels, const int32_t
  *   max_norm  positive and finite
  *   norm      device, one fp32, or NULL
  * Each result is g times an fp32 factor, rounded once.  Where the norm is no more than max_norm,
- * or is infinite or NaN, the factor is 1: in place nothing is written. */
+ * or some gradient holds an infinity or a NaN, the factor is 1: in place nothing is written.  Finite
+ * gradients are clipped even where *norm is +inf for being past fp32's range: *norm alone does not
+ * tell the two apart. */
 int nsm_clip_grads(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int n, void* const* out,
                    const int32_t* out_dtypes, float max_norm, float* norm, float* norms, void* workspace,
                    size_t workspace_bytes, nsm_stream_t stream);

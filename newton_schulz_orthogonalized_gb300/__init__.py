@@ -671,7 +671,7 @@ def adjust_logits(logits, out, history=None, length=None, history_row=None, repe
     ``history`` (int32 or int64, history rows x tokens): row r's is the first ``length[r]``
     (int32, None: all) tokens of row ``history_row[r]`` (int32, None: r).  ``repetition``,
     ``frequency`` and ``presence`` are float32, one per row.  ``bias_index`` (int32 or int64) and
-    ``bias`` (float32) are rows x k, k <= 1024.  ``mask`` (int32, mask rows x ceil(vocab / 32)) has
+    ``bias`` (float32) are rows x k, k <= 1024.  All penalties count over the one history.  ``mask`` (int32, mask rows x ceil(vocab / 32)) has
     bit v % 32 of word v // 32 set where v is allowed; row r's is ``mask_row[r]`` (int32, None: r;
     -1: everything is allowed).  Indexes outside the vocabulary do not count."""
     ptr, code, rows, vocab, ld, dev = _logits(logits)
@@ -785,7 +785,9 @@ def _workspace(workspace, device: int) -> Tuple[int, int]:
 class GradTable:
     """The places of many gradients and, for :func:`clip_grads`, of where the clipped ones go
     (``out``, None: in place).  A program whose gradients stay where they are keeps one from step to
-    step; it holds the tensors.  Each is contiguous, bf16, fp16 or fp32, all on one device."""
+    step; it holds the tensors, and the places that their memory had when it was made: one whose
+    memory is changed (``.data``, ``set_``) wants a new table.  Each is contiguous, bf16, fp16 or fp32,
+    all on one device."""
 
     def __init__(self, grads: Sequence, out: Optional[Sequence] = None):
         if _FLOAT32 is None:
@@ -850,7 +852,8 @@ class GradTable:
 def grad_norm(grads, norm, norms=None, workspace=None, stream=None) -> None:
     """Writes the norm of all gradients together to ``norm`` (float32, one element) and each
     one's to ``norms`` (float32, one per gradient, or None).  ``grads`` is a :class:`GradTable` or a
-    list of tensors; ``workspace`` has the table's ``workspace_bytes``."""
+    list of tensors; ``workspace``, which the call cannot do without, has the table's
+    ``workspace_bytes``."""
     table = grads if isinstance(grads, GradTable) else GradTable(grads)
     _check(lib().nsm_grad_norm(*table._in_args, *table._checked(norm, norms, workspace, stream)))
     _written(norm, norms)
@@ -858,8 +861,9 @@ def grad_norm(grads, norm, norms=None, workspace=None, stream=None) -> None:
 
 def clip_grads(grads, max_norm: float, norm=None, norms=None, workspace=None, stream=None) -> None:
     """Scales the gradients by min(1, max_norm / norm), in place or to the table's ``out``
-    (converted to its types), and writes the norms before clipping as :func:`grad_norm` does.
-    A norm that is infinite or NaN leaves the gradients as they are."""
+    (converted to its types), and writes the norms before clipping as :func:`grad_norm` does, with
+    the same ``workspace``.  An infinity or a NaN in some gradient leaves all as they are; finite ones
+    whose norm is past float32's range (written as infinity) are clipped."""
     table = grads if isinstance(grads, GradTable) else GradTable(grads)
     _check(lib().nsm_clip_grads(*table._in_args, *table._out_args, float(max_norm),
                                 *table._checked(norm, norms, workspace, stream)))
@@ -1075,7 +1079,8 @@ class MuonAdamW:
         into the slots, which takes the place of copying them there.  Returns the norm before
         clipping (float32, one element on the device, the same tensor at every call);
         ``grad_norms`` then holds each parameter's, Muon's first, in the order of
-        ``muon_names`` and ``adam_names``."""
+        ``muon_names`` and ``adam_names``.  The norm is that of this optimizer's parameters: one owner
+        among several clips by its own."""
         names = self.muon_names + self.adam_names
         if not names:  # an owner that got none: its norm stays 0
             if grads:

@@ -16,7 +16,7 @@
 // captured call keeps its own.  All sums run in a fixed order.
 //
 // Bound by memory: the norm of 1.4G fp32 gradients takes 772 us (7.3 TB/s), clipping them into bf16 slots
-// 1240 more (6.8 TB/s read and written); 149 tensors of 163M bf16 elements take 58 and 166 us together.
+// 1240 more (6.8 TB/s read and written); 147 tensors of 163M bf16 elements take 58 and 166 us together.
 #include "elem.cuh"
 #include "launch.cuh"
 #include "nsm_internal.h"
@@ -255,7 +255,7 @@ __device__ __forceinline__ void for_tensors(const Table<kMost>& table, int chunk
   }
 }
 
-// One type alone takes 57 registers a thread, several together twice that; and the 64-bit sums in the same
+// One type alone takes 57 registers a thread (fp16 59), several together 96; and the 64-bit sums in the same
 // kernel made its loop spill (5.7 GB of fp32 3070 us for 810), so they have one of their own.
 template <int kMost, typename T>
 __global__ void __launch_bounds__(kThreads, std::is_same<T, void>::value ? 2 : kBlocks)
@@ -562,7 +562,7 @@ cudaError_t launch_grad_clip(const GradTensor* tensors, int n, int chunks, const
   int* status = device_status_ptr();
   if (!status) return cudaErrorInvalidSymbol;
   return with_table(tensors, n, [&](const auto& t) {
-    return launch_pdl(k_grad_clip<sizeof(t.t) / sizeof(t.t[0])>, dim3(std::min(chunks, 152 * kClipBlocks)), dim3(kThreads), 0, stream, t, chunks, grad_blocks(chunks),
+    return launch_pdl(k_grad_clip<sizeof(t.t) / sizeof(t.t[0])>, dim3(std::min(chunks, kGradSms * kClipBlocks)), dim3(kThreads), 0, stream, t, chunks, grad_blocks(chunks),
                       parts, norms, totals, n_totals, max_norm, norm, in_place, status);
   });
 }

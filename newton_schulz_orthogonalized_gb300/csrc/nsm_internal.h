@@ -310,7 +310,9 @@ EmbeddingPlan embedding_plan(int64_t rows, int64_t vocab, int64_t cols);
 
 constexpr int kGradChunk = 16384;  // elements that one block sums at a time
 constexpr int kGradTable = 512;    // tensors of one launch at most
-constexpr int kGradBlocks = 152 * 4;  // blocks of one launch at most
+// A GB300's SMs, as a constant: the workspace's size and the order of the sums follow from the blocks
+constexpr int kGradSms = 152;
+constexpr int kGradBlocks = kGradSms * 4;  // blocks of one launch at most
 constexpr int kGradSmall = 32;     // chunks of a table that one cluster takes
 constexpr int kGradTotals = 8192;  // blocks' sums that every clipping block adds for itself, at most
 

@@ -81,7 +81,8 @@ constexpr int kUnitOf = 16 / sizeof(A);
 template <typename A>
 constexpr int kSliceOf = kThreads * (sizeof(A) == 4 ? 16 : 32);
 // Resident blocks of an SM.  8192 x 50257 bf16 with histories takes 281 us with 7, 341 with 8 (whose 64
-// registers a thread are too few) and 295 with 6; 2049 x 65537 fp32 203 with 8, 380 with 9, 214 with 7.
+// registers a thread are too few) and 295 with 6, 256 x 131072 bf16 to fp32 55, 59 and 60; 2049 x 65537 fp32 203 with 8,
+// 380 with 9, 214 with 7.
 template <typename A>
 constexpr int kBlocks = sizeof(A) == 4 ? 8 : 7;
 
